@@ -243,10 +243,24 @@ hss_status hss_get_error(const void* ws, hipStream_t stream);
  *     factors directly; wider batches first expand them into flat m x r /
  *     r x n factors inside the workspace (hss_apply_workspace_size counts
  *     them).  hss_grad does not take HSS_HIER2 (HSS_ERR_UNSUPPORTED).
+ *   flags & HSS_MX4: a microscaled 4-bit dense part D (MXFP4) is added to
+ *     the layer, next to S and the low-rank term (either may be empty: nnz =
+ *     0, r = 0):  Y = X (S + U V^T + D)^T.
+ *       dq_codes, dq_levels: the codes (16-byte aligned) and the scale bytes
+ *         of D (m x n) as hss_mx_quantize writes them (HSS_MXFP4).
+ *     Requires fmt == HSS_FMT_CSR, no HSS_DQ4 and no HSS_HIER2; bf16 layers
+ *     (an fp32 one returns HSS_ERR_UNSUPPORTED); 32 m ceil(n/32),
+ *     32 n ceil(m/32), and 64 max(m, b) ceil(r/32) < 2^31.  hss_grad and
+ *     hss_grad_ckpt give the gradients of S, U and V; D has none.
+ *   flags & HSS_MX4_T (with HSS_MX4): the two arrays hold D^T, an n x m
+ *     matrix, so that the transposed layer of an HSS_MX4 matrix (its input
+ *     gradient) reads the same ones.
  */
 #define HSS_COL16 1
 #define HSS_DQ4 2
 #define HSS_HIER2 4
+#define HSS_MX4 16
+#define HSS_MX4_T 32
 
 typedef struct hss_matrix {
   int32_t fmt;   /* hss_format */
@@ -261,8 +275,8 @@ typedef struct hss_matrix {
   const uint32_t* nm_meta;
   const void* U;
   const void* Vt;
-  const uint8_t* dq_codes; /* HSS_DQ4 only (else ignored) */
-  const void* dq_levels;   /* HSS_DQ4 only (else ignored) */
+  const uint8_t* dq_codes; /* HSS_DQ4, HSS_MX4 only (else ignored) */
+  const void* dq_levels;   /* HSS_DQ4, HSS_MX4 only (else ignored) */
   int32_t hier_r[4];       /* HSS_HIER2 only (else ignored): block ranks, order 00, 01, 10, 11 */
 } hss_matrix;
 
@@ -316,6 +330,10 @@ hss_status hss_apply_workspace_size(const hss_matrix* A, int32_t b, size_t* byte
  * HSS_DQ4 matrices always run the fused dense-and-sparse kernel (up to 8
  * columns per pass; no workspace: hss_apply_workspace_size returns 0 and ws
  * may be NULL).
+ * HSS_MX4 matrices: X V is kept as two bf16 terms (16 significant bits); D +
+ *   S is rounded to bf16 where an entry of S falls on a non-zero of D; all
+ *   sums are in fp32.  A NaN or infinity in X reaches every output of its
+ *   batch row.  The same call gives the same bits every time.
  * Returns HSS_ERR_INVALID_ARG for: A or X or Y null, unknown fmt/dtype,
  *   unknown flags (or HSS_COL16 with a 2:4 matrix or n > 65536; HSS_DQ4 with
  *   a 2:4 matrix, odd n or null dq arrays),
@@ -541,6 +559,68 @@ hss_status hss_gather_values(int32_t dt, int64_t nnz, const void* values, const 
  *   HSS_ERR_INVALID_ARG: bad dtype, rows or cols < 1, rows * cols >= 2^31,
  *   rows > 2,097,120, null or overlapping arrays.  HSS_ERR_HIP. */
 hss_status hss_transpose(int32_t dt, int32_t rows, int32_t cols, const void* src, void* dst, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled formats: a 4-bit dense part of the weights and 8-bit activation
+ * checkpoints.  [SQZ] keeps the outliers apart as a sparse matrix and the
+ * dense rest in few bits; here the rest is in the OCP microscaling formats,
+ * whose shared power-of-two scale keeps every value exact in bf16, so that
+ * the matrix cores take it.
+ * ------------------------------------------------------------------------
+ * Layout (rows x cols): groups of HSS_MX_GROUP = 32 consecutive columns of a
+ *   row, ng = ceil(cols / 32) per row, the last padded with zero codes.
+ *   scales  uint8[rows * ng]: E8M0; 255 = the group held a NaN or infinity and
+ *           every value of it reads as NaN.
+ *   HSS_MXFP4  codes uint8[rows * ng * 16]: byte j of a group holds columns 2j
+ *           (low nibble) and 2j + 1; nibble = sign << 3 | c, the magnitudes of
+ *           c = 0..7 being 0, 0.5, 1, 1.5, 2, 3, 4, 6 (E2M1); value = magnitude
+ *           * 2^(scale - 127).
+ *   HSS_MXINT8 codes int8[rows * ng * 32], -127 .. 127; value = code *
+ *           2^(scale - 133).
+ *   codes must be 16-byte aligned.
+ *
+ * hss_mx_quantize: src (rows x cols, fp32 or bf16, row-major) to codes and
+ *   scales.  With a the group's largest |w|: e = the exponent of a rounded to
+ *   2 (MXFP4) or 7 (MXINT8) significant bits, ties to even, kept within
+ *   [-123, 127] or [-120, 127]; the scale is 2^(e - 2) (byte e + 125) or
+ *   2^(e - 6) (byte e + 127); each code is the nearest to w / scale, ties to
+ *   even, at most 6 or 127.  So no value is off by more than half a step,
+ *   except next to the type's largest value.
+ *   residual (dt[rows * cols], nullable): src minus the quantised values,
+ *   exact; may be src itself, else must not overlap it.
+ *   NaN and infinities are kept to their group (scale 255; residual NaN).
+ * hss_mx_dequantize: dst (dt[rows * cols]) = the values, exact in either dt
+ *   for the scales hss_mx_quantize writes (MXFP4 2..252, MXINT8 7..254); a
+ *   group with another scale byte than those and 255 reads as unspecified
+ *   values.
+ *   HSS_ERR_INVALID_ARG: unknown fmt or dt, rows or cols < 1, rows * ng * 32
+ *   >= 2^31, null arrays, codes not 16-byte aligned, src or residual not
+ *   aligned to its element, arrays that overlap.  HSS_ERR_HIP. */
+#define HSS_MX_GROUP 32
+typedef enum { HSS_MXFP4 = 0, HSS_MXINT8 = 1 } hss_mx_format;
+
+/* Bytes of the two arrays of a rows x cols matrix (INVALID_ARG as above). */
+hss_status hss_mx_sizes(int32_t fmt, int32_t rows, int32_t cols, size_t* code_bytes, size_t* scale_bytes);
+hss_status hss_mx_quantize(int32_t fmt, int32_t dt, int32_t rows, int32_t cols, const void* src, void* codes,
+                           uint8_t* scales, void* residual, hipStream_t stream);
+hss_status hss_mx_dequantize(int32_t fmt, int32_t dt, int32_t rows, int32_t cols, const void* codes,
+                             const uint8_t* scales, void* dst, hipStream_t stream);
+
+/* hss_grad_ckpt: hss_grad with the layer's input kept from the forward pass
+ *   as an 8-bit checkpoint: codes and scales are X (b x n) as
+ *   hss_mx_quantize(HSS_MXINT8) wrote it, half the bytes of X in bf16.  The
+ *   gradients are those of the checkpoint's values X' (dS = G^T X' on S's
+ *   support, dU = G^T (X' V), dV^T = (G U)^T X'); layouts, NULL outputs and
+ *   the dS route as hss_grad.  X' V and G U are kept as three bf16 terms (24
+ *   significant bits), so every output carries fp32 precision.  The same
+ *   inputs give the same bits on every call.
+ *   ws: at least hss_grad_ckpt_workspace_size() bytes (no state kept).
+ *   HSS_ERR_UNSUPPORTED: as hss_grad, with round32 in place of round8.
+ *   HSS_ERR_INVALID_ARG: as hss_grad, codes not 16-byte aligned.
+ *   HSS_ERR_WORKSPACE; HSS_ERR_HIP. */
+hss_status hss_grad_ckpt_workspace_size(const hss_matrix* A, int32_t b, size_t* bytes);
+hss_status hss_grad_ckpt(const hss_matrix* A, int32_t b, const int8_t* codes, const uint8_t* scales, const void* G,
+                         float* dS, float* dU, float* dVt, void* ws, size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -689,3 +689,71 @@ def nm24_pattern(m, n, nm_meta):
         cols[:, 2 * g + 1] = 4 * g + ((nib >> 2) & 3)
     row_ptr = (np.arange(m + 1, dtype=np.int64) * (n // 2)).astype(np.int32)
     return row_ptr, cols.reshape(-1).astype(np.int32)
+
+
+# ---------------------------------------------------------------------------
+# Microscaled formats: groups of 32 columns of a row with a power-of-two scale
+# (the OCP microscaling element types E2M1 and INT8 with E8M0 scales).
+# ---------------------------------------------------------------------------
+
+MX_GROUP = 32
+MX_GRID = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def mx_encode(W64, fmt):
+    """Codes and scale bytes of an fp64 matrix holding fp32 or bf16 values.
+
+    fmt "fp4": the nearest E2M1 value, ties to the even code, two codes per
+    byte; "int8": the nearest integer, ties to even.  The group's exponent is
+    that of its largest magnitude after rounding that one to the code's
+    precision (2 or 7 significant bits).  A group with a non-finite value has
+    scale 255 and codes 0."""
+    W = np.asarray(W64, dtype=np.float64)
+    rows, cols = W.shape
+    ng = -(-cols // MX_GROUP)
+    pad = np.zeros((rows, ng * MX_GROUP))
+    pad[:, :cols] = W
+    V = pad.reshape(rows, ng, MX_GROUP)
+    scales = np.zeros((rows, ng), dtype=np.uint8)
+    codes = np.zeros((rows, ng, MX_GROUP), dtype=np.uint8 if fmt == "fp4" else np.int8)
+    bits, top, emin = (2, 2, -123) if fmt == "fp4" else (7, 6, -120)
+    for i in range(rows):
+        for g in range(ng):
+            v = V[i, g]
+            if not np.all(np.isfinite(v)):
+                scales[i, g] = 255
+                continue
+            a = float(np.max(np.abs(v)))
+            e = emin
+            if a > 0:
+                mant, ex = np.frexp(a)                       # a = mant 2^ex, mant in [1/2, 1)
+                e = int(ex) - 1 + int(np.rint(mant * 2.0 ** bits) == 2.0 ** bits)
+                e = min(max(e, emin), 127)
+            scales[i, g] = e + 127 - (2 if fmt == "fp4" else 0)
+            u = v / 2.0 ** (e - top)
+            if fmt == "int8":
+                codes[i, g] = np.clip(np.rint(u), -127, 127).astype(np.int8)
+                continue
+            d = np.abs(np.abs(u)[:, None] - MX_GRID[None, :])
+            near = d == d.min(axis=1, keepdims=True)
+            for k in range(MX_GROUP):
+                cand = np.flatnonzero(near[k])
+                c = int(cand[0]) if len(cand) == 1 else int(cand[cand % 2 == 0][0])
+                codes[i, g, k] = c | (8 if np.signbit(u[k]) else 0)
+    if fmt == "int8":
+        return codes.reshape(rows, -1), scales
+    return (codes[..., 0::2] | (codes[..., 1::2] << 4)).reshape(rows, -1), scales
+
+
+def mx_decode(codes, scales, cols, fmt):
+    """The fp64 values (rows x cols) that codes and scale bytes stand for."""
+    scales = np.asarray(scales, dtype=np.uint8)
+    rows, ng = scales.shape
+    s = np.where(scales == 255, np.nan, 2.0 ** (scales.astype(np.float64) - 127))[..., None]
+    if fmt == "int8":
+        v = np.asarray(codes, dtype=np.int8).reshape(rows, ng, MX_GROUP).astype(np.float64) / 64 * s
+    else:
+        c = np.asarray(codes, dtype=np.uint8).reshape(rows, ng, MX_GROUP // 2)
+        c = np.stack([c & 15, c >> 4], axis=3).reshape(rows, ng, MX_GROUP)
+        v = np.where(c & 8, -1.0, 1.0) * MX_GRID[c & 7] * s
+    return v.reshape(rows, -1)[:, :cols]

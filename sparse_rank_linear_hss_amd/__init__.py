@@ -20,7 +20,7 @@ from typing import Optional
 import torch
 
 from ._lib import (HSS_BF16, HSS_COL16, HSS_DQ4, HSS_ERR_NONFINITE, HSS_HIER2, HSS_F32, HSS_FMT_2OF4, HSS_FMT_CSR,
-                   HSS_MAX_BATCH, HSS_OK, HSS_OPT_BATCH_ROUTE, HSS_OPT_DECODE_FORCE_LOCAL, HSS_OPT_DECODE_MERGED,
+                   HSS_MAX_BATCH, HSS_MX4, HSS_MX4_T, HSS_MX_GROUP, HSS_MXFP4, HSS_MXINT8, HSS_OK, HSS_OPT_BATCH_ROUTE, HSS_OPT_DECODE_FORCE_LOCAL, HSS_OPT_DECODE_MERGED,
                    HSS_OPT_DECODE_RPW, HSS_OPT_DECODE_WAVE_PRODUCERS,
                    HSS_OPT_DECODE_SPIN, HSS_OPT_GRAD_DS_ROUTE, HSSError, HssMatrixStruct, LIB_PATH, check, lib,
                    status_string)
@@ -34,6 +34,8 @@ __all__ = [
     "hss_rcm_order", "hss_concentration", "hss_hier_pack", "hss_hier_pack_compact", "hss_csr_permute",
     "hss_grad", "hss_csr_transpose", "hss_gather_values", "hss_transpose", "hss_transposed_layer", "hss_backward",
     "hss_nm24_to_csr",
+    "HSS_MX4", "HSS_MX4_T", "HSS_MX_GROUP", "MXTensor", "hss_mx_quantize", "hss_mx_dequantize",
+    "hss_grad_ckpt", "hss_grad_ckpt_workspace_size", "grad_ckpt_workspace",
     "HSSMatrix", "SplitResult", "HSSError",
     "LIB_PATH", "status_string",
 ]
@@ -54,6 +56,14 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on(dev):
+    """dev as the current device (a launch goes to the current device's context)."""
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _dev(t: torch.Tensor):
@@ -172,6 +182,90 @@ def hss_get_error(ws: torch.Tensor) -> int:
     return int(lib.hss_get_error(_ptr(ws), _stream(ws.device)))
 
 
+# ---------------------------------------------------------------------------
+# Microscaled formats
+# ---------------------------------------------------------------------------
+
+_MX_FMT = {"fp4": HSS_MXFP4, "int8": HSS_MXINT8}
+
+
+class MXTensor:
+    """A rows x cols matrix in a microscaled format: groups of 32 columns of a
+    row share a power-of-two scale (the layout of hss_mx_quantize).
+
+    fmt "fp4": codes uint8 [rows, 16 ng] (two 4-bit codes per byte); "int8":
+    codes int8 [rows, 32 ng]; scales uint8 [rows, ng], ng = ceil(cols / 32)."""
+
+    __slots__ = ("fmt", "rows", "cols", "codes", "scales")
+
+    def __init__(self, fmt, rows, cols, codes, scales):
+        if fmt not in _MX_FMT:
+            raise ValueError(f"unknown microscaled format {fmt!r}: 'fp4' or 'int8'")
+        rows, cols = int(rows), int(cols)
+        ng = -(-cols // HSS_MX_GROUP)
+        want = (rows, 16 * ng) if fmt == "fp4" else (rows, 32 * ng)
+        if codes.dtype != (torch.uint8 if fmt == "fp4" else torch.int8) or codes.shape != want or \
+                not codes.is_contiguous():
+            raise ValueError(f"codes of a {rows} x {cols} {fmt} matrix: contiguous "
+                             f"{'uint8' if fmt == 'fp4' else 'int8'} {want}")
+        if scales.dtype != torch.uint8 or scales.shape != (rows, ng) or not scales.is_contiguous():
+            raise ValueError(f"scales of a {rows} x {cols} matrix: contiguous uint8 {(rows, ng)}")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
+        self.fmt, self.rows, self.cols, self.codes, self.scales = fmt, rows, cols, codes, scales
+
+    @classmethod
+    def empty(cls, fmt, rows, cols, device):
+        """Unwritten arrays, for hss_mx_quantize(..., out=)."""
+        ng = -(-int(cols) // HSS_MX_GROUP)
+        codes = torch.empty((rows, 16 * ng), dtype=torch.uint8, device=device) if fmt == "fp4" else \
+            torch.empty((rows, 32 * ng), dtype=torch.int8, device=device)
+        return cls(fmt, rows, cols, codes, torch.empty((rows, ng), dtype=torch.uint8, device=device))
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def hss_mx_quantize(W: torch.Tensor, fmt="fp4", out: Optional[MXTensor] = None, residual=None):
+    """W (rows x cols, fp32 or bf16) in a microscaled format: "fp4" (weights)
+    or "int8" (activation checkpoints), each value within half a step.
+
+    residual=True (or a tensor of W's shape and dtype, which may be W itself)
+    also writes W minus the quantised values (exact) and returns (q, residual)."""
+    dev = _dev(W)
+    if W.dim() != 2 or not W.is_contiguous():
+        raise ValueError("W must be a contiguous 2-D tensor")
+    dt = _dt(W)
+    rows, cols = W.shape
+    if out is None:
+        out = MXTensor.empty(fmt, rows, cols, dev)
+    elif out.fmt != fmt or out.rows != rows or out.cols != cols or out.device != dev:
+        raise ValueError(f"out must be a {rows} x {cols} {fmt} MXTensor on {dev}")
+    res = torch.empty_like(W) if residual is True else (residual if residual is not False else None)
+    if res is not None and (res.shape != W.shape or res.dtype != W.dtype or not res.is_contiguous() or
+                            res.device != dev):
+        raise ValueError("residual must be a contiguous tensor of W's shape, dtype and device")
+    with _on(dev):
+        check(lib.hss_mx_quantize(_MX_FMT[fmt], dt, rows, cols, W.data_ptr(), out.codes.data_ptr(),
+                                  out.scales.data_ptr(), _ptr(res), _stream(dev)), "hss_mx_quantize")
+    return out if res is None else (out, res)
+
+
+def hss_mx_dequantize(q: MXTensor, dtype=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values q stands for (rows x cols, bf16 by default or fp32; exact in both)."""
+    dev = _dev(q.codes)
+    if out is None:
+        out = torch.empty((q.rows, q.cols), dtype=dtype or torch.bfloat16, device=dev)
+    elif out.shape != (q.rows, q.cols) or not out.is_contiguous() or out.device != dev or \
+            (dtype is not None and out.dtype != dtype):
+        raise ValueError("out must be a contiguous tensor of q's shape and device")
+    with _on(dev):
+        check(lib.hss_mx_dequantize(_MX_FMT[q.fmt], _dt(out), q.rows, q.cols, q.codes.data_ptr(),
+                                    q.scales.data_ptr(), out.data_ptr(), _stream(dev)), "hss_mx_dequantize")
+    return out
+
+
 class HSSMatrix:
     """Compressed matrix S + U V^T (or S + D) in device memory; keeps its tensors alive.
 
@@ -185,10 +279,14 @@ class HSSMatrix:
     hier_r (ranks of the 2 x 2 blocks 00, 01, 10, 11) makes the low-rank term
     the compact block form (HSS_HIER2): U m x (hier_r[0] + hier_r[1]) and
     Vt sum(hier_r) x (n - n // 2) as hss_hier_pack_compact writes them, the
-    matrix in the blocks' (permuted) order."""
+    matrix in the blocks' (permuted) order.
+    mx (an "fp4" MXTensor, m x n) adds a microscaled 4-bit dense part (HSS_MX4),
+    next to S and the low-rank term; mx_t=True: mx holds its transpose, n x m
+    (HSS_MX4_T).  row_ptr may then be left out for an empty S."""
 
     def __init__(self, fmt, m, n, dtype, U=None, Vt=None, row_ptr=None, col_idx=None, values=None,
-                 nnz=None, nm_values=None, nm_meta=None, dq_codes=None, dq_levels=None, hier_r=None):
+                 nnz=None, nm_values=None, nm_meta=None, dq_codes=None, dq_levels=None, hier_r=None,
+                 mx=None, mx_t=False):
         self.fmt = _FMT[fmt]
         self.flags = HSS_COL16 if (col_idx is not None and col_idx.dtype == torch.int16) else 0
         self.hier_r = None if hier_r is None else [int(v) for v in hier_r]
@@ -198,6 +296,17 @@ class HSSMatrix:
             assert dq_levels.numel() == m * 16
             self.flags |= HSS_DQ4
         self.dq_codes, self.dq_levels = dq_codes, dq_levels
+        self.mx, self.mx_t = mx, bool(mx_t)
+        if mx is not None:
+            if dq_codes is not None:
+                raise ValueError("one dense part: dq_codes or mx")
+            if mx.fmt != "fp4" or (mx.rows, mx.cols) != ((n, m) if mx_t else (m, n)):
+                raise ValueError(f"mx must be an 'fp4' MXTensor, {'n x m' if mx_t else 'm x n'} of the {m} x {n} matrix")
+            if row_ptr is None and fmt in ("csr", HSS_FMT_CSR):
+                row_ptr = torch.zeros(int(m) + 1, dtype=torch.int32, device=mx.device)
+            self.flags |= HSS_MX4 | (HSS_MX4_T if mx_t else 0)
+        elif mx_t:
+            raise ValueError("mx_t without mx")
         self.m, self.n = int(m), int(n)
         self.dtype = dtype
         self.U, self.Vt = U, Vt
@@ -227,17 +336,21 @@ class HSSMatrix:
         s.dq_codes, s.dq_levels = _ptr(dq_codes), _ptr(dq_levels)
         if self.hier_r is not None:
             s.hier_r = (ctypes.c_int32 * 4)(*self.hier_r)
+        if mx is not None:
+            s.dq_codes, s.dq_levels = _ptr(mx.codes), _ptr(mx.scales)
         self.struct = s
 
     @classmethod
-    def from_split(cls, sp: SplitResult, U=None, V=None, Vt=None, dtype=None):
+    def from_split(cls, sp: SplitResult, U=None, V=None, Vt=None, dtype=None, mx=None):
         if V is not None:
             Vt = V.t().contiguous()
         if dtype is None:
             dtype = (sp.values if sp.values is not None else sp.nm_values).dtype
         if sp.fmt == HSS_FMT_CSR:
             return cls("csr", sp.m, sp.n, dtype, U=U, Vt=Vt, row_ptr=sp.row_ptr,
-                       col_idx=sp.col_idx, values=sp.values, nnz=sp.k)
+                       col_idx=sp.col_idx, values=sp.values, nnz=sp.k, mx=mx)
+        if mx is not None:
+            raise ValueError("a microscaled dense part goes with a CSR S")
         return cls("2:4", sp.m, sp.n, dtype, U=U, Vt=Vt, nm_values=sp.nm_values, nm_meta=sp.nm_meta)
 
     def with_col16(self) -> "HSSMatrix":
@@ -249,7 +362,7 @@ class HSSMatrix:
                          col_idx=c16 if c16 is not None else torch.zeros(0, dtype=torch.int16,
                                                                            device=self.row_ptr.device),
                          values=self.values, nnz=self.nnz, dq_codes=self.dq_codes, dq_levels=self.dq_levels,
-                         hier_r=self.hier_r)
+                         hier_r=self.hier_r, mx=self.mx, mx_t=self.mx_t)
 
     def workspace(self, b: int, device=None) -> torch.Tensor:
         """Initialised apply workspace for batch b on the current stream.
@@ -553,10 +666,11 @@ def hss_nm24_to_csr(A: HSSMatrix):
 def hss_transposed_layer(A: HSSMatrix) -> HSSMatrix:
     """A^T = S^T + V U^T as an HSSMatrix (n x m, CSR): S^T's pattern from the
     host transpose (of the 2:4 positions for a 2:4 layer), its values
-    gathered on the device, U' = V and V'^T = U^T from the stored factors.
-    hss_apply(A^T, G) is the input gradient G A."""
+    gathered on the device, U' = V and V'^T = U^T from the stored factors; a
+    microscaled dense part is shared, read transposed.  hss_apply(A^T, G) is the input gradient G A."""
     if A.flags & (HSS_DQ4 | HSS_HIER2):
         raise ValueError("the transposed layer is built for CSR and 2:4 layers with flat factors")
+    mx = dict(mx=A.mx, mx_t=not A.mx_t) if A.mx is not None else {}
     if A.fmt == HSS_FMT_2OF4:
         dev = A.nm_meta.device
         row_ptr, cols = hss_nm24_to_csr(A)
@@ -573,16 +687,59 @@ def hss_transposed_layer(A: HSSMatrix) -> HSSMatrix:
     U2 = hss_transpose(A.Vt) if A.r > 0 else None
     Vt2 = hss_transpose(A.U) if A.r > 0 else None
     At = HSSMatrix("csr", A.n, A.m, A.dtype, U=U2, Vt=Vt2, row_ptr=torch.from_numpy(rpt).to(dev),
-                   col_idx=torch.from_numpy(cit).to(dev) if nnz else None, values=vals, nnz=nnz)
+                   col_idx=torch.from_numpy(cit).to(dev) if nnz else None, values=vals, nnz=nnz, **mx)
     At.perm_from_s = perm_d
     return At
 
 
-def hss_backward(A: HSSMatrix, X: torch.Tensor, G: torch.Tensor, At: Optional[HSSMatrix] = None) -> dict:
+def hss_grad_ckpt_workspace_size(A: HSSMatrix, b: int) -> int:
+    out = ctypes.c_size_t(0)
+    check(lib.hss_grad_ckpt_workspace_size(ctypes.byref(A.struct), int(b), ctypes.byref(out)),
+          "hss_grad_ckpt_workspace_size")
+    return int(out.value)
+
+
+def grad_ckpt_workspace(A: HSSMatrix, b: int, device) -> torch.Tensor:
+    """A workspace of hss_grad_ckpt for batch b.  It keeps no state between
+    calls; calls that share it must be ordered (one stream, or events)."""
+    return torch.empty(hss_grad_ckpt_workspace_size(A, b), dtype=torch.uint8, device=device)
+
+
+def hss_grad_ckpt(A: HSSMatrix, X: MXTensor, G: torch.Tensor, dS=True, dU=True, dVt=True,
+                  out: Optional[dict] = None, ws: Optional[torch.Tensor] = None) -> dict:
+    """hss_grad with the layer's input as an 8-bit checkpoint: X is the "int8"
+    MXTensor (b x n) that hss_mx_quantize made of it in the forward pass.
+    out: tensors to write (a dict with the keys wanted, as returned); then
+    dS, dU and dVt are ignored."""
+    dev = _dev(G)
+    if X.fmt != "int8" or X.cols != A.n or X.device != dev:
+        raise ValueError("X must be an 'int8' MXTensor, b x n, on G's device")
+    b = X.rows
+    if G.shape != (b, A.m) or not G.is_contiguous() or G.dtype != A.dtype:
+        raise ValueError("G must be a contiguous b x m tensor of the matrix dtype")
+    shapes = {"dS": (A.m * (A.n // 2) if A.fmt == HSS_FMT_2OF4 else A.nnz,), "dU": (A.m, A.r), "dVt": (A.r, A.n)}
+    if out is None:
+        out = {k: torch.empty(shapes[k], dtype=torch.float32, device=dev)
+               for k, wanted in (("dS", dS), ("dU", dU), ("dVt", dVt)) if wanted}
+    for k, t in out.items():
+        if k not in shapes or t.shape != shapes[k] or t.dtype != torch.float32 or not t.is_contiguous() or \
+                t.device != dev:
+            raise ValueError("out must hold contiguous float32 tensors 'dS', 'dU', 'dVt' of the gradients' shapes")
+    if ws is None:
+        ws = grad_ckpt_workspace(A, b, dev)
+    with _on(dev):
+        check(lib.hss_grad_ckpt(ctypes.byref(A.struct), b, X.codes.data_ptr(), X.scales.data_ptr(), G.data_ptr(),
+                                _ptr(out.get("dS")), _ptr(out.get("dU")), _ptr(out.get("dVt")), ws.data_ptr(),
+                                ws.numel(), _stream(dev)), "hss_grad_ckpt")
+    return out
+
+
+def hss_backward(A: HSSMatrix, X, G: torch.Tensor, At: Optional[HSSMatrix] = None) -> dict:
     """dX (b x n, the layer dtype) = G A through the transposed layer, and
-    the fp32 parameter gradients dS, dU, dVt of hss_grad."""
+    the fp32 parameter gradients dS, dU, dVt of hss_grad, or of hss_grad_ckpt
+    where X is the 8-bit checkpoint of the layer's input."""
     if At is None:
         At = hss_transposed_layer(A)
-    out = hss_grad(A, X, G)
+    out = hss_grad_ckpt(A, X, G) if isinstance(X, MXTensor) else hss_grad(A, X, G)
     out["dX"] = hss_apply(At, G)
     return out

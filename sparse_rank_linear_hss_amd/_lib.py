@@ -30,6 +30,11 @@ HSS_OPT_DECODE_RPW = 6
 HSS_COL16 = 1  # hss_matrix.flags: CSR col_idx holds uint16 columns
 HSS_DQ4 = 2    # hss_matrix.flags: a 4-bit quantised dense part (dq_codes, dq_levels)
 HSS_HIER2 = 4  # hss_matrix.flags: compact 2 x 2 block low-rank term (hier_r)
+HSS_MX4 = 16   # hss_matrix.flags: a microscaled 4-bit dense part (codes in dq_codes, scales in dq_levels)
+HSS_MX4_T = 32  # with HSS_MX4: the arrays hold the dense part's transpose
+HSS_MXFP4 = 0
+HSS_MXINT8 = 1
+HSS_MX_GROUP = 32
 
 c_int32, c_int64, c_size_t, c_void_p = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 
@@ -98,6 +103,14 @@ def _load():
         "hss_csr_permute": (ctypes.c_int, [c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
         "hss_gather_values": (ctypes.c_int, [ctypes.c_int, c_int64, c_void_p, c_void_p, c_void_p, c_void_p]),
         "hss_transpose": (ctypes.c_int, [ctypes.c_int, c_int32, c_int32, c_void_p, c_void_p, c_void_p]),
+        "hss_mx_sizes": (ctypes.c_int, [c_int32, c_int32, c_int32, P(c_size_t), P(c_size_t)]),
+        "hss_mx_quantize": (ctypes.c_int, [c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                           c_void_p]),
+        "hss_mx_dequantize": (ctypes.c_int, [c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
+                                             c_void_p]),
+        "hss_grad_ckpt_workspace_size": (ctypes.c_int, [P(HssMatrixStruct), c_int32, P(c_size_t)]),
+        "hss_grad_ckpt": (ctypes.c_int, [P(HssMatrixStruct), c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                         c_void_p, c_void_p, c_size_t, c_void_p]),
         "hss_nm24_to_csr": (ctypes.c_int, [c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
     }
     for name, (res, args) in sig.items():

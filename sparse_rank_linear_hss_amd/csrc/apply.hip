@@ -14,6 +14,8 @@
 //   dense-and-sparse     HSS_DQ4 matrices (decode.hip, k_decode_dq): the
 //                        quantised dense part and the CSR outliers, up to 8
 //                        columns per pass, no workspace.
+//   microscaled dense    HSS_MX4 matrices (mx_apply.hip): the 4-bit dense
+//                        part with S and the low-rank term, every batch.
 //   gather SpMM          bf16 CSR from 3 to 128 columns (and beyond where S
 //   (spmm.hip)           cannot be densified): S read once, X^T rows
 //                        gathered per entry, T from a small prologue.
@@ -36,6 +38,9 @@ size_t decode_t_bytes(const hss_matrix* A);
 int decode_max_cols(const hss_matrix* A);
 int decode_dq_max_cols(const hss_matrix* A);
 void launch_decode_dq(const hss_matrix* A, int bc, const void* X, void* Y, hipStream_t s);
+size_t mx_apply_ws_bytes(const hss_matrix* A, int b);
+hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s);
+static bool is_mx(const hss_matrix* A) { return (A->flags & HSS_MX4) != 0; }
 static bool is_dq(const hss_matrix* A) { return (A->flags & HSS_DQ4) != 0; }
 static bool is_hier(const hss_matrix* A) { return (A->flags & HSS_HIER2) != 0; }
 static size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -117,6 +122,7 @@ static Route batch_route(const hss_matrix* A0, int b, const void* X) {
 // scratch, so both paths can share one workspace.
 size_t apply_ws_bytes(const hss_matrix* A0, int b) {
   if (is_dq(A0)) return 0;
+  if (is_mx(A0)) return decode_ctl_bytes() + mx_apply_ws_bytes(A0, b);
   // every route the call may take (the route can be forced at call time)
   const size_t dec = decode_t_bytes(A0);
   const hss_matrix F = is_hier(A0) ? flat_view(A0, nullptr, nullptr) : *A0;
@@ -134,6 +140,7 @@ size_t apply_ws_bytes(const hss_matrix* A0, int b) {
 // covers every route a call could be forced onto).
 size_t apply_route_ws_bytes(const hss_matrix* A0, int b, const void* X) {
   if (is_dq(A0)) return 0;
+  if (is_mx(A0)) return decode_ctl_bytes() + mx_apply_ws_bytes(A0, b);
   const hss_matrix F = is_hier(A0) ? flat_view(A0, nullptr, nullptr) : *A0;
   const hss_matrix* A = &F;
   const size_t flat = is_hier(A0) ? hier_flat_bytes(A0) : 0;
@@ -158,6 +165,7 @@ hss_status launch_apply(const hss_matrix* A, int b, const void* X, void* Y, void
     }
     return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
   }
+  if (is_mx(A)) return launch_mx_apply(A, b, X, Y, static_cast<char*>(ws) + decode_ctl_bytes(), stream);
   const Route route = batch_route(A, b, X);
   char* scratch = static_cast<char*>(ws) + decode_ctl_bytes();
   hss_matrix F;
@@ -212,7 +220,7 @@ size_t apply_group_ws_bytes(const hss_matrix* const* A, int G, int b) {
   size_t dec = 0, one = 0;
   for (int g = 0; g < G; ++g) {
     if (is_dq(A[g])) continue;  // the dense-and-sparse kernel uses no workspace
-    dec += decode_t_bytes(A[g]);
+    if (!is_mx(A[g])) dec += decode_t_bytes(A[g]);
     const size_t a = apply_ws_bytes(A[g], b) - decode_ctl_bytes();
     one = one > a ? one : a;
   }
@@ -221,8 +229,9 @@ size_t apply_group_ws_bytes(const hss_matrix* const* A, int G, int b) {
 
 hss_status launch_apply_group(const hss_matrix* const* A, int G, int b, const void* X, void* const* Y, void* ws,
                               hipStream_t stream) {
-  bool any_mfma = false;  // (or dense-and-sparse: those run one by one too)
-  for (int g = 0; g < G; ++g) any_mfma = any_mfma || batch_route(A[g], b, X) != R_DECODE || is_dq(A[g]);
+  bool any_mfma = false;  // (or a dense part, quantised or microscaled: those run one by one too)
+  for (int g = 0; g < G; ++g)
+    any_mfma = any_mfma || is_dq(A[g]) || is_mx(A[g]) || batch_route(A[g], b, X) != R_DECODE;
   if (any_mfma) {
     for (int g = 0; g < G; ++g) {
       const hss_status st = launch_apply(A[g], b, X, Y[g], ws, stream);

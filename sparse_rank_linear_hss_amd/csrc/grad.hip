@@ -202,7 +202,7 @@ static void launch_sddmm_pat(int lp, const SPattern& P, const uint16_t* Gt, cons
 // vs 0.41.
 static constexpr int kDenseDsMinB = 512;
 
-static bool ds_dense(int b) {
+bool ds_dense(int b) {
   const int forced = option(HSS_OPT_GRAD_DS_ROUTE);
   if (forced == 1) return false;
   if (forced == 2) return true;
@@ -241,6 +241,39 @@ static GradPlan plan_grad(const hss_matrix* A, int b) {
 
 size_t grad_ws_bytes(const hss_matrix* A, int b) { return plan_grad(A, b).total; }
 
+// dS from X^T and G^T (n x ldt and m x ldt, columns past b zero): the sampled
+// product, or dA = G^T X (in `dA`, m x n; over kb columns, b <= kb <= ldt) and
+// a gather, by ds_dense(b).
+void launch_ds(const hss_matrix* A, int b, int kb, int ldt, const uint16_t* Xt, const uint16_t* Gt, float* dA, float* part,
+               float* dS, hipStream_t s) {
+  const int m = A->m, n = A->n;
+  SPattern P = {};
+  P.row_ptr = A->row_ptr;
+  P.col = A->col_idx;
+  P.meta = A->nm_meta;
+  P.n = n;
+  const int pat = A->fmt == HSS_FMT_2OF4 ? PAT_NM24 : ((A->flags & HSS_COL16) ? PAT_CSR16 : PAT_CSR32);
+  if (ds_dense(b)) {
+    launch_gemm_bf16(n, m, kb, Xt, ldt, Gt, ldt, dA, n, false, part, s);
+    const dim3 grid((unsigned)((m + 3) / 4));
+    if (pat == PAT_NM24)
+      hipLaunchKernelGGL(k_ds_gather<PAT_NM24>, grid, dim3(256), 0, s, P, dA, m, n, dS);
+    else if (pat == PAT_CSR16)
+      hipLaunchKernelGGL(k_ds_gather<PAT_CSR16>, grid, dim3(256), 0, s, P, dA, m, n, dS);
+    else
+      hipLaunchKernelGGL(k_ds_gather<PAT_CSR32>, grid, dim3(256), 0, s, P, dA, m, n, dS);
+  } else {
+    int lp = 1;
+    while (lp < 64 && lp * 2 <= (ldt >> 3)) lp *= 2;
+    if (pat == PAT_NM24)
+      launch_sddmm_pat<PAT_NM24>(lp, P, Gt, Xt, m, n, ldt, dS, s);
+    else if (pat == PAT_CSR16)
+      launch_sddmm_pat<PAT_CSR16>(lp, P, Gt, Xt, m, n, ldt, dS, s);
+    else
+      launch_sddmm_pat<PAT_CSR32>(lp, P, Gt, Xt, m, n, ldt, dS, s);
+  }
+}
+
 hss_status launch_grad(const hss_matrix* A, int b, const void* X, const void* G, float* dS, float* dU, float* dVt,
                        void* ws, hipStream_t s) {
   const GradPlan p = plan_grad(A, b);
@@ -267,34 +300,7 @@ hss_status launch_grad(const hss_matrix* A, int b, const void* X, const void* G,
     launch_gemm_bf16(b, r, m, Gb, m, Ut, p.ldu, Pt, p.ldt, true, part, s);
     launch_gemm_bf16(n, r, b, Xt, p.ldt, Pt, p.ldt, dVt, n, false, part, s);
   }
-  if (want_s) {
-    SPattern P = {};
-    P.row_ptr = A->row_ptr;
-    P.col = A->col_idx;
-    P.meta = A->nm_meta;
-    P.n = n;
-    const int pat = A->fmt == HSS_FMT_2OF4 ? PAT_NM24 : ((A->flags & HSS_COL16) ? PAT_CSR16 : PAT_CSR32);
-    if (ds_dense(b)) {
-      float* dA = reinterpret_cast<float*>(base + p.da);
-      launch_gemm_bf16(n, m, b, Xt, p.ldt, Gt, p.ldt, dA, n, false, part, s);
-      const dim3 grid((unsigned)((m + 3) / 4));
-      if (pat == PAT_NM24)
-        hipLaunchKernelGGL(k_ds_gather<PAT_NM24>, grid, dim3(256), 0, s, P, dA, m, n, dS);
-      else if (pat == PAT_CSR16)
-        hipLaunchKernelGGL(k_ds_gather<PAT_CSR16>, grid, dim3(256), 0, s, P, dA, m, n, dS);
-      else
-        hipLaunchKernelGGL(k_ds_gather<PAT_CSR32>, grid, dim3(256), 0, s, P, dA, m, n, dS);
-    } else {
-      int lp = 1;
-      while (lp < 64 && lp * 2 <= (p.ldt >> 3)) lp *= 2;
-      if (pat == PAT_NM24)
-        launch_sddmm_pat<PAT_NM24>(lp, P, Gt, Xt, m, n, p.ldt, dS, s);
-      else if (pat == PAT_CSR16)
-        launch_sddmm_pat<PAT_CSR16>(lp, P, Gt, Xt, m, n, p.ldt, dS, s);
-      else
-        launch_sddmm_pat<PAT_CSR32>(lp, P, Gt, Xt, m, n, p.ldt, dS, s);
-    }
-  }
+  if (want_s) launch_ds(A, b, b, p.ldt, Xt, Gt, reinterpret_cast<float*>(base + p.da), part, dS, s);
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 

@@ -20,6 +20,14 @@ hss_status launch_gather_values(int dt, int64_t nnz, const void* values, const i
                                 hipStream_t s);
 hss_status launch_transpose(int dt, int rows, int cols, const void* src, void* dst, hipStream_t s);
 hss_status launch_nm_to_csr(int m, int n, const uint32_t* meta, int32_t* row_ptr, int32_t* col, hipStream_t s);
+// mx.hip, grad_ckpt.hip
+hss_status launch_mx_quantize(int fmt, int dt, int rows, int cols, const void* src, void* codes, uint8_t* scales,
+                              void* residual, hipStream_t s);
+hss_status launch_mx_dequantize(int fmt, int dt, int rows, int cols, const void* codes, const uint8_t* scales,
+                                void* dst, hipStream_t s);
+size_t grad_ckpt_ws_bytes(const hss_matrix* A, int b);
+hss_status launch_grad_ckpt(const hss_matrix* A, int b, const void* codes, const uint8_t* scales, const void* G,
+                            float* dS, float* dU, float* dVt, void* ws, hipStream_t s);
 }  // namespace hss
 
 // ---------------------------------------------------------------------------
@@ -77,6 +85,7 @@ constexpr int64_t kLimit = (int64_t)1 << 31;  // arrays must have fewer elements
 bool valid_dtype(int dt) { return dt == HSS_F32 || dt == HSS_BF16; }
 bool valid_fmt(int f) { return f == HSS_FMT_CSR || f == HSS_FMT_2OF4; }
 size_t dsize(int dt) { return dt == HSS_F32 ? 4 : 2; }
+int64_t up32(int64_t x) { return (x + 31) / 32 * 32; }
 
 bool overlap(const void* a, size_t abytes, const void* b, size_t bbytes) {
   const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
@@ -172,11 +181,19 @@ hss_status hss_get_error(const void* ws, hipStream_t stream) {
 }
 
 static hss_status check_matrix(const hss_matrix* A, int32_t b) {
-  if (!A || !valid_fmt(A->fmt) || !valid_dtype(A->dtype) || (A->flags & ~(HSS_COL16 | HSS_DQ4 | HSS_HIER2)) != 0)
+  if (!A || !valid_fmt(A->fmt) || !valid_dtype(A->dtype) || (A->flags & ~(HSS_COL16 | HSS_DQ4 | HSS_HIER2 | HSS_MX4 | HSS_MX4_T)) != 0)
     return HSS_ERR_INVALID_ARG;
   if ((A->flags & HSS_COL16) && (A->fmt != HSS_FMT_CSR || A->n > 65536)) return HSS_ERR_INVALID_ARG;
   const int64_t m = A->m, n = A->n, r = A->r;
   if (m <= 0 || n <= 0 || r < 0 || b < 1 || b > HSS_MAX_BATCH) return HSS_ERR_INVALID_ARG;
+  if (A->flags & (HSS_MX4 | HSS_MX4_T)) {
+    if (!(A->flags & HSS_MX4) || A->fmt != HSS_FMT_CSR || (A->flags & (HSS_DQ4 | HSS_HIER2)) || !A->dq_codes ||
+        !A->dq_levels || (uintptr_t)A->dq_codes % 16 != 0)
+      return HSS_ERR_INVALID_ARG;
+    // D and its dense copies in rows of whole groups; the factors' terms side by side
+    if (m * up32(n) >= kLimit || n * up32(m) >= kLimit || 2 * std::max<int64_t>(m, b) * up32(r) >= kLimit)
+      return HSS_ERR_INVALID_ARG;
+  }
   if (A->flags & HSS_DQ4) {
     if (A->fmt != HSS_FMT_CSR || n % 2 != 0 || !A->dq_codes || !A->dq_levels) return HSS_ERR_INVALID_ARG;
     if (r > 0) return HSS_ERR_UNSUPPORTED;
@@ -201,6 +218,7 @@ static hss_status check_matrix(const hss_matrix* A, int32_t b) {
   } else {
     if (n % 4 != 0 || !A->nm_values || !A->nm_meta) return HSS_ERR_INVALID_ARG;
   }
+  if ((A->flags & HSS_MX4) && A->dtype != HSS_BF16) return HSS_ERR_UNSUPPORTED;
   return HSS_OK;
 }
 
@@ -388,26 +406,110 @@ hss_status hss_grad_workspace_size(const hss_matrix* A, int32_t b, size_t* bytes
   return HSS_OK;
 }
 
+// The outputs of a gradient call against its b x n and b x m inputs (byte
+// ranges; null inputs are skipped) and against each other.
+static bool grad_outputs_ok(const hss_matrix* A, const void* const* in, const size_t* in_bytes, int nin, float* dS,
+                            float* dU, float* dVt) {
+  const int64_t m = A->m, n = A->n, r = A->r;
+  const int64_t stored = A->fmt == HSS_FMT_2OF4 ? m * (n / 2) : A->nnz;
+  const void* outs[3] = {dS, dU, dVt};
+  const size_t ob[3] = {(size_t)stored * 4, (size_t)m * r * 4, (size_t)r * n * 4};
+  for (int k = 0; k < 3; ++k) {
+    if (!outs[k] || ob[k] == 0) continue;
+    for (int q = 0; q < nin; ++q)
+      if (overlap(outs[k], ob[k], in[q], in_bytes[q])) return false;
+    for (int q = k + 1; q < 3; ++q)
+      if (outs[q] && ob[q] && overlap(outs[k], ob[k], outs[q], ob[q])) return false;
+  }
+  return true;
+}
+
 hss_status hss_grad(const hss_matrix* A, int32_t b, const void* X, const void* G, float* dS, float* dU, float* dVt,
                     void* ws, size_t ws_bytes, hipStream_t stream) {
   const hss_status st = check_grad(A, b);
   if (st != HSS_OK) return st;
   if (!X || !G) return HSS_ERR_INVALID_ARG;
-  const int64_t m = A->m, n = A->n, r = A->r;
-  const size_t xb = (size_t)b * n * 2, gb = (size_t)b * m * 2;
-  const int64_t stored = A->fmt == HSS_FMT_2OF4 ? m * (n / 2) : A->nnz;
-  const size_t sb = (size_t)stored * 4, ub = (size_t)m * r * 4, vb = (size_t)r * n * 4;
-  const void* outs[3] = {dS, dU, dVt};
-  const size_t ob[3] = {sb, ub, vb};
-  for (int k = 0; k < 3; ++k) {
-    if (!outs[k] || ob[k] == 0) continue;
-    if (overlap(outs[k], ob[k], X, xb) || overlap(outs[k], ob[k], G, gb)) return HSS_ERR_INVALID_ARG;
-    for (int q = k + 1; q < 3; ++q)
-      if (outs[q] && ob[q] && overlap(outs[k], ob[k], outs[q], ob[q])) return HSS_ERR_INVALID_ARG;
-  }
+  const void* in[2] = {X, G};
+  const size_t in_bytes[2] = {(size_t)b * A->n * 2, (size_t)b * A->m * 2};
+  if (!grad_outputs_ok(A, in, in_bytes, 2, dS, dU, dVt)) return HSS_ERR_INVALID_ARG;
   const size_t need = hss::grad_ws_bytes(A, b);
   if (!ws || ws_bytes < need) return HSS_ERR_WORKSPACE;
   return hss::launch_grad(A, b, X, G, dS, dU, dVt, ws, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Microscaled formats
+// ---------------------------------------------------------------------------
+hss_status hss_mx_sizes(int32_t fmt, int32_t rows, int32_t cols, size_t* code_bytes, size_t* scale_bytes) {
+  if ((fmt != HSS_MXFP4 && fmt != HSS_MXINT8) || rows < 1 || cols < 1 || rows * up32(cols) >= kLimit || !code_bytes ||
+      !scale_bytes)
+    return HSS_ERR_INVALID_ARG;
+  *code_bytes = (size_t)(rows * up32(cols)) / (fmt == HSS_MXFP4 ? 2 : 1);
+  *scale_bytes = (size_t)(rows * up32(cols)) / HSS_MX_GROUP;
+  return HSS_OK;
+}
+
+// The dense array (src, residual or dst) against codes and scales.
+static bool mx_arrays_ok(int32_t dt, int32_t rows, int32_t cols, const void* dense, const void* codes, size_t cb,
+                         const uint8_t* scales, size_t sb) {
+  const size_t db = (size_t)rows * cols * dsize(dt);
+  return (uintptr_t)dense % dsize(dt) == 0 && !overlap(dense, db, codes, cb) && !overlap(dense, db, scales, sb);
+}
+
+hss_status hss_mx_quantize(int32_t fmt, int32_t dt, int32_t rows, int32_t cols, const void* src, void* codes,
+                           uint8_t* scales, void* residual, hipStream_t stream) {
+  size_t cb = 0, sb = 0;
+  const hss_status st = hss_mx_sizes(fmt, rows, cols, &cb, &sb);
+  if (st != HSS_OK) return st;
+  if (!valid_dtype(dt) || !src || !codes || !scales || (uintptr_t)codes % 16 != 0 || overlap(codes, cb, scales, sb))
+    return HSS_ERR_INVALID_ARG;
+  if (!mx_arrays_ok(dt, rows, cols, src, codes, cb, scales, sb)) return HSS_ERR_INVALID_ARG;
+  const size_t db = (size_t)rows * cols * dsize(dt);
+  if (residual && (!mx_arrays_ok(dt, rows, cols, residual, codes, cb, scales, sb) ||
+                   (residual != src && overlap(residual, db, src, db))))
+    return HSS_ERR_INVALID_ARG;
+  return hss::launch_mx_quantize(fmt, dt, rows, cols, src, codes, scales, residual, stream);
+}
+
+hss_status hss_mx_dequantize(int32_t fmt, int32_t dt, int32_t rows, int32_t cols, const void* codes,
+                             const uint8_t* scales, void* dst, hipStream_t stream) {
+  size_t cb = 0, sb = 0;
+  const hss_status st = hss_mx_sizes(fmt, rows, cols, &cb, &sb);
+  if (st != HSS_OK) return st;
+  if (!valid_dtype(dt) || !dst || !codes || !scales || (uintptr_t)codes % 16 != 0 ||
+      !mx_arrays_ok(dt, rows, cols, dst, codes, cb, scales, sb))
+    return HSS_ERR_INVALID_ARG;
+  return hss::launch_mx_dequantize(fmt, dt, rows, cols, codes, scales, dst, stream);
+}
+
+static hss_status check_grad_ckpt(const hss_matrix* A, int32_t b) {
+  const hss_status st = check_grad(A, b);
+  if (st != HSS_OK) return st;
+  const int64_t bp = up32(b), mx = std::max(A->m, A->n), wide = std::max(mx, bp);
+  if (up32(mx) * bp * 2 >= kLimit || 3 * up32(A->r) * wide >= kLimit) return HSS_ERR_UNSUPPORTED;
+  return HSS_OK;
+}
+
+hss_status hss_grad_ckpt_workspace_size(const hss_matrix* A, int32_t b, size_t* bytes) {
+  if (!bytes) return HSS_ERR_INVALID_ARG;
+  const hss_status st = check_grad_ckpt(A, b);
+  if (st != HSS_OK) return st;
+  *bytes = hss::grad_ckpt_ws_bytes(A, b);
+  return HSS_OK;
+}
+
+hss_status hss_grad_ckpt(const hss_matrix* A, int32_t b, const int8_t* codes, const uint8_t* scales, const void* G,
+                         float* dS, float* dU, float* dVt, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const hss_status st = check_grad_ckpt(A, b);
+  if (st != HSS_OK) return st;
+  if (!codes || !scales || !G || (uintptr_t)codes % 16 != 0) return HSS_ERR_INVALID_ARG;
+  const void* in[3] = {codes, scales, G};
+  const size_t in_bytes[3] = {(size_t)(b * up32(A->n)), (size_t)(b * up32(A->n)) / HSS_MX_GROUP,
+                              (size_t)b * A->m * 2};
+  if (!grad_outputs_ok(A, in, in_bytes, 3, dS, dU, dVt)) return HSS_ERR_INVALID_ARG;
+  const size_t need = hss::grad_ckpt_ws_bytes(A, b);
+  if (!ws || ws_bytes < need) return HSS_ERR_WORKSPACE;
+  return hss::launch_grad_ckpt(A, b, codes, scales, G, dS, dU, dVt, ws, stream);
 }
 
 hss_status hss_csr_transpose(int32_t m, int32_t n, const int32_t* row_ptr, const int32_t* col_idx, int32_t* row_ptr_t,

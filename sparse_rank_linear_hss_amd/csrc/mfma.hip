@@ -964,6 +964,33 @@ void launch_gemm_bf16(int M, int N, int K, const uint16_t* A, int64_t lda, const
 
 size_t gemm_bf16_part_bytes(int M, int N, int K, int64_t ldc) { return gemm_part_bytes(M, N, K, 0) / M * ldc; }
 
+// The same over two K segments: C = A1 . B1^T + A2 . B2^T in one product
+// (K2 = 0: the first alone).
+void launch_gemm_bf16x2(int M, int N, int K1, const uint16_t* A1, int64_t lda1, const uint16_t* B1, int64_t ldb1,
+                        int K2, const uint16_t* A2, int64_t lda2, const uint16_t* B2, int64_t ldb2, void* C,
+                        int64_t ldc, bool out_bf16, float* part, hipStream_t s) {
+  GemmArgs g = {};
+  g.M = M; g.N = N; g.K1 = K1; g.K2 = K2;
+  g.nch1 = cdiv(K1, kKC);
+  g.nch = g.nch1 + cdiv(K2, kKC);
+  g.A1 = A1; g.lda1 = lda1;
+  g.B1 = B1; g.ldb1 = ldb1;
+  g.vec_a1 = aligned16(A1, lda1) && K1 % 8 == 0;
+  g.vec_b1 = aligned16(B1, ldb1) && K1 % 8 == 0;
+  if (K2 > 0) {
+    g.A2 = A2; g.lda2 = lda2;
+    g.B2 = B2; g.ldb2 = ldb2;
+    g.vec_a2 = aligned16(A2, lda2) && K2 % 8 == 0;
+    g.vec_b2 = aligned16(B2, ldb2) && K2 % 8 == 0;
+  }
+  g.C = C; g.ldc = ldc; g.out_mode = out_bf16 ? OUT_BF16 : OUT_F32;
+  run_gemm(g, A_DENSE, part, s);
+}
+
+size_t gemm_bf16x2_part_bytes(int M, int N, int K1, int K2, int64_t ldc) {
+  return gemm_part_bytes(M, N, K1, K2) / M * ldc;
+}
+
 // Partials are laid out with the output's row stride ldt (>= b).
 size_t tt_gemm_part_bytes(const hss_matrix* A, int b, int ldt) {
   return A->r > 0 ? gemm_part_bytes(b, A->r, A->n, 0) / b * ldt : 0;

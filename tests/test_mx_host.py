@@ -1,0 +1,204 @@
+"""Microscaled formats without a GPU: the oracle's encoding pinned by hand
+values, by the half-step bound and by brute force, and the library's host-side
+refusals (every call below fails its argument checks before any device work)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import hss_synth as syn
+import oracle as O
+
+FAKE = 1 << 20  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def hl():
+    import sparse_rank_linear_hss_amd as h
+    return h
+
+
+# ---------------------------------------------------------------------------
+# The oracle's encoding
+# ---------------------------------------------------------------------------
+
+def test_fp4_hand_group():
+    """Largest magnitude 6: scale 1, every grid value kept, ties to the even code."""
+    w = np.zeros((1, 32))
+    w[0, :12] = [0, 0.5, -1, 1.5, 2, -3, 4, 6, 0.25, 0.75, 2.5, 5]
+    codes, scales = O.mx_encode(w, "fp4")
+    assert scales.tolist() == [[127]]
+    nib = [c for byte in codes[0, :6] for c in (byte & 15, byte >> 4)]
+    assert nib == [0, 1, 8 | 2, 3, 4, 8 | 5, 6, 7, 0, 2, 4, 6]
+    assert O.mx_decode(codes, scales, 12, "fp4").tolist() == [[0, 0.5, -1, 1.5, 2, -3, 4, 6, 0, 1, 2, 4]]
+
+
+def test_largest_magnitude_carries_into_the_next_exponent():
+    """7 is halfway between 6 and 8: it takes 8 = 4 * 2; just below it takes 6.
+    127.5 / 64 takes 128 / 64 = 64 / 32; just below 127 / 64."""
+    for a, scale, value in ((7.0, 128, 8.0), (np.nextafter(7.0, 0), 127, 6.0)):
+        codes, scales = O.mx_encode(np.full((1, 1), a), "fp4")
+        assert scales[0, 0] == scale and O.mx_decode(codes, scales, 1, "fp4")[0, 0] == value
+    for a, scale, value in ((127.5 / 64, 128, 2.0), (np.nextafter(127.5 / 64, 0), 127, 127 / 64)):
+        codes, scales = O.mx_encode(np.full((1, 1), a), "int8")
+        assert scales[0, 0] == scale and O.mx_decode(codes, scales, 1, "int8")[0, 0] == value
+
+
+def test_int8_hand_group():
+    w = np.zeros((1, 5))
+    w[0] = [1.0, -1.984375, 0.5 / 64, 1.5 / 64, -2.5 / 64]
+    codes, scales = O.mx_encode(w, "int8")
+    assert scales.tolist() == [[127]] and codes[0, :6].tolist() == [64, -127, 0, 2, -2, 0] and codes.shape == (1, 32)
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "int8"])
+@pytest.mark.parametrize("dtype", [O.F32, O.BF16])
+def test_no_value_is_off_by_more_than_half_a_step(fmt, dtype):
+    """fp4: half a step is a quarter of the value's power of two (at least a
+    quarter of the group's scale); int8: half the group's step."""
+    W = O.widen(syn.random_matrix(9, 203, dtype, seed=5, kind="t3"), dtype)
+    codes, scales = O.mx_encode(W, fmt)
+    D = O.mx_decode(codes, scales, 203, fmt)
+    s = np.repeat(2.0 ** (scales.astype(float) - 127), 32, axis=1)[:, :203]
+    if fmt == "fp4":
+        half = np.maximum(2.0 ** np.floor(np.log2(np.maximum(np.abs(W), 1e-300))), s) / 4
+    else:
+        half = s / 64 / 2
+    assert np.all(np.abs(W - D) <= half)
+
+
+@pytest.mark.parametrize("dtype", [O.F32, O.BF16])
+def test_borders_of_the_exponent_range(dtype):
+    big = O.widen(np.array([[0x7F7F0000]], np.uint32).view(np.float32), O.F32)     # bf16's largest
+    codes, scales = O.mx_encode(big, "fp4")
+    assert scales[0, 0] == 252 and O.mx_decode(codes, scales, 1, "fp4")[0, 0] == 6 * 2.0 ** 125
+    codes, scales = O.mx_encode(big, "int8")
+    assert scales[0, 0] == 254 and O.mx_decode(codes, scales, 1, "int8")[0, 0] == 127 * 2.0 ** 121
+    for fmt, low in (("fp4", 2), ("int8", 7)):
+        codes, scales = O.mx_encode(np.array([[2.0 ** -126, 0.0]]), fmt)
+        assert scales[0, 0] == low
+    codes, scales = O.mx_encode(np.array([[np.nan, 1.0]]), "fp4")
+    assert scales[0, 0] == 255 and np.all(np.isnan(O.mx_decode(codes, scales, 2, "fp4")))
+
+
+# ---------------------------------------------------------------------------
+# Refusals of the library
+# ---------------------------------------------------------------------------
+
+def test_mx_sizes(hl):
+    lib = hl._lib.lib
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.hss_mx_sizes(0, 3, 33, ctypes.byref(c), ctypes.byref(s)) == 0 and (c.value, s.value) == (96, 6)
+    assert lib.hss_mx_sizes(1, 3, 33, ctypes.byref(c), ctypes.byref(s)) == 0 and (c.value, s.value) == (192, 6)
+    INV = hl._lib.HSS_ERR_INVALID_ARG
+    for fmt, rows, cols in ((2, 3, 33), (-1, 3, 33), (0, 0, 33), (0, 3, 0), (0, 1 << 26, 1), (1, 65536, 32768)):
+        assert lib.hss_mx_sizes(fmt, rows, cols, ctypes.byref(c), ctypes.byref(s)) == INV
+    assert lib.hss_mx_sizes(0, 3, 33, None, ctypes.byref(s)) == INV
+
+
+def test_quantize_rejects_bad_arguments(hl):
+    lib, INV = hl._lib.lib, hl._lib.HSS_ERR_INVALID_ARG
+
+    def q(fmt=0, dt=1, rows=4, cols=64, src=FAKE, codes=FAKE * 2, scales=FAKE * 3, res=None):
+        return lib.hss_mx_quantize(fmt, dt, rows, cols, src, codes, scales, res, None)
+
+    def d(fmt=0, dt=1, rows=4, cols=64, codes=FAKE * 2, scales=FAKE * 3, dst=FAKE):
+        return lib.hss_mx_dequantize(fmt, dt, rows, cols, codes, scales, dst, None)
+
+    for kw in (dict(fmt=2), dict(dt=2), dict(rows=0), dict(cols=-1), dict(rows=1 << 26, cols=1), dict(codes=None),
+               dict(scales=None), dict(codes=FAKE * 2 + 8)):
+        assert q(**kw) == INV, kw
+        assert d(**kw) == INV, kw
+    for kw in (dict(src=None), dict(scales=FAKE * 2 + 4), dict(src=FAKE + 1), dict(src=FAKE + 2, dt=0), dict(codes=FAKE + 16),
+               dict(scales=FAKE + 100), dict(res=FAKE + 2), dict(res=FAKE * 2 + 2), dict(res=FAKE * 3),
+               dict(res=FAKE * 5 + 1)):
+        assert q(**kw) == INV, kw
+    for kw in (dict(dst=None), dict(dst=FAKE + 1), dict(dst=FAKE * 2), dict(dst=FAKE * 3 - 4)):
+        assert d(**kw) == INV, kw
+
+
+def _mx(hl, **kw):
+    s = hl._lib.HssMatrixStruct()
+    s.fmt, s.dtype, s.m, s.n, s.r, s.flags, s.nnz = 0, 1, 16, 32, 4, 16, 10
+    s.row_ptr = s.col_idx = s.values = FAKE
+    s.U, s.Vt = FAKE, FAKE + 4096
+    s.dq_codes, s.dq_levels = FAKE * 6, FAKE * 7
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def test_apply_checks_a_microscaled_dense_part(hl):
+    lib = hl._lib.lib
+    INV, WS, UNS = hl._lib.HSS_ERR_INVALID_ARG, hl._lib.HSS_ERR_WORKSPACE, hl._lib.HSS_ERR_UNSUPPORTED
+
+    def apply(s, b=1, X=FAKE * 8, Y=FAKE * 9, ws=FAKE * 16, wsb=0):
+        return lib.hss_apply(ctypes.byref(s), b, X, Y, ws, wsb, None)
+
+    assert apply(_mx(hl)) == WS                                   # valid but for the workspace
+    assert apply(_mx(hl, flags=48)) == WS                         # the transposed form
+    assert apply(_mx(hl, flags=17)) == WS                         # 16-bit columns
+    assert apply(_mx(hl, nnz=0, col_idx=None, values=None, r=0, U=None, Vt=None)) == WS
+    assert apply(_mx(hl, flags=32)) == INV                        # transposed without the part
+    assert apply(_mx(hl, flags=16 | 2)) == INV                    # two dense parts
+    assert apply(_mx(hl, flags=16 | 4)) == INV                    # with the block low-rank form
+    assert apply(_mx(hl, fmt=1, nm_values=FAKE, nm_meta=FAKE)) == INV
+    assert apply(_mx(hl, dq_codes=None)) == INV
+    assert apply(_mx(hl, dq_levels=None)) == INV
+    assert apply(_mx(hl, dq_codes=FAKE * 6 + 8)) == INV
+    assert apply(_mx(hl, row_ptr=None)) == INV
+    assert apply(_mx(hl, dtype=0)) == UNS
+    assert apply(_mx(hl, m=1 << 26, n=1)) == INV                  # 32 m bytes of padded rows
+    assert apply(_mx(hl, m=1, n=1 << 26)) == INV                  # and of the transposed array
+    assert apply(_mx(hl), X=FAKE * 9, Y=FAKE * 9) == INV
+    assert apply(_mx(hl), b=2049) == INV
+    out = ctypes.c_size_t()
+    assert lib.hss_apply_workspace_size(ctypes.byref(_mx(hl)), 4, ctypes.byref(out)) == 0 and out.value > 0
+    assert lib.hss_grad_workspace_size(ctypes.byref(_mx(hl)), 4, ctypes.byref(out)) == 0
+
+
+def test_grad_ckpt_rejects_bad_arguments(hl):
+    lib = hl._lib.lib
+    INV, WS, UNS = hl._lib.HSS_ERR_INVALID_ARG, hl._lib.HSS_ERR_WORKSPACE, hl._lib.HSS_ERR_UNSUPPORTED
+
+    def grad(s, b=4, codes=FAKE * 8, scales=FAKE * 9, G=FAKE * 10, dS=FAKE * 11, dU=FAKE * 12, dVt=FAKE * 13,
+             ws=FAKE * 16, wsb=0):
+        return lib.hss_grad_ckpt(ctypes.byref(s), b, codes, scales, G, dS, dU, dVt, ws, wsb, None)
+
+    plain = _mx(hl, flags=0, dq_codes=None, dq_levels=None)
+    assert grad(plain) == WS and grad(_mx(hl)) == WS
+    assert grad(plain, ws=None, wsb=1 << 30) == WS
+    for kw in (dict(codes=None), dict(scales=None), dict(G=None), dict(codes=FAKE * 8 + 8), dict(b=0), dict(b=2049),
+               dict(dS=FAKE * 10), dict(dU=FAKE * 8 + 4), dict(dVt=FAKE * 9 + 1), dict(dU=FAKE * 11 + 4)):
+        assert grad(plain, **kw) == INV, kw
+    assert grad(_mx(hl, flags=0, dtype=0)) == UNS
+    assert grad(_mx(hl, flags=2, r=0, U=None, Vt=None)) == UNS     # a per-row table part
+    out = ctypes.c_size_t()
+    assert lib.hss_grad_ckpt_workspace_size(ctypes.byref(plain), 4, None) == INV
+    assert lib.hss_grad_ckpt_workspace_size(ctypes.byref(_mx(hl, flags=0, m=1 << 19, n=8, r=0)), 2048,
+                                            ctypes.byref(out)) == UNS
+
+
+def test_binding_checks(hl):
+    import torch
+    q = hl.MXTensor.empty("fp4", 3, 33, "cpu")
+    assert q.codes.shape == (3, 32) and q.scales.shape == (3, 2)
+    assert hl.MXTensor.empty("int8", 3, 33, "cpu").codes.shape == (3, 64)
+    with pytest.raises(ValueError):
+        hl.MXTensor("fp8", 3, 33, q.codes, q.scales)
+    with pytest.raises(ValueError):
+        hl.MXTensor("fp4", 3, 65, q.codes, q.scales)
+    with pytest.raises(ValueError):
+        hl.MXTensor("int8", 3, 33, q.codes, q.scales)
+    with pytest.raises(ValueError):
+        hl.MXTensor("fp4", 3, 33, q.codes, q.scales.t())
+    with pytest.raises(ValueError):
+        hl.hss_mx_quantize(torch.zeros(3, 33), "fp4")             # not on a GPU
+    with pytest.raises(ValueError):
+        hl.HSSMatrix("csr", 33, 3, torch.bfloat16, mx=q)          # shapes swapped
+    with pytest.raises(ValueError):
+        hl.HSSMatrix("csr", 3, 33, torch.bfloat16, mx_t=True)
+    A = hl.HSSMatrix("csr", 3, 33, torch.bfloat16, mx=q)
+    assert A.nnz == 0 and A.row_ptr.shape == (4,) and hl.hss_apply_workspace_size(A, 5) > 0
+    At = hl.HSSMatrix("csr", 33, 3, torch.bfloat16, mx=q, mx_t=True)
+    assert At.flags == hl.HSS_MX4 | hl.HSS_MX4_T
