@@ -55,7 +55,9 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle alone: building a Stream object costs more than a launch
+    index = device.index if isinstance(device, torch.device) else torch.device(device).index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _on(dev):

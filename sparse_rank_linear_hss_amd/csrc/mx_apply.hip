@@ -2,7 +2,7 @@
 //   Y = X (S + U V^T + D)^T,  D MXFP4, m x n; with HSS_MX4_T the stored array
 //   is D^T (n x m), so that a layer and its transposed layer share one copy.
 //
-// General route, any batch:
+// Up to 16 columns, D not transposed: mx_skinny.hip.  General route, any batch:
 //   W'  = D + S as dense bf16 in the workspace, rows padded to 32 columns
 //   T   = X V in fp32 (matrix cores), kept as two bf16 terms T = T1 + T2 (16
 //         significant bits, so that rounding T does not show beside the
@@ -24,6 +24,11 @@ void launch_gemm_bf16x2(int M, int N, int K1, const uint16_t* A1, int64_t lda1, 
                         int K2, const uint16_t* A2, int64_t lda2, const uint16_t* B2, int64_t ldb2, void* C,
                         int64_t ldc, bool out_bf16, float* part, hipStream_t s);
 size_t gemm_bf16x2_part_bytes(int M, int N, int K1, int K2, int64_t ldc);
+
+// mx_skinny.hip
+bool mx_skinny_supported(const hss_matrix* A, int b);
+size_t mx_skinny_ws_bytes(const hss_matrix* A, int b);
+hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s);
 
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 static int round32(int x) { return (x + 31) & ~31; }
@@ -208,11 +213,14 @@ static MxPlan plan_mx(const hss_matrix* A, int b) {
   return p;
 }
 
-size_t mx_apply_ws_bytes(const hss_matrix* A, int b) { return plan_mx(A, b).total; }
+size_t mx_apply_ws_bytes(const hss_matrix* A, int b) {
+  return mx_skinny_supported(A, b) ? mx_skinny_ws_bytes(A, b) : plan_mx(A, b).total;
+}
 
 static bool rows_ok(const void* p, int cols) { return (uintptr_t)p % 16 == 0 && cols % 32 == 0; }
 
 hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s) {
+  if (mx_skinny_supported(A, b)) return launch_mx_skinny(A, b, X, Y, ws, s);
   const MxPlan p = plan_mx(A, b);
   char* base = static_cast<char*>(ws);
   uint16_t* W = reinterpret_cast<uint16_t*>(base + p.w);
