@@ -29,6 +29,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 static constexpr int kSkCols = 16;       // columns of one call
+static constexpr int kSkGather = 4;      // columns up to which S gathers from X, not X^T
 static constexpr int kSkBatch = 4;       // chunks whose loads are in flight together
 static constexpr int kPrepSplits = 8;    // most K splits of T
 
@@ -54,15 +55,22 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
 
 // ---------------------------------------------------------------------------
 // Blocks 0 .. tb - 1: 16 rows of V^T over one K split, T partial sums
-// Tp[ks][c][rp] (c < b).  Blocks from tb: X^T (n x 16, columns past b zero).
+// Tp[ks][c][rp] (c < b).  Blocks from tb: X^T (n x 16, columns past b zero)
+// and X with rows of np (zero past n), each where its pointer is not null.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void k_mx_prep(const uint16_t* __restrict__ X, const uint16_t* __restrict__ Vt, int b,
                                                  int n, int r, int rp, int ltiles, int steps_per_split, int tb,
-                                                 float* __restrict__ Tp, uint16_t* __restrict__ Xt) {
+                                                 float* __restrict__ Tp, uint16_t* __restrict__ Xt, uint16_t* __restrict__ Xp,
+                                                 int np) {
   __shared__ float red[4][256];
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   if ((int)blockIdx.x >= tb) {
-    for (int j = ((int)blockIdx.x - tb) * 256 + t; j < n; j += ((int)gridDim.x - tb) * 256) {
+    const int first = ((int)blockIdx.x - tb) * 256 + t, step = ((int)gridDim.x - tb) * 256;
+    for (int e = first; Xp && e < b * (np >> 3); e += step) {
+      const int c = e / (np >> 3), k = (e - c * (np >> 3)) * 8;
+      *reinterpret_cast<u32x4*>(Xp + (int64_t)c * np + k) = load_row8(X + (int64_t)c * n, k, n);
+    }
+    for (int j = first; Xt && j < n; j += step) {
       uint32_t v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -107,43 +115,81 @@ struct SkinnyArgs {
   const int32_t* row_ptr;
   const void* col;
   const uint16_t* vals;
-  const uint16_t* X;
+  const uint16_t* X;   // rows of ldx, 16-byte aligned unless b == 1
   const uint16_t* Xt;  // n x 16, b > 1 and S not empty
   const uint16_t* U;
   const float* Tp;
   uint16_t* Y;
-  int m, n, b, r, rp, ng, splits, has_s, col16;
+  int m, n, b, r, rp, ng, ldx, splits, has_s, col16;
 };
 
-// S's part of one row for one column (b == 1): the lanes take its entries.
-template <typename COL>
-__device__ __forceinline__ float s_row1(const SkinnyArgs& a, const COL* __restrict__ col, int p0, int p1) {
-  float s = 0.f;
-  for (int p = p0 + lane_id(); p < p1; p += 64) {
-    const int j = (int)col[p];
-    if ((unsigned)j < (unsigned)a.n) s = fmaf(bf16lo(a.vals[p]), bf16lo(a.X[j]), s);
+// S's part of the block's 16 rows.  A wave takes R rows at once, LG = 64 / R
+// lanes each; a lane's entries are loaded four at a time (past the end the
+// last one again, with value 0), so that the chain of dependent loads -- row
+// pointers, columns, X -- is walked once for up to 4 LG (2 LG) entries.
+// Up to CB (1 or 4) columns: the lanes of a row take its entries and gather
+// each column's value of X.
+template <int LG, int CB, typename COL>
+__device__ __forceinline__ void s_rows(const SkinnyArgs& a, const COL* __restrict__ col, int p0, int p1, float (&s)[CB]) {
+  const int sl = lane_id() % LG;
+#pragma unroll
+  for (int c = 0; c < CB; ++c) s[c] = 0.f;
+  for (int p = p0 + sl; p < p1; p += 4 * LG) {
+    int j[4];
+    float v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int pp = min(p + u * LG, p1 - 1);
+      j[u] = (int)col[pp];
+      v[u] = bf16lo(a.vals[pp]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool ok = p + u * LG < p1 && (unsigned)j[u] < (unsigned)a.n;
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        const float x = bf16lo(a.X[(uint32_t)(min(c, a.b - 1) * a.ldx + (ok ? j[u] : 0))]);
+        s[c] = fmaf(ok ? v[u] : 0.f, ok ? x : 0.f, s[c]);
+      }
+    }
   }
-  return wave_sum(s);
+#pragma unroll
+  for (int c = 0; c < CB; ++c)
+#pragma unroll
+    for (int off = 1; off < LG; off <<= 1) s[c] += __shfl_xor(s[c], off, 64);
 }
 
-// S's part of one row for 16 columns: lane 2 e + h takes entries e, e + 32, ..
-// and columns 8 h .. 8 h + 7; the 32 lanes of a half are then added up in a
-// fixed tree, in which the lanes first share out the eight columns.  Column
-// 8 h + k ends in the lanes with lane % 2 = h and (lane / 2) % 8 = k.
-template <typename COL>
-__device__ __forceinline__ float s_row16(const SkinnyArgs& a, const COL* __restrict__ col, int p0, int p1) {
-  const int lane = lane_id(), h = lane & 1;
+// Sixteen columns: lane 2 e + h of a row takes entries e, e + LG / 2, .. and
+// columns 8 h .. 8 h + 7; the lanes of a half are then added up in a fixed
+// tree, in which they first share out the eight columns: column 8 h + k ends
+// in the lanes with lane % 2 = h and (lane / 2) % 8 = k.
+template <int LG, typename COL>
+__device__ __forceinline__ float s_rows16(const SkinnyArgs& a, const COL* __restrict__ col, int p0, int p1) {
+  const int lane = lane_id(), sl = lane % LG, h = lane & 1;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int p = p0 + (lane >> 1); p < p1; p += 32) {
-    const int j = (int)col[p];
-    if ((unsigned)j >= (unsigned)a.n) continue;
-    const float v = bf16lo(a.vals[p]);
-    const u32x4 x = *reinterpret_cast<const u32x4*>(a.Xt + (int64_t)j * kSkCols + 8 * h);
+  for (int p = p0 + (sl >> 1); p < p1; p += 2 * LG) {
+    int j[4];
+    float v[4];
+    u32x4 x[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      s[2 * k] = fmaf(v, bf16lo(x[k]), s[2 * k]);
-      s[2 * k + 1] = fmaf(v, bf16hi(x[k]), s[2 * k + 1]);
+    for (int u = 0; u < 4; ++u) {
+      const int pp = min(p + u * (LG / 2), p1 - 1);
+      j[u] = (int)col[pp];
+      v[u] = bf16lo(a.vals[pp]);
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool ok = p + u * (LG / 2) < p1 && (unsigned)j[u] < (unsigned)a.n;
+      x[u] = *reinterpret_cast<const u32x4*>(a.Xt + (int64_t)(ok ? j[u] : 0) * kSkCols + 8 * h);
+      if (!ok) v[u] = 0.f, x[u] = u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s[2 * k] = fmaf(v[u], bf16lo(x[u][k]), s[2 * k]);
+        s[2 * k + 1] = fmaf(v[u], bf16hi(x[u][k]), s[2 * k + 1]);
+      }
   }
   // lane bits 1..3 pick the column's bits 0..2
 #pragma unroll
@@ -155,8 +201,8 @@ __device__ __forceinline__ float s_row16(const SkinnyArgs& a, const COL* __restr
       s[k] = mine + __shfl_xor(other, 2 << bit, 64);
     }
   }
-  s[0] += __shfl_xor(s[0], 16, 64);
-  s[0] += __shfl_xor(s[0], 32, 64);
+#pragma unroll
+  for (int off = 16; off < LG; off <<= 1) s[0] += __shfl_xor(s[0], off, 64);
   return s[0];
 }
 
@@ -169,37 +215,47 @@ __global__ __launch_bounds__(64 * WV, 4) void k_mx_skinny(SkinnyArgs a) {
   const int t = threadIdx.x, lane = t & 63, w = uniform(t >> 6);
   const int row0 = (int)blockIdx.x * 16;
   const int q = lane >> 4;
-  const int nch = (a.ng + 3) >> 2;
-  const int64_t grow = (int64_t)min(row0 + (lane & 15), a.m - 1) * a.ng;
-  const uint16_t* __restrict__ xrow = a.X + (int64_t)min(lane & 15, a.b - 1) * a.n;
+  const int nch = (a.ng + 3) >> 2, nfull = a.n >> 7;  // the last chunk may be short
+  const uint32_t grow = (uint32_t)min(row0 + (lane & 15), a.m - 1) * (uint32_t)a.ng;
+  const uint32_t xoff = (uint32_t)min(lane & 15, a.b - 1) * (uint32_t)a.ldx;
 
-  u32x4 cw[kSkBatch], xv[kSkBatch][4];
+  u32x4 cw[kSkBatch], xv[2][4];
   uint32_t sb[kSkBatch];
-  // chunk c0 + WV u: past the end, a valid group's codes against zeros of X
+  // whole chunks c0 + WV u; past the last one, that one again, not used.  The
+  // codes of a batch are in flight together, X two chunks ahead.
+  auto load_x = [&](int c, u32x4 (&x)[4]) {
+    const Bytes16* xp = reinterpret_cast<const Bytes16*>(a.X + (xoff + 128 * (uint32_t)min(c, nfull - 1) + 32 * q));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = u32x4{xp[k].w[0], xp[k].w[1], xp[k].w[2], xp[k].w[3]};
+  };
   auto issue = [&](int c0) {
 #pragma unroll
     for (int u = 0; u < kSkBatch; ++u) {
-      const int g = 4 * (c0 + WV * u) + q;
-      const int64_t at = grow + min(g, a.ng - 1);
+      const uint32_t at = grow + 4 * (uint32_t)min(c0 + WV * u, nfull - 1) + q;
       cw[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.codes + at * 16));
-      sb[u] = g < a.ng ? a.scales[at] : 0u;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) xv[u][k] = load_row8(xrow, g * 32 + 8 * k, a.n);
+      sb[u] = a.scales[at];
     }
+    load_x(c0, xv[0]);
+    load_x(c0 + WV, xv[1]);
   };
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  auto compute = [&]() {
+  auto compute = [&](int c0) {
 #pragma unroll
     for (int u = 0; u < kSkBatch; ++u) {
+      if (c0 + WV * u >= nfull) break;  // the same for the whole wave
       const float sc = mx_scale(sb[u], 0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const u32x4 av = sb[u] ? mx4_to_bf16x8(cw[u][k], sc) : u32x4{0u, 0u, 0u, 0u};
-        acc = mfma16(av, xv[u][k], acc);
-      }
+      for (int k = 0; k < 4; ++k) acc = mfma16(mx4_to_bf16x8(cw[u][k], sc), xv[u & 1][k], acc);
+      if (u + 2 < kSkBatch) load_x(c0 + WV * (u + 2), xv[u & 1]);
     }
   };
-  if (w < nch) issue(w);
+  constexpr int LG = 4 * WV;  // lanes per row of S
+  int p0 = 0, p1 = 0;
+  if (a.has_s && row0 + w * (16 / WV) + lane / LG < a.m) {
+    p0 = a.row_ptr[row0 + w * (16 / WV) + lane / LG];
+    p1 = a.row_ptr[row0 + w * (16 / WV) + lane / LG + 1];
+  }
+  if (w < nfull) issue(w);
 
   const int ldt = a.rp + 8;  // rows 16 bytes apart modulo the banks
   if (a.r > 0) {
@@ -215,24 +271,38 @@ __global__ __launch_bounds__(64 * WV, 4) void k_mx_skinny(SkinnyArgs a) {
     }
   }
   if (a.has_s) {
-    for (int i = w; i < 16; i += WV) {
-      const int row = row0 + i;
-      int p0 = 0, p1 = 0;
-      if (row < a.m) p0 = a.row_ptr[row], p1 = a.row_ptr[row + 1];
-      if (a.b == 1) {
-        const float s = a.col16 ? s_row1(a, static_cast<const uint16_t*>(a.col), p0, p1)
-                                : s_row1(a, static_cast<const int32_t*>(a.col), p0, p1);
-        if (lane == 0) sred[i] = s;
-      } else {
-        const float s = a.col16 ? s_row16(a, static_cast<const uint16_t*>(a.col), p0, p1)
-                                : s_row16(a, static_cast<const int32_t*>(a.col), p0, p1);
-        if (lane < 16) sred[(8 * (lane & 1) + (lane >> 1)) * 16 + i] = s;
-      }
+    const int i = w * (16 / WV) + lane / LG;
+    const uint16_t* c16 = static_cast<const uint16_t*>(a.col);
+    const int32_t* c32 = static_cast<const int32_t*>(a.col);
+    if (a.b == 1) {
+      float s[1];
+      if (a.col16) s_rows<LG, 1>(a, c16, p0, p1, s);
+      else s_rows<LG, 1>(a, c32, p0, p1, s);
+      if (lane % LG == 0) sred[i] = s[0];
+    } else if (a.b <= kSkGather) {
+      float s[kSkGather];
+      if (a.col16) s_rows<LG, kSkGather>(a, c16, p0, p1, s);
+      else s_rows<LG, kSkGather>(a, c32, p0, p1, s);
+#pragma unroll
+      for (int c = 0; c < kSkGather; ++c)
+        if (lane % LG == c) sred[c * 16 + i] = s[c];
+    } else {
+      const float s = a.col16 ? s_rows16<LG>(a, c16, p0, p1) : s_rows16<LG>(a, c32, p0, p1);
+      if (lane % LG < 16) sred[(8 * (lane & 1) + ((lane >> 1) & 7)) * 16 + i] = s;
     }
   }
-  for (int c0 = w; c0 < nch; c0 += WV * kSkBatch) {
-    compute();
-    if (c0 + WV * kSkBatch < nch) issue(c0 + WV * kSkBatch);
+  for (int c0 = w; c0 < nfull; c0 += WV * kSkBatch) {
+    compute(c0);
+    if (c0 + WV * kSkBatch < nfull) issue(c0 + WV * kSkBatch);
+  }
+  if (nch > nfull && w == nfull % WV) {  // the short chunk: lanes past its groups hold zeros of X
+    const int g = 4 * nfull + q;
+    const uint32_t at = grow + (uint32_t)min(g, a.ng - 1);
+    const u32x4 code = *reinterpret_cast<const u32x4*>(a.codes + at * 16);
+    const float sc = g < a.ng ? mx_scale(a.scales[at], 0) : 1.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      acc = mfma16(mx4_to_bf16x8(code[k], sc), load_row8(a.X + xoff, 32 * g + 8 * k, a.n), acc);
   }
   if (a.r > 0) {
     __syncthreads();
@@ -265,7 +335,7 @@ static int round32(int x) { return (x + 31) & ~31; }
 
 struct SkinnyPlan {
   int rp, ltiles, splits, steps_per_split;
-  size_t tp, xt, total;
+  size_t tp, xt, xp, total;
 };
 
 static SkinnyPlan plan_skinny(const hss_matrix* A, int b) {
@@ -278,7 +348,8 @@ static SkinnyPlan plan_skinny(const hss_matrix* A, int b) {
   p.steps_per_split = (steps + p.splits - 1) / p.splits;
   p.tp = 0;
   p.xt = al256((size_t)p.splits * b * p.rp * 4);
-  p.total = p.xt + ((b > 1 && A->nnz > 0) ? al256((size_t)A->n * kSkCols * 2) : 0);
+  p.xp = p.xt + ((b > kSkGather && A->nnz > 0) ? al256((size_t)A->n * kSkCols * 2) : 0);
+  p.total = p.xp + (b > 1 ? al256((size_t)b * round32(A->n) * 2) : 0);
   return p;
 }
 
@@ -310,13 +381,23 @@ hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, 
   a.splits = p.splits;
   a.has_s = A->nnz > 0;
   a.col16 = (A->flags & HSS_COL16) != 0;
-  const bool need_xt = a.has_s && b > 1;
+  a.ldx = n;
+  const bool need_xt = a.has_s && b > kSkGather;
+  // rows off the 16-byte grid: 16-byte loads of X at 2-byte addresses cost the
+  // main launch more than a copy (2731 x 5003, 13 columns: 14.8 against 9.6 us)
+  const bool need_xp = b > 1 && (n % 8 != 0 || (uintptr_t)X % 16 != 0);
   const int tb = r > 0 ? p.ltiles * p.splits : 0;
-  const int xb = need_xt ? std::min((n + 255) / 256, 256) : 0;
+  const int xb = need_xt || need_xp ? std::min((n + 255) / 256, 256) : 0;
   if (tb + xb > 0)
     hipLaunchKernelGGL(k_mx_prep, dim3((unsigned)(tb + xb)), dim3(256), 0, s, a.X,
                        static_cast<const uint16_t*>(A->Vt), b, n, r, p.rp, std::max(p.ltiles, 1), p.steps_per_split,
-                       tb, reinterpret_cast<float*>(base + p.tp), reinterpret_cast<uint16_t*>(base + p.xt));
+                       tb, reinterpret_cast<float*>(base + p.tp),
+                       need_xt ? reinterpret_cast<uint16_t*>(base + p.xt) : nullptr,
+                       need_xp ? reinterpret_cast<uint16_t*>(base + p.xp) : nullptr, round32(n));
+  if (need_xp) {
+    a.X = reinterpret_cast<const uint16_t*>(base + p.xp);
+    a.ldx = round32(n);
+  }
   const unsigned grid = (unsigned)((m + 15) / 16);
   const size_t tl = r > 0 ? (size_t)b * 2 * (p.rp + 8) * 2 : 0;
   const int nch = (a.ng + 3) / 4;
