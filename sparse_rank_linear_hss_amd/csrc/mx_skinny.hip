@@ -1,8 +1,10 @@
 // HSS_MX4 apply for up to 16 columns (decode): Y = X (S + U V^T + D)^T straight
-// from the 4-bit codes, in one launch (two when there is a low-rank term, or
-// an S and more than one column).  Bound by the codes' stream from HBM.
+// from the 4-bit codes, in one launch (two when there is a low-rank term, an S
+// and more than four columns, or X off the 16-byte grid).  Bound by the codes'
+// stream from HBM.  Up to four columns: k_mx_gemv, on the vector units, below.
+// From five on: k_mx_skinny, on the matrix cores.
 //
-// A block owns 16 rows of D.  Its waves split the columns into chunks of 128:
+// k_mx_skinny: a block owns 16 rows of D.  Its waves split the columns into chunks of 128:
 // lane l of a wave reads the 16 bytes of row l % 16, group l / 16 of the chunk
 // -- one group, one scale byte -- and decodes them (v_cvt_scalef32, two values
 // an instruction) into four A operands of v_mfma_f32_16x16x32_bf16.  The
@@ -122,6 +124,17 @@ struct SkinnyArgs {
   uint16_t* Y;
   int m, n, b, r, rp, ng, ldx, splits, has_s, col16;
 };
+
+// Element e of T: its K splits' partial sums, loaded together, added in order.
+__device__ __forceinline__ float t_sum(const SkinnyArgs& a, int e) {
+  float p[kPrepSplits];
+#pragma unroll
+  for (int ks = 0; ks < kPrepSplits; ++ks) p[ks] = a.Tp[(uint32_t)min(ks, a.splits - 1) * (uint32_t)(a.b * a.rp) + e];
+  float v = p[0];
+#pragma unroll
+  for (int ks = 1; ks < kPrepSplits; ++ks) v += ks < a.splits ? p[ks] : 0.f;
+  return v;
+}
 
 // S's part of the block's 16 rows.  A wave takes R rows at once, LG = 64 / R
 // lanes each; a lane's entries are loaded four at a time (past the end the
@@ -260,8 +273,7 @@ __global__ __launch_bounds__(64 * WV, 4) void k_mx_skinny(SkinnyArgs a) {
   const int ldt = a.rp + 8;  // rows 16 bytes apart modulo the banks
   if (a.r > 0) {
     for (int e = t; e < a.b * a.rp; e += 64 * WV) {
-      float v = 0.f;
-      for (int ks = 0; ks < a.splits; ++ks) v += a.Tp[(int64_t)ks * a.b * a.rp + e];
+      const float v = t_sum(a, e);
       const int c = e / a.rp, l = e - c * a.rp;
       const uint16_t hi = f32_to_bf16(v);
       // an infinity leaves 0, not the NaN of inf - inf
@@ -328,10 +340,176 @@ __global__ __launch_bounds__(64 * WV, 4) void k_mx_skinny(SkinnyArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// One to four columns, k_mx_gemv<BC, RW>: a wave owns RW rows and walks their
+// columns in chunks of 2048, one group (16 bytes of codes, 32 columns) per
+// lane, so that a row's codes come in whole lines.  A group's values meet the
+// lane's 32 columns of X, read once from LDS for all RW rows, in
+// v_dot2_f32_bf16: 16 conversions and 16 BC products per group, where the
+// matrix cores would fill 16 columns whatever BC is and want four times the
+// codes' bytes of X from the vector memory path.  S and U T are added to the
+// lanes' partial sums, and one wave sum per row and column ends it.
+// X sits in LDS piece-major: 16-byte piece k of group g of a chunk at 64 k + g,
+// so that neighbouring lanes read neighbouring pieces.
+// ---------------------------------------------------------------------------
+static constexpr int kGvWaves = 4;
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
+}
+
+// bf16 index of column j within X's LDS image.
+__device__ __forceinline__ int gv_at(int j) {
+  return ((((j >> 11) * 4 + ((j >> 3) & 3)) * 64 + ((j >> 5) & 63)) << 3) + (j & 7);
+}
+
+template <int BC, int RW>
+__global__ __launch_bounds__(64 * kGvWaves) void k_mx_gemv(SkinnyArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  const int nch = (a.ng + 63) >> 6;                  // chunks of 64 groups
+  const int plane = nch * 2048;                      // bf16 of one column's image
+  uint16_t* xs = reinterpret_cast<uint16_t*>(lds);   // [BC][plane]
+  float* Ts = reinterpret_cast<float*>(xs + BC * plane);  // [BC][rp]
+  const int t = threadIdx.x, lane = t & 63, w = uniform(t >> 6);
+  const int row0 = ((int)blockIdx.x * kGvWaves + w) * RW;
+  uint32_t grow[RW];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) grow[i] = (uint32_t)min(row0 + i, a.m - 1) * (uint32_t)a.ng;
+
+  u32x4 cw[2][RW];
+  uint32_t sb[2][RW];
+  // lanes past the row's last group read that one again, against zeros of X
+  auto issue = [&](int c, u32x4 (&cv)[RW], uint32_t (&sv)[RW]) {
+    const uint32_t g = (uint32_t)min(64 * c + lane, a.ng - 1);
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      cv[i] = *reinterpret_cast<const u32x4*>(a.codes + (grow[i] + g) * 16);
+      sv[i] = a.scales[grow[i] + g];
+    }
+  };
+  issue(0, cw[0], sb[0]);
+  // the first 64 entries of each row of S
+  int p0[RW], p1[RW], j0[RW];
+  uint32_t v0[RW];
+  if (a.has_s) {
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      p0[i] = a.row_ptr[min(row0 + i, a.m - 1)];
+      p1[i] = a.row_ptr[min(row0 + i, a.m - 1) + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      const int p = p0[i] + lane;
+      j0[i] = -1, v0[i] = 0u;
+      if (p < p1[i]) {
+        j0[i] = a.col16 ? (int)static_cast<const uint16_t*>(a.col)[p] : static_cast<const int32_t*>(a.col)[p];
+        v0[i] = a.vals[p];
+      }
+    }
+  }
+  for (int e = t; e < nch * 256; e += 64 * kGvWaves) {
+    const int at = ((((e >> 8) * 4 + (e & 3)) * 64 + ((e >> 2) & 63)) << 3);
+#pragma unroll
+    for (int c = 0; c < BC; ++c)
+      *reinterpret_cast<u32x4*>(xs + c * plane + at) = load_row8(a.X + (int64_t)min(c, a.b - 1) * a.n, 8 * e, a.n);
+  }
+  if (a.r > 0) {
+    for (int e = t; e < a.b * a.rp; e += 64 * kGvWaves) Ts[e] = t_sum(a, e);
+  }
+  __syncthreads();
+
+  float acc[RW][BC];
+#pragma unroll
+  for (int i = 0; i < RW; ++i)
+#pragma unroll
+    for (int c = 0; c < BC; ++c) acc[i][c] = 0.f;
+  auto compute = [&](int ch, const u32x4 (&cv)[RW], const uint32_t (&sv)[RW]) {
+    float sc[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) sc[i] = mx_scale(sv[i], 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      u32x4 x[BC];
+#pragma unroll
+      for (int c = 0; c < BC; ++c)
+        x[c] = *reinterpret_cast<const u32x4*>(xs + c * plane + (((ch * 4 + k) * 64 + lane) << 3));
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        const u32x4 d = mx4_to_bf16x8(cv[i][k], sc[i]);
+#pragma unroll
+        for (int c = 0; c < BC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][c] = dot2(d[e], x[c][e], acc[i][c]);
+      }
+    }
+  };
+  // pairs of chunks, so that the two register sets are named at compile time
+  for (int ch = 0; ch < nch; ch += 2) {
+    if (ch + 1 < nch) issue(ch + 1, cw[1], sb[1]);
+    compute(ch, cw[0], sb[0]);
+    if (ch + 1 < nch) {
+      if (ch + 2 < nch) issue(ch + 2, cw[0], sb[0]);
+      compute(ch + 1, cw[1], sb[1]);
+    }
+  }
+  if (a.has_s) {
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      for (int p = p0[i] + lane;;) {
+        if ((unsigned)j0[i] < (unsigned)a.n) {
+          const float v = bf16lo(v0[i]);
+#pragma unroll
+          for (int c = 0; c < BC; ++c) acc[i][c] = fmaf(v, bf16lo(xs[c * plane + gv_at(j0[i])]), acc[i][c]);
+        }
+        p += 64;
+        if (p >= p1[i]) break;
+        j0[i] = a.col16 ? (int)static_cast<const uint16_t*>(a.col)[p] : static_cast<const int32_t*>(a.col)[p];
+        v0[i] = a.vals[p];
+      }
+    }
+  }
+  for (int l = 8 * lane; l < a.r; l += 512) {
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      const u32x4 u = load_row8(a.U + (int64_t)min(row0 + i, a.m - 1) * a.r, l, a.r);
+#pragma unroll
+      for (int c = 0; c < BC; ++c) {
+        const float* T = Ts + min(c, a.b - 1) * a.rp + l;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[i][c] = fmaf(bf16lo(u[e]), T[2 * e], acc[i][c]);
+          acc[i][c] = fmaf(bf16hi(u[e]), T[2 * e + 1], acc[i][c]);
+        }
+      }
+    }
+  }
+  // result q = i BC + c goes to lane q
+  float y = 0.f;
+#pragma unroll
+  for (int i = 0; i < RW; ++i)
+#pragma unroll
+    for (int c = 0; c < BC; ++c) {
+      const float v = wave_sum(acc[i][c]);
+      if (lane == i * BC + c) y = v;
+    }
+  const int c = lane % BC, row = row0 + lane / BC;
+  if (lane < RW * BC && c < a.b && row < a.m) a.Y[(int64_t)c * a.m + row] = f32_to_bf16(y);
+}
+
+// ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 static int round32(int x) { return (x + 31) & ~31; }
+
+static size_t gv_plane_bytes(int n) { return (size_t)((mx_groups(n) + 63) / 64) * 4096; }
+
+// Up to four columns whose X (and T) fit 64 KiB of LDS, of rows long enough
+// to give most lanes a group.
+static bool gv_supported(const hss_matrix* A, int b) {
+  if (b > 4 || A->n < 1024) return false;
+  return (size_t)(b > 2 ? 4 : b) * gv_plane_bytes(A->n) + (size_t)b * round32(A->r) * 4 <= 64 * 1024;
+}
 
 struct SkinnyPlan {
   int rp, ltiles, splits, steps_per_split;
@@ -382,10 +560,11 @@ hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, 
   a.has_s = A->nnz > 0;
   a.col16 = (A->flags & HSS_COL16) != 0;
   a.ldx = n;
-  const bool need_xt = a.has_s && b > kSkGather;
+  const bool gemv = gv_supported(A, b);
+  const bool need_xt = a.has_s && b > kSkGather && !gemv;
   // rows off the 16-byte grid: 16-byte loads of X at 2-byte addresses cost the
   // main launch more than a copy (2731 x 5003, 13 columns: 14.8 against 9.6 us)
-  const bool need_xp = b > 1 && (n % 8 != 0 || (uintptr_t)X % 16 != 0);
+  const bool need_xp = !gemv && b > 1 && (n % 8 != 0 || (uintptr_t)X % 16 != 0);
   const int tb = r > 0 ? p.ltiles * p.splits : 0;
   const int xb = need_xt || need_xp ? std::min((n + 255) / 256, 256) : 0;
   if (tb + xb > 0)
@@ -397,6 +576,24 @@ hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, 
   if (need_xp) {
     a.X = reinterpret_cast<const uint16_t*>(base + p.xp);
     a.ldx = round32(n);
+  }
+  if (gemv) {
+    const size_t lds = (size_t)(b > 2 ? 4 : b) * gv_plane_bytes(n) + (size_t)b * p.rp * 4;
+    // two rows a wave while that leaves every SIMD a wave or two, else four
+    const bool four = m > 8192;
+    const unsigned gv = (unsigned)((m + kGvWaves * (four ? 4 : 2) - 1) / (kGvWaves * (four ? 4 : 2)));
+    const dim3 block(64 * kGvWaves);
+    if (b == 1) {
+      if (four) hipLaunchKernelGGL((k_mx_gemv<1, 4>), dim3(gv), block, lds, s, a);
+      else hipLaunchKernelGGL((k_mx_gemv<1, 2>), dim3(gv), block, lds, s, a);
+    } else if (b == 2) {
+      if (four) hipLaunchKernelGGL((k_mx_gemv<2, 4>), dim3(gv), block, lds, s, a);
+      else hipLaunchKernelGGL((k_mx_gemv<2, 2>), dim3(gv), block, lds, s, a);
+    } else {
+      if (four) hipLaunchKernelGGL((k_mx_gemv<4, 4>), dim3(gv), block, lds, s, a);
+      else hipLaunchKernelGGL((k_mx_gemv<4, 2>), dim3(gv), block, lds, s, a);
+    }
+    return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
   }
   const unsigned grid = (unsigned)((m + 15) / 16);
   const size_t tl = r > 0 ? (size_t)b * 2 * (p.rp + 8) * 2 : 0;
