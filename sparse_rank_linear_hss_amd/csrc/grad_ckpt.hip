@@ -8,48 +8,61 @@
 //
 // T and P are sums of n (m) products held in fp32.  The matrix cores take
 // bf16, so each is split into three bf16 terms (24 significant bits) and the
-// products with G and X' are summed over the terms: the gradients are as
-// exact as fp32 products would be.
+// products with G and X' are summed over the terms, K = 3 b with the other
+// operand repeating: the gradients are as exact as fp32 products would be.
+//
+// Launches: k_ck_prep (X'^T, G^T, U^T and padded rows where a product needs
+// them), one grouped product for T^T and P^T with K split, k_ck_terms (the
+// splits' sums, as terms), one grouped product for dU and dV^T, and dS.
 #include <algorithm>
 
+#include "mm_group.h"
 #include "mx_common.h"
 
 namespace hss {
 
-void launch_gemm_bf16x2(int M, int N, int K1, const uint16_t* A1, int64_t lda1, const uint16_t* B1, int64_t ldb1,
-                        int K2, const uint16_t* A2, int64_t lda2, const uint16_t* B2, int64_t ldb2, void* C,
-                        int64_t ldc, bool out_bf16, float* part, hipStream_t s);
-size_t gemm_bf16x2_part_bytes(int M, int N, int K1, int K2, int64_t ldc);
-void launch_mx_pad(const uint16_t* src, int rows, int cols, int colsp, int rep, uint16_t* dst, hipStream_t s);
-void launch_mx_terms(const float* T, int rows, int cols, int64_t ld, int colsp, int terms, uint16_t* dst,
-                     hipStream_t s);
 void launch_ds(const hss_matrix* A, int b, int kb, int ldt, const uint16_t* Xt, const uint16_t* Gt, float* dA,
                float* part, float* dS, hipStream_t s);
 bool ds_dense(int b);
+size_t gemm_bf16x2_part_bytes(int M, int N, int K1, int K2, int64_t ldc);
 
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 static int round32(int x) { return (x + 31) & ~31; }
 
 // ---------------------------------------------------------------------------
-// dst (cols x ldt) = src (rows x cols)^T in bf16, zero for rows <= c < ldt
-// (ldt a multiple of 32), and a row-major copy with rows padded to colsp
-// (zero past cols; null = none).  64 x 64 tiles through LDS; thread t holds
-// 16 columns of tile row t / 4.  CKPT: src is an int8 checkpoint.
+// A task turns src (rows x cols, bf16 or an int8 checkpoint) into bf16
+//   dst  (cols x ldt) = src^T, zero for rows <= c < ldt; null = none
+//   copy (rows x colsp), src with rows padded by zeros;  null = none
+// (ldt and colsp multiples of 32).  64 x 64 tiles through LDS; thread t holds
+// 16 columns of tile row t / 4.  Up to four tasks share a launch.
 // ---------------------------------------------------------------------------
-template <bool CKPT>
-__global__ __launch_bounds__(256) void k_ck_transpose(const void* __restrict__ src, const uint8_t* __restrict__ scales,
-                                                      int rows, int cols, int ldt, uint16_t* __restrict__ dst,
-                                                      uint16_t* __restrict__ copy, int colsp, int tiles_c) {
+struct CkTask {
+  const void* src;
+  const uint8_t* scales;  // of a checkpoint; null: src is bf16
+  uint16_t* dst;
+  uint16_t* copy;
+  int rows, cols, ldt, colsp, tiles_c, blocks;
+};
+struct CkTasks {
+  CkTask t[4];
+  int count;
+};
+
+__global__ __launch_bounds__(256) void k_ck_prep(CkTasks tasks) {
   __shared__ __align__(16) uint16_t tile[64][64 + 8];
-  const int r0 = (int)(blockIdx.x / (unsigned)tiles_c) * 64, c0 = (int)(blockIdx.x % (unsigned)tiles_c) * 64;
+  int block = (int)blockIdx.x, which = 0;
+  while (which + 1 < tasks.count && block >= tasks.t[which].blocks) block -= tasks.t[which++].blocks;
+  const CkTask& k_ = tasks.t[which];
+  const int rows = k_.rows, cols = k_.cols;
+  const int r0 = block / k_.tiles_c * 64, c0 = block % k_.tiles_c * 64;
   const int t = threadIdx.x;
   const int row = r0 + (t >> 2), col = c0 + 16 * (t & 3);
   uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};  // 16 bf16
   if (row < rows && col < cols) {
-    if constexpr (CKPT) {
+    if (k_.scales) {
       const int64_t g = (int64_t)row * mx_groups(cols) + (col >> 5);
-      const u32x4 code = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(src) + g * 32 + (col & 16));
-      const float scale = mx_scale(scales[g], 6);
+      const u32x4 code = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(k_.src) + g * 32 + (col & 16));
+      const float scale = mx_scale(k_.scales[g], 6);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float v[4];
@@ -58,7 +71,7 @@ __global__ __launch_bounds__(256) void k_ck_transpose(const void* __restrict__ s
         w[2 * k + 1] = mx_pack_hi(v[2], v[3]);
       }
     } else {
-      const uint16_t* p = static_cast<const uint16_t*>(src) + (int64_t)row * cols + col;
+      const uint16_t* p = static_cast<const uint16_t*>(k_.src) + (int64_t)row * cols + col;
       if (col + 16 <= cols) {
         const Bytes16 a = reinterpret_cast<const Bytes16*>(p)[0], b = reinterpret_cast<const Bytes16*>(p)[1];
 #pragma unroll
@@ -72,11 +85,12 @@ __global__ __launch_bounds__(256) void k_ck_transpose(const void* __restrict__ s
       }
     }
   }
-  if (copy && row < rows && col < colsp) {
-    u32x4* o = reinterpret_cast<u32x4*>(copy + (int64_t)row * colsp + col);
+  if (k_.copy && row < rows && col < k_.colsp) {
+    u32x4* o = reinterpret_cast<u32x4*>(k_.copy + (int64_t)row * k_.colsp + col);
     o[0] = u32x4{w[0], w[1], w[2], w[3]};
     o[1] = u32x4{w[4], w[5], w[6], w[7]};
   }
+  if (!k_.dst) return;  // the same for the whole block
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     tile[16 * (t & 3) + 2 * k][t >> 2] = (uint16_t)w[k];
@@ -86,38 +100,72 @@ __global__ __launch_bounds__(256) void k_ck_transpose(const void* __restrict__ s
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int q = t + 256 * h, j = q >> 3, c = (q & 7) * 8;
-    if (c0 + j < cols && r0 + c < ldt)
-      *reinterpret_cast<u32x4*>(dst + (int64_t)(c0 + j) * ldt + r0 + c) = *reinterpret_cast<const u32x4*>(&tile[j][c]);
+    if (c0 + j < cols && r0 + c < k_.ldt)
+      *reinterpret_cast<u32x4*>(k_.dst + (int64_t)(c0 + j) * k_.ldt + r0 + c) = *reinterpret_cast<const u32x4*>(&tile[j][c]);
   }
 }
 
-static void launch_ck_transpose(bool ckpt, const void* src, const uint8_t* scales, int rows, int cols, int ldt,
-                                uint16_t* dst, uint16_t* copy, int colsp, hipStream_t s) {
-  // the grid covers the padded columns too when a copy is written
-  const int tiles_c = (std::max(cols, copy ? colsp : 0) + 63) / 64;
-  const dim3 grid((unsigned)tiles_c * (unsigned)((ldt + 63) / 64));
-  if (ckpt)
-    hipLaunchKernelGGL(k_ck_transpose<true>, grid, dim3(256), 0, s, src, scales, rows, cols, ldt, dst, copy, colsp,
-                       tiles_c);
-  else
-    hipLaunchKernelGGL(k_ck_transpose<false>, grid, dim3(256), 0, s, src, scales, rows, cols, ldt, dst, copy, colsp,
-                       tiles_c);
+static void add_task(CkTasks& ts, const void* src, const uint8_t* scales, int rows, int cols, uint16_t* dst, int ldt,
+                     uint16_t* copy, int colsp) {
+  CkTask t = {src, scales, dst, copy, rows, cols, ldt, colsp, 0, 0};
+  t.tiles_c = (std::max(cols, copy ? colsp : 0) + 63) / 64;
+  t.blocks = t.tiles_c * ((std::max(rows, dst ? ldt : 0) + 63) / 64);
+  ts.t[ts.count++] = t;
 }
 
-// out[k] = a[k] + b[k]
-__global__ __launch_bounds__(256) void k_ck_add(const float* __restrict__ a, const float* __restrict__ b, int64_t count,
-                                                float* __restrict__ out) {
-  for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < count; k += (int64_t)gridDim.x * 256)
-    out[k] = a[k] + b[k];
+// ---------------------------------------------------------------------------
+// Terms of T^T and P^T: dst[l][z][ldt], z < 3, from the sum of the splits'
+// partial products [split][l][ldt]; zero for c >= b.  Term z is what the terms
+// before it leave, rounded to nearest.
+// ---------------------------------------------------------------------------
+struct CkTerms {
+  const float* src[2];
+  uint16_t* dst[2];
+  int splits[2];
+  int count, r, b, ldt;
+};
+
+__global__ __launch_bounds__(256) void k_ck_terms(CkTerms a) {
+  const uint32_t per = (uint32_t)a.ldt >> 2, total = (uint32_t)a.r * per;
+  for (uint32_t e = blockIdx.x * 256u + threadIdx.x; e < total * (uint32_t)a.count; e += gridDim.x * 256u) {
+    const int which = e >= total;
+    const uint32_t q = e - (which ? total : 0u);
+    const uint32_t l = q / per, c = (q - l * per) * 4;
+    const float* src = a.src[which] + (int64_t)l * a.ldt + c;
+    const int64_t zs = (int64_t)a.r * a.ldt;
+    float4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int z = 0; z < a.splits[which]; ++z) {
+      const float4 v = *reinterpret_cast<const float4*>(src + z * zs);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = (int)c + k < a.b ? v[k] : 0.f;
+#pragma unroll
+    for (int z = 0; z < 3; ++z) {
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        h[k] = f32_to_bf16(v[k]);
+        // (an infinity leaves 0, not the NaN of inf - inf)
+        v[k] = (h[k] & 0x7fffu) == 0x7f80u ? 0.f : v[k] - __uint_as_float(h[k] << 16);
+      }
+      *reinterpret_cast<mx_u32x2*>(a.dst[which] + ((int64_t)l * 3 + z) * a.ldt + c) =
+          mx_u32x2{h[0] | h[1] << 16, h[2] | h[3] << 16};
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Workspace
 // ---------------------------------------------------------------------------
 struct CkPlan {
-  int ldt, np, mp;
-  size_t xb, xt, gt, gb, vt, ut, tf, t3, s0, s1, da, part, total;
+  int ldt, np, mp, zt, zp;  // padded sizes; K splits of T and P
+  size_t xb, xt, gt, gb, vt, ut, tf, pf, t3, p3, da, part, total;
 };
+
+static constexpr int kCkBlocks = 512;  // blocks of the T and P launch
 
 static CkPlan plan_ck(const hss_matrix* A, int b) {
   CkPlan p;
@@ -125,29 +173,22 @@ static CkPlan plan_ck(const hss_matrix* A, int b) {
   p.ldt = round32(b);
   p.np = round32(n);
   p.mp = round32(m);
+  p.zt = r > 0 ? mm_splits(r, b, p.np, kCkBlocks / 2) : 0;
+  p.zp = r > 0 ? mm_splits(r, b, p.mp, kCkBlocks / 2) : 0;
   size_t off = 0;
-  p.xb = off; off += al256((size_t)b * p.np * 2);
-  p.xt = off; off += al256((size_t)n * p.ldt * 2);
-  p.gt = off; off += al256((size_t)m * p.ldt * 2);
-  p.gb = off; off += al256((size_t)b * p.mp * 2);
-  p.vt = off; off += al256((size_t)r * p.np * 2);
-  p.ut = off; off += al256((size_t)r * p.mp * 2);
-  p.tf = off; off += al256((size_t)r * p.ldt * 4);
-  p.t3 = off; off += al256((size_t)r * p.ldt * 6);
-  p.s0 = off; off += al256((size_t)r * std::max(m, n) * 4);
-  p.s1 = off; off += al256((size_t)r * std::max(m, n) * 4);
-  p.da = off; off += ds_dense(b) ? al256((size_t)m * n * 4) : 0;
-  size_t part = 0;
-  if (r > 0) {
-    part = std::max(part, gemm_bf16x2_part_bytes(b, r, p.np, 0, p.ldt));
-    part = std::max(part, gemm_bf16x2_part_bytes(b, r, p.mp, 0, p.ldt));
-    for (int k2 = 0; k2 <= p.ldt; k2 += p.ldt) {
-      part = std::max(part, gemm_bf16x2_part_bytes(r, m, p.ldt, k2, r));
-      part = std::max(part, gemm_bf16x2_part_bytes(n, r, p.ldt, k2, n));
-    }
-  }
-  if (ds_dense(b)) part = std::max(part, gemm_bf16x2_part_bytes(n, m, p.ldt, 0, n));
-  p.part = off; off += al256(part);
+  auto take = [&](size_t bytes) { const size_t at = off; off += al256(bytes); return at; };
+  p.xb = take((size_t)b * p.np * 2);
+  p.xt = take((size_t)n * p.ldt * 2);
+  p.gt = take((size_t)m * p.ldt * 2);
+  p.gb = take((size_t)b * p.mp * 2);
+  p.vt = take((size_t)r * p.np * 2);
+  p.ut = take((size_t)r * p.mp * 2);
+  p.tf = take((size_t)p.zt * r * p.ldt * 4);
+  p.pf = take((size_t)p.zp * r * p.ldt * 4);
+  p.t3 = take((size_t)r * p.ldt * 6);
+  p.p3 = take((size_t)r * p.ldt * 6);
+  p.da = take(ds_dense(b) ? (size_t)m * n * 4 : 0);
+  p.part = take(ds_dense(b) ? gemm_bf16x2_part_bytes(n, m, p.ldt, 0, n) : 0);
   p.total = off;
   return p;
 }
@@ -161,49 +202,57 @@ hss_status launch_grad_ckpt(const hss_matrix* A, int b, const void* codes, const
   const CkPlan p = plan_ck(A, b);
   char* base = static_cast<char*>(ws);
   auto u16 = [&](size_t off) { return reinterpret_cast<uint16_t*>(base + off); };
-  uint16_t *Xb = u16(p.xb), *Xt = u16(p.xt), *Gt = u16(p.gt), *T3 = u16(p.t3);
-  float* Tf = reinterpret_cast<float*>(base + p.tf);
-  float* part = reinterpret_cast<float*>(base + p.part);
-  float* S0 = reinterpret_cast<float*>(base + p.s0);
-  float* S1 = reinterpret_cast<float*>(base + p.s1);
+  auto f32 = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
   const int m = A->m, n = A->n, r = A->r, ldt = p.ldt;
   const int64_t stored = A->fmt == HSS_FMT_2OF4 ? (int64_t)m * (n / 2) : A->nnz;
   const bool want_s = dS && stored > 0, want_u = dU && r > 0, want_v = dVt && r > 0;
   if (!want_s && !want_u && !want_v) return HSS_OK;
-  launch_ck_transpose(true, codes, scales, b, n, ldt, Xt, want_u ? Xb : nullptr, p.np, s);
-  const uint16_t* Gb = static_cast<const uint16_t*>(G);
-  const bool copy_g = want_v && !rows_ok(G, m);
-  if (want_u || want_s || copy_g)
-    launch_ck_transpose(false, G, nullptr, b, m, ldt, Gt, copy_g ? u16(p.gb) : nullptr, p.mp, s);
-  if (copy_g) Gb = u16(p.gb);
-  // C[n * ldc + m] over the three terms of T3, in a fixed order: (t1 + t2) + t3
-  auto sum3 = [&](int M, int N, const uint16_t* A3, bool a_terms, const uint16_t* B3, float* out, int ldc) {
-    const int la = a_terms ? 3 * ldt : ldt, lb = a_terms ? ldt : 3 * ldt;
-    const int oa = a_terms ? ldt : 0, ob = a_terms ? 0 : ldt;
-    launch_gemm_bf16x2(M, N, ldt, A3, la, B3, lb, ldt, A3 + oa, la, B3 + ob, lb, S0, ldc, false, part, s);
-    launch_gemm_bf16x2(M, N, ldt, A3 + 2 * oa, la, B3 + 2 * ob, lb, 0, nullptr, 0, nullptr, 0, S1, ldc, false, part, s);
-    const int64_t count = (int64_t)N * ldc;
-    hipLaunchKernelGGL(k_ck_add, dim3((unsigned)std::min<int64_t>((count + 255) / 256, 4096)), dim3(256), 0, s, S0, S1,
-                       count, out);
-  };
-  if (want_u) {
-    const uint16_t* Vb = static_cast<const uint16_t*>(A->Vt);
-    if (!rows_ok(A->Vt, n)) {
-      launch_mx_pad(Vb, r, n, p.np, 1, u16(p.vt), s);
-      Vb = u16(p.vt);
-    }
-    launch_gemm_bf16x2(b, r, p.np, Xb, p.np, Vb, p.np, 0, nullptr, 0, nullptr, 0, Tf, ldt, false, part, s);
-    launch_mx_terms(Tf, r, b, ldt, ldt, 3, T3, s);
-    sum3(r, m, T3, true, Gt, dU, r);
+
+  CkTasks ts = {};
+  const bool want_xt = want_v || want_s, want_gt = want_u || want_s;
+  add_task(ts, codes, scales, b, n, want_xt ? u16(p.xt) : nullptr, ldt, want_u ? u16(p.xb) : nullptr, p.np);
+  const bool copy_g = want_v && !rows_ok(G, m), copy_v = want_u && !rows_ok(A->Vt, n);
+  if (want_gt || copy_g)
+    add_task(ts, G, nullptr, b, m, want_gt ? u16(p.gt) : nullptr, ldt, copy_g ? u16(p.gb) : nullptr, p.mp);
+  if (want_v) add_task(ts, A->U, nullptr, m, r, u16(p.ut), p.mp, nullptr, 0);
+  if (copy_v) add_task(ts, A->Vt, nullptr, r, n, nullptr, 0, u16(p.vt), p.np);
+  unsigned blocks = 0;
+  for (int k = 0; k < ts.count; ++k) blocks += (unsigned)ts.t[k].blocks;
+  hipLaunchKernelGGL(k_ck_prep, dim3(blocks), dim3(256), 0, s, ts);
+
+  if (want_u || want_v) {
+    MmProblem q[2] = {};
+    CkTerms t = {};
+    t.r = r; t.b = b; t.ldt = ldt;
+    int k = 0;
+    auto product = [&](const uint16_t* a_rows, const uint16_t* b_rows, int K, int splits, size_t out, size_t terms) {
+      q[k].A = a_rows; q[k].lda = K; q[k].M = r;
+      q[k].B = b_rows; q[k].ldb = K; q[k].N = b;
+      q[k].K = K;
+      q[k].C = f32(out); q[k].ldc = ldt; q[k].zstride = (int64_t)r * ldt;
+      q[k].splits = splits;
+      t.src[k] = f32(out); t.dst[k] = u16(terms); t.splits[k] = splits;
+      t.count = ++k;
+    };
+    if (want_u) product(copy_v ? u16(p.vt) : static_cast<const uint16_t*>(A->Vt), u16(p.xb), p.np, p.zt, p.tf, p.t3);
+    if (want_v) product(u16(p.ut), copy_g ? u16(p.gb) : static_cast<const uint16_t*>(G), p.mp, p.zp, p.pf, p.p3);
+    launch_mm_group(q, k, s);
+    const int64_t work = (int64_t)t.count * r * (ldt / 4);
+    hipLaunchKernelGGL(k_ck_terms, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 4096)), dim3(256), 0, s, t);
+    MmProblem o[2] = {};
+    k = 0;
+    auto gradient = [&](size_t terms, size_t rows, int count, float* out, int64_t ldc, int trans) {
+      o[k].A = u16(terms); o[k].lda = 3 * ldt; o[k].M = r;
+      o[k].B = u16(rows); o[k].ldb = ldt; o[k].N = count; o[k].wrap_b = ldt;
+      o[k].K = 3 * ldt;
+      o[k].C = out; o[k].ldc = ldc; o[k].trans = trans;
+      ++k;
+    };
+    if (want_u) gradient(p.t3, p.gt, m, dU, r, 1);
+    if (want_v) gradient(p.p3, p.xt, n, dVt, n, 0);
+    launch_mm_group(o, k, s);
   }
-  if (want_v) {
-    uint16_t* Ut = u16(p.ut);
-    launch_ck_transpose(false, A->U, nullptr, m, r, p.mp, Ut, nullptr, 0, s);
-    launch_gemm_bf16x2(b, r, p.mp, Gb, p.mp, Ut, p.mp, 0, nullptr, 0, nullptr, 0, Tf, ldt, false, part, s);
-    launch_mx_terms(Tf, r, b, ldt, ldt, 3, T3, s);
-    sum3(n, r, Xt, false, T3, dVt, n);
-  }
-  if (want_s) launch_ds(A, b, ldt, ldt, Xt, Gt, reinterpret_cast<float*>(base + p.da), part, dS, s);
+  if (want_s) launch_ds(A, b, ldt, ldt, u16(p.xt), u16(p.gt), f32(p.da), f32(p.part), dS, s);
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 

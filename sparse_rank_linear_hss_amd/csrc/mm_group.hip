@@ -1,0 +1,157 @@
+// Grouped small matrix products on the matrix cores, C = A . B^T in fp32.
+//
+// The products of a gradient with a low rank have one short side (r) and a
+// long K or a long other side: alone they fill a part of the chip, and a
+// launch costs as much as the work.  So independent ones share a launch, and
+// K is split where the tiles are few (the reader adds the partial products in
+// order).  Tile BM x 128 (BM = 64 or 128, the rank's side), 4 waves, K in
+// stages of 64 through two LDS buffers with the next stage's loads in flight;
+// one barrier per stage.
+#include <algorithm>
+
+#include "mm_group.h"
+
+namespace hss {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+static constexpr int kMmN = 128, kMmK = 64;
+
+struct MmArgs {
+  MmProblem p[kMmGroup];
+  int count;
+};
+
+// Slot of 16-byte chunk c (0..7) of a 128-byte LDS row: the rows that a
+// fragment read takes together (8 in a 128-byte bank window, or every second
+// of 16 in a 256-byte one) get distinct slots.
+__device__ __forceinline__ int mm_slot(int row, int c) { return c ^ ((row >> 1) & 7) ^ ((row & 1) << 2); }
+
+template <int BM>
+__global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_mm(MmArgs args) {
+  constexpr int FM = BM / 32, FN = 4;
+  constexpr int AV = BM / 32, BV = kMmN / 32;  // 16-byte chunks per thread and stage
+  __shared__ __align__(16) uint16_t lds[2][(BM + kMmN) * kMmK];
+  int block = (int)blockIdx.x, which = 0;
+  while (which + 1 < args.count && block >= args.p[which].blocks) block -= args.p[which++].blocks;
+  const MmProblem& p = args.p[which];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, q = lane >> 4;
+  const int tn = block % p.tiles_n, rest = block / p.tiles_n;
+  const int z = rest % p.splits, tm = rest / p.splits;
+  const int m0 = tm * BM, n0 = tn * kMmN;
+  const int s0 = z * p.stages_per_split, s1 = min(s0 + p.stages_per_split, (p.K + kMmK - 1) / kMmK);
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  u32x4 ra[AV], rb[BV];
+  const int c = t & 7, r0 = t >> 3;  // chunk and first row of this thread's loads
+  auto load = [&](int s) {
+    const int k = s * kMmK + 8 * c;
+    const bool in = k < p.K;
+    int ka = k, kb = k;
+    ka -= ka >= 2 * p.wrap_a ? 2 * p.wrap_a : (ka >= p.wrap_a ? p.wrap_a : 0);
+    kb -= kb >= 2 * p.wrap_b ? 2 * p.wrap_b : (kb >= p.wrap_b ? p.wrap_b : 0);
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < AV; ++i)
+      ra[i] = in ? *reinterpret_cast<const u32x4*>(p.A + (int64_t)min(m0 + r0 + 32 * i, p.M - 1) * p.lda + ka) : zero;
+#pragma unroll
+    for (int i = 0; i < BV; ++i)
+      rb[i] = in ? *reinterpret_cast<const u32x4*>(p.B + (int64_t)min(n0 + r0 + 32 * i, p.N - 1) * p.ldb + kb) : zero;
+  };
+  auto store = [&](uint16_t* buf) {
+#pragma unroll
+    for (int i = 0; i < AV; ++i)
+      *reinterpret_cast<u32x4*>(buf + (r0 + 32 * i) * kMmK + 8 * mm_slot(r0 + 32 * i, c)) = ra[i];
+#pragma unroll
+    for (int i = 0; i < BV; ++i)
+      *reinterpret_cast<u32x4*>(buf + (BM + r0 + 32 * i) * kMmK + 8 * mm_slot(r0 + 32 * i, c)) = rb[i];
+  };
+  const int wm = (w >> 1) * (BM / 2), wn = (w & 1) * 64;
+  auto compute = [&](const uint16_t* buf) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      bf16x8 af[FM], bf[FN];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int row = wm + 16 * i + (lane & 15);
+        af[i] = *reinterpret_cast<const bf16x8*>(buf + row * kMmK + 8 * mm_slot(row, 4 * ks + q));
+      }
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int row = wn + 16 * j + (lane & 15);
+        bf[j] = *reinterpret_cast<const bf16x8*>(buf + (BM + row) * kMmK + 8 * mm_slot(row, 4 * ks + q));
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], bf[j], acc[i][j], 0, 0, 0);
+    }
+  };
+  if (s0 < s1) {
+    load(s0);
+    store(lds[0]);
+    if (s0 + 1 < s1) load(s0 + 1);
+    __syncthreads();
+    for (int s = s0; s < s1; ++s) {
+      const int odd = (s - s0) & 1;
+      compute(lds[odd]);
+      if (s + 1 < s1) store(lds[odd ^ 1]);
+      if (s + 2 < s1) load(s + 2);
+      __syncthreads();
+    }
+  }
+  // lane holds rows 4 q + e of column lane % 16 of each block
+  float* C = p.C + (int64_t)z * p.zstride;
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int n = n0 + wn + 16 * j + (lane & 15);
+    if (n >= p.N) continue;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int m = m0 + wm + 16 * i + 4 * q;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (m + e < p.M) C[p.trans ? (int64_t)n * p.ldc + m + e : (int64_t)(m + e) * p.ldc + n] = acc[i][j][e];
+    }
+  }
+}
+
+static int mm_tile_m(int M) { return M > 64 ? 128 : 64; }
+
+int mm_splits(int M, int N, int K, int target) {
+  const int tiles = ((M + mm_tile_m(M) - 1) / mm_tile_m(M)) * ((N + kMmN - 1) / kMmN);
+  const int stages = (K + kMmK - 1) / kMmK;
+  const int want = std::max(1, std::min(target / tiles, stages / 2));
+  const int per = (stages + want - 1) / want;
+  return (stages + per - 1) / per;
+}
+
+void launch_mm_group(const MmProblem* p, int count, hipStream_t s) {
+  MmArgs a = {};
+  int bm = 64, blocks = 0;
+  for (int i = 0; i < count; ++i) bm = std::max(bm, mm_tile_m(p[i].M));
+  for (int i = 0; i < count; ++i) {
+    MmProblem& q = a.p[a.count++];
+    q = p[i];
+    if (q.wrap_a <= 0) q.wrap_a = q.K;
+    if (q.wrap_b <= 0) q.wrap_b = q.K;
+    if (q.splits < 1) q.splits = 1;
+    const int stages = (q.K + kMmK - 1) / kMmK;
+    q.stages_per_split = (stages + q.splits - 1) / q.splits;
+    q.tiles_n = (q.N + kMmN - 1) / kMmN;
+    q.blocks = q.tiles_n * q.splits * ((q.M + bm - 1) / bm);
+    blocks += q.blocks;
+  }
+  if (bm == 64)
+    hipLaunchKernelGGL(k_mm<64>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL(k_mm<128>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+}
+
+}  // namespace hss
