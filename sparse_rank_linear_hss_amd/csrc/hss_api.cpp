@@ -86,6 +86,7 @@ bool valid_dtype(int dt) { return dt == HSS_F32 || dt == HSS_BF16; }
 bool valid_fmt(int f) { return f == HSS_FMT_CSR || f == HSS_FMT_2OF4; }
 size_t dsize(int dt) { return dt == HSS_F32 ? 4 : 2; }
 int64_t up32(int64_t x) { return (x + 31) / 32 * 32; }
+int64_t up64(int64_t x) { return (x + 63) / 64 * 64; }
 
 bool overlap(const void* a, size_t abytes, const void* b, size_t bbytes) {
   const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
@@ -191,7 +192,7 @@ static hss_status check_matrix(const hss_matrix* A, int32_t b) {
         !A->dq_levels || (uintptr_t)A->dq_codes % 16 != 0)
       return HSS_ERR_INVALID_ARG;
     // D and its dense copies in rows of whole groups; the factors' terms side by side
-    if (m * up32(n) >= kLimit || n * up32(m) >= kLimit || 2 * std::max<int64_t>(m, b) * up32(r) >= kLimit)
+    if (std::max<int64_t>(m, b) * up64(n) >= kLimit || n * up64(m) >= kLimit || r * up64(n) >= kLimit || 2 * std::max<int64_t>(m, b) * up32(r) >= kLimit)
       return HSS_ERR_INVALID_ARG;
   }
   if (A->flags & HSS_DQ4) {

@@ -3,7 +3,7 @@
 //   is D^T (n x m), so that a layer and its transposed layer share one copy.
 //
 // Up to 16 columns, D not transposed: mx_skinny.hip.  General route, any batch:
-//   W'  = D + S as dense bf16 in the workspace, rows padded to 32 columns
+//   W'  = D + S as dense bf16 in the workspace, rows padded to 64 columns
 //   T   = X V in fp32 (matrix cores), kept as two bf16 terms T = T1 + T2 (16
 //         significant bits, so that rounding T does not show beside the
 //         rounding of Y)
@@ -11,10 +11,11 @@
 //         accumulation, rounded to bf16 once.
 // D is exact in bf16 and S is bf16: W' rounds only where an entry of S falls
 // on a non-zero of D.  Operands whose rows the matrix-core kernels cannot read
-// in 16-byte pieces (n or r not a multiple of 32, unaligned bases) are copied
+// in 16-byte pieces (n not a multiple of 64, unaligned bases) are copied
 // into padded rows first.
 #include <algorithm>
 
+#include "gemm256.h"
 #include "mx_common.h"
 
 namespace hss {
@@ -51,15 +52,19 @@ __global__ __launch_bounds__(256) void k_mx_densify(const uint8_t* __restrict__ 
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int row = blockIdx.x * 4 + w;
   if (row >= m) return;  // no block-wide barrier below
-  const int ng = np >> 5;
+  const int ng = mx_groups(n);
   uint16_t* L = seg[w];
   const int p0 = row_ptr[row], p1 = row_ptr[row + 1];
   for (int c0 = 0; c0 < np; c0 += kMxSeg) {
     const int len = min(kMxSeg, np - c0);  // a multiple of 32
     for (int j = 8 * lane; j < len; j += 512) {
-      const int64_t g = (int64_t)row * ng + ((c0 + j) >> 5);
-      const uint32_t word = *reinterpret_cast<const uint32_t*>(codes + g * 16 + ((j >> 1) & 12));
-      *reinterpret_cast<u32x4*>(L + j) = mx4_to_bf16x8(word, mx_scale(scales[g], 0));
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (((c0 + j) >> 5) < ng) {
+        const int64_t g = (int64_t)row * ng + ((c0 + j) >> 5);
+        const uint32_t word = *reinterpret_cast<const uint32_t*>(codes + g * 16 + ((j >> 1) & 12));
+        v = mx4_to_bf16x8(word, mx_scale(scales[g], 0));
+      }
+      *reinterpret_cast<u32x4*>(L + j) = v;
     }
     // A wave's LDS accesses complete in issue order; the empty asm keeps the
     // compiler from reordering the three phases.
@@ -189,6 +194,8 @@ void launch_mx_terms(const float* T, int rows, int cols, int64_t ld, int colsp, 
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+static constexpr int kG256MinTiles = 128;
+
 struct MxPlan {
   int np, rp;
   size_t w, x, vt, u, tf, tb, part, total;
@@ -197,7 +204,7 @@ struct MxPlan {
 static MxPlan plan_mx(const hss_matrix* A, int b) {
   MxPlan p;
   const int m = A->m, n = A->n, r = A->r;
-  p.np = round32(n);
+  p.np = (n + 63) & ~63;
   p.rp = r > 0 ? round32(r) : 0;
   size_t off = 0;
   p.w = off;  off += al256((size_t)m * p.np * 2);
@@ -217,7 +224,7 @@ size_t mx_apply_ws_bytes(const hss_matrix* A, int b) {
   return mx_skinny_supported(A, b) ? mx_skinny_ws_bytes(A, b) : plan_mx(A, b).total;
 }
 
-static bool rows_ok(const void* p, int cols) { return (uintptr_t)p % 16 == 0 && cols % 32 == 0; }
+static bool rows_ok(const void* p, int cols) { return (uintptr_t)p % 16 == 0 && cols % 64 == 0; }
 
 hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s) {
   if (mx_skinny_supported(A, b)) return launch_mx_skinny(A, b, X, Y, ws, s);
@@ -268,7 +275,10 @@ hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, v
     launch_mx_terms(Tf, b, r, r, rp, 2, Tb, s);
     launch_mx_pad(static_cast<const uint16_t*>(A->U), m, r, rp, 2, Ub, s);
   }
-  launch_gemm_bf16x2(m, b, np, W, np, Xb, np, 2 * rp, Ub, 2 * rp, Tb, 2 * rp, Y, m, true, part, s);
+  if (((m + 255) / 256) * ((b + 255) / 256) >= kG256MinTiles && gemm256_ok(m, b, np, np, np, 2 * rp, 2 * rp, 2 * rp))
+    launch_gemm256_bf16(m, b, np, W, np, Xb, np, 2 * rp, Ub, 2 * rp, Tb, 2 * rp, Y, m, s);
+  else
+    launch_gemm_bf16x2(m, b, np, W, np, Xb, np, 2 * rp, Ub, 2 * rp, Tb, 2 * rp, Y, m, true, part, s);
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 
