@@ -249,8 +249,9 @@ hss_status hss_get_error(const void* ws, hipStream_t stream);
  *       dq_codes, dq_levels: the codes (16-byte aligned) and the scale bytes
  *         of D (m x n) as hss_mx_quantize writes them (HSS_MXFP4).
  *     Requires fmt == HSS_FMT_CSR, no HSS_DQ4 and no HSS_HIER2; bf16 layers
- *     (an fp32 one returns HSS_ERR_UNSUPPORTED); 64 max(m, b, r) ceil(n/64),
- *     64 n ceil(m/64) and 64 max(m, b) ceil(r/32) < 2^31.  hss_grad and
+ *     (an fp32 one returns HSS_ERR_UNSUPPORTED); 64 max(b, r) ceil(n/64),
+ *     64 n ceil(m/64), 64 m (ceil(n/64) + ceil(r/32)) and 64 b ceil(r/32)
+ *     < 2^31.  hss_grad and
  *     hss_grad_ckpt give the gradients of S, U and V; D has none.
  *   flags & HSS_MX4_T (with HSS_MX4): the two arrays hold D^T, an n x m
  *     matrix, so that the transposed layer of an HSS_MX4 matrix (its input

@@ -9,11 +9,11 @@ enum : int { G256_BF16 = 0 };
 
 // Whether the operands suit k_gemm256: K segments in whole stages of 64, rows
 // of whole 16-byte chunks (aligned bases), 32-bit byte offsets.
-bool gemm256_ok(int M, int N, int K1, int lda1, int ldb1, int K2, int lda2, int ldb2);
+bool gemm256_ok(int M, int N, int K1, int lda, int ldb1, int K2, int ldb2);
 
-// C[n * ldc + m] (bf16) = A1 . B1^T + A2 . B2^T (K2 = 0: the first alone).
-void launch_gemm256_bf16(int M, int N, int K1, const uint16_t* A1, int lda1, const uint16_t* B1, int ldb1, int K2,
-                         const uint16_t* A2, int lda2, const uint16_t* B2, int ldb2, void* C, int64_t ldc,
-                         hipStream_t s);
+// C[n * ldc + m] (bf16) = A . [B1 | B2]^T: A's rows hold K1 + K2 columns
+// (K2 = 0: no second segment).
+void launch_gemm256_bf16(int M, int N, const uint16_t* A, int lda, int K1, const uint16_t* B1, int ldb1, int K2,
+                         const uint16_t* B2, int ldb2, void* C, int64_t ldc, hipStream_t s);
 
 }  // namespace hss

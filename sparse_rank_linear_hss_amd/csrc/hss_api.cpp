@@ -192,7 +192,7 @@ static hss_status check_matrix(const hss_matrix* A, int32_t b) {
         !A->dq_levels || (uintptr_t)A->dq_codes % 16 != 0)
       return HSS_ERR_INVALID_ARG;
     // D and its dense copies in rows of whole groups; the factors' terms side by side
-    if (std::max<int64_t>(m, b) * up64(n) >= kLimit || n * up64(m) >= kLimit || r * up64(n) >= kLimit || 2 * std::max<int64_t>(m, b) * up32(r) >= kLimit)
+    if (std::max<int64_t>(m, b) * up64(n) >= kLimit || m * (up64(n) + 2 * up32(r)) >= kLimit || n * up64(m) >= kLimit || r * up64(n) >= kLimit || 2 * std::max<int64_t>(m, b) * up32(r) >= kLimit)
       return HSS_ERR_INVALID_ARG;
   }
   if (A->flags & HSS_DQ4) {

@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256) void k_mx_densify(const uint8_t* __restrict__ 
                                                     const int32_t* __restrict__ row_ptr,
                                                     const COL* __restrict__ col_idx,
                                                     const uint16_t* __restrict__ vals, int m, int n, int np,
-                                                    uint16_t* __restrict__ W) {
+                                                    int ldw, uint16_t* __restrict__ W) {
   __shared__ __align__(16) uint16_t seg[4][kMxSeg];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int row = blockIdx.x * 4 + w;
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256) void k_mx_densify(const uint8_t* __restrict__ 
     }
     asm volatile("" ::: "memory");
     for (int j = 8 * lane; j < len; j += 512)
-      *reinterpret_cast<u32x4*>(W + (int64_t)row * np + c0 + j) = *reinterpret_cast<const u32x4*>(L + j);
+      *reinterpret_cast<u32x4*>(W + (int64_t)row * ldw + c0 + j) = *reinterpret_cast<const u32x4*>(L + j);
     asm volatile("" ::: "memory");
   }
 }
@@ -86,7 +86,8 @@ __global__ __launch_bounds__(256) void k_mx_densify(const uint8_t* __restrict__ 
 static constexpr int kTrI = 64, kTrJ = 128;
 __global__ __launch_bounds__(256) void k_mx_densify_t(const uint8_t* __restrict__ codes,
                                                       const uint8_t* __restrict__ scales, int m, int n, int np,
-                                                      int tiles_j, uint16_t* __restrict__ W) {
+                                                      int ldw, int tiles_j,
+                                                      uint16_t* __restrict__ W) {
   __shared__ __align__(16) uint16_t tile[kTrJ][kTrI + 8];
   const int i0 = (int)(blockIdx.x / (unsigned)tiles_j) * kTrI, j0 = (int)(blockIdx.x % (unsigned)tiles_j) * kTrJ;
   const int ng = mx_groups(m);
@@ -114,7 +115,7 @@ __global__ __launch_bounds__(256) void k_mx_densify_t(const uint8_t* __restrict_
   for (int q = t; q < kTrJ * (kTrI / 8); q += 256) {
     const int j = q >> 3, c = (q & 7) * 8;
     if (j0 + j < m && i0 + c < np)
-      *reinterpret_cast<u32x4*>(W + (int64_t)(j0 + j) * np + i0 + c) = *reinterpret_cast<const u32x4*>(&tile[j][c]);
+      *reinterpret_cast<u32x4*>(W + (int64_t)(j0 + j) * ldw + i0 + c) = *reinterpret_cast<const u32x4*>(&tile[j][c]);
   }
 }
 
@@ -122,11 +123,11 @@ __global__ __launch_bounds__(256) void k_mx_densify_t(const uint8_t* __restrict_
 template <typename COL>
 __global__ __launch_bounds__(256) void k_mx_add_csr(const int32_t* __restrict__ row_ptr,
                                                     const COL* __restrict__ col_idx,
-                                                    const uint16_t* __restrict__ vals, int m, int n, int np,
+                                                    const uint16_t* __restrict__ vals, int m, int n, int ldw,
                                                     uint16_t* __restrict__ W) {
   const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (row >= m) return;
-  uint16_t* Wr = W + (int64_t)row * np;
+  uint16_t* Wr = W + (int64_t)row * ldw;
   const int p1 = row_ptr[row + 1];
   for (int p = row_ptr[row] + lane_id(); p < p1; p += 64) {
     const int c = (int)col_idx[p];
@@ -135,9 +136,10 @@ __global__ __launch_bounds__(256) void k_mx_add_csr(const int32_t* __restrict__ 
   }
 }
 
-// dst rows of `rep` copies of [src row | zeros] (colsp columns each, a multiple of 8).
+// `rep` copies of [src row | zeros] (colsp columns each, a multiple of 8) in
+// rows of ldd.
 __global__ __launch_bounds__(256) void k_mx_pad(const uint16_t* __restrict__ src, int rows, int cols, int colsp,
-                                                int rep, uint16_t* __restrict__ dst) {
+                                                int rep, int64_t ldd, uint16_t* __restrict__ dst) {
   const uint32_t per = (uint32_t)colsp >> 3, total = (uint32_t)rows * per;
   for (uint32_t q = blockIdx.x * 256u + threadIdx.x; q < total; q += gridDim.x * 256u) {
     const uint32_t row = q / per;
@@ -154,7 +156,7 @@ __global__ __launch_bounds__(256) void k_mx_pad(const uint16_t* __restrict__ src
         v[k] = lo | hi << 16;
       }
     }
-    for (int z = 0; z < rep; ++z) *reinterpret_cast<u32x4*>(dst + ((int64_t)row * rep + z) * colsp + c) = v;
+    for (int z = 0; z < rep; ++z) *reinterpret_cast<u32x4*>(dst + row * ldd + (int64_t)z * colsp + c) = v;
   }
 }
 
@@ -178,10 +180,11 @@ __global__ __launch_bounds__(256) void k_mx_terms(const float* __restrict__ T, i
   }
 }
 
-void launch_mx_pad(const uint16_t* src, int rows, int cols, int colsp, int rep, uint16_t* dst, hipStream_t s) {
+void launch_mx_pad(const uint16_t* src, int rows, int cols, int colsp, int rep, int64_t ldd, uint16_t* dst,
+                   hipStream_t s) {
   const int64_t total = (int64_t)rows * (colsp >> 3);
   const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, 4096);
-  hipLaunchKernelGGL(k_mx_pad, dim3(grid), dim3(256), 0, s, src, rows, cols, colsp, rep, dst);
+  hipLaunchKernelGGL(k_mx_pad, dim3(grid), dim3(256), 0, s, src, rows, cols, colsp, rep, ldd, dst);
 }
 
 void launch_mx_terms(const float* T, int rows, int cols, int64_t ld, int colsp, int terms, uint16_t* dst,
@@ -198,7 +201,7 @@ static constexpr int kG256MinTiles = 128;
 
 struct MxPlan {
   int np, rp;
-  size_t w, x, vt, u, tf, tb, part, total;
+  size_t w, x, vt, tf, tb, part, total;
 };
 
 static MxPlan plan_mx(const hss_matrix* A, int b) {
@@ -207,10 +210,9 @@ static MxPlan plan_mx(const hss_matrix* A, int b) {
   p.np = (n + 63) & ~63;
   p.rp = r > 0 ? round32(r) : 0;
   size_t off = 0;
-  p.w = off;  off += al256((size_t)m * p.np * 2);
+  p.w = off;  off += al256((size_t)m * (p.np + 2 * p.rp) * 2);
   p.x = off;  off += al256((size_t)b * p.np * 2);
   p.vt = off; off += al256((size_t)r * p.np * 2);
-  p.u = off;  off += al256((size_t)m * p.rp * 4);
   p.tf = off; off += al256((size_t)b * r * 4);
   p.tb = off; off += al256((size_t)b * p.rp * 4);
   p.part = off;
@@ -231,11 +233,11 @@ hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, v
   const MxPlan p = plan_mx(A, b);
   char* base = static_cast<char*>(ws);
   uint16_t* W = reinterpret_cast<uint16_t*>(base + p.w);
-  uint16_t* Ub = reinterpret_cast<uint16_t*>(base + p.u);
   float* Tf = reinterpret_cast<float*>(base + p.tf);
   uint16_t* Tb = reinterpret_cast<uint16_t*>(base + p.tb);
   float* part = reinterpret_cast<float*>(base + p.part);
-  const int m = A->m, n = A->n, r = A->r, np = p.np, rp = p.rp;
+  const int m = A->m, n = A->n, r = A->r, np = p.np, rp = p.rp, ldw = np + 2 * rp;
+  uint16_t* Ub = W + np;  // [W' | U | U]
   const dim3 rows4((unsigned)((m + 3) / 4));
   const uint8_t* codes = A->dq_codes;
   const uint8_t* scales = static_cast<const uint8_t*>(A->dq_levels);
@@ -244,41 +246,41 @@ hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, v
   if (A->flags & HSS_MX4_T) {
     const int tiles_j = (m + kTrJ - 1) / kTrJ;
     hipLaunchKernelGGL(k_mx_densify_t, dim3((unsigned)tiles_j * (unsigned)((np + kTrI - 1) / kTrI)), dim3(256), 0, s,
-                       codes, scales, m, n, np, tiles_j, W);
+                       codes, scales, m, n, np, ldw, tiles_j, W);
     if (A->nnz > 0) {
       if (A->flags & HSS_COL16)
-        hipLaunchKernelGGL(k_mx_add_csr<uint16_t>, rows4, dim3(256), 0, s, A->row_ptr, col16, vals, m, n, np, W);
+        hipLaunchKernelGGL(k_mx_add_csr<uint16_t>, rows4, dim3(256), 0, s, A->row_ptr, col16, vals, m, n, ldw, W);
       else
-        hipLaunchKernelGGL(k_mx_add_csr<int32_t>, rows4, dim3(256), 0, s, A->row_ptr, A->col_idx, vals, m, n, np, W);
+        hipLaunchKernelGGL(k_mx_add_csr<int32_t>, rows4, dim3(256), 0, s, A->row_ptr, A->col_idx, vals, m, n, ldw, W);
     }
   } else if (A->flags & HSS_COL16) {
     hipLaunchKernelGGL(k_mx_densify<uint16_t>, rows4, dim3(256), 0, s, codes, scales, A->row_ptr, col16,
-                       vals, m, n, np, W);
+                       vals, m, n, np, ldw, W);
   } else {
     hipLaunchKernelGGL(k_mx_densify<int32_t>, rows4, dim3(256), 0, s, codes, scales, A->row_ptr,
-                       A->col_idx, vals, m, n, np, W);
+                       A->col_idx, vals, m, n, np, ldw, W);
   }
   const uint16_t* Xb = static_cast<const uint16_t*>(X);
   if (!rows_ok(X, n)) {
     uint16_t* xp = reinterpret_cast<uint16_t*>(base + p.x);
-    launch_mx_pad(Xb, b, n, np, 1, xp, s);
+    launch_mx_pad(Xb, b, n, np, 1, np, xp, s);
     Xb = xp;
   }
   if (r > 0) {
     const uint16_t* Vb = static_cast<const uint16_t*>(A->Vt);
     if (!rows_ok(A->Vt, n)) {
       uint16_t* vp = reinterpret_cast<uint16_t*>(base + p.vt);
-      launch_mx_pad(Vb, r, n, np, 1, vp, s);
+      launch_mx_pad(Vb, r, n, np, 1, np, vp, s);
       Vb = vp;
     }
     launch_gemm_bf16x2(r, b, np, Vb, np, Xb, np, 0, nullptr, 0, nullptr, 0, Tf, r, false, part, s);
     launch_mx_terms(Tf, b, r, r, rp, 2, Tb, s);
-    launch_mx_pad(static_cast<const uint16_t*>(A->U), m, r, rp, 2, Ub, s);
+    launch_mx_pad(static_cast<const uint16_t*>(A->U), m, r, rp, 2, ldw, Ub, s);
   }
-  if (((m + 255) / 256) * ((b + 255) / 256) >= kG256MinTiles && gemm256_ok(m, b, np, np, np, 2 * rp, 2 * rp, 2 * rp))
-    launch_gemm256_bf16(m, b, np, W, np, Xb, np, 2 * rp, Ub, 2 * rp, Tb, 2 * rp, Y, m, s);
+  if (((m + 255) / 256) * ((b + 255) / 256) >= kG256MinTiles && gemm256_ok(m, b, np, ldw, np, 2 * rp, 2 * rp))
+    launch_gemm256_bf16(m, b, W, ldw, np, Xb, np, 2 * rp, Tb, 2 * rp, Y, m, s);
   else
-    launch_gemm_bf16x2(m, b, np, W, np, Xb, np, 2 * rp, Ub, 2 * rp, Tb, 2 * rp, Y, m, true, part, s);
+    launch_gemm_bf16x2(m, b, np, W, ldw, Xb, np, 2 * rp, Ub, ldw, Tb, 2 * rp, Y, m, true, part, s);
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 
