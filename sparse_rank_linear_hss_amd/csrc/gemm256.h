@@ -5,15 +5,18 @@
 
 namespace hss {
 
-enum : int { G256_BF16 = 0 };
+enum : int { G256_BF16 = 0, G256_PART = 1 };
 
 // Whether the operands suit k_gemm256: K segments in whole stages of 64, rows
 // of whole 16-byte chunks (aligned bases), 32-bit byte offsets.
 bool gemm256_ok(int M, int N, int K1, int lda, int ldb1, int K2, int ldb2);
 
+// Bytes of the partial products where K is split.
+size_t gemm256_part_bytes(int M, int N, int K);
+
 // C[n * ldc + m] (bf16) = A . [B1 | B2]^T: A's rows hold K1 + K2 columns
 // (K2 = 0: no second segment).
 void launch_gemm256_bf16(int M, int N, const uint16_t* A, int lda, int K1, const uint16_t* B1, int ldb1, int K2,
-                         const uint16_t* B2, int ldb2, void* C, int64_t ldc, hipStream_t s);
+                         const uint16_t* B2, int ldb2, void* C, int64_t ldc, float* part, hipStream_t s);
 
 }  // namespace hss

@@ -2,7 +2,8 @@
 //   Y = X (S + U V^T + D)^T,  D MXFP4, m x n; with HSS_MX4_T the stored array
 //   is D^T (n x m), so that a layer and its transposed layer share one copy.
 //
-// Up to 16 columns, D not transposed: mx_skinny.hip.  General route, any batch:
+// Up to 16 columns, D not transposed: mx_skinny.hip; else up to 256 columns:
+// mx_gemm.hip.  Beyond:
 //   W'  = D + S as dense bf16 in the workspace, rows padded to 64 columns
 //   T   = X V in fp32 (matrix cores), kept as two bf16 terms T = T1 + T2 (16
 //         significant bits, so that rounding T does not show beside the
@@ -16,6 +17,7 @@
 #include <algorithm>
 
 #include "gemm256.h"
+#include "mm_group.h"
 #include "mx_common.h"
 
 namespace hss {
@@ -31,6 +33,12 @@ bool mx_skinny_supported(const hss_matrix* A, int b);
 size_t mx_skinny_ws_bytes(const hss_matrix* A, int b);
 hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s);
 
+// mx_gemm.hip
+bool mx_gemm_supported(int b);
+size_t mx_gemm_ws_bytes(const hss_matrix* A, int b);
+hss_status launch_mx_gemm(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s);
+void launch_mx_tsum(const float* Tp, int splits, int b, int r, int rp, uint16_t* Tb, hipStream_t s);
+
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 static int round32(int x) { return (x + 31) & ~31; }
 
@@ -39,6 +47,15 @@ static int round32(int x) { return (x + 31) & ~31; }
 // decoded codes first, then the row's entries of S added to them (an entry's
 // column occurs once per row, so no two lanes meet), then 16-byte stores.
 // ---------------------------------------------------------------------------
+// The row's two copies of U, rp columns each (zero past r), by one wave.
+__device__ __forceinline__ void put_u(const uint16_t* __restrict__ U, int row, int r, int rp, uint16_t* __restrict__ dst) {
+  for (int l = 8 * lane_id(); l < rp; l += 512) {
+    const u32x4 v = r % 8 == 0 ? load_row8<true>(U + (int64_t)row * r, l, r) : load_row8(U + (int64_t)row * r, l, r);
+    *reinterpret_cast<u32x4*>(dst + l) = v;
+    *reinterpret_cast<u32x4*>(dst + rp + l) = v;
+  }
+}
+
 static constexpr int kMxSeg = 4096;  // columns per segment: 8 KiB of LDS per wave
 
 template <typename COL>
@@ -47,7 +64,8 @@ __global__ __launch_bounds__(256) void k_mx_densify(const uint8_t* __restrict__ 
                                                     const int32_t* __restrict__ row_ptr,
                                                     const COL* __restrict__ col_idx,
                                                     const uint16_t* __restrict__ vals, int m, int n, int np,
-                                                    int ldw, uint16_t* __restrict__ W) {
+                                                    int ldw, const uint16_t* __restrict__ U, int r, int rp,
+                                                    uint16_t* __restrict__ W) {
   __shared__ __align__(16) uint16_t seg[4][kMxSeg];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int row = blockIdx.x * 4 + w;
@@ -79,6 +97,7 @@ __global__ __launch_bounds__(256) void k_mx_densify(const uint8_t* __restrict__ 
       *reinterpret_cast<u32x4*>(W + (int64_t)row * ldw + c0 + j) = *reinterpret_cast<const u32x4*>(L + j);
     asm volatile("" ::: "memory");
   }
+  put_u(U, row, r, rp, W + (int64_t)row * ldw + np);
 }
 
 // W' = D^T, m x np from the stored n x m codes: tiles of 64 stored rows (W'
@@ -119,11 +138,12 @@ __global__ __launch_bounds__(256) void k_mx_densify_t(const uint8_t* __restrict_
   }
 }
 
-// W' += S: one wave per row, one entry per lane and step.
+// W' += S, and U behind it: one wave per row, one entry per lane and step.
 template <typename COL>
 __global__ __launch_bounds__(256) void k_mx_add_csr(const int32_t* __restrict__ row_ptr,
                                                     const COL* __restrict__ col_idx,
-                                                    const uint16_t* __restrict__ vals, int m, int n, int ldw,
+                                                    const uint16_t* __restrict__ vals, int m, int n, int np, int ldw,
+                                                    const uint16_t* __restrict__ U, int r, int rp,
                                                     uint16_t* __restrict__ W) {
   const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (row >= m) return;
@@ -134,74 +154,32 @@ __global__ __launch_bounds__(256) void k_mx_add_csr(const int32_t* __restrict__ 
     if ((unsigned)c < (unsigned)n)
       Wr[c] = f32_to_bf16(__uint_as_float((uint32_t)Wr[c] << 16) + __uint_as_float((uint32_t)vals[p] << 16));
   }
+  put_u(U, row, r, rp, Wr + np);
 }
 
-// `rep` copies of [src row | zeros] (colsp columns each, a multiple of 8) in
-// rows of ldd.
+// [src row | zeros] in rows of colsp (a multiple of 8).
 __global__ __launch_bounds__(256) void k_mx_pad(const uint16_t* __restrict__ src, int rows, int cols, int colsp,
-                                                int rep, int64_t ldd, uint16_t* __restrict__ dst) {
+                                                uint16_t* __restrict__ dst) {
   const uint32_t per = (uint32_t)colsp >> 3, total = (uint32_t)rows * per;
   for (uint32_t q = blockIdx.x * 256u + threadIdx.x; q < total; q += gridDim.x * 256u) {
     const uint32_t row = q / per;
     const int c = (int)(q - row * per) * 8;
-    const uint16_t* p = src + (int64_t)row * cols + c;
-    u32x4 v;
-    if (c + 8 <= cols) {
-      const Bytes16 a = *reinterpret_cast<const Bytes16*>(p);
-      v = u32x4{a.w[0], a.w[1], a.w[2], a.w[3]};
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = c + 2 * k < cols ? p[2 * k] : 0u, hi = c + 2 * k + 1 < cols ? p[2 * k + 1] : 0u;
-        v[k] = lo | hi << 16;
-      }
-    }
-    for (int z = 0; z < rep; ++z) *reinterpret_cast<u32x4*>(dst + row * ldd + (int64_t)z * colsp + c) = v;
+    *reinterpret_cast<u32x4*>(dst + (int64_t)row * colsp + c) = load_row8(src + (int64_t)row * cols, c, cols);
   }
 }
 
-// T (rows x cols fp32) as `terms` bf16 terms side by side (colsp columns
-// each, zero past cols): term z is the rest after the terms before it,
-// rounded to nearest.
-__global__ __launch_bounds__(256) void k_mx_terms(const float* __restrict__ T, int rows, int cols, int64_t ld,
-                                                  int colsp, int terms, uint16_t* __restrict__ dst) {
-  const uint32_t total = (uint32_t)rows * (uint32_t)colsp;
-  for (uint32_t q = blockIdx.x * 256u + threadIdx.x; q < total; q += gridDim.x * 256u) {
-    const uint32_t row = q / (uint32_t)colsp;
-    const int c = (int)(q - row * (uint32_t)colsp);
-    float v = c < cols ? T[row * ld + c] : 0.f;
-    for (int z = 0; z < terms; ++z) {
-      const uint16_t h = f32_to_bf16(v);
-      dst[((int64_t)row * terms + z) * colsp + c] = h;
-      // (an infinity leaves 0, not the NaN of inf - inf)
-      const float hf = __uint_as_float((uint32_t)h << 16);
-      v = (h & 0x7fffu) == 0x7f80u ? 0.f : v - hf;
-    }
-  }
-}
-
-void launch_mx_pad(const uint16_t* src, int rows, int cols, int colsp, int rep, int64_t ldd, uint16_t* dst,
-                   hipStream_t s) {
+static void launch_mx_pad(const uint16_t* src, int rows, int cols, int colsp, uint16_t* dst, hipStream_t s) {
   const int64_t total = (int64_t)rows * (colsp >> 3);
   const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, 4096);
-  hipLaunchKernelGGL(k_mx_pad, dim3(grid), dim3(256), 0, s, src, rows, cols, colsp, rep, ldd, dst);
-}
-
-void launch_mx_terms(const float* T, int rows, int cols, int64_t ld, int colsp, int terms, uint16_t* dst,
-                     hipStream_t s) {
-  const int64_t total = (int64_t)rows * colsp;
-  const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, 4096);
-  hipLaunchKernelGGL(k_mx_terms, dim3(grid), dim3(256), 0, s, T, rows, cols, ld, colsp, terms, dst);
+  hipLaunchKernelGGL(k_mx_pad, dim3(grid), dim3(256), 0, s, src, rows, cols, colsp, dst);
 }
 
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-static constexpr int kG256MinTiles = 128;
-
 struct MxPlan {
-  int np, rp;
-  size_t w, x, vt, tf, tb, part, total;
+  int np, rp, zt;
+  size_t w, x, vt, tp, tb, part, total;
 };
 
 static MxPlan plan_mx(const hss_matrix* A, int b) {
@@ -209,78 +187,86 @@ static MxPlan plan_mx(const hss_matrix* A, int b) {
   const int m = A->m, n = A->n, r = A->r;
   p.np = (n + 63) & ~63;
   p.rp = r > 0 ? round32(r) : 0;
+  p.zt = r > 0 ? mm_splits(r, b, p.np, 512) : 0;
   size_t off = 0;
-  p.w = off;  off += al256((size_t)m * (p.np + 2 * p.rp) * 2);
-  p.x = off;  off += al256((size_t)b * p.np * 2);
-  p.vt = off; off += al256((size_t)r * p.np * 2);
-  p.tf = off; off += al256((size_t)b * r * 4);
-  p.tb = off; off += al256((size_t)b * p.rp * 4);
-  p.part = off;
-  const size_t pt = r > 0 ? gemm_bf16x2_part_bytes(r, b, p.np, 0, r) : 0;
-  off += al256(std::max(pt, gemm_bf16x2_part_bytes(m, b, p.np, 2 * p.rp, m)));
+  auto take = [&](size_t bytes) { const size_t at = off; off += al256(bytes); return at; };
+  p.w = take((size_t)m * (p.np + 2 * p.rp) * 2);
+  p.x = take((size_t)b * p.np * 2);
+  p.vt = take((size_t)r * p.np * 2);
+  p.tp = take((size_t)p.zt * b * p.rp * 4);
+  p.tb = take((size_t)b * p.rp * 4);
+  p.part = take(std::max(gemm_bf16x2_part_bytes(m, b, p.np, 2 * p.rp, m), gemm256_part_bytes(m, b, p.np + 2 * p.rp)));
   p.total = off;
   return p;
 }
 
 size_t mx_apply_ws_bytes(const hss_matrix* A, int b) {
-  return mx_skinny_supported(A, b) ? mx_skinny_ws_bytes(A, b) : plan_mx(A, b).total;
+  if (mx_skinny_supported(A, b)) return mx_skinny_ws_bytes(A, b);
+  return mx_gemm_supported(b) ? mx_gemm_ws_bytes(A, b) : plan_mx(A, b).total;
 }
 
 static bool rows_ok(const void* p, int cols) { return (uintptr_t)p % 16 == 0 && cols % 64 == 0; }
 
 hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s) {
   if (mx_skinny_supported(A, b)) return launch_mx_skinny(A, b, X, Y, ws, s);
+  if (mx_gemm_supported(b)) return launch_mx_gemm(A, b, X, Y, ws, s);
   const MxPlan p = plan_mx(A, b);
   char* base = static_cast<char*>(ws);
-  uint16_t* W = reinterpret_cast<uint16_t*>(base + p.w);
-  float* Tf = reinterpret_cast<float*>(base + p.tf);
-  uint16_t* Tb = reinterpret_cast<uint16_t*>(base + p.tb);
-  float* part = reinterpret_cast<float*>(base + p.part);
+  auto u16 = [&](size_t off) { return reinterpret_cast<uint16_t*>(base + off); };
+  auto f32 = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
   const int m = A->m, n = A->n, r = A->r, np = p.np, rp = p.rp, ldw = np + 2 * rp;
-  uint16_t* Ub = W + np;  // [W' | U | U]
+  uint16_t* W = u16(p.w);  // [W' | U | U]
   const dim3 rows4((unsigned)((m + 3) / 4));
   const uint8_t* codes = A->dq_codes;
   const uint8_t* scales = static_cast<const uint8_t*>(A->dq_levels);
   const uint16_t* vals = static_cast<const uint16_t*>(A->values);
   const uint16_t* col16 = reinterpret_cast<const uint16_t*>(A->col_idx);
+  const uint16_t* U = static_cast<const uint16_t*>(A->U);
+  const bool c16 = (A->flags & HSS_COL16) != 0;
   if (A->flags & HSS_MX4_T) {
     const int tiles_j = (m + kTrJ - 1) / kTrJ;
     hipLaunchKernelGGL(k_mx_densify_t, dim3((unsigned)tiles_j * (unsigned)((np + kTrI - 1) / kTrI)), dim3(256), 0, s,
                        codes, scales, m, n, np, ldw, tiles_j, W);
-    if (A->nnz > 0) {
-      if (A->flags & HSS_COL16)
-        hipLaunchKernelGGL(k_mx_add_csr<uint16_t>, rows4, dim3(256), 0, s, A->row_ptr, col16, vals, m, n, ldw, W);
+    if (A->nnz > 0 || r > 0) {
+      if (c16)
+        hipLaunchKernelGGL(k_mx_add_csr<uint16_t>, rows4, dim3(256), 0, s, A->row_ptr, col16, vals, m, n, np, ldw, U, r,
+                           rp, W);
       else
-        hipLaunchKernelGGL(k_mx_add_csr<int32_t>, rows4, dim3(256), 0, s, A->row_ptr, A->col_idx, vals, m, n, ldw, W);
+        hipLaunchKernelGGL(k_mx_add_csr<int32_t>, rows4, dim3(256), 0, s, A->row_ptr, A->col_idx, vals, m, n, np, ldw,
+                           U, r, rp, W);
     }
-  } else if (A->flags & HSS_COL16) {
-    hipLaunchKernelGGL(k_mx_densify<uint16_t>, rows4, dim3(256), 0, s, codes, scales, A->row_ptr, col16,
-                       vals, m, n, np, ldw, W);
+  } else if (c16) {
+    hipLaunchKernelGGL(k_mx_densify<uint16_t>, rows4, dim3(256), 0, s, codes, scales, A->row_ptr, col16, vals, m, n, np,
+                       ldw, U, r, rp, W);
   } else {
-    hipLaunchKernelGGL(k_mx_densify<int32_t>, rows4, dim3(256), 0, s, codes, scales, A->row_ptr,
-                       A->col_idx, vals, m, n, np, ldw, W);
+    hipLaunchKernelGGL(k_mx_densify<int32_t>, rows4, dim3(256), 0, s, codes, scales, A->row_ptr, A->col_idx, vals, m, n,
+                       np, ldw, U, r, rp, W);
   }
   const uint16_t* Xb = static_cast<const uint16_t*>(X);
   if (!rows_ok(X, n)) {
-    uint16_t* xp = reinterpret_cast<uint16_t*>(base + p.x);
-    launch_mx_pad(Xb, b, n, np, 1, np, xp, s);
-    Xb = xp;
+    launch_mx_pad(Xb, b, n, np, u16(p.x), s);
+    Xb = u16(p.x);
   }
   if (r > 0) {
     const uint16_t* Vb = static_cast<const uint16_t*>(A->Vt);
     if (!rows_ok(A->Vt, n)) {
-      uint16_t* vp = reinterpret_cast<uint16_t*>(base + p.vt);
-      launch_mx_pad(Vb, r, n, np, 1, np, vp, s);
-      Vb = vp;
+      launch_mx_pad(Vb, r, n, np, u16(p.vt), s);
+      Vb = u16(p.vt);
     }
-    launch_gemm_bf16x2(r, b, np, Vb, np, Xb, np, 0, nullptr, 0, nullptr, 0, Tf, r, false, part, s);
-    launch_mx_terms(Tf, b, r, r, rp, 2, Tb, s);
-    launch_mx_pad(static_cast<const uint16_t*>(A->U), m, r, rp, 2, ldw, Ub, s);
+    MmProblem q = {};
+    q.A = Vb; q.lda = np; q.M = r;
+    q.B = Xb; q.ldb = np; q.N = b;
+    q.K = np;
+    q.C = f32(p.tp); q.ldc = rp; q.trans = 1; q.zstride = (int64_t)b * rp;
+    q.splits = p.zt;
+    launch_mm_group(&q, 1, s);
+    launch_mx_tsum(f32(p.tp), p.zt, b, r, rp, u16(p.tb), s);
   }
-  if (((m + 255) / 256) * ((b + 255) / 256) >= kG256MinTiles && gemm256_ok(m, b, np, ldw, np, 2 * rp, 2 * rp))
-    launch_gemm256_bf16(m, b, W, ldw, np, Xb, np, 2 * rp, Tb, 2 * rp, Y, m, s);
+  // measured against k_gemm_h from 300 columns on: 5 - 20 % faster throughout
+  if (gemm256_ok(m, b, np, ldw, np, 2 * rp, 2 * rp))
+    launch_gemm256_bf16(m, b, W, ldw, np, Xb, np, 2 * rp, u16(p.tb), 2 * rp, Y, m, f32(p.part), s);
   else
-    launch_gemm_bf16x2(m, b, np, W, ldw, Xb, np, 2 * rp, Ub, ldw, Tb, 2 * rp, Y, m, true, part, s);
+    launch_gemm_bf16x2(m, b, np, W, ldw, Xb, np, 2 * rp, W + np, ldw, u16(p.tb), 2 * rp, Y, m, true, f32(p.part), s);
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 

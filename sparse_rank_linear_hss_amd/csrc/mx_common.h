@@ -57,4 +57,47 @@ __device__ __forceinline__ void mx8_to_f32x4(uint32_t codes, float scale, float*
   for (int k = 0; k < 4; ++k) v[k] = (float)((int32_t)(codes << (24 - 8 * k)) >> 24) * scale;
 }
 
+// Eight bf16 at any 2-byte aligned address.
+__device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ p) {
+  const Bytes16 a = *reinterpret_cast<const Bytes16*>(p);
+  return u32x4{a.w[0], a.w[1], a.w[2], a.w[3]};
+}
+
+// Eight bf16 of a row of n at column k, zeros past the end.  WHOLE: n is a
+// multiple of 8 (no column-by-column tail, whose loads the compiler waits for
+// one by one -- so callers branch on n once for a whole kernel).
+template <bool WHOLE = false>
+__device__ __forceinline__ u32x4 load_row8(const uint16_t* __restrict__ row, int k, int n) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (WHOLE ? k < n : k + 8 <= n) {
+    v = load8(row + k);
+  } else if (!WHOLE && k < n) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t lo = k + 2 * e < n ? row[k + 2 * e] : 0u, hi = k + 2 * e + 1 < n ? row[k + 2 * e + 1] : 0u;
+      v[e] = lo | hi << 16;
+    }
+  }
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// k_mx_prep (mx_skinny.hip): T = X V in K splits, X^T, padded X and U.
+// ---------------------------------------------------------------------------
+static constexpr int kMxPrepSplits = 8;  // most K splits of T
+
+struct MxPrep {
+  const uint16_t* X;
+  const uint16_t* Vt;
+  float* Tp;      // [splits][b][rp], with r > 0
+  uint16_t* Xt;   // n x ldt; null = none
+  uint16_t* Xp;   // b x np;  null = none
+  const uint16_t* U;
+  uint16_t* Up;   // m x rp;  null = none
+  int m, b, n, r, rp, ltiles, splits, steps_per_split, tb, xb, ldt, np;
+};
+
+MxPrep mx_prep_plan(const hss_matrix* A, int b);  // the sizes of T
+void launch_mx_prep(MxPrep p, hipStream_t s);
+
 }  // namespace hss

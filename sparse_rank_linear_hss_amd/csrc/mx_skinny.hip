@@ -22,6 +22,7 @@
 // over blocks (the partial sums are added by the reader, in order), and X^T
 // for the gathers of S.
 #include <algorithm>
+#include <type_traits>
 
 #include "mx_common.h"
 
@@ -33,82 +34,96 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 static constexpr int kSkCols = 16;       // columns of one call
 static constexpr int kSkGather = 4;      // columns up to which S gathers from X, not X^T
 static constexpr int kSkBatch = 4;       // chunks whose loads are in flight together
-static constexpr int kPrepSplits = 8;    // most K splits of T
-
-// Eight bf16 of a row of n at column k, zeros past the end.
-__device__ __forceinline__ u32x4 load_row8(const uint16_t* __restrict__ row, int k, int n) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (k + 8 <= n) {
-    const Bytes16 a = *reinterpret_cast<const Bytes16*>(row + k);
-    v = u32x4{a.w[0], a.w[1], a.w[2], a.w[3]};
-  } else if (k < n) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = k + 2 * e < n ? row[k + 2 * e] : 0u, hi = k + 2 * e + 1 < n ? row[k + 2 * e + 1] : 0u;
-      v[e] = lo | hi << 16;
-    }
-  }
-  return v;
-}
 
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
-// Blocks 0 .. tb - 1: 16 rows of V^T over one K split, T partial sums
-// Tp[ks][c][rp] (c < b).  Blocks from tb: X^T (n x 16, columns past b zero)
-// and X with rows of np (zero past n), each where its pointer is not null.
+// What a launch needs of X.  Blocks 0 .. tb - 1: 16 rows of V^T times 16
+// columns over one K split, T partial sums Tp[ks][c][rp] (c < b).  Blocks from
+// tb: X^T (n x ldt, zero past b), X with rows of np (zero past n) and U with
+// rows of rp, each where its pointer is not null.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void k_mx_prep(const uint16_t* __restrict__ X, const uint16_t* __restrict__ Vt, int b,
-                                                 int n, int r, int rp, int ltiles, int steps_per_split, int tb,
-                                                 float* __restrict__ Tp, uint16_t* __restrict__ Xt, uint16_t* __restrict__ Xp,
-                                                 int np) {
+__global__ __launch_bounds__(256) void k_mx_prep(MxPrep a) {
   __shared__ float red[4][256];
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  if ((int)blockIdx.x >= tb) {
-    const int first = ((int)blockIdx.x - tb) * 256 + t, step = ((int)gridDim.x - tb) * 256;
-    for (int e = first; Xp && e < b * (np >> 3); e += step) {
-      const int c = e / (np >> 3), k = (e - c * (np >> 3)) * 8;
-      *reinterpret_cast<u32x4*>(Xp + (int64_t)c * np + k) = load_row8(X + (int64_t)c * n, k, n);
+  const uint16_t* __restrict__ X = a.X;
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, b = a.b, n = a.n;
+  if ((int)blockIdx.x >= a.tb) {
+    const int64_t first = ((int64_t)blockIdx.x - a.tb) * 256 + t, step = (int64_t)(a.xb) * 256;
+    const int per = a.np >> 3;
+    for (int64_t e = first; a.Xp && e < (int64_t)b * per; e += step) {
+      const int c = (int)(e / per), k = (int)(e - (int64_t)c * per) * 8;
+      *reinterpret_cast<u32x4*>(a.Xp + (int64_t)c * a.np + k) = load_row8(X + (int64_t)c * n, k, n);
     }
-    for (int j = first; Xt && j < n; j += step) {
-      uint32_t v[8];
+    for (int64_t e = first; a.Up && e < (int64_t)a.m * (a.rp >> 3); e += step) {
+      const int i = (int)(e / (a.rp >> 3)), l = (int)(e - (int64_t)i * (a.rp >> 3)) * 8;
+      *reinterpret_cast<u32x4*>(a.Up + (int64_t)i * a.rp + l) = load_row8(a.U + (int64_t)i * a.r, l, a.r);
+    }
+    for (int64_t e = first; a.Xt && e < (int64_t)n * (a.ldt >> 3); e += step) {
+      const int c0 = (int)(e / n) * 8, j = (int)(e - (int64_t)(c0 >> 3) * n);
+      u32x4 v;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t lo = 2 * k < b ? X[(int64_t)(2 * k) * n + j] : 0u;
-        const uint32_t hi = 2 * k + 1 < b ? X[(int64_t)(2 * k + 1) * n + j] : 0u;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = c0 + 2 * k < b ? X[(int64_t)(c0 + 2 * k) * n + j] : 0u;
+        const uint32_t hi = c0 + 2 * k + 1 < b ? X[(int64_t)(c0 + 2 * k + 1) * n + j] : 0u;
         v[k] = lo | hi << 16;
       }
-      u32x4* o = reinterpret_cast<u32x4*>(Xt + (int64_t)j * kSkCols);
-      o[0] = u32x4{v[0], v[1], v[2], v[3]};
-      o[1] = u32x4{v[4], v[5], v[6], v[7]};
+      *reinterpret_cast<u32x4*>(a.Xt + (int64_t)j * a.ldt + c0) = v;
     }
     return;
   }
-  const int lt = (int)blockIdx.x % ltiles, ks = (int)blockIdx.x / ltiles;
-  const int steps = (n + 31) >> 5;
-  const int s0 = ks * steps_per_split, s1 = min(s0 + steps_per_split, steps);
-  const uint16_t* vrow = Vt + (int64_t)min(16 * lt + (lane & 15), r - 1) * n;
-  const uint16_t* xrow = X + (int64_t)min(lane & 15, b - 1) * n;
+  const int lt = (int)blockIdx.x % a.ltiles, rest = (int)blockIdx.x / a.ltiles;
+  const int ks = rest % a.splits, c0 = rest / a.splits * 16;
+  const int steps = (n + 31) >> 5, full = n >> 5;
+  const int s0 = ks * a.steps_per_split, s1 = min(s0 + a.steps_per_split, steps), f1 = min(s1, full);
+  const uint16_t* vrow = a.Vt + (int64_t)min(16 * lt + (lane & 15), a.r - 1) * n;
+  const uint16_t* xrow = X + (int64_t)min(c0 + (lane & 15), b - 1) * n;
+  const int k0 = 8 * (lane >> 4);
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int s = s0 + w; s < s1; s += 16) {
+  for (int s = s0 + w; s < f1; s += 16) {  // whole steps; past the last one that one again, not used
     u32x4 va[4], xa[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int k = s + 4 * u < s1 ? 32 * (s + 4 * u) + 8 * (lane >> 4) : n;  // n: zeros
-      va[u] = load_row8(vrow, k, n);
-      xa[u] = load_row8(xrow, k, n);
+      const int k = 32 * min(s + 4 * u, f1 - 1) + k0;
+      va[u] = load8(vrow + k);
+      xa[u] = load8(xrow + k);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) acc = mfma16(va[u], xa[u], acc);
+    for (int u = 0; u < 4; ++u)
+      if (s + 4 * u < f1) acc = mfma16(va[u], xa[u], acc);
   }
+  if (s1 > f1 && w == 0) acc = mfma16(load_row8(vrow, 32 * f1 + k0, n), load_row8(xrow, 32 * f1 + k0, n), acc);
   // lane holds rows 4 (lane / 16) + i of column lane % 16
 #pragma unroll
   for (int i = 0; i < 4; ++i) red[w][(lane & 15) * 16 + 4 * (lane >> 4) + i] = acc[i];
   __syncthreads();
-  const int c = t >> 4, l = 16 * lt + (t & 15);
-  if (c < b && l < rp) Tp[((int64_t)ks * b + c) * rp + l] = l < r ? (red[0][t] + red[1][t]) + (red[2][t] + red[3][t]) : 0.f;
+  const int c = c0 + (t >> 4), l = 16 * lt + (t & 15);
+  if (c < b && l < a.rp)
+    a.Tp[((int64_t)ks * b + c) * a.rp + l] = l < a.r ? (red[0][t] + red[1][t]) + (red[2][t] + red[3][t]) : 0.f;
+}
+
+MxPrep mx_prep_plan(const hss_matrix* A, int b) {
+  MxPrep p = {};
+  p.m = A->m; p.b = b; p.n = A->n; p.r = A->r;
+  p.rp = A->r > 0 ? (A->r + 31) & ~31 : 0;
+  p.ltiles = std::max(p.rp / 16, 1);
+  const int steps = (A->n + 31) / 32, tiles = p.ltiles * ((b + 15) / 16);
+  // four waves of up to four steps each per split, fewer splits where the
+  // tiles fill the chip by themselves
+  p.splits = std::max(1, std::min({kMxPrepSplits, (steps + 15) / 16, (1024 + tiles - 1) / tiles}));
+  p.steps_per_split = (steps + p.splits - 1) / p.splits;
+  p.tb = A->r > 0 ? tiles * p.splits : 0;
+  return p;
+}
+
+void launch_mx_prep(MxPrep p, hipStream_t s) {
+  if (p.Xt || p.Xp || p.Up) {
+    const int64_t work = std::max({p.Xt ? (int64_t)p.n * (p.ldt / 8) : 0, p.Xp ? (int64_t)p.b * (p.np / 8) : 0,
+                                   p.Up ? (int64_t)p.m * (p.rp / 8) : 0});
+    p.xb = (int)std::min<int64_t>((work + 255) / 256, 1024);
+  }
+  if (p.tb + p.xb > 0) hipLaunchKernelGGL(k_mx_prep, dim3((unsigned)(p.tb + p.xb)), dim3(256), 0, s, p);
 }
 
 struct SkinnyArgs {
@@ -127,12 +142,12 @@ struct SkinnyArgs {
 
 // Element e of T: its K splits' partial sums, loaded together, added in order.
 __device__ __forceinline__ float t_sum(const SkinnyArgs& a, int e) {
-  float p[kPrepSplits];
+  float p[kMxPrepSplits];
 #pragma unroll
-  for (int ks = 0; ks < kPrepSplits; ++ks) p[ks] = a.Tp[(uint32_t)min(ks, a.splits - 1) * (uint32_t)(a.b * a.rp) + e];
+  for (int ks = 0; ks < kMxPrepSplits; ++ks) p[ks] = a.Tp[(uint32_t)min(ks, a.splits - 1) * (uint32_t)(a.b * a.rp) + e];
   float v = p[0];
 #pragma unroll
-  for (int ks = 1; ks < kPrepSplits; ++ks) v += ks < a.splits ? p[ks] : 0.f;
+  for (int ks = 1; ks < kMxPrepSplits; ++ks) v += ks < a.splits ? p[ks] : 0.f;
   return v;
 }
 
@@ -320,8 +335,9 @@ __global__ __launch_bounds__(64 * WV, 4) void k_mx_skinny(SkinnyArgs a) {
     __syncthreads();
     const uint16_t* __restrict__ urow = a.U + (int64_t)min(row0 + (lane & 15), a.m - 1) * a.r;
     const uint16_t* tl = Tl + 2 * min(lane & 15, a.b - 1) * ldt + 8 * q;
+    const bool whole = a.r % 8 == 0;
     for (int j = w; j < (a.rp >> 5); j += WV) {
-      const u32x4 uv = load_row8(urow, 32 * j + 8 * q, a.r);
+      const u32x4 uv = whole ? load_row8<true>(urow, 32 * j + 8 * q, a.r) : load_row8(urow, 32 * j + 8 * q, a.r);
       acc = mfma16(uv, *reinterpret_cast<const u32x4*>(tl + 32 * j), acc);
       acc = mfma16(uv, *reinterpret_cast<const u32x4*>(tl + ldt + 32 * j), acc);
     }
@@ -407,12 +423,26 @@ __global__ __launch_bounds__(64 * kGvWaves) void k_mx_gemv(SkinnyArgs a) {
       }
     }
   }
-  for (int e = t; e < nch * 256; e += 64 * kGvWaves) {
-    const int at = ((((e >> 8) * 4 + (e & 3)) * 64 + ((e >> 2) & 63)) << 3);
+  auto stage_x = [&](auto whole) {
+    for (int e0 = t; e0 < nch * 256; e0 += 256 * kGvWaves) {
+      u32x4 x[4][BC];
 #pragma unroll
-    for (int c = 0; c < BC; ++c)
-      *reinterpret_cast<u32x4*>(xs + c * plane + at) = load_row8(a.X + (int64_t)min(c, a.b - 1) * a.n, 8 * e, a.n);
-  }
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int c = 0; c < BC; ++c)
+          x[u][c] = load_row8<decltype(whole)::value>(a.X + (int64_t)min(c, a.b - 1) * a.n, 8 * (e0 + 64 * kGvWaves * u), a.n);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = e0 + 64 * kGvWaves * u;
+        const int at = ((((e >> 8) * 4 + (e & 3)) * 64 + ((e >> 2) & 63)) << 3);
+#pragma unroll
+        for (int c = 0; c < BC; ++c)
+          if (e < nch * 256) *reinterpret_cast<u32x4*>(xs + c * plane + at) = x[u][c];
+      }
+    }
+  };
+  if (a.n % 8 == 0) stage_x(std::true_type());
+  else stage_x(std::false_type());
   if (a.r > 0) {
     for (int e = t; e < a.b * a.rp; e += 64 * kGvWaves) Ts[e] = t_sum(a, e);
   }
@@ -468,21 +498,27 @@ __global__ __launch_bounds__(64 * kGvWaves) void k_mx_gemv(SkinnyArgs a) {
       }
     }
   }
-  for (int l = 8 * lane; l < a.r; l += 512) {
+  auto add_ut = [&](auto whole) {
+    for (int l = 8 * lane; l < a.r; l += 512) {
+      u32x4 u[RW];
 #pragma unroll
-    for (int i = 0; i < RW; ++i) {
-      const u32x4 u = load_row8(a.U + (int64_t)min(row0 + i, a.m - 1) * a.r, l, a.r);
+      for (int i = 0; i < RW; ++i)
+        u[i] = load_row8<decltype(whole)::value>(a.U + (int64_t)min(row0 + i, a.m - 1) * a.r, l, a.r);
 #pragma unroll
       for (int c = 0; c < BC; ++c) {
         const float* T = Ts + min(c, a.b - 1) * a.rp + l;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[i][c] = fmaf(bf16lo(u[e]), T[2 * e], acc[i][c]);
-          acc[i][c] = fmaf(bf16hi(u[e]), T[2 * e + 1], acc[i][c]);
-        }
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int i = 0; i < RW; ++i) {
+            acc[i][c] = fmaf(bf16lo(u[i][e]), T[2 * e], acc[i][c]);
+            acc[i][c] = fmaf(bf16hi(u[i][e]), T[2 * e + 1], acc[i][c]);
+          }
       }
     }
-  }
+  };
+  if (a.r % 8 == 0) add_ut(std::true_type());
+  else add_ut(std::false_type());
   // result q = i BC + c goes to lane q
   float y = 0.f;
 #pragma unroll
@@ -512,20 +548,15 @@ static bool gv_supported(const hss_matrix* A, int b) {
 }
 
 struct SkinnyPlan {
-  int rp, ltiles, splits, steps_per_split;
+  MxPrep prep;
   size_t tp, xt, xp, total;
 };
 
 static SkinnyPlan plan_skinny(const hss_matrix* A, int b) {
   SkinnyPlan p = {};
-  p.rp = A->r > 0 ? round32(A->r) : 0;
-  p.ltiles = p.rp / 16;
-  const int steps = (A->n + 31) / 32;
-  // four waves of up to four steps each per split
-  p.splits = std::max(1, std::min(kPrepSplits, (steps + 15) / 16));
-  p.steps_per_split = (steps + p.splits - 1) / p.splits;
+  p.prep = mx_prep_plan(A, b);
   p.tp = 0;
-  p.xt = al256((size_t)p.splits * b * p.rp * 4);
+  p.xt = al256((size_t)p.prep.splits * b * p.prep.rp * 4);
   p.xp = p.xt + ((b > kSkGather && A->nnz > 0) ? al256((size_t)A->n * kSkCols * 2) : 0);
   p.total = p.xp + (b > 1 ? al256((size_t)b * round32(A->n) * 2) : 0);
   return p;
@@ -554,9 +585,9 @@ hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, 
   a.U = static_cast<const uint16_t*>(A->U);
   a.Tp = reinterpret_cast<const float*>(base + p.tp);
   a.Y = static_cast<uint16_t*>(Y);
-  a.m = m; a.n = n; a.b = b; a.r = r; a.rp = p.rp;
+  a.m = m; a.n = n; a.b = b; a.r = r; a.rp = p.prep.rp;
   a.ng = mx_groups(n);
-  a.splits = p.splits;
+  a.splits = p.prep.splits;
   a.has_s = A->nnz > 0;
   a.col16 = (A->flags & HSS_COL16) != 0;
   a.ldx = n;
@@ -565,20 +596,21 @@ hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, 
   // rows off the 16-byte grid: 16-byte loads of X at 2-byte addresses cost the
   // main launch more than a copy (2731 x 5003, 13 columns: 14.8 against 9.6 us)
   const bool need_xp = !gemv && b > 1 && (n % 8 != 0 || (uintptr_t)X % 16 != 0);
-  const int tb = r > 0 ? p.ltiles * p.splits : 0;
-  const int xb = need_xt || need_xp ? std::min((n + 255) / 256, 256) : 0;
-  if (tb + xb > 0)
-    hipLaunchKernelGGL(k_mx_prep, dim3((unsigned)(tb + xb)), dim3(256), 0, s, a.X,
-                       static_cast<const uint16_t*>(A->Vt), b, n, r, p.rp, std::max(p.ltiles, 1), p.steps_per_split,
-                       tb, reinterpret_cast<float*>(base + p.tp),
-                       need_xt ? reinterpret_cast<uint16_t*>(base + p.xt) : nullptr,
-                       need_xp ? reinterpret_cast<uint16_t*>(base + p.xp) : nullptr, round32(n));
+  MxPrep pr = p.prep;
+  pr.X = a.X;
+  pr.Vt = static_cast<const uint16_t*>(A->Vt);
+  pr.Tp = reinterpret_cast<float*>(base + p.tp);
+  pr.ldt = kSkCols;
+  pr.np = round32(n);
+  if (need_xt) pr.Xt = reinterpret_cast<uint16_t*>(base + p.xt);
+  if (need_xp) pr.Xp = reinterpret_cast<uint16_t*>(base + p.xp);
+  launch_mx_prep(pr, s);
   if (need_xp) {
     a.X = reinterpret_cast<const uint16_t*>(base + p.xp);
     a.ldx = round32(n);
   }
   if (gemv) {
-    const size_t lds = (size_t)(b > 2 ? 4 : b) * gv_plane_bytes(n) + (size_t)b * p.rp * 4;
+    const size_t lds = (size_t)(b > 2 ? 4 : b) * gv_plane_bytes(n) + (size_t)b * a.rp * 4;
     // two rows a wave while that leaves every SIMD a wave or two, else four
     const bool four = m > 8192;
     const unsigned gv = (unsigned)((m + kGvWaves * (four ? 4 : 2) - 1) / (kGvWaves * (four ? 4 : 2)));
@@ -596,7 +628,7 @@ hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, 
     return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
   }
   const unsigned grid = (unsigned)((m + 15) / 16);
-  const size_t tl = r > 0 ? (size_t)b * 2 * (p.rp + 8) * 2 : 0;
+  const size_t tl = r > 0 ? (size_t)b * 2 * (a.rp + 8) * 2 : 0;
   const int nch = (a.ng + 3) / 4;
   // Waves per block: enough to hold a row tile's codes in flight, fewer when
   // the blocks fill the chip anyway.
