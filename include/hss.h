@@ -616,7 +616,8 @@ hss_status hss_mx_dequantize(int32_t fmt, int32_t dt, int32_t rows, int32_t cols
  *   significant bits), so every output carries fp32 precision.  The same
  *   inputs give the same bits on every call.
  *   ws: at least hss_grad_ckpt_workspace_size() bytes (no state kept).
- *   HSS_ERR_UNSUPPORTED: as hss_grad, with round32 in place of round8.
+ *   HSS_ERR_UNSUPPORTED: as hss_grad, or max(m, n) round64(b) * 2 or
+ *   3 round32(r) max(m, n, round64(b)) >= 2^31.
  *   HSS_ERR_INVALID_ARG: as hss_grad, codes not 16-byte aligned.
  *   HSS_ERR_WORKSPACE; HSS_ERR_HIP. */
 hss_status hss_grad_ckpt_workspace_size(const hss_matrix* A, int32_t b, size_t* bytes);

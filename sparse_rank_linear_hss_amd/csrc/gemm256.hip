@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "gemm256.h"
+#include "s_pattern.h"
 
 namespace hss {
 
@@ -41,6 +42,8 @@ struct G256Args {
   void* C;
   int64_t ldc;
   int tiles_m, tiles_n, stages_per_split;
+  SPattern S;             // G256_DS
+  const int32_t* tptr;    // G256_DS, CSR: k_ds_tiles' table
 };
 
 static constexpr int kKS = 64;  // K per stage
@@ -263,6 +266,56 @@ __global__ __launch_bounds__(256, 1) void k_gemm256(G256Args g) {
                 float4{acc[i][j][4 * vg], acc[i][j][4 * vg + 1], acc[i][j][4 * vg + 2], acc[i][j][4 * vg + 3]};
         }
       }
+  } else {  // G256_DS32, 16, NM: dS[p] = C[row of p][column of p] for S's entries within the tile
+    constexpr int PAT = OUT - G256_DS;
+    float* dS = static_cast<float*>(g.C);
+    // 64 rows at a time through LDS (rows 128 g + 32 i + 0..31 at 32 g + 0..31), the
+    // two buffers in turn; four threads take a row's entries
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      float* L = reinterpret_cast<float*>(i & 1 ? buf1 : buf0);
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          L[(32 * (w >> 1) + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * TL::TN + wn + 32 * j + (lane & 31)] = acc[i][j][v];
+      __syncthreads();
+      const int lrow = t >> 2, row = m0 + 128 * (lrow >> 5) + 32 * i + (lrow & 31);
+      if (row < g.M) {
+        int64_t rs, p, pe;
+        if constexpr (PAT == PAT_NM24) {
+          rs = (int64_t)row * (g.N >> 1);
+          p = rs + (n0 >> 1), pe = rs + (min(n0 + TL::TN, g.N) >> 1);
+        } else {
+          rs = g.S.row_ptr[row];
+          p = g.tptr[(int64_t)row * (g.tiles_n + 1) + tn], pe = g.tptr[(int64_t)row * (g.tiles_n + 1) + tn + 1];
+        }
+        for (p += t & 3; p < pe; p += 4) {
+          const int c = pat_col<PAT>(g.S, row, rs, p) - n0;
+          if ((unsigned)c < (unsigned)TL::TN) dS[p] = L[lrow * TL::TN + c];
+        }
+      }
+    }
+  }
+}
+
+// tptr[row][t] = the first entry of the row at or past column 256 t (t = 0:
+// its first, t = tiles: its end), by binary search.
+template <int PAT>
+__global__ __launch_bounds__(256) void k_ds_tiles(SPattern S, int m, int tiles, int32_t* __restrict__ tptr) {
+  const int64_t total = (int64_t)m * (tiles + 1);
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    const int row = (int)(e / (tiles + 1)), t = (int)(e - (int64_t)row * (tiles + 1));
+    const int32_t rs = S.row_ptr[row];
+    int32_t lo = rs, hi = S.row_ptr[row + 1];
+    if (t == 0) hi = lo;
+    if (t == tiles) lo = hi;
+    while (lo < hi) {
+      const int32_t mid = lo + (hi - lo) / 2;
+      if (pat_col<PAT>(S, row, rs, mid) < 256 * t) lo = mid + 1;
+      else hi = mid;
+    }
+    tptr[e] = lo;
   }
 }
 
@@ -356,6 +409,39 @@ void launch_gemm256_bf16(int M, int N, const uint16_t* A, int lda, int K1, const
   const int64_t work = (int64_t)N * mp / 4;
   hipLaunchKernelGGL(k_gemm256_sum, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 8192)), dim3(256), 0, s, part,
                      splits, M, N, mp, ldc, static_cast<uint16_t*>(C));
+}
+
+size_t gemm256_ds_bytes(const hss_matrix* A) {
+  return A->fmt == HSS_FMT_2OF4 ? 0 : (size_t)A->m * ((A->n + 255) / 256 + 1) * 4;
+}
+
+void launch_gemm256_ds(const hss_matrix* A, int K, const uint16_t* Gt, const uint16_t* Xt, int ld, float* dS,
+                       int32_t* tptr, hipStream_t s) {
+  G256Args g = {};
+  g.A = Gt; g.B1 = Xt;
+  g.M = A->m; g.N = A->n; g.K1 = K;
+  g.lda = g.ldb1 = ld;
+  g.C = dS;
+  g.tiles_m = (g.M + 255) / 256;
+  g.tiles_n = (g.N + 255) / 256;
+  g.stages_per_split = K / kKS;
+  g.S = s_pattern(A);
+  g.tptr = tptr;
+  const dim3 grid((unsigned)(g.tiles_m * g.tiles_n));
+  const int pat = s_pattern_kind(A);
+  if (pat == PAT_NM24) {
+    hipLaunchKernelGGL((k_gemm256<4, G256_DS + PAT_NM24, false>), grid, dim3(256), 0, s, g);
+    return;
+  }
+  const int64_t work = (int64_t)g.M * (g.tiles_n + 1);
+  const dim3 tg((unsigned)std::min<int64_t>((work + 255) / 256, 8192));
+  if (pat == PAT_CSR16) {
+    hipLaunchKernelGGL(k_ds_tiles<PAT_CSR16>, tg, dim3(256), 0, s, g.S, g.M, g.tiles_n, tptr);
+    hipLaunchKernelGGL((k_gemm256<4, G256_DS + PAT_CSR16, false>), grid, dim3(256), 0, s, g);
+  } else {
+    hipLaunchKernelGGL(k_ds_tiles<PAT_CSR32>, tg, dim3(256), 0, s, g.S, g.M, g.tiles_n, tptr);
+    hipLaunchKernelGGL((k_gemm256<4, G256_DS + PAT_CSR32, false>), grid, dim3(256), 0, s, g);
+  }
 }
 
 }  // namespace hss

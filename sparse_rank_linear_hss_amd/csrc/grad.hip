@@ -25,6 +25,7 @@
 #include <vector>
 
 #include "hss_internal.h"
+#include "s_pattern.h"
 
 namespace hss {
 
@@ -46,43 +47,6 @@ static int round8(int x) { return (x + 7) & ~7; }
 // LP partial sums meet in an xor butterfly (fixed order).
 // ---------------------------------------------------------------------------
 static constexpr int kSdUnroll = 4;
-
-// S's stored positions: CSR (int32 or 16-bit columns) or 2:4 (row i holds
-// n / 2 entries, entry 2g + s the s-th kept column of group g, from the
-// nibble at bits 4 (g % 8) of metadata word g / 8).
-enum : int { PAT_CSR32 = 0, PAT_CSR16 = 1, PAT_NM24 = 2 };
-
-struct SPattern {
-  const int32_t* row_ptr;  // CSR
-  const void* col;         // CSR columns
-  const uint32_t* meta;    // 2:4 metadata, m x ceil(n / 32)
-  int n;
-};
-
-template <int PAT>
-__device__ __forceinline__ void pat_row(const SPattern& P, int i, int64_t& rs, int64_t& re) {
-  if constexpr (PAT == PAT_NM24) {
-    rs = (int64_t)i * (P.n >> 1);
-    re = rs + (P.n >> 1);
-  } else {
-    rs = P.row_ptr[i];
-    re = P.row_ptr[i + 1];
-  }
-}
-
-template <int PAT>
-__device__ __forceinline__ int pat_col(const SPattern& P, int i, int64_t rs, int64_t p) {
-  if constexpr (PAT == PAT_CSR32) {
-    return static_cast<const int32_t*>(P.col)[p];
-  } else if constexpr (PAT == PAT_CSR16) {
-    return static_cast<const uint16_t*>(P.col)[p];
-  } else {
-    const int q = (int)(p - rs), g = q >> 1;
-    const uint32_t w = P.meta[(int64_t)i * ((P.n + 31) >> 5) + (g >> 3)];
-    const uint32_t nib = (w >> (4 * (g & 7))) & 15u;
-    return 4 * g + (int)((q & 1) ? (nib >> 2) & 3u : nib & 3u);
-  }
-}
 
 template <int LP, int PAT>
 __global__ __launch_bounds__(256) void k_sddmm(SPattern P, const uint16_t* __restrict__ Gt,
@@ -202,7 +166,7 @@ static void launch_sddmm_pat(int lp, const SPattern& P, const uint16_t* Gt, cons
 // vs 0.41.
 static constexpr int kDenseDsMinB = 512;
 
-bool ds_dense(int b) {
+static bool ds_dense(int b) {
   const int forced = option(HSS_OPT_GRAD_DS_ROUTE);
   if (forced == 1) return false;
   if (forced == 2) return true;
@@ -241,37 +205,18 @@ static GradPlan plan_grad(const hss_matrix* A, int b) {
 
 size_t grad_ws_bytes(const hss_matrix* A, int b) { return plan_grad(A, b).total; }
 
-// dS from X^T and G^T (n x ldt and m x ldt, columns past b zero): the sampled
-// product, or dA = G^T X (in `dA`, m x n; over kb columns, b <= kb <= ldt) and
-// a gather, by ds_dense(b).
-void launch_ds(const hss_matrix* A, int b, int kb, int ldt, const uint16_t* Xt, const uint16_t* Gt, float* dA, float* part,
-               float* dS, hipStream_t s) {
-  const int m = A->m, n = A->n;
-  SPattern P = {};
-  P.row_ptr = A->row_ptr;
-  P.col = A->col_idx;
-  P.meta = A->nm_meta;
-  P.n = n;
-  const int pat = A->fmt == HSS_FMT_2OF4 ? PAT_NM24 : ((A->flags & HSS_COL16) ? PAT_CSR16 : PAT_CSR32);
-  if (ds_dense(b)) {
-    launch_gemm_bf16(n, m, kb, Xt, ldt, Gt, ldt, dA, n, false, part, s);
-    const dim3 grid((unsigned)((m + 3) / 4));
-    if (pat == PAT_NM24)
-      hipLaunchKernelGGL(k_ds_gather<PAT_NM24>, grid, dim3(256), 0, s, P, dA, m, n, dS);
-    else if (pat == PAT_CSR16)
-      hipLaunchKernelGGL(k_ds_gather<PAT_CSR16>, grid, dim3(256), 0, s, P, dA, m, n, dS);
-    else
-      hipLaunchKernelGGL(k_ds_gather<PAT_CSR32>, grid, dim3(256), 0, s, P, dA, m, n, dS);
-  } else {
-    int lp = 1;
-    while (lp < 64 && lp * 2 <= (ldt >> 3)) lp *= 2;
-    if (pat == PAT_NM24)
-      launch_sddmm_pat<PAT_NM24>(lp, P, Gt, Xt, m, n, ldt, dS, s);
-    else if (pat == PAT_CSR16)
-      launch_sddmm_pat<PAT_CSR16>(lp, P, Gt, Xt, m, n, ldt, dS, s);
-    else
-      launch_sddmm_pat<PAT_CSR32>(lp, P, Gt, Xt, m, n, ldt, dS, s);
-  }
+// dS by sampled products, from X^T and G^T (n x ldt and m x ldt, columns past b zero).
+void launch_sddmm(const hss_matrix* A, int ldt, const uint16_t* Xt, const uint16_t* Gt, float* dS, hipStream_t s) {
+  const SPattern P = s_pattern(A);
+  const int pat = s_pattern_kind(A);
+  int lp = 1;
+  while (lp < 64 && lp * 2 <= (ldt >> 3)) lp *= 2;
+  if (pat == PAT_NM24)
+    launch_sddmm_pat<PAT_NM24>(lp, P, Gt, Xt, A->m, A->n, ldt, dS, s);
+  else if (pat == PAT_CSR16)
+    launch_sddmm_pat<PAT_CSR16>(lp, P, Gt, Xt, A->m, A->n, ldt, dS, s);
+  else
+    launch_sddmm_pat<PAT_CSR32>(lp, P, Gt, Xt, A->m, A->n, ldt, dS, s);
 }
 
 hss_status launch_grad(const hss_matrix* A, int b, const void* X, const void* G, float* dS, float* dU, float* dVt,
@@ -300,7 +245,21 @@ hss_status launch_grad(const hss_matrix* A, int b, const void* X, const void* G,
     launch_gemm_bf16(b, r, m, Gb, m, Ut, p.ldu, Pt, p.ldt, true, part, s);
     launch_gemm_bf16(n, r, b, Xt, p.ldt, Pt, p.ldt, dVt, n, false, part, s);
   }
-  if (want_s) launch_ds(A, b, b, p.ldt, Xt, Gt, reinterpret_cast<float*>(base + p.da), part, dS, s);
+  if (want_s && ds_dense(b)) {
+    float* dA = reinterpret_cast<float*>(base + p.da);
+    launch_gemm_bf16(n, m, b, Xt, p.ldt, Gt, p.ldt, dA, n, false, part, s);
+    const SPattern P = s_pattern(A);
+    const int pat = s_pattern_kind(A);
+    const dim3 grid((unsigned)((m + 3) / 4));
+    if (pat == PAT_NM24)
+      hipLaunchKernelGGL(k_ds_gather<PAT_NM24>, grid, dim3(256), 0, s, P, dA, m, n, dS);
+    else if (pat == PAT_CSR16)
+      hipLaunchKernelGGL(k_ds_gather<PAT_CSR16>, grid, dim3(256), 0, s, P, dA, m, n, dS);
+    else
+      hipLaunchKernelGGL(k_ds_gather<PAT_CSR32>, grid, dim3(256), 0, s, P, dA, m, n, dS);
+  } else if (want_s) {
+    launch_sddmm(A, p.ldt, Xt, Gt, dS, s);
+  }
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 

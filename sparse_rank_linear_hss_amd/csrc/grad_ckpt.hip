@@ -13,18 +13,19 @@
 //
 // Launches: k_ck_prep (X'^T, G^T, U^T and padded rows where a product needs
 // them), one grouped product for T^T and P^T with K split, k_ck_terms (the
-// splits' sums, as terms), one grouped product for dU and dV^T, and dS.
+// splits' sums, as terms), one grouped product for dU and dV^T (with a sum
+// where K is split), and dS: sampled products, or dense tiles of
+// G^T X' of which only S's entries leave the chip (gemm256.hip).
 #include <algorithm>
 
+#include "gemm256.h"
 #include "mm_group.h"
 #include "mx_common.h"
 
 namespace hss {
 
-void launch_ds(const hss_matrix* A, int b, int kb, int ldt, const uint16_t* Xt, const uint16_t* Gt, float* dA,
-               float* part, float* dS, hipStream_t s);
-bool ds_dense(int b);
-size_t gemm_bf16x2_part_bytes(int M, int N, int K1, int K2, int64_t ldc);
+// grad.hip
+void launch_sddmm(const hss_matrix* A, int ldt, const uint16_t* Xt, const uint16_t* Gt, float* dS, hipStream_t s);
 
 static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 static int round32(int x) { return (x + 31) & ~31; }
@@ -157,20 +158,61 @@ __global__ __launch_bounds__(256) void k_ck_terms(CkTerms a) {
   }
 }
 
+// dst[e] = the splits' partial products of it, added in order.
+struct CkSum {
+  const float* src[2];
+  float* dst[2];
+  int64_t size[2];
+  int splits[2];
+  int count;
+};
+
+__global__ __launch_bounds__(256) void k_ck_sum(CkSum a) {
+  const int64_t total = a.size[0] + a.size[1];
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    const int which = e >= a.size[0];
+    const int64_t q = which ? e - a.size[0] : e;
+    float v = 0.f;
+#pragma unroll 4
+    for (int z = 0; z < a.splits[which]; ++z) v += a.src[which][z * a.size[which] + q];
+    a.dst[which][q] = v;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Workspace
 // ---------------------------------------------------------------------------
 struct CkPlan {
-  int ldt, np, mp, zt, zp;  // padded sizes; K splits of T and P
-  size_t xb, xt, gt, gb, vt, ut, tf, pf, t3, p3, da, part, total;
+  int ldt, np, mp, zt, zp, zo;  // padded sizes; K splits of T, of P and of dU and dV
+  size_t xb, xt, gt, gb, vt, ut, tf, pf, t3, p3, o, tptr, total;
 };
 
+// dS by dense tiles of G^T X' (k_gemm256) or by sampled products (k_sddmm):
+// the less of the two estimates, in us, unless HSS_OPT_GRAD_DS_ROUTE forces
+// one.  Both were fitted to sampled / dense measurements: 8192^2 3 % of S, 128
+// tokens 47 / 61, 256 90 / 72, 512 175 / 97, 1024 444 / 147; 4096^2 3 %, 128
+// 20 / 21, 512 70 / 35; 4096^2 0.5 %, 512 26 / 32, 1024 32 / 43.
+static bool dense_ds(const hss_matrix* A, int b) {
+  const int forced = option(HSS_OPT_GRAD_DS_ROUTE);
+  if (forced) return forced == 2;
+  const double stored = A->fmt == HSS_FMT_2OF4 ? 0.5 * A->m * A->n : (double)A->nnz;
+  const int64_t tiles = (int64_t)((A->m + 255) / 256) * ((A->n + 255) / 256);
+  return 8 + 0.17e-6 * stored * b > 10 + (double)((tiles + 255) / 256) * (0.0225 * b + 10);
+}
+
 static constexpr int kCkBlocks = 512;  // blocks of the T and P launch
+
+// K splits of the products for dU and dV^T together (one launch): none where
+// their tiles or a short K leave nothing to gain from it.
+static int mm_splits_pair(int r, int m, int n, int K) {
+  const int tiles = ((r + 127) / 128) * ((m + 127) / 128 + (n + 127) / 128), stages = (K + 63) / 64;
+  return std::max(1, std::min(512 / tiles, stages / 24));
+}
 
 static CkPlan plan_ck(const hss_matrix* A, int b) {
   CkPlan p;
   const int m = A->m, n = A->n, r = A->r;
-  p.ldt = round32(b);
+  p.ldt = dense_ds(A, b) ? (b + 63) & ~63 : round32(b);  // whole stages of k_gemm256
   p.np = round32(n);
   p.mp = round32(m);
   p.zt = r > 0 ? mm_splits(r, b, p.np, kCkBlocks / 2) : 0;
@@ -187,8 +229,9 @@ static CkPlan plan_ck(const hss_matrix* A, int b) {
   p.pf = take((size_t)p.zp * r * p.ldt * 4);
   p.t3 = take((size_t)r * p.ldt * 6);
   p.p3 = take((size_t)r * p.ldt * 6);
-  p.da = take(ds_dense(b) ? (size_t)m * n * 4 : 0);
-  p.part = take(ds_dense(b) ? gemm_bf16x2_part_bytes(n, m, p.ldt, 0, n) : 0);
+  p.zo = r > 0 ? mm_splits_pair(r, m, n, 3 * p.ldt) : 1;
+  p.o = take(p.zo > 1 ? (size_t)p.zo * r * (m + n) * 4 : 0);
+  p.tptr = take(dense_ds(A, b) ? gemm256_ds_bytes(A) : 0);
   p.total = off;
   return p;
 }
@@ -240,19 +283,33 @@ hss_status launch_grad_ckpt(const hss_matrix* A, int b, const void* codes, const
     const int64_t work = (int64_t)t.count * r * (ldt / 4);
     hipLaunchKernelGGL(k_ck_terms, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 4096)), dim3(256), 0, s, t);
     MmProblem o[2] = {};
+    CkSum sum = {};
     k = 0;
+    size_t at = p.o;
     auto gradient = [&](size_t terms, size_t rows, int count, float* out, int64_t ldc, int trans) {
+      const int64_t size = (int64_t)r * count;
       o[k].A = u16(terms); o[k].lda = 3 * ldt; o[k].M = r;
       o[k].B = u16(rows); o[k].ldb = ldt; o[k].N = count; o[k].wrap_b = ldt;
       o[k].K = 3 * ldt;
-      o[k].C = out; o[k].ldc = ldc; o[k].trans = trans;
-      ++k;
+      o[k].C = p.zo > 1 ? f32(at) : out; o[k].ldc = ldc; o[k].trans = trans;
+      o[k].splits = p.zo; o[k].zstride = size;
+      sum.src[k] = f32(at); sum.dst[k] = out; sum.size[k] = size; sum.splits[k] = mm_actual_splits(3 * ldt, p.zo);
+      sum.count = ++k;
+      at += (size_t)p.zo * size * 4;
     };
     if (want_u) gradient(p.t3, p.gt, m, dU, r, 1);
     if (want_v) gradient(p.p3, p.xt, n, dVt, n, 0);
     launch_mm_group(o, k, s);
+    if (p.zo > 1)
+      hipLaunchKernelGGL(k_ck_sum, dim3((unsigned)std::min<int64_t>((sum.size[0] + sum.size[1] + 255) / 256, 4096)),
+                         dim3(256), 0, s, sum);
   }
-  if (want_s) launch_ds(A, b, ldt, ldt, u16(p.xt), u16(p.gt), f32(p.da), f32(p.part), dS, s);
+  if (want_s) {
+    if (dense_ds(A, b))
+      launch_gemm256_ds(A, ldt, u16(p.gt), u16(p.xt), ldt, dS, reinterpret_cast<int32_t*>(base + p.tptr), s);
+    else
+      launch_sddmm(A, ldt, u16(p.xt), u16(p.gt), dS, s);
+  }
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 

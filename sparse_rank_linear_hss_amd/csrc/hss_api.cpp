@@ -486,7 +486,7 @@ hss_status hss_mx_dequantize(int32_t fmt, int32_t dt, int32_t rows, int32_t cols
 static hss_status check_grad_ckpt(const hss_matrix* A, int32_t b) {
   const hss_status st = check_grad(A, b);
   if (st != HSS_OK) return st;
-  const int64_t bp = up32(b), mx = std::max(A->m, A->n), wide = std::max(mx, bp);
+  const int64_t bp = up64(b), mx = std::max(A->m, A->n), wide = std::max(mx, bp);
   if (up32(mx) * bp * 2 >= kLimit || 3 * up32(A->r) * wide >= kLimit) return HSS_ERR_UNSUPPORTED;
   return HSS_OK;
 }

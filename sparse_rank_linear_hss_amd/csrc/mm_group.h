@@ -23,6 +23,8 @@ struct MmProblem {
 
 // K splits that give about `target` blocks (at least two K stages each).
 int mm_splits(int M, int N, int K, int target);
+// The splits that a request for `splits` of K gives (whole K stages, none empty).
+int mm_actual_splits(int K, int splits);
 void launch_mm_group(const MmProblem* p, int count, hipStream_t s);
 
 }  // namespace hss

@@ -48,29 +48,31 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_mm(MmArgs args) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  u32x4 ra[AV], rb[BV];
+  struct Regs {
+    u32x4 a[AV], b[BV];
+  };
   const int c = t & 7, r0 = t >> 3;  // chunk and first row of this thread's loads
-  auto load = [&](int s) {
-    const int k = s * kMmK + 8 * c;
-    const bool in = k < p.K;
+  auto load = [&](int s, Regs& r) {
+    const int k = min(s * kMmK + 8 * c, p.K - 8);  // past the end: a valid chunk, stored as zeros
     int ka = k, kb = k;
     ka -= ka >= 2 * p.wrap_a ? 2 * p.wrap_a : (ka >= p.wrap_a ? p.wrap_a : 0);
     kb -= kb >= 2 * p.wrap_b ? 2 * p.wrap_b : (kb >= p.wrap_b ? p.wrap_b : 0);
+#pragma unroll
+    for (int i = 0; i < AV; ++i)
+      r.a[i] = *reinterpret_cast<const u32x4*>(p.A + (int64_t)min(m0 + r0 + 32 * i, p.M - 1) * p.lda + ka);
+#pragma unroll
+    for (int i = 0; i < BV; ++i)
+      r.b[i] = *reinterpret_cast<const u32x4*>(p.B + (int64_t)min(n0 + r0 + 32 * i, p.N - 1) * p.ldb + kb);
+  };
+  auto store = [&](int s, uint16_t* buf, const Regs& r) {
+    const bool in = s * kMmK + 8 * c < p.K;
     const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < AV; ++i)
-      ra[i] = in ? *reinterpret_cast<const u32x4*>(p.A + (int64_t)min(m0 + r0 + 32 * i, p.M - 1) * p.lda + ka) : zero;
+      *reinterpret_cast<u32x4*>(buf + (r0 + 32 * i) * kMmK + 8 * mm_slot(r0 + 32 * i, c)) = in ? r.a[i] : zero;
 #pragma unroll
     for (int i = 0; i < BV; ++i)
-      rb[i] = in ? *reinterpret_cast<const u32x4*>(p.B + (int64_t)min(n0 + r0 + 32 * i, p.N - 1) * p.ldb + kb) : zero;
-  };
-  auto store = [&](uint16_t* buf) {
-#pragma unroll
-    for (int i = 0; i < AV; ++i)
-      *reinterpret_cast<u32x4*>(buf + (r0 + 32 * i) * kMmK + 8 * mm_slot(r0 + 32 * i, c)) = ra[i];
-#pragma unroll
-    for (int i = 0; i < BV; ++i)
-      *reinterpret_cast<u32x4*>(buf + (BM + r0 + 32 * i) * kMmK + 8 * mm_slot(r0 + 32 * i, c)) = rb[i];
+      *reinterpret_cast<u32x4*>(buf + (BM + r0 + 32 * i) * kMmK + 8 * mm_slot(r0 + 32 * i, c)) = in ? r.b[i] : zero;
   };
   const int wm = (w >> 1) * (BM / 2), wn = (w & 1) * 64;
   auto compute = [&](const uint16_t* buf) {
@@ -94,17 +96,27 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_mm(MmArgs args) {
     }
   };
   if (s0 < s1) {
-    load(s0);
-    store(lds[0]);
-    if (s0 + 1 < s1) load(s0 + 1);
+    Regs ra, rb;
+    load(s0, ra);
+    load(min(s0 + 1, s1 - 1), rb);
+    store(s0, lds[0], ra);
     __syncthreads();
-    for (int s = s0; s < s1; ++s) {
-      const int odd = (s - s0) & 1;
-      compute(lds[odd]);
-      if (s + 1 < s1) store(lds[odd ^ 1]);
-      if (s + 2 < s1) load(s + 2);
+    // pairs of stages, then an odd last one: with an exit from the middle the
+    // compiler moves the register sets about, and waits for their loads
+    int s = s0;
+    for (; s + 1 < s1; s += 2) {
+      load(min(s + 2, s1 - 1), ra);
+      __builtin_amdgcn_sched_barrier(0);  // the loads first: the compiler would sink them
+      compute(lds[0]);
+      store(s + 1, lds[1], rb);
+      __syncthreads();
+      load(min(s + 3, s1 - 1), rb);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(lds[1]);
+      store(min(s + 2, s1 - 1), lds[0], ra);
       __syncthreads();
     }
+    if (s < s1) compute(lds[0]);
   }
   // lane holds rows 4 q + e of column lane % 16 of each block
   float* C = p.C + (int64_t)z * p.zstride;
@@ -132,6 +144,11 @@ int mm_splits(int M, int N, int K, int target) {
   return (stages + per - 1) / per;
 }
 
+int mm_actual_splits(int K, int splits) {
+  const int stages = (K + kMmK - 1) / kMmK, per = (stages + splits - 1) / splits;
+  return (stages + per - 1) / per;
+}
+
 void launch_mm_group(const MmProblem* p, int count, hipStream_t s) {
   MmArgs a = {};
   int bm = 64, blocks = 0;
@@ -141,8 +158,8 @@ void launch_mm_group(const MmProblem* p, int count, hipStream_t s) {
     q = p[i];
     if (q.wrap_a <= 0) q.wrap_a = q.K;
     if (q.wrap_b <= 0) q.wrap_b = q.K;
-    if (q.splits < 1) q.splits = 1;
     const int stages = (q.K + kMmK - 1) / kMmK;
+    q.splits = mm_actual_splits(q.K, std::max(q.splits, 1));
     q.stages_per_split = (stages + q.splits - 1) / q.splits;
     q.tiles_n = (q.N + kMmN - 1) / kMmN;
     q.blocks = q.tiles_n * q.splits * ((q.M + bm - 1) / bm);

@@ -72,6 +72,7 @@ __global__ __launch_bounds__(256) void k_mx_densify(const uint8_t* __restrict__ 
   if (row >= m) return;  // no block-wide barrier below
   const int ng = mx_groups(n);
   uint16_t* L = seg[w];
+  put_u(U, row, r, rp, W + (int64_t)row * ldw + np);
   const int p0 = row_ptr[row], p1 = row_ptr[row + 1];
   for (int c0 = 0; c0 < np; c0 += kMxSeg) {
     const int len = min(kMxSeg, np - c0);  // a multiple of 32
@@ -97,7 +98,6 @@ __global__ __launch_bounds__(256) void k_mx_densify(const uint8_t* __restrict__ 
       *reinterpret_cast<u32x4*>(W + (int64_t)row * ldw + c0 + j) = *reinterpret_cast<const u32x4*>(L + j);
     asm volatile("" ::: "memory");
   }
-  put_u(U, row, r, rp, W + (int64_t)row * ldw + np);
 }
 
 // W' = D^T, m x np from the stored n x m codes: tiles of 64 stored rows (W'
