@@ -200,14 +200,11 @@ static bool dense_ds(const hss_matrix* A, int b) {
   return 8 + 0.17e-6 * stored * b > 10 + (double)((tiles + 255) / 256) * (0.0225 * b + 10);
 }
 
-static constexpr int kCkBlocks = 512;  // blocks of the T and P launch
+static constexpr int kCkBlocks = 256;  // blocks of the T and P launch
 
-// K splits of the products for dU and dV^T together (one launch): none where
-// their tiles or a short K leave nothing to gain from it.
-static int mm_splits_pair(int r, int m, int n, int K) {
-  const int tiles = ((r + 127) / 128) * ((m + 127) / 128 + (n + 127) / 128), stages = (K + 63) / 64;
-  return std::max(1, std::min(512 / tiles, stages / 24));
-}
+// K splits of the products for dU and dV^T (one launch): the three terms,
+// where K is long enough for the sum of their partial products to pay.
+static int uv_splits(int ldt) { return ldt >= 1024 ? 3 : 1; }
 
 static CkPlan plan_ck(const hss_matrix* A, int b) {
   CkPlan p;
@@ -229,7 +226,7 @@ static CkPlan plan_ck(const hss_matrix* A, int b) {
   p.pf = take((size_t)p.zp * r * p.ldt * 4);
   p.t3 = take((size_t)r * p.ldt * 6);
   p.p3 = take((size_t)r * p.ldt * 6);
-  p.zo = r > 0 ? mm_splits_pair(r, m, n, 3 * p.ldt) : 1;
+  p.zo = r > 0 ? uv_splits(p.ldt) : 1;
   p.o = take(p.zo > 1 ? (size_t)p.zo * r * (m + n) * 4 : 0);
   p.tptr = take(dense_ds(A, b) ? gemm256_ds_bytes(A) : 0);
   p.total = off;

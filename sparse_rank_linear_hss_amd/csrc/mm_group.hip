@@ -120,18 +120,19 @@ __global__ __launch_bounds__(256, BM == 64 ? 3 : 2) void k_mm(MmArgs args) {
   }
   // lane holds rows 4 q + e of column lane % 16 of each block
   float* C = p.C + (int64_t)z * p.zstride;
+  const int M = p.M, N = p.N;
+  const int64_t sm = p.trans ? 1 : p.ldc, sn = p.trans ? p.ldc : 1;
+  float* at = C + (m0 + wm + 4 * q) * sm + (n0 + wn + (lane & 15)) * sn;
+  const int mleft = M - (m0 + wm + 4 * q), nleft = N - (n0 + wn + (lane & 15));
 #pragma unroll
-  for (int j = 0; j < FN; ++j) {
-    const int n = n0 + wn + 16 * j + (lane & 15);
-    if (n >= p.N) continue;
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int m = m0 + wm + 16 * i + 4 * q;
+    for (int e = 0; e < 4; ++e) {
+      float* row = at + (16 * i + e) * sm;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (m + e < p.M) C[p.trans ? (int64_t)n * p.ldc + m + e : (int64_t)(m + e) * p.ldc + n] = acc[i][j][e];
+      for (int j = 0; j < FN; ++j)
+        if (16 * i + e < mleft && 16 * j < nleft) row[16 * j * sn] = acc[i][j][e];
     }
-  }
 }
 
 static int mm_tile_m(int M) { return M > 64 ? 128 : 64; }

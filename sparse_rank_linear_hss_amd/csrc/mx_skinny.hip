@@ -50,18 +50,19 @@ __global__ __launch_bounds__(256) void k_mx_prep(MxPrep a) {
   const uint16_t* __restrict__ X = a.X;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6, b = a.b, n = a.n;
   if ((int)blockIdx.x >= a.tb) {
-    const int64_t first = ((int64_t)blockIdx.x - a.tb) * 256 + t, step = (int64_t)(a.xb) * 256;
-    const int per = a.np >> 3;
-    for (int64_t e = first; a.Xp && e < (int64_t)b * per; e += step) {
-      const int c = (int)(e / per), k = (int)(e - (int64_t)c * per) * 8;
+    // item counts are below 2^28 and a step below 2^18: no wrap
+    const uint32_t first = (blockIdx.x - (uint32_t)a.tb) * 256u + t, step = (uint32_t)a.xb * 256u;
+    const uint32_t per = (uint32_t)a.np >> 3, peru = (uint32_t)a.rp >> 3;
+    for (uint32_t e = first; a.Xp && e < (uint32_t)b * per; e += step) {
+      const int c = (int)(e / per), k = (int)(e - (uint32_t)c * per) * 8;
       *reinterpret_cast<u32x4*>(a.Xp + (int64_t)c * a.np + k) = load_row8(X + (int64_t)c * n, k, n);
     }
-    for (int64_t e = first; a.Up && e < (int64_t)a.m * (a.rp >> 3); e += step) {
-      const int i = (int)(e / (a.rp >> 3)), l = (int)(e - (int64_t)i * (a.rp >> 3)) * 8;
+    for (uint32_t e = first; a.Up && e < (uint32_t)a.m * peru; e += step) {
+      const int i = (int)(e / peru), l = (int)(e - (uint32_t)i * peru) * 8;
       *reinterpret_cast<u32x4*>(a.Up + (int64_t)i * a.rp + l) = load_row8(a.U + (int64_t)i * a.r, l, a.r);
     }
-    for (int64_t e = first; a.Xt && e < (int64_t)n * (a.ldt >> 3); e += step) {
-      const int c0 = (int)(e / n) * 8, j = (int)(e - (int64_t)(c0 >> 3) * n);
+    for (uint32_t e = first; a.Xt && e < (uint32_t)n * (uint32_t)(a.ldt >> 3); e += step) {
+      const int c0 = (int)(e / (uint32_t)n) * 8, j = (int)(e - (uint32_t)(c0 >> 3) * (uint32_t)n);
       u32x4 v;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -191,32 +192,40 @@ __device__ __forceinline__ void s_rows(const SkinnyArgs& a, const COL* __restric
 // columns 8 h .. 8 h + 7; the lanes of a half are then added up in a fixed
 // tree, in which they first share out the eight columns: column 8 h + k ends
 // in the lanes with lane % 2 = h and (lane / 2) % 8 = k.
+// The first four entries come in j, v (s_request16), requested before the codes.
 template <int LG, typename COL>
-__device__ __forceinline__ float s_rows16(const SkinnyArgs& a, const COL* __restrict__ col, int p0, int p1) {
+__device__ __forceinline__ void s_request16(const SkinnyArgs& a, const COL* __restrict__ col, int p, int p1,
+                                            int (&j)[4], uint32_t (&v)[4]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int pp = max(min(p + u * (LG / 2), p1 - 1), 0);  // an empty S has no call here
+    j[u] = (int)col[pp];
+    v[u] = a.vals[pp];
+  }
+}
+
+template <int LG, typename COL>
+__device__ __forceinline__ float s_rows16(const SkinnyArgs& a, const COL* __restrict__ col, int p0, int p1, int (&j)[4],
+                                          uint32_t (&v)[4]) {
   const int lane = lane_id(), sl = lane % LG, h = lane & 1;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int p = p0 + (sl >> 1); p < p1; p += 2 * LG) {
-    int j[4];
-    float v[4];
     u32x4 x[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int pp = min(p + u * (LG / 2), p1 - 1);
-      j[u] = (int)col[pp];
-      v[u] = bf16lo(a.vals[pp]);
-    }
+    float f[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const bool ok = p + u * (LG / 2) < p1 && (unsigned)j[u] < (unsigned)a.n;
       x[u] = *reinterpret_cast<const u32x4*>(a.Xt + (int64_t)(ok ? j[u] : 0) * kSkCols + 8 * h);
-      if (!ok) v[u] = 0.f, x[u] = u32x4{0u, 0u, 0u, 0u};
+      f[u] = bf16lo(v[u]);
+      if (!ok) f[u] = 0.f, x[u] = u32x4{0u, 0u, 0u, 0u};
     }
+    if (p + 2 * LG < p1) s_request16<LG>(a, col, p + 2 * LG, p1, j, v);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        s[2 * k] = fmaf(v[u], bf16lo(x[u][k]), s[2 * k]);
-        s[2 * k + 1] = fmaf(v[u], bf16hi(x[u][k]), s[2 * k + 1]);
+        s[2 * k] = fmaf(f[u], bf16lo(x[u][k]), s[2 * k]);
+        s[2 * k + 1] = fmaf(f[u], bf16hi(x[u][k]), s[2 * k + 1]);
       }
   }
   // lane bits 1..3 pick the column's bits 0..2
@@ -283,6 +292,12 @@ __global__ __launch_bounds__(64 * WV, 4) void k_mx_skinny(SkinnyArgs a) {
     p0 = a.row_ptr[row0 + w * (16 / WV) + lane / LG];
     p1 = a.row_ptr[row0 + w * (16 / WV) + lane / LG + 1];
   }
+  int sj[4] = {0, 0, 0, 0};
+  uint32_t sv[4] = {0u, 0u, 0u, 0u};
+  if (a.has_s && a.b > kSkGather) {
+    if (a.col16) s_request16<LG>(a, static_cast<const uint16_t*>(a.col), p0 + (lane % LG >> 1), p1, sj, sv);
+    else s_request16<LG>(a, static_cast<const int32_t*>(a.col), p0 + (lane % LG >> 1), p1, sj, sv);
+  }
   if (w < nfull) issue(w);
 
   const int ldt = a.rp + 8;  // rows 16 bytes apart modulo the banks
@@ -314,7 +329,7 @@ __global__ __launch_bounds__(64 * WV, 4) void k_mx_skinny(SkinnyArgs a) {
       for (int c = 0; c < kSkGather; ++c)
         if (lane % LG == c) sred[c * 16 + i] = s[c];
     } else {
-      const float s = a.col16 ? s_rows16<LG>(a, c16, p0, p1) : s_rows16<LG>(a, c32, p0, p1);
+      const float s = a.col16 ? s_rows16<LG>(a, c16, p0, p1, sj, sv) : s_rows16<LG>(a, c32, p0, p1, sj, sv);
       if (lane % LG < 16) sred[(8 * (lane & 1) + ((lane >> 1) & 7)) * 16 + i] = s;
     }
   }
