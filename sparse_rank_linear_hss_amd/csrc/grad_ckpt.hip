@@ -8,8 +8,8 @@
 //
 // T and P are sums of n (m) products held in fp32.  The matrix cores take
 // bf16, so each is split into three bf16 terms (24 significant bits) and the
-// products with G and X' are summed over the terms, K = 3 b with the other
-// operand repeating: the gradients are as exact as fp32 products would be.
+// products with G and X' are summed over the terms: the gradients are as exact
+// as fp32 products would be.
 //
 // Launches: k_ck_prep (X'^T, G^T, U^T and padded rows where a product needs
 // them), one grouped product for T^T and P^T with K split, k_ck_terms (the
@@ -202,9 +202,12 @@ static bool dense_ds(const hss_matrix* A, int b) {
 
 static constexpr int kCkBlocks = 256;  // blocks of the T and P launch
 
-// K splits of the products for dU and dV^T (one launch): the three terms,
-// where K is long enough for the sum of their partial products to pay.
-static int uv_splits(int ldt) { return ldt >= 1024 ? 3 : 1; }
+// K splits of the products for dU and dV^T (one launch): enough for a block
+// per CU, where K is long enough for the sum of the partial products to pay.
+static int uv_splits(int r, int m, int n, int ldt) {
+  const int tiles = (r + 127) / 128 * ((m + 127) / 128 + (n + 127) / 128);
+  return std::max(1, std::min((255 + tiles) / tiles, ldt / 512));
+}
 
 static CkPlan plan_ck(const hss_matrix* A, int b) {
   CkPlan p;
@@ -226,7 +229,7 @@ static CkPlan plan_ck(const hss_matrix* A, int b) {
   p.pf = take((size_t)p.zp * r * p.ldt * 4);
   p.t3 = take((size_t)r * p.ldt * 6);
   p.p3 = take((size_t)r * p.ldt * 6);
-  p.zo = r > 0 ? uv_splits(p.ldt) : 1;
+  p.zo = r > 0 ? uv_splits(r, m, n, p.ldt) : 1;
   p.o = take(p.zo > 1 ? (size_t)p.zo * r * (m + n) * 4 : 0);
   p.tptr = take(dense_ds(A, b) ? gemm256_ds_bytes(A) : 0);
   p.total = off;
@@ -276,7 +279,7 @@ hss_status launch_grad_ckpt(const hss_matrix* A, int b, const void* codes, const
     };
     if (want_u) product(copy_v ? u16(p.vt) : static_cast<const uint16_t*>(A->Vt), u16(p.xb), p.np, p.zt, p.tf, p.t3);
     if (want_v) product(u16(p.ut), copy_g ? u16(p.gb) : static_cast<const uint16_t*>(G), p.mp, p.zp, p.pf, p.p3);
-    launch_mm_group(q, k, s);
+    launch_mm_group(q, k, false, s);
     const int64_t work = (int64_t)t.count * r * (ldt / 4);
     hipLaunchKernelGGL(k_ck_terms, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 4096)), dim3(256), 0, s, t);
     MmProblem o[2] = {};
@@ -286,17 +289,16 @@ hss_status launch_grad_ckpt(const hss_matrix* A, int b, const void* codes, const
     auto gradient = [&](size_t terms, size_t rows, int count, float* out, int64_t ldc, int trans) {
       const int64_t size = (int64_t)r * count;
       o[k].A = u16(terms); o[k].lda = 3 * ldt; o[k].M = r;
-      o[k].B = u16(rows); o[k].ldb = ldt; o[k].N = count; o[k].wrap_b = ldt;
-      o[k].K = 3 * ldt;
+      o[k].B = u16(rows); o[k].ldb = ldt; o[k].N = count; o[k].K = ldt;
       o[k].C = p.zo > 1 ? f32(at) : out; o[k].ldc = ldc; o[k].trans = trans;
       o[k].splits = p.zo; o[k].zstride = size;
-      sum.src[k] = f32(at); sum.dst[k] = out; sum.size[k] = size; sum.splits[k] = mm_actual_splits(3 * ldt, p.zo);
+      sum.src[k] = f32(at); sum.dst[k] = out; sum.size[k] = size; sum.splits[k] = mm_actual_splits(ldt, p.zo);
       sum.count = ++k;
       at += (size_t)p.zo * size * 4;
     };
     if (want_u) gradient(p.t3, p.gt, m, dU, r, 1);
     if (want_v) gradient(p.p3, p.xt, n, dVt, n, 0);
-    launch_mm_group(o, k, s);
+    launch_mm_group(o, k, true, s);
     if (p.zo > 1)
       hipLaunchKernelGGL(k_ck_sum, dim3((unsigned)std::min<int64_t>((sum.size[0] + sum.size[1] + 255) / 256, 4096)),
                          dim3(256), 0, s, sum);

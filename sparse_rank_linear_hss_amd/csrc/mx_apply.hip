@@ -259,7 +259,7 @@ hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, v
     q.K = np;
     q.C = f32(p.tp); q.ldc = rp; q.trans = 1; q.zstride = (int64_t)b * rp;
     q.splits = p.zt;
-    launch_mm_group(&q, 1, s);
+    launch_mm_group(&q, 1, false, s);
     launch_mx_tsum(f32(p.tp), p.zt, b, r, rp, u16(p.tb), s);
   }
   // measured against k_gemm_h from 300 columns on: 5 - 20 % faster throughout
