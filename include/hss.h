@@ -308,7 +308,9 @@ hss_status hss_apply_workspace_size(const hss_matrix* A, int32_t b, size_t* byte
  *     batch sizes, may share one workspace if they are ORDERED (one stream,
  *     or events between streams); two calls that overlap in time must use
  *     different workspaces -- overlapping calls on one workspace can make
- *     both return wrong values with no error.  The epoch wraps after 2^32 - 1
+ *     both return wrong values with no error.  HSS_MX4 matrices keep no state
+ *     in a workspace and leave dense data in it: one that served them is
+ *     initialised again before it serves other matrices.  The epoch wraps after 2^32 - 1
  *     calls and skips the tag that a zero-filled word carries.
  * Execution: bf16 2:4 with 3 <= b <= 64 (n % 128 == 0; nm_values, nm_meta
  * and X 16-byte aligned) runs on the sparse matrix cores: S's stored values
@@ -353,7 +355,8 @@ hss_status hss_apply(const hss_matrix* A, int32_t b, const void* X, void* Y, voi
  * hss_apply, with the workspace replaced by a scratch array that the library
  * holds in each GPU's memory: hss_noalloc_scratch_bytes() bytes (16 MiB),
  * kept until the process ends, and cleared by the first call on each device
- * (on that call's stream).  The call allocates and frees nothing.
+ * (on that call's stream); HSS_MX4 matrices have one of the same size of
+ * their own.  The call allocates and frees nothing.
  * HSS_ERR_WORKSPACE when the route this call takes needs more workspace
  * than the scratch holds (e.g. a large CSR layer densified for the matrix
  * cores at prefill batches): use hss_apply with a workspace of

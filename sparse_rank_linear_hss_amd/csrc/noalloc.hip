@@ -11,6 +11,10 @@
 // them to start from zeros.  Later calls keep the state the previous call
 // left, as the decode kernel expects.  Every call on one GPU shares the array:
 // calls that overlap in time on one GPU race and may return wrong values.
+//
+// HSS_MX4 matrices have a second array of the same size: their scratch holds
+// dense data and keeps no state, and a word of it left among the decode
+// kernel's T words could carry the tag of a later call.
 #include <mutex>
 
 #include "hss_internal.h"
@@ -21,34 +25,39 @@ static constexpr size_t kScratchBytes = (size_t)16 << 20;  // 16 MiB per GPU
 static constexpr int kMaxDevices = 64;
 
 static __device__ __align__(256) unsigned char scratch[kScratchBytes];
+static __device__ __align__(256) unsigned char scratch_mx[kScratchBytes];
 
 namespace {
 std::mutex g_mu;
-void* g_ptr[kMaxDevices] = {};  // device address of `scratch` on each device, once looked up
+// device addresses of `scratch` and `scratch_mx` on each device, once looked up
+void* g_ptr[kMaxDevices] = {};
+void* g_ptr_mx[kMaxDevices] = {};
 
 // The device address of this device's scratch; clears it on the first call
-// (on `stream`).  nullptr (and *st set) if the lookup or the clear fails.
-void* device_scratch(hipStream_t stream, hss_status* st) {
+// (on `stream`; the one for HSS_MX4 needs none).  nullptr (and *st set) if the lookup or the clear fails.
+void* device_scratch(bool mx, hipStream_t stream, hss_status* st) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) {
     *st = HSS_ERR_HIP;
     return nullptr;
   }
   std::lock_guard<std::mutex> lock(g_mu);
-  if (!g_ptr[dev]) {
+  void** slot = mx ? &g_ptr_mx[dev] : &g_ptr[dev];
+  if (!*slot) {
     void* p = nullptr;
-    if (hipGetSymbolAddress(&p, HIP_SYMBOL(scratch)) != hipSuccess || !p) {
+    const hipError_t e = mx ? hipGetSymbolAddress(&p, HIP_SYMBOL(scratch_mx)) : hipGetSymbolAddress(&p, HIP_SYMBOL(scratch));
+    if (e != hipSuccess || !p) {
       *st = HSS_ERR_HIP;
       return nullptr;
     }
-    if (launch_zero_fill(p, kScratchBytes, stream) != HSS_OK) {
+    if (!mx && launch_zero_fill(p, kScratchBytes, stream) != HSS_OK) {
       *st = HSS_ERR_HIP;
       return nullptr;
     }
-    g_ptr[dev] = p;
+    *slot = p;
   }
   *st = HSS_OK;
-  return g_ptr[dev];
+  return *slot;
 }
 }  // namespace
 
@@ -62,7 +71,7 @@ extern "C" hss_status hss_apply_noalloc(const hss_matrix* A, int32_t b, const vo
   if (st != HSS_OK) return st;
   if (hss::apply_route_ws_bytes(A, b, X) > hss::kScratchBytes) return HSS_ERR_WORKSPACE;
   hss_status sst = HSS_OK;
-  void* ws = hss::device_scratch(stream, &sst);
+  void* ws = hss::device_scratch((A->flags & HSS_MX4) != 0, stream, &sst);
   if (!ws) return sst;
   return hss::launch_apply(A, b, X, Y, ws, stream);
 }
