@@ -84,8 +84,10 @@ int hss_version(void);
  *       matrix cores; forces a bf16 call with b >= 2 onto that route where
  *       the route supports the matrix.  Workspace sizes cover every route.
  *   HSS_OPT_GRAD_DS_ROUTE (HSS_GRAD_DS_ROUTE = sparse | dense): 0 = by batch
- *       size (default), 1 = sampled product, 2 = dense G^T X then gather.
- *       Query hss_grad_workspace_size with the same setting.
+ *       size (default; hss_grad_ckpt: by estimated time), 1 = sampled product,
+ *       2 = dense G^T X, of which S's entries are kept.  Query
+ *       hss_grad_workspace_size (hss_grad_ckpt_workspace_size) with the same
+ *       setting.
  *   HSS_OPT_DECODE_SPIN   (HSS_DECODE_SPIN = count): polls of a stale T word
  *       before a block computes that T row itself (default 4096).
  *   HSS_OPT_DECODE_MERGED (HSS_DECODE_MERGED = 0): 1 (default) = T rows
@@ -393,13 +395,13 @@ hss_status hss_apply_workspace_init(void* ws, size_t ws_bytes, hipStream_t strea
  * ONE launch per pass of up to 8 columns instead of G; on the matrix cores
  * the matrices are applied one after another.
  *   1 <= G <= HSS_MAX_GROUP; every A[g] valid for hss_apply with batch b, all
- *   with the same n, dtype and fmt (m, r and the arrays may differ).
+ *   with the same n, dtype, fmt and flags (m, r and the arrays may differ).
  *   Y[g] device outputs, pairwise disjoint and disjoint from X.
  *   ws: at least hss_apply_group_workspace_size() bytes, initialised once
  *   by hss_apply_workspace_init; the same state rules as hss_apply (it may
  *   also serve hss_apply calls).
  * Returns HSS_ERR_INVALID_ARG for: A, X or Y null, G out of range, any matrix
- *   invalid, mismatched n/dtype/fmt, overlapping outputs; HSS_ERR_WORKSPACE for
+ *   invalid, mismatched n/dtype/fmt/flags, overlapping outputs; HSS_ERR_WORKSPACE for
  *   a null or short workspace; HSS_ERR_HIP if a launch fails.
  */
 #define HSS_MAX_GROUP 4

@@ -56,7 +56,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(device) -> int:
     # the handle alone: building a Stream object costs more than a launch
-    index = device.index if isinstance(device, torch.device) else torch.device(device).index
+    device = device if isinstance(device, torch.device) else torch.device(device)
+    if device.type != "cuda":
+        raise ValueError(f"expected a GPU device, got {device}")
+    index = device.index
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
@@ -304,6 +307,8 @@ class HSSMatrix:
                 raise ValueError("one dense part: dq_codes or mx")
             if mx.fmt != "fp4" or (mx.rows, mx.cols) != ((n, m) if mx_t else (m, n)):
                 raise ValueError(f"mx must be an 'fp4' MXTensor, {'n x m' if mx_t else 'm x n'} of the {m} x {n} matrix")
+            if any(t is not None and t.device != mx.device for t in (U, Vt, row_ptr, col_idx, values)):
+                raise ValueError(f"the matrix's tensors must be on mx's device, {mx.device}")
             if row_ptr is None and fmt in ("csr", HSS_FMT_CSR):
                 row_ptr = torch.zeros(int(m) + 1, dtype=torch.int32, device=mx.device)
             self.flags |= HSS_MX4 | (HSS_MX4_T if mx_t else 0)
@@ -410,19 +415,26 @@ def hss_apply_workspace_size(A: HSSMatrix, b: int) -> int:
     return int(out.value)
 
 
+def _same_device(A: HSSMatrix, dev):
+    if A.mx is not None and A.mx.device != dev:
+        raise ValueError(f"the matrix is on {A.mx.device}, the call on {dev}")
+
+
 def hss_apply(A: HSSMatrix, X: torch.Tensor, Y: Optional[torch.Tensor] = None,
               ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y (b x m) = X (b x n) (S + U V^T)^T on the current stream."""
     dev = _dev(X)
     if X.dim() != 2 or X.shape[1] != A.n or not X.is_contiguous() or X.dtype != A.dtype:
         raise ValueError("X must be a contiguous b x n tensor of the matrix dtype")
+    _same_device(A, dev)
     b = X.shape[0]
     if Y is None:
         Y = torch.empty((b, A.m), dtype=A.dtype, device=dev)
-    if ws is None:
-        ws = A.workspace(b, dev)
-    check(lib.hss_apply(ctypes.byref(A.struct), b, _ptr(X), _ptr(Y), _ptr(ws), ws.numel(),
-                        _stream(dev)), "hss_apply")
+    with _on(dev):
+        if ws is None:
+            ws = A.workspace(b, dev)
+        check(lib.hss_apply(ctypes.byref(A.struct), b, _ptr(X), _ptr(Y), _ptr(ws), ws.numel(),
+                            _stream(dev)), "hss_apply")
     return Y
 
 
@@ -435,8 +447,10 @@ def hss_apply_noalloc(A: HSSMatrix, X: torch.Tensor, Y: torch.Tensor) -> torch.T
         raise ValueError("X must be a contiguous b x n tensor of the matrix dtype")
     if Y.shape != (X.shape[0], A.m) or not Y.is_contiguous() or Y.dtype != A.dtype:
         raise ValueError("Y must be a contiguous b x m tensor of the matrix dtype")
-    check(lib.hss_apply_noalloc(ctypes.byref(A.struct), X.shape[0], _ptr(X), _ptr(Y), _stream(dev)),
-          "hss_apply_noalloc")
+    _same_device(A, dev)
+    with _on(dev):
+        check(lib.hss_apply_noalloc(ctypes.byref(A.struct), X.shape[0], _ptr(X), _ptr(Y), _stream(dev)),
+              "hss_apply_noalloc")
     return Y
 
 
@@ -460,16 +474,18 @@ def hss_apply_group(As, X: torch.Tensor, Ys=None, ws: Optional[torch.Tensor] = N
     for A in As:
         if X.dim() != 2 or X.shape[1] != A.n or not X.is_contiguous() or X.dtype != A.dtype:
             raise ValueError("X must be a contiguous b x n tensor of every matrix's dtype")
+        _same_device(A, dev)
     b = X.shape[0]
     if Ys is None:
         Ys = [torch.empty((b, A.m), dtype=A.dtype, device=dev) for A in As]
-    if ws is None:
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("create the workspace before graph capture and pass it as ws=")
-        ws = apply_workspace(hss_apply_group_workspace_size(As, b), dev)
     yp = (ctypes.c_void_p * len(As))(*[_ptr(Y) for Y in Ys])
-    check(lib.hss_apply_group(_group_structs(As), len(As), b, _ptr(X), yp, _ptr(ws), ws.numel(),
-                              _stream(dev)), "hss_apply_group")
+    with _on(dev):
+        if ws is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("create the workspace before graph capture and pass it as ws=")
+            ws = apply_workspace(hss_apply_group_workspace_size(As, b), dev)
+        check(lib.hss_apply_group(_group_structs(As), len(As), b, _ptr(X), yp, _ptr(ws), ws.numel(),
+                                  _stream(dev)), "hss_apply_group")
     return Ys
 
 
@@ -716,6 +732,7 @@ def hss_grad_ckpt(A: HSSMatrix, X: MXTensor, G: torch.Tensor, dS=True, dU=True, 
     dev = _dev(G)
     if X.fmt != "int8" or X.cols != A.n or X.device != dev:
         raise ValueError("X must be an 'int8' MXTensor, b x n, on G's device")
+    _same_device(A, dev)
     b = X.rows
     if G.shape != (b, A.m) or not G.is_contiguous() or G.dtype != A.dtype:
         raise ValueError("G must be a contiguous b x m tensor of the matrix dtype")
@@ -729,6 +746,8 @@ def hss_grad_ckpt(A: HSSMatrix, X: MXTensor, G: torch.Tensor, dS=True, dU=True, 
             raise ValueError("out must hold contiguous float32 tensors 'dS', 'dU', 'dVt' of the gradients' shapes")
     if ws is None:
         ws = grad_ckpt_workspace(A, b, dev)
+    elif ws.device != dev:
+        raise ValueError(f"ws must be on {dev}")
     with _on(dev):
         check(lib.hss_grad_ckpt(ctypes.byref(A.struct), b, X.codes.data_ptr(), X.scales.data_ptr(), G.data_ptr(),
                                 _ptr(out.get("dS")), _ptr(out.get("dU")), _ptr(out.get("dVt")), ws.data_ptr(),

@@ -183,6 +183,7 @@ __global__ __launch_bounds__(256) void k_ck_sum(CkSum a) {
 // Workspace
 // ---------------------------------------------------------------------------
 struct CkPlan {
+  bool dense;  // dense_ds()
   int ldt, np, mp, zt, zp, zo;  // padded sizes; K splits of T, of P and of dU and dV
   size_t xb, xt, gt, gb, vt, ut, tf, pf, t3, p3, o, tptr, total;
 };
@@ -212,7 +213,8 @@ static int uv_splits(int r, int m, int n, int ldt) {
 static CkPlan plan_ck(const hss_matrix* A, int b) {
   CkPlan p;
   const int m = A->m, n = A->n, r = A->r;
-  p.ldt = dense_ds(A, b) ? (b + 63) & ~63 : round32(b);  // whole stages of k_gemm256
+  p.dense = dense_ds(A, b);
+  p.ldt = p.dense ? (b + 63) & ~63 : round32(b);  // whole stages of k_gemm256
   p.np = round32(n);
   p.mp = round32(m);
   p.zt = r > 0 ? mm_splits(r, b, p.np, kCkBlocks / 2) : 0;
@@ -231,7 +233,7 @@ static CkPlan plan_ck(const hss_matrix* A, int b) {
   p.p3 = take((size_t)r * p.ldt * 6);
   p.zo = r > 0 ? uv_splits(r, m, n, p.ldt) : 1;
   p.o = take(p.zo > 1 ? (size_t)p.zo * r * (m + n) * 4 : 0);
-  p.tptr = take(dense_ds(A, b) ? gemm256_ds_bytes(A) : 0);
+  p.tptr = take(p.dense ? gemm256_ds_bytes(A) : 0);
   p.total = off;
   return p;
 }
@@ -304,7 +306,7 @@ hss_status launch_grad_ckpt(const hss_matrix* A, int b, const void* codes, const
                          dim3(256), 0, s, sum);
   }
   if (want_s) {
-    if (dense_ds(A, b))
+    if (p.dense)
       launch_gemm256_ds(A, ldt, u16(p.gt), u16(p.xt), ldt, dS, reinterpret_cast<int32_t*>(base + p.tptr), s);
     else
       launch_sddmm(A, ldt, u16(p.xt), u16(p.gt), dS, s);

@@ -219,3 +219,59 @@ def test_kept_weights_are_not_written(H):
         before = [t.clone() for t in held]
         H.hss_apply(A, X), H.hss_apply(At, G), H.hss_grad_ckpt(A, ck, G)
         assert all(torch.equal(a, b_) for a, b_ in zip(held, before))
+
+
+@pytest.mark.parametrize("b", [1, 8, 200, 300])
+def test_arrays_past_2_gib(H, b):
+    """A dense part whose bf16 copy has more than 2^31 bytes, both directions
+    (beyond 256 columns such a copy is made): a sample of the outputs, the last
+    ones among them, in float64.  S in the last rows."""
+    import torch
+    m, n, r = 33001, 32800, 8
+    g = torch.Generator(device="cuda").manual_seed(b)
+    ng = n // 32
+    codes = torch.randint(0, 256, (m, 16 * ng), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.randint(118, 122, (m, ng), dtype=torch.uint8, device="cuda", generator=g)
+    rp = torch.zeros(m + 1, dtype=torch.int32, device="cuda")
+    rp[-2:] = torch.tensor([2, 5], device="cuda")
+    cols = torch.tensor([0, n - 1, 5, 6, n - 1], device="cuda")
+    srow = torch.tensor([m - 2, m - 2, m - 1, m - 1, m - 1], device="cuda")
+    vals = torch.tensor([0.5, -0.25, 0.75, 1.0, -1.5], device="cuda").bfloat16()
+    for p in range(5):                                            # D kept zero under S
+        at = codes[srow[p], cols[p] // 32 * 16 + cols[p] % 32 // 2]
+        at &= 0xF0 if cols[p] % 2 == 0 else 0x0F
+    U = (0.05 * torch.randn(m, r, device="cuda", generator=g)).bfloat16()
+    Vt = (0.05 * torch.randn(r, n, device="cuda", generator=g)).bfloat16()
+    A = H.HSSMatrix("csr", m, n, torch.bfloat16, U=U, Vt=Vt, row_ptr=rp, col_idx=cols.int(), values=vals, nnz=5,
+                    mx=H.MXTensor("fp4", m, n, codes, scales))
+
+    def values(rows, gs):                                         # D[rows][columns of the groups gs]
+        by = codes.view(m, ng, 16)[rows][:, gs]
+        q = torch.stack((by & 15, by >> 4), -1).flatten(2)
+        ex, frac = ((q >> 1) & 3).double(), (q & 1).double()
+        v = torch.where(ex == 0, 0.5 * frac, (1 + 0.5 * frac) * 2.0 ** (ex - 1)) * (1 - 2 * (q >> 3).double())
+        return (v * 2.0 ** (scales[rows][:, gs].double() - 127)[..., None]).flatten(1)
+
+    for trans in (False, True):
+        M = H.hss_transposed_layer(A) if trans else A
+        X = torch.randn(b, M.n, device="cuda", generator=g).bfloat16()
+        Y = H.hss_apply(M, X)
+        X64 = X.double()
+        if trans:
+            gs = torch.tensor([0, 1, 500, ng - 2, ng - 1], device="cuda")
+            at = (gs[:, None] * 32 + torch.arange(32, device="cuda")).flatten()
+            W = values(torch.arange(m, device="cuda"), gs).t().contiguous()
+            for p in range(5):
+                W[at == cols[p], srow[p]] += vals[p].double()
+            left, right = U.double(), Vt.double()[:, at].contiguous()
+        else:
+            at = torch.cat((torch.arange(0, m, 701, device="cuda"), torch.arange(m - 9, m, device="cuda")))
+            W = values(at, torch.arange(ng, device="cuda"))
+            for p in range(5):
+                W[at == srow[p], cols[p]] += vals[p].double()
+            left, right = Vt.double().t().contiguous(), U.double()[at].t().contiguous()
+        Wt = W.t().contiguous()
+        ref = X64 @ Wt + (X64 @ left) @ right
+        N = X64.abs() @ Wt.abs() + (X64.abs() @ left.abs()) @ right.abs()
+        err = (Y[:, at].double() - ref).abs()
+        assert torch.all(err <= 2.0 ** -8 * ref.abs() + ((2 * M.n + 2 * r + 2) * U24 + 2.0 ** -16) * N)

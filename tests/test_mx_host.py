@@ -202,3 +202,26 @@ def test_binding_checks(hl):
     assert A.nnz == 0 and A.row_ptr.shape == (4,) and hl.hss_apply_workspace_size(A, 5) > 0
     At = hl.HSSMatrix("csr", 33, 3, torch.bfloat16, mx=q, mx_t=True)
     assert At.flags == hl.HSS_MX4 | hl.HSS_MX4_T
+
+
+def test_binding_refuses_other_devices(hl):
+    """A CPU workspace, and a dense part on another device than the rest."""
+    import torch
+    with pytest.raises(ValueError):
+        hl.hss_apply_workspace_init(torch.zeros(4096, dtype=torch.uint8))
+    q = hl.MXTensor.empty("fp4", 3, 33, "cpu")
+    with pytest.raises(ValueError):
+        hl.HSSMatrix("csr", 3, 33, torch.bfloat16, mx=q, U=torch.empty(3, 2, dtype=torch.bfloat16, device="meta"),
+                     Vt=torch.empty(2, 33, dtype=torch.bfloat16, device="meta"))
+
+
+def test_group_takes_one_kind_of_matrix(hl):
+    """HSS_MX4 matrices are grouped among themselves (they leave dense data where
+    others keep state)."""
+    lib, INV = hl._lib.lib, hl._lib.HSS_ERR_INVALID_ARG
+    P = ctypes.POINTER(hl._lib.HssMatrixStruct)
+    out = ctypes.c_size_t()
+    mx, plain = _mx(hl), _mx(hl, flags=0, dq_codes=None, dq_levels=None)
+    for mats, want in (((mx, mx), 0), ((mx, plain), INV), ((plain, mx), INV), ((mx, _mx(hl, flags=48)), INV)):
+        arr = (P * 2)(*[ctypes.pointer(s) for s in mats])
+        assert lib.hss_apply_group_workspace_size(arr, 2, 1, ctypes.byref(out)) == want
