@@ -55,20 +55,25 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device) -> int:
-    # the handle alone: building a Stream object costs more than a launch
     device = device if isinstance(device, torch.device) else torch.device(device)
     if device.type != "cuda":
         raise ValueError(f"expected a GPU device, got {device}")
-    index = device.index
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+    return _raw_stream(torch.cuda.current_device() if device.index is None else device.index)
 
 
-def _on(dev):
-    """dev as the current device (a launch goes to the current device's context)."""
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+# A decode call is bound by its host side (4096 x 4096, one column: the launch
+# itself takes 3.5 us), so the calls below read the handles that torch.cuda's
+# own functions wrap, and make X's device current only where it is not: a launch
+# goes to the current device.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-_HERE = contextlib.nullcontext()
+def _index(t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensor must be on a GPU device")
+    return index
 
 
 def _dev(t: torch.Tensor):
@@ -201,7 +206,7 @@ class MXTensor:
     fmt "fp4": codes uint8 [rows, 16 ng] (two 4-bit codes per byte); "int8":
     codes int8 [rows, 32 ng]; scales uint8 [rows, ng], ng = ceil(cols / 32)."""
 
-    __slots__ = ("fmt", "rows", "cols", "codes", "scales")
+    __slots__ = ("fmt", "rows", "cols", "codes", "scales", "index")
 
     def __init__(self, fmt, rows, cols, codes, scales):
         if fmt not in _MX_FMT:
@@ -218,6 +223,7 @@ class MXTensor:
         if codes.device != scales.device:
             raise ValueError("codes and scales must be on one device")
         self.fmt, self.rows, self.cols, self.codes, self.scales = fmt, rows, cols, codes, scales
+        self.index = codes.get_device()
 
     @classmethod
     def empty(cls, fmt, rows, cols, device):
@@ -238,36 +244,45 @@ def hss_mx_quantize(W: torch.Tensor, fmt="fp4", out: Optional[MXTensor] = None, 
 
     residual=True (or a tensor of W's shape and dtype, which may be W itself)
     also writes W minus the quantised values (exact) and returns (q, residual)."""
-    dev = _dev(W)
-    if W.dim() != 2 or not W.is_contiguous():
+    index = _index(W)
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return hss_mx_quantize(W, fmt, out, residual)
+    shape = W.shape
+    if len(shape) != 2 or not W.is_contiguous():
         raise ValueError("W must be a contiguous 2-D tensor")
-    dt = _dt(W)
-    rows, cols = W.shape
+    rows, cols = shape
     if out is None:
-        out = MXTensor.empty(fmt, rows, cols, dev)
-    elif out.fmt != fmt or out.rows != rows or out.cols != cols or out.device != dev:
-        raise ValueError(f"out must be a {rows} x {cols} {fmt} MXTensor on {dev}")
-    res = torch.empty_like(W) if residual is True else (residual if residual is not False else None)
-    if res is not None and (res.shape != W.shape or res.dtype != W.dtype or not res.is_contiguous() or
-                            res.device != dev):
-        raise ValueError("residual must be a contiguous tensor of W's shape, dtype and device")
-    with _on(dev):
-        check(lib.hss_mx_quantize(_MX_FMT[fmt], dt, rows, cols, W.data_ptr(), out.codes.data_ptr(),
-                                  out.scales.data_ptr(), _ptr(res), _stream(dev)), "hss_mx_quantize")
+        out = MXTensor.empty(fmt, rows, cols, W.device)
+    elif out.fmt != fmt or out.rows != rows or out.cols != cols or out.index != index:
+        raise ValueError(f"out must be a {rows} x {cols} {fmt} MXTensor on {W.device}")
+    res = None
+    if residual is not False and residual is not None:
+        res = torch.empty_like(W) if residual is True else residual
+        if res.shape != shape or res.dtype != W.dtype or not res.is_contiguous() or res.get_device() != index:
+            raise ValueError("residual must be a contiguous tensor of W's shape, dtype and device")
+    code = lib.hss_mx_quantize(_MX_FMT[fmt], _dt(W), rows, cols, W.data_ptr(), out.codes.data_ptr(),
+                               out.scales.data_ptr(), None if res is None else res.data_ptr(), _raw_stream(index))
+    if code:
+        check(code, "hss_mx_quantize")
     return out if res is None else (out, res)
 
 
 def hss_mx_dequantize(q: MXTensor, dtype=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values q stands for (rows x cols, bf16 by default or fp32; exact in both)."""
-    dev = _dev(q.codes)
+    index = _index(q.codes)
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return hss_mx_dequantize(q, dtype, out)
     if out is None:
-        out = torch.empty((q.rows, q.cols), dtype=dtype or torch.bfloat16, device=dev)
-    elif out.shape != (q.rows, q.cols) or not out.is_contiguous() or out.device != dev or \
+        out = torch.empty((q.rows, q.cols), dtype=dtype or torch.bfloat16, device=q.device)
+    elif out.shape != (q.rows, q.cols) or not out.is_contiguous() or out.get_device() != index or \
             (dtype is not None and out.dtype != dtype):
         raise ValueError("out must be a contiguous tensor of q's shape and device")
-    with _on(dev):
-        check(lib.hss_mx_dequantize(_MX_FMT[q.fmt], _dt(out), q.rows, q.cols, q.codes.data_ptr(),
-                                    q.scales.data_ptr(), out.data_ptr(), _stream(dev)), "hss_mx_dequantize")
+    code = lib.hss_mx_dequantize(_MX_FMT[q.fmt], _dt(out), q.rows, q.cols, q.codes.data_ptr(), q.scales.data_ptr(),
+                                 out.data_ptr(), _raw_stream(index))
+    if code:
+        check(code, "hss_mx_dequantize")
     return out
 
 
@@ -415,26 +430,31 @@ def hss_apply_workspace_size(A: HSSMatrix, b: int) -> int:
     return int(out.value)
 
 
-def _same_device(A: HSSMatrix, dev):
-    if A.mx is not None and A.mx.device != dev:
-        raise ValueError(f"the matrix is on {A.mx.device}, the call on {dev}")
+def _check_x(A: HSSMatrix, X: torch.Tensor, index: int) -> int:
+    shape = X.shape
+    if len(shape) != 2 or shape[1] != A.n or not X.is_contiguous() or X.dtype != A.dtype:
+        raise ValueError("X must be a contiguous b x n tensor of the matrix dtype")
+    if A.mx is not None and A.mx.index != index:
+        raise ValueError(f"the matrix is on {A.mx.device}, X on {X.device}")
+    return shape[0]
 
 
 def hss_apply(A: HSSMatrix, X: torch.Tensor, Y: Optional[torch.Tensor] = None,
               ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y (b x m) = X (b x n) (S + U V^T)^T on the current stream."""
-    dev = _dev(X)
-    if X.dim() != 2 or X.shape[1] != A.n or not X.is_contiguous() or X.dtype != A.dtype:
-        raise ValueError("X must be a contiguous b x n tensor of the matrix dtype")
-    _same_device(A, dev)
-    b = X.shape[0]
+    index = _index(X)
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return hss_apply(A, X, Y, ws)
+    b = _check_x(A, X, index)
     if Y is None:
-        Y = torch.empty((b, A.m), dtype=A.dtype, device=dev)
-    with _on(dev):
-        if ws is None:
-            ws = A.workspace(b, dev)
-        check(lib.hss_apply(ctypes.byref(A.struct), b, _ptr(X), _ptr(Y), _ptr(ws), ws.numel(),
-                            _stream(dev)), "hss_apply")
+        Y = torch.empty((b, A.m), dtype=A.dtype, device=X.device)
+    if ws is None:
+        ws = A.workspace(b, X.device)
+    code = lib.hss_apply(ctypes.byref(A.struct), b, X.data_ptr(), Y.data_ptr(), ws.data_ptr(), ws.numel(),
+                         _raw_stream(index))
+    if code:
+        check(code, "hss_apply")
     return Y
 
 
@@ -442,15 +462,16 @@ def hss_apply_noalloc(A: HSSMatrix, X: torch.Tensor, Y: torch.Tensor) -> torch.T
     """Y (b x m, preallocated) = X (b x n) (S + U V^T)^T on the current stream,
     with the library's own per-GPU scratch instead of a workspace: the call
     allocates nothing.  Calls that overlap in time on one GPU race."""
-    dev = _dev(X)
-    if X.dim() != 2 or X.shape[1] != A.n or not X.is_contiguous() or X.dtype != A.dtype:
-        raise ValueError("X must be a contiguous b x n tensor of the matrix dtype")
-    if Y.shape != (X.shape[0], A.m) or not Y.is_contiguous() or Y.dtype != A.dtype:
+    index = _index(X)
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return hss_apply_noalloc(A, X, Y)
+    b = _check_x(A, X, index)
+    if Y.shape != (b, A.m) or not Y.is_contiguous() or Y.dtype != A.dtype:
         raise ValueError("Y must be a contiguous b x m tensor of the matrix dtype")
-    _same_device(A, dev)
-    with _on(dev):
-        check(lib.hss_apply_noalloc(ctypes.byref(A.struct), X.shape[0], _ptr(X), _ptr(Y), _stream(dev)),
-              "hss_apply_noalloc")
+    code = lib.hss_apply_noalloc(ctypes.byref(A.struct), b, X.data_ptr(), Y.data_ptr(), _raw_stream(index))
+    if code:
+        check(code, "hss_apply_noalloc")
     return Y
 
 
@@ -469,23 +490,22 @@ def hss_apply_group_workspace_size(As, b: int) -> int:
 def hss_apply_group(As, X: torch.Tensor, Ys=None, ws: Optional[torch.Tensor] = None):
     """Y_g = X (S_g + U_g V_g^T)^T for every matrix of As (same n, dtype and
     format), in one launch per decode pass; returns the list of Y_g."""
-    dev = _dev(X)
-    As = list(As)
+    index = _index(X)
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return hss_apply_group(As, X, Ys, ws)
+    As, b = list(As), 0
     for A in As:
-        if X.dim() != 2 or X.shape[1] != A.n or not X.is_contiguous() or X.dtype != A.dtype:
-            raise ValueError("X must be a contiguous b x n tensor of every matrix's dtype")
-        _same_device(A, dev)
-    b = X.shape[0]
+        b = _check_x(A, X, index)
     if Ys is None:
-        Ys = [torch.empty((b, A.m), dtype=A.dtype, device=dev) for A in As]
+        Ys = [torch.empty((b, A.m), dtype=A.dtype, device=X.device) for A in As]
+    if ws is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("create the workspace before graph capture and pass it as ws=")
+        ws = apply_workspace(hss_apply_group_workspace_size(As, b), X.device)
     yp = (ctypes.c_void_p * len(As))(*[_ptr(Y) for Y in Ys])
-    with _on(dev):
-        if ws is None:
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("create the workspace before graph capture and pass it as ws=")
-            ws = apply_workspace(hss_apply_group_workspace_size(As, b), dev)
-        check(lib.hss_apply_group(_group_structs(As), len(As), b, _ptr(X), yp, _ptr(ws), ws.numel(),
-                                  _stream(dev)), "hss_apply_group")
+    check(lib.hss_apply_group(_group_structs(As), len(As), b, _ptr(X), yp, _ptr(ws), ws.numel(),
+                              _raw_stream(index)), "hss_apply_group")
     return Ys
 
 
@@ -729,10 +749,14 @@ def hss_grad_ckpt(A: HSSMatrix, X: MXTensor, G: torch.Tensor, dS=True, dU=True, 
     MXTensor (b x n) that hss_mx_quantize made of it in the forward pass.
     out: tensors to write (a dict with the keys wanted, as returned); then
     dS, dU and dVt are ignored."""
-    dev = _dev(G)
-    if X.fmt != "int8" or X.cols != A.n or X.device != dev:
+    index, dev = _index(G), G.device
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return hss_grad_ckpt(A, X, G, dS, dU, dVt, out, ws)
+    if X.fmt != "int8" or X.cols != A.n or X.index != index:
         raise ValueError("X must be an 'int8' MXTensor, b x n, on G's device")
-    _same_device(A, dev)
+    if A.mx is not None and A.mx.index != index:
+        raise ValueError(f"the matrix is on {A.mx.device}, G on {dev}")
     b = X.rows
     if G.shape != (b, A.m) or not G.is_contiguous() or G.dtype != A.dtype:
         raise ValueError("G must be a contiguous b x m tensor of the matrix dtype")
@@ -740,18 +764,18 @@ def hss_grad_ckpt(A: HSSMatrix, X: MXTensor, G: torch.Tensor, dS=True, dU=True, 
     if out is None:
         out = {k: torch.empty(shapes[k], dtype=torch.float32, device=dev)
                for k, wanted in (("dS", dS), ("dU", dU), ("dVt", dVt)) if wanted}
-    for k, t in out.items():
-        if k not in shapes or t.shape != shapes[k] or t.dtype != torch.float32 or not t.is_contiguous() or \
-                t.device != dev:
-            raise ValueError("out must hold contiguous float32 tensors 'dS', 'dU', 'dVt' of the gradients' shapes")
+    else:
+        for k, t in out.items():
+            if k not in shapes or t.shape != shapes[k] or t.dtype != torch.float32 or not t.is_contiguous() or \
+                    t.get_device() != index:
+                raise ValueError("out must hold contiguous float32 tensors 'dS', 'dU', 'dVt' of the gradients' shapes")
     if ws is None:
         ws = grad_ckpt_workspace(A, b, dev)
-    elif ws.device != dev:
+    elif ws.get_device() != index:
         raise ValueError(f"ws must be on {dev}")
-    with _on(dev):
-        check(lib.hss_grad_ckpt(ctypes.byref(A.struct), b, X.codes.data_ptr(), X.scales.data_ptr(), G.data_ptr(),
-                                _ptr(out.get("dS")), _ptr(out.get("dU")), _ptr(out.get("dVt")), ws.data_ptr(),
-                                ws.numel(), _stream(dev)), "hss_grad_ckpt")
+    check(lib.hss_grad_ckpt(ctypes.byref(A.struct), b, X.codes.data_ptr(), X.scales.data_ptr(), G.data_ptr(),
+                            _ptr(out.get("dS")), _ptr(out.get("dU")), _ptr(out.get("dVt")), ws.data_ptr(),
+                            ws.numel(), _raw_stream(index)), "hss_grad_ckpt")
     return out
 
 

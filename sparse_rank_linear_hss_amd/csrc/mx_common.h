@@ -84,7 +84,9 @@ __device__ __forceinline__ u32x4 load_row8(const uint16_t* __restrict__ row, int
 // ---------------------------------------------------------------------------
 // k_mx_prep (mx_skinny.hip): T = X V in K splits, X^T, padded X and U.
 // ---------------------------------------------------------------------------
-static constexpr int kMxPrepSplits = 8;  // most K splits of T
+// Most K splits of T (4096 x 11008, one column, r 64: 11.4 us in all, with 8
+// splits 12.2).
+static constexpr int kMxPrepSplits = 16;
 
 struct MxPrep {
   const uint16_t* X;
@@ -92,9 +94,10 @@ struct MxPrep {
   float* Tp;      // [splits][b][rp], with r > 0
   uint16_t* Xt;   // n x ldt; null = none
   uint16_t* Xp;   // b x np;  null = none
+  uint16_t* Xo;   // X in k_mx_skinny's operand order, nch chunks of 2048 values; null = none
   const uint16_t* U;
   uint16_t* Up;   // m x rp;  null = none
-  int m, b, n, r, rp, ltiles, splits, steps_per_split, tb, xb, ldt, np;
+  int m, b, n, r, rp, ltiles, splits, steps_per_split, tb, xb, ldt, np, nch;
 };
 
 MxPrep mx_prep_plan(const hss_matrix* A, int b);  // the sizes of T

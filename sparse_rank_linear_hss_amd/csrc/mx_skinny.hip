@@ -1,7 +1,7 @@
 // HSS_MX4 apply for up to 16 columns (decode): Y = X (S + U V^T + D)^T straight
 // from the 4-bit codes, in one launch (two when there is a low-rank term, an S
-// and more than four columns, or X off the 16-byte grid).  Bound by the codes'
-// stream from HBM.  Up to four columns: k_mx_gemv, on the vector units, below.
+// and more than four columns, or X's rows are long or off the 16-byte grid).
+// Bound by the codes' stream from HBM.  Up to four columns: k_mx_gemv, on the vector units, below.
 // From five on: k_mx_skinny, on the matrix cores.
 //
 // k_mx_skinny: a block owns 16 rows of D.  Its waves split the columns into chunks of 128:
@@ -10,7 +10,8 @@
 // an instruction) into four A operands of v_mfma_f32_16x16x32_bf16.  The
 // product's order along K is free as long as both operands share it: operand t
 // holds codes 8 t .. 8 t + 7 of the lane's group, and the B operand of lane l
-// the 16 bytes of X[l % 16] at the same columns.  So the codes go from memory
+// the 16 bytes of X[l % 16] at the same columns, from X's rows or from a copy
+// of X in just that order.  So the codes go from memory
 // to the matrix cores without passing through LDS, and one column costs as
 // much as sixteen.  Columns past b repeat column b - 1 and are dropped.
 //
@@ -19,8 +20,8 @@
 // meet in LDS and are added in a fixed order.
 //
 // k_mx_prep makes what the main launch needs of X: T = X V in fp32, K split
-// over blocks (the partial sums are added by the reader, in order), and X^T
-// for the gathers of S.
+// over blocks (the partial sums are added by the reader, in order), X^T for
+// the gathers of S, and X in operand order.
 #include <algorithm>
 #include <type_traits>
 
@@ -33,7 +34,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 static constexpr int kSkCols = 16;       // columns of one call
 static constexpr int kSkGather = 4;      // columns up to which S gathers from X, not X^T
-static constexpr int kSkBatch = 4;       // chunks whose loads are in flight together
+static constexpr int kSkBatch = 6;       // most chunks of a wave whose loads are in flight together
 
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -56,6 +57,12 @@ __global__ __launch_bounds__(256) void k_mx_prep(MxPrep a) {
     for (uint32_t e = first; a.Xp && e < (uint32_t)b * per; e += step) {
       const int c = (int)(e / per), k = (int)(e - (uint32_t)c * per) * 8;
       *reinterpret_cast<u32x4*>(a.Xp + (int64_t)c * a.np + k) = load_row8(X + (int64_t)c * n, k, n);
+    }
+    // X in k_mx_skinny's operand order: piece 256 c + 64 k + l holds, for row l %
+    // 16, columns 128 c + 32 (l / 16) + 8 k ..
+    for (uint32_t e = first; a.Xo && e < (uint32_t)a.nch * 256u; e += step) {
+      const int l = (int)(e & 63u), k = 128 * (int)(e >> 8) + 32 * (l >> 4) + 8 * (int)((e >> 6) & 3u);
+      *reinterpret_cast<u32x4*>(a.Xo + (int64_t)e * 8) = load_row8(X + (int64_t)min(l & 15, b - 1) * n, k, n);
     }
     for (uint32_t e = first; a.Up && e < (uint32_t)a.m * peru; e += step) {
       const int i = (int)(e / peru), l = (int)(e - (uint32_t)i * peru) * 8;
@@ -119,8 +126,8 @@ MxPrep mx_prep_plan(const hss_matrix* A, int b) {
 }
 
 void launch_mx_prep(MxPrep p, hipStream_t s) {
-  if (p.Xt || p.Xp || p.Up) {
-    const int64_t work = std::max({p.Xt ? (int64_t)p.n * (p.ldt / 8) : 0, p.Xp ? (int64_t)p.b * (p.np / 8) : 0,
+  if (p.Xt || p.Xp || p.Xo || p.Up) {
+    const int64_t work = std::max({p.Xt ? (int64_t)p.n * (p.ldt / 8) : 0, p.Xp ? (int64_t)p.b * (p.np / 8) : 0, (int64_t)(p.Xo ? p.nch * 256 : 0),
                                    p.Up ? (int64_t)p.m * (p.rp / 8) : 0});
     p.xb = (int)std::min<int64_t>((work + 255) / 256, 1024);
   }
@@ -134,6 +141,7 @@ struct SkinnyArgs {
   const void* col;
   const uint16_t* vals;
   const uint16_t* X;   // rows of ldx, 16-byte aligned unless b == 1
+  const uint16_t* Xo;  // X in operand order; null = none
   const uint16_t* Xt;  // n x 16, b > 1 and S not empty
   const uint16_t* U;
   const float* Tp;
@@ -243,7 +251,9 @@ __device__ __forceinline__ float s_rows16(const SkinnyArgs& a, const COL* __rest
   return s[0];
 }
 
-template <int WV>
+// WV waves, B chunks of a wave in flight (at least 2: X comes two chunks ahead).
+// XO: X comes in operand order (k_mx_prep), whole chunks with zeros past n.
+template <int WV, int B, bool XO>
 __global__ __launch_bounds__(64 * WV, 4) void k_mx_skinny(SkinnyArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   float* red = reinterpret_cast<float*>(lds);                       // [WV][16 columns][16 rows]
@@ -252,23 +262,31 @@ __global__ __launch_bounds__(64 * WV, 4) void k_mx_skinny(SkinnyArgs a) {
   const int t = threadIdx.x, lane = t & 63, w = uniform(t >> 6);
   const int row0 = (int)blockIdx.x * 16;
   const int q = lane >> 4;
-  const int nch = (a.ng + 3) >> 2, nfull = a.n >> 7;  // the last chunk may be short
+  const int nch = (a.ng + 3) >> 2, nfull = XO ? nch : a.n >> 7;  // else the last chunk may be short
   const uint32_t grow = (uint32_t)min(row0 + (lane & 15), a.m - 1) * (uint32_t)a.ng;
   const uint32_t xoff = (uint32_t)min(lane & 15, a.b - 1) * (uint32_t)a.ldx;
 
-  u32x4 cw[kSkBatch], xv[2][4];
-  uint32_t sb[kSkBatch];
+  u32x4 cw[B], xv[2][4];
+  uint32_t sb[B];
   // whole chunks c0 + WV u; past the last one, that one again, not used.  The
   // codes of a batch are in flight together, X two chunks ahead.
   auto load_x = [&](int c, u32x4 (&x)[4]) {
-    const Bytes16* xp = reinterpret_cast<const Bytes16*>(a.X + (xoff + 128 * (uint32_t)min(c, nfull - 1) + 32 * q));
+    if constexpr (XO) {
+      const u32x4* xp = reinterpret_cast<const u32x4*>(a.Xo) + (256 * (uint32_t)min(c, nfull - 1) + lane);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = u32x4{xp[k].w[0], xp[k].w[1], xp[k].w[2], xp[k].w[3]};
+      for (int k = 0; k < 4; ++k) x[k] = xp[64 * k];
+    } else {
+      const Bytes16* xp = reinterpret_cast<const Bytes16*>(a.X + (xoff + 128 * (uint32_t)min(c, nfull - 1) + 32 * q));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = u32x4{xp[k].w[0], xp[k].w[1], xp[k].w[2], xp[k].w[3]};
+    }
   };
   auto issue = [&](int c0) {
 #pragma unroll
-    for (int u = 0; u < kSkBatch; ++u) {
-      const uint32_t at = grow + 4 * (uint32_t)min(c0 + WV * u, nfull - 1) + q;
+    for (int u = 0; u < B; ++u) {
+      uint32_t g = 4 * (uint32_t)min(c0 + WV * u, nfull - 1) + q;
+      if constexpr (XO) g = min(g, (uint32_t)a.ng - 1u);  // past the row: its last group again, against zeros
+      const uint32_t at = grow + g;
       cw[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.codes + at * 16));
       sb[u] = a.scales[at];
     }
@@ -278,12 +296,12 @@ __global__ __launch_bounds__(64 * WV, 4) void k_mx_skinny(SkinnyArgs a) {
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   auto compute = [&](int c0) {
 #pragma unroll
-    for (int u = 0; u < kSkBatch; ++u) {
+    for (int u = 0; u < B; ++u) {
       if (c0 + WV * u >= nfull) break;  // the same for the whole wave
       const float sc = mx_scale(sb[u], 0);
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc = mfma16(mx4_to_bf16x8(cw[u][k], sc), xv[u & 1][k], acc);
-      if (u + 2 < kSkBatch) load_x(c0 + WV * (u + 2), xv[u & 1]);
+      if (u + 2 < B) load_x(c0 + WV * (u + 2), xv[u & 1]);
     }
   };
   constexpr int LG = 4 * WV;  // lanes per row of S
@@ -333,11 +351,11 @@ __global__ __launch_bounds__(64 * WV, 4) void k_mx_skinny(SkinnyArgs a) {
       if (lane % LG < 16) sred[(8 * (lane & 1) + ((lane >> 1) & 7)) * 16 + i] = s;
     }
   }
-  for (int c0 = w; c0 < nfull; c0 += WV * kSkBatch) {
+  for (int c0 = w; c0 < nfull; c0 += WV * B) {
     compute(c0);
-    if (c0 + WV * kSkBatch < nfull) issue(c0 + WV * kSkBatch);
+    if (c0 + WV * B < nfull) issue(c0 + WV * B);
   }
-  if (nch > nfull && w == nfull % WV) {  // the short chunk: lanes past its groups hold zeros of X
+  if (!XO && nch > nfull && w == nfull % WV) {  // the short chunk: lanes past its groups hold zeros of X
     const int g = 4 * nfull + q;
     const uint32_t at = grow + (uint32_t)min(g, a.ng - 1);
     const u32x4 code = *reinterpret_cast<const u32x4*>(a.codes + at * 16);
@@ -573,7 +591,7 @@ static SkinnyPlan plan_skinny(const hss_matrix* A, int b) {
   p.tp = 0;
   p.xt = al256((size_t)p.prep.splits * b * p.prep.rp * 4);
   p.xp = p.xt + ((b > kSkGather && A->nnz > 0) ? al256((size_t)A->n * kSkCols * 2) : 0);
-  p.total = p.xp + (b > 1 ? al256((size_t)b * round32(A->n) * 2) : 0);
+  p.total = p.xp + (b > 1 ? (size_t)((mx_groups(A->n) + 3) / 4) * 4096 : 0);
   return p;
 }
 
@@ -584,6 +602,20 @@ bool mx_skinny_supported(const hss_matrix* A, int b) {
 }
 
 size_t mx_skinny_ws_bytes(const hss_matrix* A, int b) { return plan_skinny(A, b).total; }
+
+template <int WV, bool XO>
+static void launch_skinny(const SkinnyArgs& a, int batch, unsigned grid, size_t tl, hipStream_t s) {
+  const dim3 block(64 * WV);
+  const size_t lds = (WV + 1) * 1024 + tl;
+  switch (batch) {
+    case 1:
+    case 2: hipLaunchKernelGGL((k_mx_skinny<WV, 2, XO>), dim3(grid), block, lds, s, a); break;
+    case 3: hipLaunchKernelGGL((k_mx_skinny<WV, 3, XO>), dim3(grid), block, lds, s, a); break;
+    case 4: hipLaunchKernelGGL((k_mx_skinny<WV, 4, XO>), dim3(grid), block, lds, s, a); break;
+    case 5: hipLaunchKernelGGL((k_mx_skinny<WV, 5, XO>), dim3(grid), block, lds, s, a); break;
+    default: hipLaunchKernelGGL((k_mx_skinny<WV, 6, XO>), dim3(grid), block, lds, s, a); break;
+  }
+}
 
 hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s) {
   const SkinnyPlan p = plan_skinny(A, b);
@@ -608,22 +640,23 @@ hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, 
   a.ldx = n;
   const bool gemv = gv_supported(A, b);
   const bool need_xt = a.has_s && b > kSkGather && !gemv;
-  // rows off the 16-byte grid: 16-byte loads of X at 2-byte addresses cost the
-  // main launch more than a copy (2731 x 5003, 13 columns: 14.8 against 9.6 us)
-  const bool need_xp = !gemv && b > 1 && (n % 8 != 0 || (uintptr_t)X % 16 != 0);
+  // X in operand order: a load is then 1 KiB in a row, where rows of X make a
+  // line of every lane's 64 bytes (us in all, 5 - 13 columns: 2731 x 5003
+  // 12.3 against 13.7, 4096 x 11008 18.3 against 21.9, 8192^2 23.1 against
+  // 25.5).  With neither S nor a low-rank term it would cost a launch of its
+  // own: 2731 x 2528 5.7 against 4.9, x 5024 7.7 against 7.3, 4096^2 7.5
+  // against 7.9; so there only for long rows, or rows off the 16-byte grid.
+  const bool need_xo = !gemv && b > 1 && (r > 0 || need_xt || n > 5120 || n % 8 != 0 || (uintptr_t)X % 16 != 0);
   MxPrep pr = p.prep;
   pr.X = a.X;
   pr.Vt = static_cast<const uint16_t*>(A->Vt);
   pr.Tp = reinterpret_cast<float*>(base + p.tp);
   pr.ldt = kSkCols;
-  pr.np = round32(n);
+  pr.nch = (a.ng + 3) / 4;
   if (need_xt) pr.Xt = reinterpret_cast<uint16_t*>(base + p.xt);
-  if (need_xp) pr.Xp = reinterpret_cast<uint16_t*>(base + p.xp);
+  if (need_xo) pr.Xo = reinterpret_cast<uint16_t*>(base + p.xp);
   launch_mx_prep(pr, s);
-  if (need_xp) {
-    a.X = reinterpret_cast<const uint16_t*>(base + p.xp);
-    a.ldx = round32(n);
-  }
+  a.Xo = pr.Xo;
   if (gemv) {
     const size_t lds = (size_t)(b > 2 ? 4 : b) * gv_plane_bytes(n) + (size_t)b * a.rp * 4;
     // two rows a wave while that leaves every SIMD a wave or two, else four
@@ -644,15 +677,19 @@ hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, 
   }
   const unsigned grid = (unsigned)((m + 15) / 16);
   const size_t tl = r > 0 ? (size_t)b * 2 * (a.rp + 8) * 2 : 0;
-  const int nch = (a.ng + 3) / 4;
-  // Waves per block: enough to hold a row tile's codes in flight, fewer when
-  // the blocks fill the chip anyway.
-  if (nch <= 4 * kSkBatch || grid > 512)
-    hipLaunchKernelGGL(k_mx_skinny<4>, dim3(grid), dim3(256), 5 * 1024 + tl, s, a);
-  else if (nch <= 8 * kSkBatch)
-    hipLaunchKernelGGL(k_mx_skinny<8>, dim3(grid), dim3(512), 9 * 1024 + tl, s, a);
-  else
-    hipLaunchKernelGGL(k_mx_skinny<16>, dim3(grid), dim3(1024), 17 * 1024 + tl, s, a);
+  // Four waves a block where rows are short or the blocks fill the chip anyway,
+  // else eight (4096 x 11008, 8 columns, D alone: 13.5 us; 16 waves 16.1).  A
+  // wave's chunks in as few batches as possible, all of about the same size,
+  // since a short batch loads its last chunk over again: 2731 x 5024, 13
+  // columns, D alone, five chunks a wave: 7.4 us in one batch, 8.6 as 4 + 1.
+  const int nfull = a.Xo ? pr.nch : n >> 7;
+  const bool wide = nfull > 16 && grid <= 512;
+  const int per = std::max(1, (nfull + (wide ? 7 : 3)) / (wide ? 8 : 4));
+  const int batches = (per + kSkBatch - 1) / kSkBatch, batch = (per + batches - 1) / batches;
+  if (a.Xo && wide) launch_skinny<8, true>(a, batch, grid, tl, s);
+  else if (a.Xo) launch_skinny<4, true>(a, batch, grid, tl, s);
+  else if (wide) launch_skinny<8, false>(a, batch, grid, tl, s);
+  else launch_skinny<4, false>(a, batch, grid, tl, s);
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 
