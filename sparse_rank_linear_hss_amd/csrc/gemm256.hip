@@ -269,6 +269,20 @@ __global__ __launch_bounds__(256, 1) void k_gemm256(G256Args g) {
   } else {  // G256_DS32, 16, NM: dS[p] = C[row of p][column of p] for S's entries within the tile
     constexpr int PAT = OUT - G256_DS;
     float* dS = static_cast<float*>(g.C);
+    // the entries' ranges of this thread's rows, requested together
+    int32_t pb[FM], pt[FM];
+    int64_t rs[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int row = min(m0 + 128 * (t >> 7) + 32 * i + ((t >> 2) & 31), g.M - 1);
+      if constexpr (PAT == PAT_NM24) {
+        rs[i] = (int64_t)row * (g.N >> 1);
+        pb[i] = n0 >> 1, pt[i] = min(n0 + TL::TN, g.N) >> 1;
+      } else {
+        rs[i] = 0;
+        pb[i] = g.tptr[(int64_t)row * (g.tiles_n + 1) + tn], pt[i] = g.tptr[(int64_t)row * (g.tiles_n + 1) + tn + 1];
+      }
+    }
     // 64 rows at a time through LDS (rows 128 g + 32 i + 0..31 at 32 g + 0..31), the
     // two buffers in turn; four threads take a row's entries
 #pragma unroll
@@ -282,16 +296,9 @@ __global__ __launch_bounds__(256, 1) void k_gemm256(G256Args g) {
       __syncthreads();
       const int lrow = t >> 2, row = m0 + 128 * (lrow >> 5) + 32 * i + (lrow & 31);
       if (row < g.M) {
-        int64_t rs, p, pe;
-        if constexpr (PAT == PAT_NM24) {
-          rs = (int64_t)row * (g.N >> 1);
-          p = rs + (n0 >> 1), pe = rs + (min(n0 + TL::TN, g.N) >> 1);
-        } else {
-          rs = g.S.row_ptr[row];
-          p = g.tptr[(int64_t)row * (g.tiles_n + 1) + tn], pe = g.tptr[(int64_t)row * (g.tiles_n + 1) + tn + 1];
-        }
-        for (p += t & 3; p < pe; p += 4) {
-          const int c = pat_col<PAT>(g.S, row, rs, p) - n0;
+        const int64_t pe = rs[i] + pt[i];
+        for (int64_t p = rs[i] + pb[i] + (t & 3); p < pe; p += 4) {
+          const int c = pat_col<PAT>(g.S, row, rs[i], p) - n0;
           if ((unsigned)c < (unsigned)TL::TN) dS[p] = L[lrow * TL::TN + c];
         }
       }

@@ -203,11 +203,13 @@ static bool dense_ds(const hss_matrix* A, int b) {
 
 static constexpr int kCkBlocks = 256;  // blocks of the T and P launch
 
-// K splits of the products for dU and dV^T (one launch): enough for a block
-// per CU, where K is long enough for the sum of the partial products to pay.
+// K splits of the products for dU and dV^T (one launch): enough for two blocks
+// per CU (8192^2, 2048 tokens, r 128, us for all gradients: 338; for one block
+// 346; unsplit 368), where K is long enough for the sum of the partial products
+// to pay.
 static int uv_splits(int r, int m, int n, int ldt) {
   const int tiles = (r + 127) / 128 * ((m + 127) / 128 + (n + 127) / 128);
-  return std::max(1, std::min((255 + tiles) / tiles, ldt / 512));
+  return std::max(1, std::min((511 + tiles) / tiles, ldt / 512));
 }
 
 static CkPlan plan_ck(const hss_matrix* A, int b) {

@@ -35,17 +35,35 @@ __device__ __forceinline__ void mm_write(const MmProblem& p, int z, int row0, in
   const int lane = threadIdx.x & 63, q = lane >> 4;
   float* C = p.C + (int64_t)z * p.zstride;
   const int M = p.M, N = p.N;
-  const int64_t sm = p.trans ? 1 : p.ldc, sn = p.trans ? p.ldc : 1;
-  float* at = C + (row0 + 4 * q) * sm + (col0 + (lane & 15)) * sn;
   const int mleft = M - (row0 + 4 * q), nleft = N - (col0 + (lane & 15));
+  if (p.trans) {  // a lane's four rows lie side by side
+    float* at = C + (row0 + 4 * q) + (col0 + (lane & 15)) * p.ldc;
+    const bool vec = ((p.ldc | p.zstride) & 3) == 0 && ((uintptr_t)p.C & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        if (16 * j >= nleft) continue;
+        float* o = at + 16 * j * p.ldc + 16 * i;
+        if (vec && 16 * i + 4 <= mleft) {
+          *reinterpret_cast<f32x4*>(o) = acc[i][j];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * i + e < mleft) o[e] = acc[i][j][e];
+        }
+      }
+    return;
+  }
+  float* at = C + (row0 + 4 * q) * p.ldc + (col0 + (lane & 15));
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float* row = at + (16 * i + e) * sm;
+      float* row = at + (16 * i + e) * p.ldc;
 #pragma unroll
       for (int j = 0; j < FN; ++j)
-        if (16 * i + e < mleft && 16 * j < nleft) row[16 * j * sn] = acc[i][j][e];
+        if (16 * i + e < mleft && 16 * j < nleft) row[16 * j] = acc[i][j][e];
     }
 }
 

@@ -43,9 +43,10 @@ static size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 static int round32(int x) { return (x + 31) & ~31; }
 
 // ---------------------------------------------------------------------------
-// W' = D + S, one wave per row, kMxSeg columns at a time through LDS: the
-// decoded codes first, then the row's entries of S added to them (an entry's
-// column occurs once per row, so no two lanes meet), then 16-byte stores.
+// W' = D + S.  A wave takes 2048 columns of a row, a lane one group of them
+// (16 bytes of codes): decoded into LDS, then the row's entries of S there
+// added (an entry's column occurs once per row, so no two lanes meet), then
+// 16-byte stores, 1 KiB a wave.  Bound by the stores (8192^2: 34.6 us, 4.9 TB/s).
 // ---------------------------------------------------------------------------
 // The row's two copies of U, rp columns each (zero past r), by one wave.
 __device__ __forceinline__ void put_u(const uint16_t* __restrict__ U, int row, int r, int rp, uint16_t* __restrict__ dst) {
@@ -56,7 +57,11 @@ __device__ __forceinline__ void put_u(const uint16_t* __restrict__ U, int row, i
   }
 }
 
-static constexpr int kMxSeg = 4096;  // columns per segment: 8 KiB of LDS per wave
+static constexpr int kMxSeg = 2048;  // columns of one wave: 4 KiB of LDS
+
+// Where column c of a wave's segment lies: the group's 16-byte pieces are
+// permuted by the group, so that the lanes' stores of them do not conflict.
+__device__ __forceinline__ int seg_at(int c) { return (c & ~31) | ((((c >> 3) ^ (c >> 6)) & 3) << 3) | (c & 7); }
 
 template <typename COL>
 __global__ __launch_bounds__(256) void k_mx_densify(const uint8_t* __restrict__ codes,
@@ -65,38 +70,41 @@ __global__ __launch_bounds__(256) void k_mx_densify(const uint8_t* __restrict__ 
                                                     const COL* __restrict__ col_idx,
                                                     const uint16_t* __restrict__ vals, int m, int n, int np,
                                                     int ldw, const uint16_t* __restrict__ U, int r, int rp,
-                                                    uint16_t* __restrict__ W) {
+                                                    int segs, uint16_t* __restrict__ W) {
   __shared__ __align__(16) uint16_t seg[4][kMxSeg];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int row = blockIdx.x * 4 + w;
+  const uint32_t unit = blockIdx.x * 4u + (uint32_t)w;
+  const int row = (int)(unit / (uint32_t)segs), c0 = (int)(unit - (uint32_t)row * (uint32_t)segs) * kMxSeg;
   if (row >= m) return;  // no block-wide barrier below
-  const int ng = mx_groups(n);
+  const int ng = mx_groups(n), g = (c0 >> 5) + lane;
   uint16_t* L = seg[w];
-  put_u(U, row, r, rp, W + (int64_t)row * ldw + np);
+  u32x4 code = {0u, 0u, 0u, 0u};
+  float sc = 1.f;
+  if (g < ng) {
+    const int64_t at = (int64_t)row * ng + g;
+    code = *reinterpret_cast<const u32x4*>(codes + at * 16);
+    sc = mx_scale(scales[at], 0);
+  }
   const int p0 = row_ptr[row], p1 = row_ptr[row + 1];
-  for (int c0 = 0; c0 < np; c0 += kMxSeg) {
-    const int len = min(kMxSeg, np - c0);  // a multiple of 32
-    for (int j = 8 * lane; j < len; j += 512) {
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (((c0 + j) >> 5) < ng) {
-        const int64_t g = (int64_t)row * ng + ((c0 + j) >> 5);
-        const uint32_t word = *reinterpret_cast<const uint32_t*>(codes + g * 16 + ((j >> 1) & 12));
-        v = mx4_to_bf16x8(word, mx_scale(scales[g], 0));
-      }
-      *reinterpret_cast<u32x4*>(L + j) = v;
+  if (c0 == 0) put_u(U, row, r, rp, W + (int64_t)row * ldw + np);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) *reinterpret_cast<u32x4*>(L + seg_at(32 * lane + 8 * k)) = mx4_to_bf16x8(code[k], sc);
+  // A wave's LDS accesses complete in issue order; the empty asm keeps the
+  // compiler from reordering the three phases.
+  asm volatile("" ::: "memory");
+  for (int p = p0 + lane; p < p1; p += 64) {
+    const int c = (int)col_idx[p] - c0;
+    if ((unsigned)c < (unsigned)min(kMxSeg, n - c0)) {
+      uint16_t* at = L + seg_at(c);
+      *at = f32_to_bf16(__uint_as_float((uint32_t)*at << 16) + __uint_as_float((uint32_t)vals[p] << 16));
     }
-    // A wave's LDS accesses complete in issue order; the empty asm keeps the
-    // compiler from reordering the three phases.
-    asm volatile("" ::: "memory");
-    for (int p = p0 + lane; p < p1; p += 64) {
-      const int c = (int)col_idx[p];
-      if ((unsigned)(c - c0) < (unsigned)len && c < n)
-        L[c - c0] = f32_to_bf16(__uint_as_float((uint32_t)L[c - c0] << 16) + __uint_as_float((uint32_t)vals[p] << 16));
-    }
-    asm volatile("" ::: "memory");
-    for (int j = 8 * lane; j < len; j += 512)
-      *reinterpret_cast<u32x4*>(W + (int64_t)row * ldw + c0 + j) = *reinterpret_cast<const u32x4*>(L + j);
-    asm volatile("" ::: "memory");
+  }
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int j = 8 * lane + 512 * k;
+    if (c0 + j < np)
+      *reinterpret_cast<u32x4*>(W + (int64_t)row * ldw + c0 + j) = *reinterpret_cast<const u32x4*>(L + seg_at(j));
   }
 }
 
@@ -187,7 +195,9 @@ static MxPlan plan_mx(const hss_matrix* A, int b) {
   const int m = A->m, n = A->n, r = A->r;
   p.np = (n + 63) & ~63;
   p.rp = r > 0 ? round32(r) : 0;
-  p.zt = r > 0 ? mm_splits(r, b, p.np, 512) : 0;
+  // a block per CU; two cost more in partial products (8192^2, 1024 columns, r
+  // 256: 191 us in all against 211)
+  p.zt = r > 0 ? mm_splits(r, b, p.np, 256) : 0;
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off += al256(bytes); return at; };
   p.w = take((size_t)m * (p.np + 2 * p.rp) * 2);
@@ -235,12 +245,15 @@ hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, v
         hipLaunchKernelGGL(k_mx_add_csr<int32_t>, rows4, dim3(256), 0, s, A->row_ptr, A->col_idx, vals, m, n, np, ldw,
                            U, r, rp, W);
     }
-  } else if (c16) {
-    hipLaunchKernelGGL(k_mx_densify<uint16_t>, rows4, dim3(256), 0, s, codes, scales, A->row_ptr, col16, vals, m, n, np,
-                       ldw, U, r, rp, W);
   } else {
-    hipLaunchKernelGGL(k_mx_densify<int32_t>, rows4, dim3(256), 0, s, codes, scales, A->row_ptr, A->col_idx, vals, m, n,
-                       np, ldw, U, r, rp, W);
+    const int segs = (np + kMxSeg - 1) / kMxSeg;
+    const dim3 grid((unsigned)(((int64_t)m * segs + 3) / 4));
+    if (c16)
+      hipLaunchKernelGGL(k_mx_densify<uint16_t>, grid, dim3(256), 0, s, codes, scales, A->row_ptr, col16, vals, m, n,
+                         np, ldw, U, r, rp, segs, W);
+    else
+      hipLaunchKernelGGL(k_mx_densify<int32_t>, grid, dim3(256), 0, s, codes, scales, A->row_ptr, A->col_idx, vals, m,
+                         n, np, ldw, U, r, rp, segs, W);
   }
   const uint16_t* Xb = static_cast<const uint16_t*>(X);
   if (!rows_ok(X, n)) {
