@@ -455,10 +455,13 @@ hss_status launch_mx_gemm(const hss_matrix* A, int b, const void* X, void* Y, vo
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 
-// Columns up to which this route is taken.  Measured against the dense copy
-// and its products (4096^2, 0.5 % of S, us): forward 64 columns 14.4 against
-// 35.7, 128 27 against 28, 256 36 against 39, 512 55 against 47; input
-// gradient 64 columns 23 against 37.5, 256 40 against 42, 512 63 against 50.
-bool mx_gemm_supported(int b) { return b <= kMgMaxCols; }
+// Whether this route is taken.  Measured against the dense copy and its
+// products (0.5 % of S, r 64, us; forward, input gradient):
+//   4096^2         128 columns 28 against 42, 33 against 47;  256: 41 against 47, 49 against 51;  384: 58 against 51
+//   4096 x 11008   128 columns 50 against 70, 60 against 76;  256: 82 against 76, 104 against 86
+//   8192^2         128 columns 60 against 79, 77 against 95;  256: 103 against 95, 137 against 115
+bool mx_gemm_supported(const hss_matrix* A, int b) {
+  return b <= kMgMaxCols && (b <= 128 || (int64_t)A->m * A->n <= (int64_t)1 << 25);
+}
 
 }  // namespace hss
