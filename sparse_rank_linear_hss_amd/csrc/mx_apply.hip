@@ -2,8 +2,8 @@
 //   Y = X (S + U V^T + D)^T,  D MXFP4, m x n; with HSS_MX4_T the stored array
 //   is D^T (n x m), so that a layer and its transposed layer share one copy.
 //
-// Up to 16 columns, D not transposed: mx_skinny.hip; else up to 128 columns, or
-// 256 of smaller matrices: mx_gemm.hip.  Beyond:
+// Up to 16 columns, D not transposed: mx_skinny.hip; else up to 256 columns:
+// mx_gemm.hip.  Beyond:
 //   W'  = D + S as dense bf16 in the workspace, rows padded to 64 columns
 //   T   = X V in fp32 (matrix cores), kept as two bf16 terms T = T1 + T2 (16
 //         significant bits, so that rounding T does not show beside the
@@ -34,7 +34,7 @@ size_t mx_skinny_ws_bytes(const hss_matrix* A, int b);
 hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s);
 
 // mx_gemm.hip
-bool mx_gemm_supported(const hss_matrix* A, int b);
+bool mx_gemm_supported(int b);
 size_t mx_gemm_ws_bytes(const hss_matrix* A, int b);
 hss_status launch_mx_gemm(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s);
 void launch_mx_tsum(const float* Tp, int splits, int b, int r, int rp, uint16_t* Tb, hipStream_t s);
@@ -212,14 +212,14 @@ static MxPlan plan_mx(const hss_matrix* A, int b) {
 
 size_t mx_apply_ws_bytes(const hss_matrix* A, int b) {
   if (mx_skinny_supported(A, b)) return mx_skinny_ws_bytes(A, b);
-  return mx_gemm_supported(A, b) ? mx_gemm_ws_bytes(A, b) : plan_mx(A, b).total;
+  return mx_gemm_supported(b) ? mx_gemm_ws_bytes(A, b) : plan_mx(A, b).total;
 }
 
 static bool rows_ok(const void* p, int cols) { return (uintptr_t)p % 16 == 0 && cols % 64 == 0; }
 
 hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s) {
   if (mx_skinny_supported(A, b)) return launch_mx_skinny(A, b, X, Y, ws, s);
-  if (mx_gemm_supported(A, b)) return launch_mx_gemm(A, b, X, Y, ws, s);
+  if (mx_gemm_supported(b)) return launch_mx_gemm(A, b, X, Y, ws, s);
   const MxPlan p = plan_mx(A, b);
   char* base = static_cast<char*>(ws);
   auto u16 = [&](size_t off) { return reinterpret_cast<uint16_t*>(base + off); };

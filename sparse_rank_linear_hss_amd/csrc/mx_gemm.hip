@@ -360,7 +360,13 @@ struct MxGemmPlan {
 static MxGemmPlan plan_mx_gemm(const hss_matrix* A, int b) {
   MxGemmPlan p = {};
   p.prep = mx_prep_plan(A, b);
-  p.bn = b <= 32 ? 32 : 64;
+  // 128 columns a tile decode the codes once for twice the columns, in half the
+  // blocks: for large products (us at 64 / 128: 8192^2, 128 columns 60 / 55,
+  // input gradient 77 / 63; 4096^2, 256 columns 41 / 39, 49 / 44; but 128
+  // columns 29 / 31, 33 / 32; 2049 x 1999, 256 columns 26 / 30, 25 / 27)
+  const int64_t work = (int64_t)A->m * A->n * ((b + 127) / 128);
+  const bool wide = b > 64 && work >= (int64_t)1 << ((A->flags & HSS_MX4_T) ? 24 : 25);
+  p.bn = b <= 32 ? 32 : wide ? 128 : 64;
   p.tiles_m = (A->m + kMgM - 1) / kMgM;
   p.tiles_n = (b + p.bn - 1) / p.bn;
   p.nst1 = (A->n + kMgK - 1) / kMgK;
@@ -391,7 +397,8 @@ size_t mx_gemm_ws_bytes(const hss_matrix* A, int b) { return plan_mx_gemm(A, b).
 template <bool TRANS>
 static void launch_tile(const MxGemmArgs& a, int bn, unsigned grid, hipStream_t s) {
   if (bn == 32) hipLaunchKernelGGL((k_mx_gemm<TRANS, 32>), dim3(grid), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_mx_gemm<TRANS, 64>), dim3(grid), dim3(256), 0, s, a);
+  else if (bn == 64) hipLaunchKernelGGL((k_mx_gemm<TRANS, 64>), dim3(grid), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_mx_gemm<TRANS, 128>), dim3(grid), dim3(256), 0, s, a);
 }
 
 hss_status launch_mx_gemm(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s) {
@@ -455,13 +462,11 @@ hss_status launch_mx_gemm(const hss_matrix* A, int b, const void* X, void* Y, vo
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 
-// Whether this route is taken.  Measured against the dense copy and its
-// products (0.5 % of S, r 64, us; forward, input gradient):
-//   4096^2         128 columns 28 against 42, 33 against 47;  256: 41 against 47, 49 against 51;  384: 58 against 51
-//   4096 x 11008   128 columns 50 against 70, 60 against 76;  256: 82 against 76, 104 against 86
-//   8192^2         128 columns 60 against 79, 77 against 95;  256: 103 against 95, 137 against 115
-bool mx_gemm_supported(const hss_matrix* A, int b) {
-  return b <= kMgMaxCols && (b <= 128 || (int64_t)A->m * A->n <= (int64_t)1 << 25);
-}
+// Columns up to which this route is taken.  Measured against the dense copy
+// and its products (0.5 % of S, r 64, us; forward, input gradient):
+//   4096^2         128 columns 28 against 42, 32 against 47;  256: 39 against 47, 44 against 51;  384: 58 against 51
+//   4096 x 11008   128 columns 48 against 70, 60 against 76;  256: 73 against 77, 85 against 87
+//   8192^2         128 columns 55 against 79, 63 against 95;  256: 89 against 96, 106 against 112
+bool mx_gemm_supported(int b) { return b <= kMgMaxCols; }
 
 }  // namespace hss

@@ -224,7 +224,7 @@ def test_kept_weights_are_not_written(H):
 @pytest.mark.parametrize("b", [1, 8, 100, 200, 300])
 def test_arrays_past_2_gib(H, b):
     """A dense part whose bf16 copy has more than 2^31 bytes, both directions
-    (beyond 128 columns such a copy is made): a sample of the outputs, the last
+    (beyond 256 columns such a copy is made): a sample of the outputs, the last
     ones among them, in float64.  S in the last rows."""
     import torch
     m, n, r = 33001, 32800, 8
