@@ -346,6 +346,10 @@ class HSSMatrix:
             assert U.dtype == dtype and Vt.dtype == dtype and U.is_contiguous() and Vt.is_contiguous()
         self.row_ptr, self.col_idx, self.values = row_ptr, col_idx, values
         self.nm_values, self.nm_meta = nm_values, nm_meta
+        held = (U, Vt, row_ptr, col_idx, values, nm_values, nm_meta, dq_codes, dq_levels,
+                None if mx is None else mx.codes)
+        on = {t.get_device() for t in held if t is not None}
+        self.index = on.pop() if len(on) == 1 else None  # the GPU that holds all of it
         self.nnz = int(nnz if nnz is not None else (values.numel() if values is not None else 0))
         self._ws = {}
         s = HssMatrixStruct()
@@ -361,6 +365,7 @@ class HSSMatrix:
         if mx is not None:
             s.dq_codes, s.dq_levels = _ptr(mx.codes), _ptr(mx.scales)
         self.struct = s
+        self._ref = ctypes.byref(s)
 
     @classmethod
     def from_split(cls, sp: SplitResult, U=None, V=None, Vt=None, dtype=None, mx=None):
@@ -434,25 +439,42 @@ def _check_x(A: HSSMatrix, X: torch.Tensor, index: int) -> int:
     shape = X.shape
     if len(shape) != 2 or shape[1] != A.n or not X.is_contiguous() or X.dtype != A.dtype:
         raise ValueError("X must be a contiguous b x n tensor of the matrix dtype")
-    if A.mx is not None and A.mx.index != index:
-        raise ValueError(f"the matrix is on {A.mx.device}, X on {X.device}")
+    if A.index != index:
+        raise ValueError(f"the matrix must be on X's device, {X.device}, with all its tensors")
     return shape[0]
+
+
+def _check_y(A: HSSMatrix, Y: torch.Tensor, b: int, index: int) -> None:
+    if Y.shape != (b, A.m) or Y.dtype != A.dtype or not Y.is_contiguous() or Y.get_device() != index:
+        raise ValueError("Y must be a contiguous b x m tensor of the matrix dtype, on X's device")
+
+
+def _check_ws(ws: torch.Tensor, index: int) -> None:
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the device of the call's other tensors")
 
 
 def hss_apply(A: HSSMatrix, X: torch.Tensor, Y: Optional[torch.Tensor] = None,
               ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y (b x m) = X (b x n) (S + U V^T)^T on the current stream."""
-    index = _index(X)
+    index = X.get_device()
     if index != _current_device():
-        with torch.cuda.device(index):
+        with torch.cuda.device(_index(X)):
             return hss_apply(A, X, Y, ws)
-    b = _check_x(A, X, index)
+    # the checks of _check_x, _check_y and _check_ws, written out: two calls less in a decode step
+    shape, dtype = X.shape, A.dtype
+    if len(shape) != 2 or shape[1] != A.n or X.dtype != dtype or A.index != index or not X.is_contiguous():
+        _check_x(A, X, index)
+    b = shape[0]
     if Y is None:
-        Y = torch.empty((b, A.m), dtype=A.dtype, device=X.device)
+        Y = torch.empty((b, A.m), dtype=dtype, device=X.device)
+    elif Y.shape != (b, A.m) or Y.dtype != dtype or Y.get_device() != index or not Y.is_contiguous():
+        _check_y(A, Y, b, index)
     if ws is None:
         ws = A.workspace(b, X.device)
-    code = lib.hss_apply(ctypes.byref(A.struct), b, X.data_ptr(), Y.data_ptr(), ws.data_ptr(), ws.numel(),
-                         _raw_stream(index))
+    elif ws.get_device() != index or not ws.is_contiguous():
+        _check_ws(ws, index)
+    code = lib.hss_apply(A._ref, b, X.data_ptr(), Y.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(index))
     if code:
         check(code, "hss_apply")
     return Y
@@ -467,9 +489,8 @@ def hss_apply_noalloc(A: HSSMatrix, X: torch.Tensor, Y: torch.Tensor) -> torch.T
         with torch.cuda.device(index):
             return hss_apply_noalloc(A, X, Y)
     b = _check_x(A, X, index)
-    if Y.shape != (b, A.m) or not Y.is_contiguous() or Y.dtype != A.dtype:
-        raise ValueError("Y must be a contiguous b x m tensor of the matrix dtype")
-    code = lib.hss_apply_noalloc(ctypes.byref(A.struct), b, X.data_ptr(), Y.data_ptr(), _raw_stream(index))
+    _check_y(A, Y, b, index)
+    code = lib.hss_apply_noalloc(A._ref, b, X.data_ptr(), Y.data_ptr(), _raw_stream(index))
     if code:
         check(code, "hss_apply_noalloc")
     return Y
@@ -499,10 +520,17 @@ def hss_apply_group(As, X: torch.Tensor, Ys=None, ws: Optional[torch.Tensor] = N
         b = _check_x(A, X, index)
     if Ys is None:
         Ys = [torch.empty((b, A.m), dtype=A.dtype, device=X.device) for A in As]
+    elif len(Ys) != len(As):
+        raise ValueError(f"{len(As)} matrices, {len(Ys)} outputs")
+    else:
+        for A, Y in zip(As, Ys):
+            _check_y(A, Y, b, index)
     if ws is None:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("create the workspace before graph capture and pass it as ws=")
         ws = apply_workspace(hss_apply_group_workspace_size(As, b), X.device)
+    else:
+        _check_ws(ws, index)
     yp = (ctypes.c_void_p * len(As))(*[_ptr(Y) for Y in Ys])
     check(lib.hss_apply_group(_group_structs(As), len(As), b, _ptr(X), yp, _ptr(ws), ws.numel(),
                               _raw_stream(index)), "hss_apply_group")
@@ -641,8 +669,11 @@ def hss_grad(A: HSSMatrix, X: torch.Tensor, G: torch.Tensor, dS=True, dU=True, d
     if X.dim() != 2 or X.shape[1] != A.n or not X.is_contiguous() or X.dtype != A.dtype:
         raise ValueError("X must be a contiguous b x n tensor of the matrix dtype")
     b = X.shape[0]
-    if G.shape != (b, A.m) or not G.is_contiguous() or G.dtype != A.dtype:
-        raise ValueError("G must be a contiguous b x m tensor of the matrix dtype")
+    index = X.get_device()
+    if G.shape != (b, A.m) or not G.is_contiguous() or G.dtype != A.dtype or G.get_device() != index:
+        raise ValueError("G must be a contiguous b x m tensor of the matrix dtype, on X's device")
+    if A.index != index:
+        raise ValueError(f"the matrix must be on X's device, {X.device}, with all its tensors")
     out = {}
     if dS:
         stored = A.m * (A.n // 2) if A.fmt == HSS_FMT_2OF4 else A.nnz
@@ -655,6 +686,8 @@ def hss_grad(A: HSSMatrix, X: torch.Tensor, G: torch.Tensor, dS=True, dU=True, d
         size = ctypes.c_size_t(0)
         check(lib.hss_grad_workspace_size(ctypes.byref(A.struct), b, ctypes.byref(size)), "hss_grad_workspace_size")
         ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
+    else:
+        _check_ws(ws, index)
     check(lib.hss_grad(ctypes.byref(A.struct), b, _ptr(X), _ptr(G), _ptr(out.get("dS")), _ptr(out.get("dU")),
                        _ptr(out.get("dVt")), _ptr(ws), ws.numel(), _stream(dev)), "hss_grad")
     return out
@@ -755,8 +788,8 @@ def hss_grad_ckpt(A: HSSMatrix, X: MXTensor, G: torch.Tensor, dS=True, dU=True, 
             return hss_grad_ckpt(A, X, G, dS, dU, dVt, out, ws)
     if X.fmt != "int8" or X.cols != A.n or X.index != index:
         raise ValueError("X must be an 'int8' MXTensor, b x n, on G's device")
-    if A.mx is not None and A.mx.index != index:
-        raise ValueError(f"the matrix is on {A.mx.device}, G on {dev}")
+    if A.index != index:
+        raise ValueError(f"the matrix must be on G's device, {dev}, with all its tensors")
     b = X.rows
     if G.shape != (b, A.m) or not G.is_contiguous() or G.dtype != A.dtype:
         raise ValueError("G must be a contiguous b x m tensor of the matrix dtype")
@@ -771,8 +804,8 @@ def hss_grad_ckpt(A: HSSMatrix, X: MXTensor, G: torch.Tensor, dS=True, dU=True, 
                 raise ValueError("out must hold contiguous float32 tensors 'dS', 'dU', 'dVt' of the gradients' shapes")
     if ws is None:
         ws = grad_ckpt_workspace(A, b, dev)
-    elif ws.get_device() != index:
-        raise ValueError(f"ws must be on {dev}")
+    else:
+        _check_ws(ws, index)
     check(lib.hss_grad_ckpt(ctypes.byref(A.struct), b, X.codes.data_ptr(), X.scales.data_ptr(), G.data_ptr(),
                             _ptr(out.get("dS")), _ptr(out.get("dU")), _ptr(out.get("dVt")), ws.data_ptr(),
                             ws.numel(), _raw_stream(index)), "hss_grad_ckpt")

@@ -225,3 +225,112 @@ def test_group_takes_one_kind_of_matrix(hl):
     for mats, want in (((mx, mx), 0), ((mx, plain), INV), ((plain, mx), INV), ((mx, _mx(hl, flags=48)), INV)):
         arr = (P * 2)(*[ctypes.pointer(s) for s in mats])
         assert lib.hss_apply_group_workspace_size(arr, 2, 1, ctypes.byref(out)) == want
+
+
+@pytest.fixture
+def bound(hl, monkeypatch):
+    """The binding with its library calls recorded, CPU tensors standing for the
+    current device's (their index is -1) and `elsewhere` for another device's."""
+    import torch
+
+    class Elsewhere(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            real = getattr(hl._lib.lib, name)
+            if name.endswith("_size") or name == "hss_noalloc_scratch_bytes":
+                return real
+            return lambda *a: calls.append(name) or 0
+
+    monkeypatch.setattr(hl, "lib", Lib())
+    monkeypatch.setattr(hl, "_current_device", lambda: -1)
+    monkeypatch.setattr(hl, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(hl, "_index", lambda t: t.get_device())
+    return calls, lambda t: t.as_subclass(Elsewhere)
+
+
+def _cpu_layer(hl, kind):
+    import torch
+    bf = torch.bfloat16
+    U, Vt = torch.zeros(3, 2, dtype=bf), torch.zeros(2, 33, dtype=bf)
+    if kind == "mx":
+        return hl.HSSMatrix("csr", 3, 33, bf, U=U, Vt=Vt, mx=hl.MXTensor.empty("fp4", 3, 33, "cpu"))
+    return hl.HSSMatrix("csr", 3, 33, bf, U=U, Vt=Vt, row_ptr=torch.zeros(4, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("kind", ["mx", "csr"])
+def test_applies_refuse_outputs_and_workspaces_that_do_not_fit(hl, bound, kind):
+    """What the kernels would write or read out of range: Y of another shape,
+    type, layout or device, a workspace on another device or with strides, and
+    a matrix that lies elsewhere than X."""
+    import torch
+    calls, elsewhere = bound
+    bf = torch.bfloat16
+    A = _cpu_layer(hl, kind)
+    X, Y = torch.zeros(5, 33, dtype=bf), torch.zeros(5, 3, dtype=bf)
+    size = max(hl.hss_apply_workspace_size(A, 5), hl.hss_apply_group_workspace_size([A, A], 5))
+    ws = torch.zeros(size, dtype=torch.uint8)
+    hl.hss_apply(A, X, Y, ws), hl.hss_apply_noalloc(A, X, Y), hl.hss_apply_group([A, A], X, [Y, Y.clone()], ws)
+    assert calls == ["hss_apply", "hss_apply_noalloc", "hss_apply_group"]
+    bad_y = [torch.zeros(5, 2, dtype=bf), torch.zeros(3, 5, dtype=bf), torch.zeros(4, 3, dtype=bf), torch.zeros(15, dtype=bf),
+             torch.zeros(5, 3), torch.zeros(3, 5, dtype=bf).t(), torch.zeros(5, 6, dtype=bf)[:, ::2], elsewhere(Y)]
+    for y in bad_y:
+        for call in (lambda: hl.hss_apply(A, X, y, ws), lambda: hl.hss_apply_noalloc(A, X, y),
+                     lambda: hl.hss_apply_group([A, A], X, [Y, y], ws)):
+            with pytest.raises(ValueError):
+                call()
+    for w in (elsewhere(ws), torch.zeros(1, dtype=torch.uint8).expand(size), torch.zeros(2 * size, dtype=torch.uint8)[::2]):
+        for call in (lambda: hl.hss_apply(A, X, Y, w), lambda: hl.hss_apply_group([A, A], X, [Y, Y.clone()], w)):
+            with pytest.raises(ValueError):
+                call()
+    for x in (torch.zeros(5, 32, dtype=bf), torch.zeros(5, 33), torch.zeros(33, dtype=bf), torch.zeros(33, 5, dtype=bf).t()):
+        with pytest.raises(ValueError):
+            hl.hss_apply(A, x, Y, ws)
+    with pytest.raises(ValueError):
+        hl.hss_apply_group([A, A], X, [Y], ws)
+    A.index = 1                                                    # the matrix elsewhere
+    for call in (lambda: hl.hss_apply(A, X, Y, ws), lambda: hl.hss_apply_noalloc(A, X, Y),
+                 lambda: hl.hss_apply_group([A], X, [Y], ws)):
+        with pytest.raises(ValueError):
+            call()
+    assert len(calls) == 3
+
+
+def test_a_matrix_over_two_devices_has_no_device(hl, bound):
+    import torch
+    calls, elsewhere = bound
+    bf = torch.bfloat16
+    A = hl.HSSMatrix("csr", 3, 33, bf, U=elsewhere(torch.zeros(3, 2, dtype=bf)), Vt=torch.zeros(2, 33, dtype=bf),
+                     row_ptr=torch.zeros(4, dtype=torch.int32))
+    assert A.index is None
+    with pytest.raises(ValueError):
+        hl.hss_apply_noalloc(A, torch.zeros(1, 33, dtype=bf), torch.zeros(1, 3, dtype=bf))
+    assert not calls
+
+
+def test_gradients_refuse_inputs_and_workspaces_elsewhere(hl, bound, monkeypatch):
+    import torch
+    calls, elsewhere = bound
+    monkeypatch.setattr(hl, "_dev", lambda t: t.device)
+    monkeypatch.setattr(hl, "_stream", lambda device: 0)
+    bf = torch.bfloat16
+    A = _cpu_layer(hl, "csr")
+    X, G, ck = torch.zeros(5, 33, dtype=bf), torch.zeros(5, 3, dtype=bf), hl.MXTensor.empty("int8", 5, 33, "cpu")
+    hl.hss_grad(A, X, G), hl.hss_grad_ckpt(A, ck, G)
+    assert calls == ["hss_grad", "hss_grad_ckpt"]
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    calls_in = [lambda A=A: hl.hss_grad(A, X, elsewhere(G)), lambda A=A: hl.hss_grad(A, X, G, ws=elsewhere(ws)),
+                lambda A=A: hl.hss_grad(A, X, G, ws=ws[:1].expand(1 << 20)),
+                lambda A=A: hl.hss_grad_ckpt(A, ck, G, ws=elsewhere(ws)),
+                lambda A=A: hl.hss_grad_ckpt(A, ck, G, ws=ws[:1].expand(1 << 20))]
+    A.index = 1
+    calls_in += [lambda: hl.hss_grad(A, X, G), lambda: hl.hss_grad_ckpt(A, ck, G)]
+    for k, call in enumerate(calls_in):
+        A.index = 1 if k >= 5 else -1
+        with pytest.raises(ValueError):
+            call()
+    assert len(calls) == 2
