@@ -76,6 +76,12 @@ def _index(t: torch.Tensor) -> int:
     return index
 
 
+def _on(t: torch.Tensor):
+    """Scope with t's GPU current (nothing to do where it is, or for a CPU tensor, which the call then refuses)."""
+    index = t.get_device()
+    return contextlib.nullcontext() if index < 0 or index == _current_device() else torch.cuda.device(index)
+
+
 def _dev(t: torch.Tensor):
     if not t.is_cuda:
         raise ValueError("tensor must be on a GPU device")
@@ -171,16 +177,18 @@ def hss_split(W: torch.Tensor, fmt="csr", k: Optional[int] = None, frac=(5, 100)
         out.row_ptr = torch.empty(m + 1, dtype=torch.int32, device=dev)
         out.col_idx = torch.empty(max(out.k, 0), dtype=torch.int32, device=dev)
         out.values = torch.empty(max(out.k, 0), dtype=W.dtype, device=dev)
-        code = lib.hss_split(f, dt, m, n, _ptr(W), out.k, _ptr(out.row_ptr),
-                             _ptr(out.col_idx) if out.k > 0 else None,
-                             _ptr(out.values) if out.k > 0 else None, None, None, _ptr(res),
-                             _ptr(ws), ws_bytes, _stream(dev))
+        with _on(W):
+            code = lib.hss_split(f, dt, m, n, _ptr(W), out.k, _ptr(out.row_ptr),
+                                 _ptr(out.col_idx) if out.k > 0 else None,
+                                 _ptr(out.values) if out.k > 0 else None, None, None, _ptr(res),
+                                 _ptr(ws), ws_bytes, _stream(dev))
     else:
         out.k = (m * n) // 2 if k is None else int(k)
         out.nm_values = torch.empty((m, n // 2), dtype=W.dtype, device=dev)
         out.nm_meta = torch.empty((m, (n + 31) // 32), dtype=torch.int32, device=dev)
-        code = lib.hss_split(f, dt, m, n, _ptr(W), out.k, None, None, None, _ptr(out.nm_values),
-                             _ptr(out.nm_meta), _ptr(res), _ptr(ws), ws_bytes, _stream(dev))
+        with _on(W):
+            code = lib.hss_split(f, dt, m, n, _ptr(W), out.k, None, None, None, _ptr(out.nm_values),
+                                 _ptr(out.nm_meta), _ptr(res), _ptr(ws), ws_bytes, _stream(dev))
     check(code, "hss_split")
     if check_finite:
         check(hss_get_error(ws), "hss_split")
@@ -416,7 +424,8 @@ class HSSMatrix:
 def hss_apply_workspace_init(ws: torch.Tensor) -> torch.Tensor:
     """Put an apply workspace in its initial state (a kernel on the current
     stream); call once before its first apply."""
-    check(lib.hss_apply_workspace_init(_ptr(ws), ws.numel(), _stream(ws.device)), "hss_apply_workspace_init")
+    with _on(ws):
+        check(lib.hss_apply_workspace_init(_ptr(ws), ws.numel(), _stream(ws.device)), "hss_apply_workspace_init")
     return ws
 
 
@@ -544,8 +553,9 @@ def hss_csr_cols_to_u16(col_idx: torch.Tensor, n: int) -> torch.Tensor:
     if col_idx.dtype != torch.int32 or not col_idx.is_contiguous():
         raise ValueError("col_idx must be a contiguous int32 tensor")
     out = torch.empty(col_idx.numel(), dtype=torch.int16, device=dev)
-    check(lib.hss_csr_cols_to_u16(_ptr(col_idx), col_idx.numel(), int(n), _ptr(out), _stream(dev)),
-          "hss_csr_cols_to_u16")
+    with _on(col_idx):
+        check(lib.hss_csr_cols_to_u16(_ptr(col_idx), col_idx.numel(), int(n), _ptr(out), _stream(dev)),
+              "hss_csr_cols_to_u16")
     return out
 
 
@@ -579,8 +589,9 @@ def hss_concentration(W: torch.Tensor, perm: Optional[torch.Tensor] = None) -> t
     out = torch.empty(3, dtype=torch.float64, device=dev)
     if perm is not None and (perm.dtype != torch.int32 or perm.numel() != n or not perm.is_contiguous()):
         raise ValueError("perm must be a contiguous int32 tensor of n entries")
-    check(lib.hss_concentration(_DT[W.dtype], m, n, _ptr(W), _ptr(perm), _ptr(out), _ptr(ws), ws.numel(),
-                                _stream(dev)), "hss_concentration")
+    with _on(W):
+        check(lib.hss_concentration(_DT[W.dtype], m, n, _ptr(W), _ptr(perm), _ptr(out), _ptr(ws), ws.numel(),
+                                    _stream(dev)), "hss_concentration")
     return out
 
 
@@ -605,8 +616,9 @@ def hss_hier_pack(U, Vt, m: int, n: int, perm: Optional[torch.Tensor] = None):
     r_arr = (ctypes.c_int32 * 4)(*r)
     u_arr = (ctypes.c_void_p * 4)(*[_ptr(u) for u in U])
     v_arr = (ctypes.c_void_p * 4)(*[_ptr(v) for v in Vt])
-    check(lib.hss_hier_pack(_DT[dtype], int(m), int(n), r_arr, u_arr, v_arr, _ptr(perm), _ptr(Ucat), _ptr(Vtcat),
-                            _stream(dev)), "hss_hier_pack")
+    with _on(Ucat):
+        check(lib.hss_hier_pack(_DT[dtype], int(m), int(n), r_arr, u_arr, v_arr, _ptr(perm), _ptr(Ucat), _ptr(Vtcat),
+                                _stream(dev)), "hss_hier_pack")
     return Ucat, Vtcat
 
 
@@ -632,8 +644,9 @@ def hss_hier_pack_compact(U, Vt, m: int, n: int):
     r_arr = (ctypes.c_int32 * 4)(*r)
     u_arr = (ctypes.c_void_p * 4)(*[_ptr(u) for u in U])
     v_arr = (ctypes.c_void_p * 4)(*[_ptr(v) for v in Vt])
-    check(lib.hss_hier_pack_compact(_DT[dtype], int(m), int(n), r_arr, u_arr, v_arr, _ptr(Uc), _ptr(Vtc),
-                                    _stream(dev)), "hss_hier_pack_compact")
+    with _on(Uc):
+        check(lib.hss_hier_pack_compact(_DT[dtype], int(m), int(n), r_arr, u_arr, v_arr, _ptr(Uc), _ptr(Vtc),
+                                        _stream(dev)), "hss_hier_pack_compact")
     return Uc, Vtc
 
 
@@ -688,8 +701,9 @@ def hss_grad(A: HSSMatrix, X: torch.Tensor, G: torch.Tensor, dS=True, dU=True, d
         ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
     else:
         _check_ws(ws, index)
-    check(lib.hss_grad(ctypes.byref(A.struct), b, _ptr(X), _ptr(G), _ptr(out.get("dS")), _ptr(out.get("dU")),
-                       _ptr(out.get("dVt")), _ptr(ws), ws.numel(), _stream(dev)), "hss_grad")
+    with _on(X):
+        check(lib.hss_grad(ctypes.byref(A.struct), b, _ptr(X), _ptr(G), _ptr(out.get("dS")), _ptr(out.get("dU")),
+                           _ptr(out.get("dVt")), _ptr(ws), ws.numel(), _stream(dev)), "hss_grad")
     return out
 
 
@@ -711,8 +725,9 @@ def hss_csr_transpose(row_ptr, col_idx, m: int, n: int):
 def hss_gather_values(values: torch.Tensor, perm: torch.Tensor) -> torch.Tensor:
     """values[perm] on the device (bits copied)."""
     out = torch.empty(perm.numel(), dtype=values.dtype, device=values.device)
-    check(lib.hss_gather_values(_DT[values.dtype], perm.numel(), _ptr(values), _ptr(perm), _ptr(out),
-                                _stream(values.device)), "hss_gather_values")
+    with _on(values):
+        check(lib.hss_gather_values(_DT[values.dtype], perm.numel(), _ptr(values), _ptr(perm), _ptr(out),
+                                    _stream(values.device)), "hss_gather_values")
     return out
 
 
@@ -720,7 +735,8 @@ def hss_transpose(t: torch.Tensor) -> torch.Tensor:
     """A contiguous 2-D fp32 / bf16 device tensor transposed by the library."""
     rows, cols = t.shape
     out = torch.empty((cols, rows), dtype=t.dtype, device=t.device)
-    check(lib.hss_transpose(_DT[t.dtype], rows, cols, _ptr(t), _ptr(out), _stream(t.device)), "hss_transpose")
+    with _on(t):
+        check(lib.hss_transpose(_DT[t.dtype], rows, cols, _ptr(t), _ptr(out), _stream(t.device)), "hss_transpose")
     return out
 
 
@@ -730,7 +746,8 @@ def hss_nm24_to_csr(A: HSSMatrix):
     dev = A.nm_meta.device
     rp = torch.empty(A.m + 1, dtype=torch.int32, device=dev)
     ci = torch.empty(A.m * (A.n // 2), dtype=torch.int32, device=dev)
-    check(lib.hss_nm24_to_csr(A.m, A.n, _ptr(A.nm_meta), _ptr(rp), _ptr(ci), _stream(dev)), "hss_nm24_to_csr")
+    with _on(A.nm_meta):
+        check(lib.hss_nm24_to_csr(A.m, A.n, _ptr(A.nm_meta), _ptr(rp), _ptr(ci), _stream(dev)), "hss_nm24_to_csr")
     return rp, ci
 
 

@@ -334,3 +334,47 @@ def test_gradients_refuse_inputs_and_workspaces_elsewhere(hl, bound, monkeypatch
         with pytest.raises(ValueError):
             call()
     assert len(calls) == 2
+
+
+def test_backward_launches_on_the_device_of_its_tensors(hl, bound, monkeypatch):
+    """hss_backward with every tensor on another GPU than the current one: each
+    launch of its parts (transposes, workspace, gradients, apply) is made with
+    that GPU current."""
+    import contextlib
+
+    import torch
+    calls, elsewhere = bound
+    current, seen = [0], []
+
+    @contextlib.contextmanager
+    def device(index):
+        before, current[0] = current[0], index
+        yield
+        current[0] = before
+
+    class Lib:
+        def __getattr__(self, name):
+            real = getattr(hl._lib.lib, name)
+            if name.endswith("_size") or name in ("hss_csr_transpose", "hss_apply_group_workspace_size"):
+                return real
+            return lambda *a: seen.append((name, current[0])) or 0
+
+    new = lambda *a, dtype=None, device=None: elsewhere(torch.zeros(*a, dtype=dtype))
+    monkeypatch.setattr(hl, "lib", Lib())
+    monkeypatch.setattr(hl, "_current_device", lambda: current[0])
+    monkeypatch.setattr(hl, "_stream", lambda dev: 0)
+    monkeypatch.setattr(hl, "_dev", lambda t: t.device)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch, "empty", new)
+    monkeypatch.setattr(torch, "from_numpy", lambda a, f=torch.from_numpy: elsewhere(f(a)))
+    bf = torch.bfloat16
+    A = hl.HSSMatrix("csr", 3, 33, bf, U=elsewhere(torch.zeros(3, 2, dtype=bf)), Vt=elsewhere(torch.zeros(2, 33, dtype=bf)),
+                     row_ptr=elsewhere(torch.tensor([0, 1, 1, 2], dtype=torch.int32)),
+                     col_idx=elsewhere(torch.tensor([4, 7], dtype=torch.int32)), values=elsewhere(torch.zeros(2, dtype=bf)))
+    hl.hss_backward(A, elsewhere(torch.zeros(5, 33, dtype=bf)), elsewhere(torch.zeros(5, 3, dtype=bf)))
+    names = [n for n, _ in seen]
+    for name in ("hss_gather_values", "hss_transpose", "hss_grad", "hss_apply_workspace_init", "hss_apply"):
+        assert name in names
+    assert all(index == 1 for _, index in seen), seen
+    assert current == [0]
