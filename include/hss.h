@@ -301,19 +301,17 @@ hss_status hss_apply_workspace_size(const hss_matrix* A, int32_t b, size_t* byte
  *             even of the fp32 result.
  * ws: at least hss_apply_workspace_size() bytes, initialised ONCE by
  *     hss_apply_workspace_init before its first apply.  The fused decode
- *     kernel keeps state in it from call to call: a 32-bit call epoch, 64
- *     arrival counters (all in the first 16 KiB) and the tagged words through
- *     which its blocks hand T = V^T x to each other (a word is used only when
- *     its tag is the current epoch + 1, so a word left by an earlier call is
- *     never taken for this one's).  The caller must not write to the
- *     workspace after the init.  Any number of calls, with any matrices and
+ *     kernel keeps state in it from call to call: a call epoch and arrival
+ *     counters (in the first 32 KiB) and the tagged words through which its
+ *     blocks hand T = V^T x to each other (a word is used only when its tag is
+ *     the current epoch's, so a word left by one of the 4,128,767 calls before
+ *     is never taken for this one's; a tag is a signalling NaN, which nothing
+ *     that another route computes and leaves there can be).  The caller must
+ *     not write to the workspace after the init.  Any number of calls, with any matrices and
  *     batch sizes, may share one workspace if they are ORDERED (one stream,
  *     or events between streams); two calls that overlap in time must use
  *     different workspaces -- overlapping calls on one workspace can make
- *     both return wrong values with no error.  HSS_MX4 matrices keep no state
- *     in a workspace and leave dense data in it: one that served them is
- *     initialised again before it serves other matrices.  The epoch wraps after 2^32 - 1
- *     calls and skips the tag that a zero-filled word carries.
+ *     both return wrong values with no error.
  * Execution: bf16 2:4 with 3 <= b <= 64 (n % 128 == 0; nm_values, nm_meta
  * and X 16-byte aligned) runs on the sparse matrix cores: S's stored values
  * and 2-bit indices are the operands of v_smfmac as they are, with fp32

@@ -456,3 +456,66 @@ def test_apply_group_col16(H):
     y16 = H.hss_apply_group([A.with_col16() for A in mats], X)
     for a, c in zip(y32, y16):
         assert O.bits_equal(to_host(a), to_host(c))
+
+
+@pytest.mark.parametrize("b", [1, 2])
+def test_apply_tags_are_no_number(H, b):
+    """The tag half of every T word a call leaves is 0 or a signalling NaN (as
+    fp32, and its upper half as bf16), which no result, zero or index of
+    another call's buffers can be."""
+    A, xs, _ = _tagged_layer(H, b, r=24)
+    ws = H.apply_workspace(H.hss_apply_workspace_size(A, b), "cuda")
+    for x in xs:
+        H.hss_apply(A, x, ws=ws)
+    words = to_host(ws)[32768:32768 + (len(to_host(ws)) - 32768) // 8 * 8].view(np.uint32)
+    tags = words[1::2][words[1::2] != 0]
+    assert len(tags) >= 8 * 24 * b
+    for bits, quiet, inf in ((tags, 0x400000, 0x7F800000), (tags >> 16, 0x40, 0x7F80)):
+        assert np.all(bits & inf == inf) and np.all(bits & quiet == 0) and np.all(bits & (quiet - 1) != 0)
+
+
+def test_apply_epoch_wraps(H):
+    """Calls around the last epoch, 63 * 2^16 - 1, whose tags are those of the
+    first ones again."""
+    import torch
+    A, xs, expect = _tagged_layer(H, 1, r=24)
+    ws = H.apply_workspace(H.hss_apply_workspace_size(A, 1), "cuda")
+    epoch = ws[:4].view(torch.int32)
+    epoch.fill_((63 << 16) - 3)
+    for k in range(6):
+        assert O.bits_equal(to_host(H.hss_apply(A, xs[k % 3], ws=ws)), expect[k % 3]), k
+        assert int(epoch) == ((63 << 16) - 2 + k) % (63 << 16)
+
+
+def _tagged_layer(H, b, r, m=1030, n=512):
+    W = syn.random_matrix(m, n, O.BF16, seed=61, kind="t3")
+    ref = O.split_csr(W, O.BF16, O.topk_count(m, n, 5, 100))
+    A = _matrix(H, "csr", O.BF16, m, n, ref, *_factors(m, n, r, O.BF16, 62))
+    xs = [to_dev(syn.random_matrix(b, n, O.BF16, seed=63 + i, kind="normal", scale=1.0), O.BF16) for i in range(3)]
+    return A, xs, [to_host(H.hss_apply(A, x)) for x in xs]
+
+
+@pytest.mark.parametrize("kind", ["csr", "mx"])
+@pytest.mark.parametrize("b", [1, 2])
+def test_apply_after_dense_data_in_its_workspace(H, b, kind):
+    """A batch whose dense weights (a value, then a zero, all along) fill the
+    workspace, then a decode call on it, at the call count whose bits are that
+    value: every result equals the one from a fresh workspace."""
+    import torch
+    A, xs, expect = _tagged_layer(H, b, r=40)
+    dm, dn, db = 64, 1024, 300
+    row_ptr = torch.arange(0, dm * dn // 2 + 1, dn // 2, dtype=torch.int32, device="cuda")
+    cols = torch.arange(0, dn, 2, dtype=torch.int32, device="cuda").repeat(dm)
+    values = torch.empty(len(cols), dtype=torch.bfloat16, device="cuda")
+    mx = H.hss_mx_quantize(torch.zeros(dm, dn, device="cuda"), "fp4") if kind == "mx" else None
+    D = H.HSSMatrix("csr", dm, dn, torch.bfloat16, row_ptr=row_ptr, col_idx=cols, values=values, mx=mx)
+    dx = torch.ones(db, dn, dtype=torch.bfloat16, device="cuda")
+    ws = H.apply_workspace(max(H.hss_apply_workspace_size(A, b), H.hss_apply_workspace_size(D, db)), "cuda")
+    y = torch.empty((b, A.m), dtype=torch.bfloat16, device="cuda")
+    one = 0x3F80                                                  # bf16's 1
+    for _ in range(one - 1):
+        H.hss_apply(A, xs[0], y, ws)
+    for k in range(12):                                           # 1, and the values after it
+        values.view(torch.int16).fill_(one + k)
+        H.hss_apply(D, dx, ws=ws)
+        assert O.bits_equal(to_host(H.hss_apply(A, xs[k % 3], ws=ws)), expect[k % 3]), k
