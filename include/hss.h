@@ -355,8 +355,9 @@ hss_status hss_apply(const hss_matrix* A, int32_t b, const void* X, void* Y, voi
  * hss_apply, with the workspace replaced by a scratch array that the library
  * holds in each GPU's memory: hss_noalloc_scratch_bytes() bytes (16 MiB),
  * kept until the process ends, and cleared by the first call on each device
- * (on that call's stream); HSS_MX4 matrices have one of the same size of
- * their own.  The call allocates and frees nothing.
+ * (on that call's stream; one of an HSS_MX4 matrix, which needs no cleared
+ * scratch, leaves that to the first other call).  The call allocates and frees
+ * nothing.
  * HSS_ERR_WORKSPACE when the route this call takes needs more workspace
  * than the scratch holds (e.g. a large CSR layer densified for the matrix
  * cores at prefill batches): use hss_apply with a workspace of

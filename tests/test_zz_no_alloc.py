@@ -88,3 +88,23 @@ def test_noalloc_refuses_a_route_larger_than_its_scratch(H):
     code = H._lib.lib.hss_apply_noalloc(ctypes.byref(A.struct), 2048, X.data_ptr(), Y.data_ptr(),
                                         torch.cuda.current_stream().cuda_stream)
     assert code == H._lib.HSS_ERR_WORKSPACE
+
+
+def test_noalloc_scratch_is_one_array_for_every_kind(H):
+    """A microscaled layer whose call fills the scratch far past the decode
+    kernel's words, and leaves dense weights there, between decode calls: the
+    library holds one scratch per GPU, and every call gives the bits of the call
+    with a workspace of its own."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(5)
+    W = torch.randn(500, 1024, device="cuda", generator=g).bfloat16()
+    sp = H.hss_split(W, "csr")
+    D = H.HSSMatrix.from_split(sp, mx=H.hss_mx_quantize(W, "fp4"))
+    A = H.HSSMatrix.from_split(sp, U=torch.randn(500, 40, device="cuda", generator=g).bfloat16(),
+                               Vt=torch.randn(40, 1024, device="cuda", generator=g).bfloat16())
+    assert 2 << 20 < H.hss_apply_workspace_size(D, 300) <= H._lib.lib.hss_noalloc_scratch_bytes()
+    for rep in range(4):
+        for M, b in ((D, 300), (A, 1), (D, 40), (A, 2), (A, 1), (D, 1), (A, 1)):
+            X = torch.randn(b, 1024, device="cuda", generator=g).bfloat16()
+            Y = torch.empty((b, 500), dtype=torch.bfloat16, device="cuda")
+            assert torch.equal(H.hss_apply_noalloc(M, X, Y), H.hss_apply(M, X)), (rep, b)
