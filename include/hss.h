@@ -291,7 +291,10 @@ typedef struct hss_matrix {
 hss_status hss_csr_cols_to_u16(const int32_t* col_idx, int64_t nnz, int32_t n, uint16_t* out,
                                hipStream_t stream);
 
-/* Workspace bytes hss_apply needs for this matrix and batch size. */
+/* Workspace bytes hss_apply needs for this matrix and batch size; for an
+ * HSS_MX4 matrix also for every smaller batch.  (Other matrices can need more
+ * at a smaller batch, on the matrix cores: ask for each that is to be served,
+ * and take the largest.) */
 hss_status hss_apply_workspace_size(const hss_matrix* A, int32_t b, size_t* bytes);
 
 /* Y (b x m, row-major) = X (b x n, row-major) times (S + U V^T)^T, plus the

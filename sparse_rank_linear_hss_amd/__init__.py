@@ -359,7 +359,7 @@ class HSSMatrix:
         on = {t.get_device() for t in held if t is not None}
         self.index = on.pop() if len(on) == 1 else None  # the GPU that holds all of it
         self.nnz = int(nnz if nnz is not None else (values.numel() if values is not None else 0))
-        self._ws = {}
+        self._ws, self._ws_sizes = {}, {}
         s = HssMatrixStruct()
         s.fmt, s.dtype = self.fmt, _DT[dtype]
         s.m, s.n, s.r, s.flags = self.m, self.n, self.r, self.flags
@@ -406,7 +406,9 @@ class HSSMatrix:
         its workspace from call to call, so calls that may overlap in time --
         those on different streams -- must not share one.  Calls on one
         stream are ordered and share it safely."""
-        size = hss_apply_workspace_size(self, b)
+        size = self._ws_sizes.get(b)
+        if size is None:
+            size = self._ws_sizes[b] = hss_apply_workspace_size(self, b)
         if device is None:
             held = [t for t in (self.U, self.row_ptr, self.values, self.nm_values, self.dq_codes) if t is not None]
             device = held[0].device

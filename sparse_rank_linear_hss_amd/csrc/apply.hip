@@ -39,6 +39,7 @@ int decode_max_cols(const hss_matrix* A);
 int decode_dq_max_cols(const hss_matrix* A);
 void launch_decode_dq(const hss_matrix* A, int bc, const void* X, void* Y, hipStream_t s);
 size_t mx_apply_ws_bytes(const hss_matrix* A, int b);
+size_t mx_apply_ws_bytes_up_to(const hss_matrix* A, int b);
 hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s);
 static bool is_mx(const hss_matrix* A) { return (A->flags & HSS_MX4) != 0; }
 static bool is_dq(const hss_matrix* A) { return (A->flags & HSS_DQ4) != 0; }
@@ -136,6 +137,12 @@ size_t apply_ws_bytes(const hss_matrix* A0, int b) {
   return decode_ctl_bytes() + (dec > mx ? dec : mx);
 }
 
+// What hss_apply_workspace_size answers: for HSS_MX4 enough for every smaller
+// batch too.
+size_t apply_ws_query_bytes(const hss_matrix* A, int b) {
+  return is_mx(A) ? decode_ctl_bytes() + mx_apply_ws_bytes_up_to(A, b) : apply_ws_bytes(A, b);
+}
+
 // Workspace bytes of the route this call takes (hss_apply_workspace_size
 // covers every route a call could be forced onto).
 size_t apply_route_ws_bytes(const hss_matrix* A0, int b, const void* X) {
@@ -216,12 +223,12 @@ hss_status launch_zero_fill(void* p, size_t bytes, hipStream_t s) {
 // Grouped apply of G matrices sharing X.  Decode batches: one fused launch
 // per pass over all G matrices (their T words side by side after the control
 // region).  Matrix-core batches: one apply per matrix, in order.
-size_t apply_group_ws_bytes(const hss_matrix* const* A, int G, int b) {
+size_t apply_group_ws_bytes(const hss_matrix* const* A, int G, int b, bool query) {
   size_t dec = 0, one = 0;
   for (int g = 0; g < G; ++g) {
     if (is_dq(A[g])) continue;  // the dense-and-sparse kernel uses no workspace
     if (!is_mx(A[g])) dec += decode_t_bytes(A[g]);
-    const size_t a = apply_ws_bytes(A[g], b) - decode_ctl_bytes();
+    const size_t a = (query ? apply_ws_query_bytes(A[g], b) : apply_ws_bytes(A[g], b)) - decode_ctl_bytes();
     one = one > a ? one : a;
   }
   return decode_ctl_bytes() + (dec > one ? dec : one);

@@ -11,8 +11,9 @@ enum : int { G256_BF16 = 0, G256_PART = 1, G256_DS = 2 /* + the kind of S's patt
 // of whole 16-byte chunks (aligned bases), 32-bit byte offsets.
 bool gemm256_ok(int M, int N, int K1, int lda, int ldb1, int K2, int ldb2);
 
-// Bytes of the partial products where K is split.
-size_t gemm256_part_bytes(int M, int N, int K);
+// Bytes of the partial products where K is split, enough for every N from
+// `from` to N (of one count of tiles: 64 t < from <= N <= 64 (t + 1)).
+size_t gemm256_part_bytes(int M, int from, int N, int K);
 
 // C[n * ldc + m] (bf16) = A . [B1 | B2]^T: A's rows hold K1 + K2 columns
 // (K2 = 0: no second segment).

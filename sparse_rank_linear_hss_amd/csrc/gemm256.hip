@@ -377,9 +377,11 @@ bool gemm256_ok(int M, int N, int K1, int lda, int ldb1, int K2, int ldb2) {
   return K1 > 0 && K1 % 64 == 0 && K2 % 64 == 0 && fits(M, lda) && fits(N, ldb1) && (K2 == 0 || fits(N, ldb2));
 }
 
-size_t gemm256_part_bytes(int M, int N, int K) {
-  const G256Cfg c = g256_cfg(M, N, K);
-  return c.splits > 1 ? (size_t)c.splits * N * ((M + 3) / 4 * 4) * 4 : 0;
+size_t gemm256_part_bytes(int M, int from, int N, int K) {
+  // as N grows among the same tiles, only the cost of the partial products
+  // does, by its number of them: the choice moves to fewer
+  const int splits = std::max(g256_cfg(M, from, K).splits, g256_cfg(M, N, K).splits);
+  return splits > 1 ? (size_t)splits * N * ((M + 3) / 4 * 4) * 4 : 0;
 }
 
 template <int FN, int OUT>

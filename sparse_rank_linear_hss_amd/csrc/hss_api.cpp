@@ -235,7 +235,7 @@ hss_status hss_apply_workspace_size(const hss_matrix* A, int32_t b, size_t* byte
   if (!bytes) return HSS_ERR_INVALID_ARG;
   hss_status st = check_matrix(A, b);
   if (st != HSS_OK) return st;
-  *bytes = hss::apply_ws_bytes(A, b);
+  *bytes = hss::apply_ws_query_bytes(A, b);
   return HSS_OK;
 }
 
@@ -278,7 +278,7 @@ hss_status hss_apply_group_workspace_size(const hss_matrix* const* A, int32_t G,
   if (!bytes) return HSS_ERR_INVALID_ARG;
   const hss_status st = check_group(A, G, b);
   if (st != HSS_OK) return st;
-  *bytes = hss::apply_group_ws_bytes(A, G, b);
+  *bytes = hss::apply_group_ws_bytes(A, G, b, true);
   return HSS_OK;
 }
 
@@ -296,7 +296,7 @@ hss_status hss_apply_group(const hss_matrix* const* A, int32_t G, int32_t b, con
     for (int h = 0; h < g; ++h)
       if (overlap(Y[h], (size_t)b * A[h]->m * es, Y[g], yb)) return HSS_ERR_INVALID_ARG;
   }
-  if (!ws || ws_bytes < hss::apply_group_ws_bytes(A, G, b)) return HSS_ERR_WORKSPACE;
+  if (!ws || ws_bytes < hss::apply_group_ws_bytes(A, G, b, false)) return HSS_ERR_WORKSPACE;
   return hss::launch_apply_group(A, G, b, X, Y, ws, stream);
 }
 

@@ -190,7 +190,9 @@ struct MxPlan {
   size_t w, x, vt, tp, tb, part, total;
 };
 
-static MxPlan plan_mx(const hss_matrix* A, int b) {
+// from: the least batch that the workspace is to serve besides b (b's own
+// plan, or one of the same 64 columns).
+static MxPlan plan_mx(const hss_matrix* A, int b, int from) {
   MxPlan p;
   const int m = A->m, n = A->n, r = A->r;
   p.np = (n + 63) & ~63;
@@ -205,14 +207,28 @@ static MxPlan plan_mx(const hss_matrix* A, int b) {
   p.vt = take((size_t)r * p.np * 2);
   p.tp = take((size_t)p.zt * b * p.rp * 4);
   p.tb = take((size_t)b * p.rp * 4);
-  p.part = take(std::max(gemm_bf16x2_part_bytes(m, b, p.np, 2 * p.rp, m), gemm256_part_bytes(m, b, p.np + 2 * p.rp)));
+  p.part = take(std::max(gemm_bf16x2_part_bytes(m, b, p.np, 2 * p.rp, m), gemm256_part_bytes(m, from, b, p.np + 2 * p.rp)));
   p.total = off;
   return p;
 }
 
 size_t mx_apply_ws_bytes(const hss_matrix* A, int b) {
   if (mx_skinny_supported(A, b)) return mx_skinny_ws_bytes(A, b);
-  return mx_gemm_supported(b) ? mx_gemm_ws_bytes(A, b) : plan_mx(A, b).total;
+  return mx_gemm_supported(b) ? mx_gemm_ws_bytes(A, b) : plan_mx(A, b, b).total;
+}
+
+// The most that a batch of up to b columns needs: a plan depends on b through
+// its count of 16 columns (of 64 beyond the middle route) and grows with b
+// among those of one count, but for the K splits of the large products.
+size_t mx_apply_ws_bytes_up_to(const hss_matrix* A, int b) {
+  size_t most = 0;
+  for (int c = 1; c <= b && c < 16; ++c) most = std::max(most, mx_apply_ws_bytes(A, c));
+  int c = 16;
+  for (; c < b && mx_gemm_supported(c); c += 16) most = std::max(most, mx_apply_ws_bytes(A, c));
+  if (c >= b) return std::max(most, mx_apply_ws_bytes(A, b));
+  // c is the first multiple of 16 beyond the middle route, whose last batch is a multiple of 64
+  for (int from = c - 15; from <= b; from += 64) most = std::max(most, plan_mx(A, std::min(from + 63, b), from).total);
+  return most;
 }
 
 static bool rows_ok(const void* p, int cols) { return (uintptr_t)p % 16 == 0 && cols % 64 == 0; }
@@ -220,7 +236,7 @@ static bool rows_ok(const void* p, int cols) { return (uintptr_t)p % 16 == 0 && 
 hss_status launch_mx_apply(const hss_matrix* A, int b, const void* X, void* Y, void* ws, hipStream_t s) {
   if (mx_skinny_supported(A, b)) return launch_mx_skinny(A, b, X, Y, ws, s);
   if (mx_gemm_supported(b)) return launch_mx_gemm(A, b, X, Y, ws, s);
-  const MxPlan p = plan_mx(A, b);
+  const MxPlan p = plan_mx(A, b, b);
   char* base = static_cast<char*>(ws);
   auto u16 = [&](size_t off) { return reinterpret_cast<uint16_t*>(base + off); };
   auto f32 = [&](size_t off) { return reinterpret_cast<float*>(base + off); };

@@ -428,3 +428,17 @@ def test_captured_step_replays(H, b):
         g = H.hss_grad_ckpt(A, H.hss_mx_quantize(X, "int8"), G)
         want = e + [g["dS"], g["dU"], g["dVt"]]
         assert all(torch.equal(a, w) for a, w in zip(got, want))
+
+
+def test_workspace_sized_for_the_largest_batch(H):
+    """One workspace, of the size of the largest batch, for every smaller one:
+    the bits of calls with workspaces of their own."""
+    A = _layer(H, 400, 1536, 40, seed=31)[0]
+    At = H.hss_transposed_layer(A)
+    for L in (A, At):
+        for top in (65, 129, 600):
+            ws = H.apply_workspace(H.hss_apply_workspace_size(L, top), "cuda")
+            for b in (1, 16, 17, 64, 65, 128, 129, 256, 257, 385, 559, 600):
+                if b <= top:
+                    X = to_dev(syn.random_matrix(b, L.n, BF, seed=b, kind="normal", scale=1.0), BF)
+                    assert O.bits_equal(to_host(H.hss_apply(L, X, ws=ws)), to_host(H.hss_apply(L, X)))

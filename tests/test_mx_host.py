@@ -378,3 +378,28 @@ def test_backward_launches_on_the_device_of_its_tensors(hl, bound, monkeypatch):
         assert name in names
     assert all(index == 1 for _, index in seen), seen
     assert current == [0]
+
+
+SIZES = [(4096, 4096, 64, 1000, 16), (4096, 4096, 0, 0, 16), (4096, 4096, 64, 1000, 48), (8192, 8192, 512, 1000, 16),
+         (512, 4096, 0, 0, 16), (11000, 640, 24, 3, 16), (4096, 11008, 64, 5, 48), (33, 700, 900, 7, 16), (1, 1, 0, 0, 16)]
+
+
+@pytest.mark.parametrize("case", SIZES, ids=["x".join(map(str, c)) for c in SIZES])
+def test_a_workspace_serves_every_smaller_batch(hl, case):
+    """hss_apply_workspace_size never goes down as b goes up, for one matrix and
+    for a group, and is never less than a call asks for."""
+    lib, WS = hl._lib.lib, hl._lib.HSS_ERR_WORKSPACE
+    m, n, r, nnz, flags = case
+    s = _mx(hl, m=m, n=n, r=r, nnz=nnz, flags=flags)
+    P = ctypes.POINTER(hl._lib.HssMatrixStruct)
+    pair = (P * 2)(ctypes.pointer(s), ctypes.pointer(_mx(hl, m=2 * m, n=n, r=0, nnz=0, flags=flags)))
+    out, last, last_pair = ctypes.c_size_t(), 0, 0
+    for b in range(1, 2049):
+        assert lib.hss_apply_workspace_size(ctypes.byref(s), b, ctypes.byref(out)) == 0
+        assert out.value >= last, b
+        last = out.value
+        if b % 16 in (0, 1):
+            assert lib.hss_apply_group_workspace_size(pair, 2, b, ctypes.byref(out)) == 0
+            assert out.value >= max(last, last_pair), b
+            last_pair = out.value
+    assert lib.hss_apply(ctypes.byref(s), 2048, FAKE * (1 << 14), FAKE * (1 << 16), FAKE, 32768 - 1, None) == WS
