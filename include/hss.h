@@ -86,8 +86,8 @@ int hss_version(void);
  *   HSS_OPT_GRAD_DS_ROUTE (HSS_GRAD_DS_ROUTE = sparse | dense): 0 = by batch
  *       size (default; hss_grad_ckpt: by estimated time), 1 = sampled product,
  *       2 = dense G^T X, of which S's entries are kept.  Query
- *       hss_grad_workspace_size (hss_grad_ckpt_workspace_size) with the same
- *       setting.
+ *       hss_grad_workspace_size with the same setting
+ *       (hss_grad_ckpt_workspace_size covers both routes).
  *   HSS_OPT_DECODE_SPIN   (HSS_DECODE_SPIN = count): polls of a stale T word
  *       before a block computes that T row itself (default 4096).
  *   HSS_OPT_DECODE_MERGED (HSS_DECODE_MERGED = 0): 1 (default) = T rows
@@ -622,7 +622,8 @@ hss_status hss_mx_dequantize(int32_t fmt, int32_t dt, int32_t rows, int32_t cols
  *   the dS route as hss_grad.  X' V and G U are kept as three bf16 terms (24
  *   significant bits), so every output carries fp32 precision.  The same
  *   inputs give the same bits on every call.
- *   ws: at least hss_grad_ckpt_workspace_size() bytes (no state kept).
+ *   ws: at least hss_grad_ckpt_workspace_size() bytes (no state kept), which
+ *   serve every smaller batch too.
  *   HSS_ERR_UNSUPPORTED: as hss_grad, or max(m, n) round64(b) * 2 or
  *   3 round32(r) max(m, n, round64(b)) >= 2^31.
  *   HSS_ERR_INVALID_ARG: as hss_grad, codes not 16-byte aligned.

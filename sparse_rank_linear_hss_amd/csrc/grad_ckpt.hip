@@ -212,10 +212,10 @@ static int uv_splits(int r, int m, int n, int ldt) {
   return std::max(1, std::min((511 + tiles) / tiles, ldt / 512));
 }
 
-static CkPlan plan_ck(const hss_matrix* A, int b) {
+static CkPlan plan_ck(const hss_matrix* A, int b, bool dense) {
   CkPlan p;
   const int m = A->m, n = A->n, r = A->r;
-  p.dense = dense_ds(A, b);
+  p.dense = dense;
   p.ldt = p.dense ? (b + 63) & ~63 : round32(b);  // whole stages of k_gemm256
   p.np = round32(n);
   p.mp = round32(m);
@@ -240,13 +240,22 @@ static CkPlan plan_ck(const hss_matrix* A, int b) {
   return p;
 }
 
-size_t grad_ckpt_ws_bytes(const hss_matrix* A, int b) { return plan_ck(A, b).total; }
+size_t grad_ckpt_ws_bytes(const hss_matrix* A, int b) { return plan_ck(A, b, dense_ds(A, b)).total; }
+
+// The most that a batch of up to b columns needs, on either route of dS: the
+// dense one has the longer rows and a table more; its plan depends on b through
+// its count of 64 columns, and grows with b among those of one count.
+size_t grad_ckpt_ws_bytes_up_to(const hss_matrix* A, int b) {
+  size_t most = plan_ck(A, b, true).total;
+  for (int c = 64; c < b; c += 64) most = std::max(most, plan_ck(A, c, true).total);
+  return most;
+}
 
 static bool rows_ok(const void* p, int cols) { return (uintptr_t)p % 16 == 0 && cols % 32 == 0; }
 
 hss_status launch_grad_ckpt(const hss_matrix* A, int b, const void* codes, const uint8_t* scales, const void* G,
                             float* dS, float* dU, float* dVt, void* ws, hipStream_t s) {
-  const CkPlan p = plan_ck(A, b);
+  const CkPlan p = plan_ck(A, b, dense_ds(A, b));
   char* base = static_cast<char*>(ws);
   auto u16 = [&](size_t off) { return reinterpret_cast<uint16_t*>(base + off); };
   auto f32 = [&](size_t off) { return reinterpret_cast<float*>(base + off); };

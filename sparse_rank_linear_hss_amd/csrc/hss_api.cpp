@@ -26,6 +26,7 @@ hss_status launch_mx_quantize(int fmt, int dt, int rows, int cols, const void* s
 hss_status launch_mx_dequantize(int fmt, int dt, int rows, int cols, const void* codes, const uint8_t* scales,
                                 void* dst, hipStream_t s);
 size_t grad_ckpt_ws_bytes(const hss_matrix* A, int b);
+size_t grad_ckpt_ws_bytes_up_to(const hss_matrix* A, int b);
 hss_status launch_grad_ckpt(const hss_matrix* A, int b, const void* codes, const uint8_t* scales, const void* G,
                             float* dS, float* dU, float* dVt, void* ws, hipStream_t s);
 }  // namespace hss
@@ -495,7 +496,7 @@ hss_status hss_grad_ckpt_workspace_size(const hss_matrix* A, int32_t b, size_t* 
   if (!bytes) return HSS_ERR_INVALID_ARG;
   const hss_status st = check_grad_ckpt(A, b);
   if (st != HSS_OK) return st;
-  *bytes = hss::grad_ckpt_ws_bytes(A, b);
+  *bytes = hss::grad_ckpt_ws_bytes_up_to(A, b);
   return HSS_OK;
 }
 

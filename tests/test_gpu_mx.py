@@ -442,3 +442,18 @@ def test_workspace_sized_for_the_largest_batch(H):
                 if b <= top:
                     X = to_dev(syn.random_matrix(b, L.n, BF, seed=b, kind="normal", scale=1.0), BF)
                     assert O.bits_equal(to_host(H.hss_apply(L, X, ws=ws)), to_host(H.hss_apply(L, X)))
+
+
+def test_gradient_workspace_sized_for_the_largest_batch(H, hss_opt):
+    """One workspace, of the size of the largest batch, for smaller ones and on
+    either route of dS: the bits of calls with workspaces of their own."""
+    import torch
+    A = _layer(H, 700, 1300, 33, seed=32, frac=(3, 100))[0]
+    ws = H.grad_ckpt_workspace(A, 1409, "cuda")
+    for route in ("auto", "sparse", "dense"):
+        hss_opt("grad_ds_route", route)
+        for b in (1, 64, 257, 513, 1281, 1408, 1409):
+            ck = H.hss_mx_quantize(to_dev(syn.random_matrix(b, A.n, BF, seed=b, kind="normal", scale=1.0), BF), "int8")
+            G = to_dev(syn.random_matrix(b, A.m, BF, seed=b + 1, kind="normal", scale=1.0), BF)
+            got, want = H.hss_grad_ckpt(A, ck, G, ws=ws), H.hss_grad_ckpt(A, ck, G)
+            assert all(torch.equal(got[k], want[k]) for k in want), (route, b)

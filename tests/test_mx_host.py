@@ -403,3 +403,23 @@ def test_a_workspace_serves_every_smaller_batch(hl, case):
             assert out.value >= max(last, last_pair), b
             last_pair = out.value
     assert lib.hss_apply(ctypes.byref(s), 2048, FAKE * (1 << 14), FAKE * (1 << 16), FAKE, 32768 - 1, None) == WS
+
+
+@pytest.mark.parametrize("case", [(4096, 4096, 64, 800000), (8192, 8192, 128, 2000000), (1501, 2777, 41, 80000), (64, 11008, 40, 7000)],
+                         ids=lambda c: f"{c[0]}x{c[1]}")
+def test_a_gradient_workspace_serves_every_smaller_batch(hl, case):
+    """hss_grad_ckpt_workspace_size never goes down as b goes up, and does not
+    depend on the route of dS."""
+    lib, out = hl._lib.lib, ctypes.c_size_t()
+    m, n, r, nnz = case
+    s = _mx(hl, m=m, n=n, r=r, nnz=nnz, flags=0, dq_codes=None, dq_levels=None)
+    sizes = []
+    for b in range(1, 2049):
+        assert lib.hss_grad_ckpt_workspace_size(ctypes.byref(s), b, ctypes.byref(out)) == 0
+        sizes.append(out.value)
+    assert sizes == sorted(sizes)
+    for route in ("sparse", "dense"):
+        with hl.option("grad_ds_route", route):
+            for b in (1, 33, 600, 2048):
+                assert hl._lib.lib.hss_grad_ckpt_workspace_size(ctypes.byref(s), b, ctypes.byref(out)) == 0
+                assert out.value == sizes[b - 1]
