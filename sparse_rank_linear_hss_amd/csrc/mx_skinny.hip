@@ -643,10 +643,18 @@ hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, 
   // X in operand order: a load is then 1 KiB in a row, where rows of X make a
   // line of every lane's 64 bytes (us in all, 5 - 13 columns: 2731 x 5003
   // 12.3 against 13.7, 4096 x 11008 18.3 against 21.9, 8192^2 23.1 against
-  // 25.5).  With neither S nor a low-rank term it would cost a launch of its
-  // own: 2731 x 2528 5.7 against 4.9, x 5024 7.7 against 7.3, 4096^2 7.5
-  // against 7.9; so there only for long rows, or rows off the 16-byte grid.
-  const bool need_xo = !gemv && b > 1 && (r > 0 || need_xt || n > 5120 || n % 8 != 0 || (uintptr_t)X % 16 != 0);
+  // 25.5).  With neither S nor a low-rank term it costs a launch of its own,
+  // about 2 us, which pays only where every block reads much of X (and for rows
+  // off the 16-byte grid).  D alone, us for the rows / the copy, in graphs over
+  // 0.4 GB of matrices: 4096 x 4096, 13 columns 7.4 / 7.9, 16 8.1 / 8.1; 4096 x
+  // 8192, 5 columns 10.4 / 12.2, 8 11.4 / 12.2, 13 12.7 / 12.2; 4096 x 11008, 5
+  // columns 12.0 / 14.2, 8 13.7 / 14.1, 13 16.0 / 14.2.  With more blocks than
+  // fit at once (grid > 512) from a smaller X on: 11008 x 2528, 13 columns 12.0
+  // / 10.9; 11008 x 4096, 8 columns 14.9 / 15.0, 13 17.2 / 14.8; 11008 x 8192,
+  // 5 columns 25.6 / 27.8, 8 29.7 / 27.9.
+  const unsigned grid = (unsigned)((m + 15) / 16);
+  const bool long_x = (int64_t)b * n > (grid > 512 ? 40960 : 65536);
+  const bool need_xo = !gemv && b > 1 && (r > 0 || need_xt || long_x || n % 8 != 0 || (uintptr_t)X % 16 != 0);
   MxPrep pr = p.prep;
   pr.X = a.X;
   pr.Vt = static_cast<const uint16_t*>(A->Vt);
@@ -675,7 +683,6 @@ hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, 
     }
     return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
   }
-  const unsigned grid = (unsigned)((m + 15) / 16);
   const size_t tl = r > 0 ? (size_t)b * 2 * (a.rp + 8) * 2 : 0;
   // Four waves a block where rows are short or the blocks fill the chip anyway,
   // else eight (4096 x 11008, 8 columns, D alone: 13.5 us; 16 waves 16.1).  A
