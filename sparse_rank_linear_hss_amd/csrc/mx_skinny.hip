@@ -667,8 +667,14 @@ hss_status launch_mx_skinny(const hss_matrix* A, int b, const void* X, void* Y, 
   a.Xo = pr.Xo;
   if (gemv) {
     const size_t lds = (size_t)(b > 2 ? 4 : b) * gv_plane_bytes(n) + (size_t)b * a.rp * 4;
-    // two rows a wave while that leaves every SIMD a wave or two, else four
-    const bool four = m > 8192;
+    // Two rows a wave, four where the rows are many: fewer waves then read X
+    // from LDS (us at two / four, D alone, in graphs over 0.4 GB of matrices:
+    // n 4096, one column 8192 rows 5.9 / 6.3, 9216 6.5 / 7.1, 11008 7.2 / 7.3,
+    // 16384 9.5 / 9.0, 32768 15.1 / 14.7; two columns 9216 7.7 / 8.2, 11008 8.5 /
+    // 8.3, 16384 10.8 / 10.4; four columns 6144 8.0 / 8.5, 8192 9.3 / 8.8, 11008
+    // 12.1 / 11.0, 16384 15.0 / 13.6.  n 1024 alike.  The one exception: n
+    // 8192, one column, 16384 rows 15.3 / 16.4).
+    const bool four = m > (b > 2 ? 8192 : 12288);
     const unsigned gv = (unsigned)((m + kGvWaves * (four ? 4 : 2) - 1) / (kGvWaves * (four ? 4 : 2)));
     const dim3 block(64 * kGvWaves);
     if (b == 1) {

@@ -53,7 +53,7 @@ def _check(H, A, W, X, met=None):
 # One to four columns on the vector units: two and four rows a wave, whole and
 # ragged rows of X and U, rows of S of more than 64 entries, b = 3 in a kernel of four
 GEMV = [(1030, 1024, 64, 0.1), (1031, 1027, 37, 0.02), (8195, 4100, 0, 0.003), (9001, 1027, 37, 0.01), (8200, 1024, 64, 0.0),
-        (8193, 2056, 0, 0.09), (5, 1500, 3, 0.2)]
+        (8193, 2056, 0, 0.09), (5, 1500, 3, 0.2), (12290, 1024, 64, 0.08), (12801, 1027, 37, 0.01)]
 
 
 @pytest.mark.parametrize("b", [1, 2, 3, 4])
