@@ -753,13 +753,39 @@ def hss_nm24_to_csr(A: HSSMatrix):
     return rp, ci
 
 
-def hss_transposed_layer(A: HSSMatrix) -> HSSMatrix:
+def _rewrite_transposed(A: HSSMatrix, out: HSSMatrix) -> HSSMatrix:
+    """A's values and factors into the transposed layer `out`: no host work, no allocation."""
+    nnz = A.m * (A.n // 2) if A.fmt == HSS_FMT_2OF4 else A.nnz
+    perm = getattr(out, "perm_from_s", None)
+    if perm is None or (out.m, out.n, out.r, out.dtype, out.nnz) != (A.n, A.m, A.r, A.dtype, nnz) or \
+            out.mx is not A.mx or (A.mx is not None and out.mx_t == A.mx_t) or out.index != A.index:
+        raise ValueError("out must be a transposed layer that hss_transposed_layer made of a layer like A")
+    held = out.row_ptr
+    with _on(held):
+        stream = _stream(held.device)
+        if nnz:
+            values = A.nm_values if A.fmt == HSS_FMT_2OF4 else A.values
+            check(lib.hss_gather_values(_DT[A.dtype], nnz, _ptr(values), _ptr(perm), _ptr(out.values), stream),
+                  "hss_gather_values")
+        if A.r > 0:
+            check(lib.hss_transpose(_DT[A.dtype], A.r, A.n, _ptr(A.Vt), _ptr(out.U), stream), "hss_transpose")
+            check(lib.hss_transpose(_DT[A.dtype], A.m, A.r, _ptr(A.U), _ptr(out.Vt), stream), "hss_transpose")
+    return out
+
+
+def hss_transposed_layer(A: HSSMatrix, out: Optional[HSSMatrix] = None) -> HSSMatrix:
     """A^T = S^T + V U^T as an HSSMatrix (n x m, CSR): S^T's pattern from the
     host transpose (of the 2:4 positions for a 2:4 layer), its values
     gathered on the device, U' = V and V'^T = U^T from the stored factors; a
-    microscaled dense part is shared, read transposed.  hss_apply(A^T, G) is the input gradient G A."""
+    microscaled dense part is shared, read transposed.  hss_apply(A^T, G) is the input gradient G A.
+
+    S's values, U and V are copied: after they change (an optimizer's step),
+    out = the layer this call returned before writes them again from A's, in
+    place and on the device (S's pattern must be the same)."""
     if A.flags & (HSS_DQ4 | HSS_HIER2):
         raise ValueError("the transposed layer is built for CSR and 2:4 layers with flat factors")
+    if out is not None:
+        return _rewrite_transposed(A, out)
     mx = dict(mx=A.mx, mx_t=not A.mx_t) if A.mx is not None else {}
     if A.fmt == HSS_FMT_2OF4:
         dev = A.nm_meta.device
@@ -834,7 +860,9 @@ def hss_grad_ckpt(A: HSSMatrix, X: MXTensor, G: torch.Tensor, dS=True, dU=True, 
 def hss_backward(A: HSSMatrix, X, G: torch.Tensor, At: Optional[HSSMatrix] = None) -> dict:
     """dX (b x n, the layer dtype) = G A through the transposed layer, and
     the fp32 parameter gradients dS, dU, dVt of hss_grad, or of hss_grad_ckpt
-    where X is the 8-bit checkpoint of the layer's input."""
+    where X is the 8-bit checkpoint of the layer's input.  At: the transposed
+    layer, of A's present values (hss_transposed_layer(A, out=At) writes them
+    again); without it one is made, with S's pattern transposed on the host."""
     if At is None:
         At = hss_transposed_layer(A)
     out = hss_grad_ckpt(A, X, G) if isinstance(X, MXTensor) else hss_grad(A, X, G)

@@ -457,3 +457,42 @@ def test_gradient_workspace_sized_for_the_largest_batch(H, hss_opt):
             G = to_dev(syn.random_matrix(b, A.m, BF, seed=b + 1, kind="normal", scale=1.0), BF)
             got, want = H.hss_grad_ckpt(A, ck, G, ws=ws), H.hss_grad_ckpt(A, ck, G)
             assert all(torch.equal(got[k], want[k]) for k in want), (route, b)
+
+
+@pytest.mark.parametrize("kind", ["mx", "csr", "col16", "2:4", "empty"])
+def test_transposed_layer_written_again(H, kind):
+    """After S's values, U and V changed in place, the transposed layer written
+    again holds the bits of a new one, in its old arrays; captured too."""
+    import torch
+    m, n, r = 96, 160, 12
+    if kind == "2:4":
+        W = to_dev(syn.random_matrix(m, n, BF, seed=2, kind="t3"), BF)
+        U, V = syn.factors(m, n, r, BF, 2)
+        A = H.HSSMatrix.from_split(H.hss_split(W, "2:4"), U=to_dev(U, BF), Vt=to_dev(np.ascontiguousarray(V.T), BF))
+    else:
+        A = _layer(H, m, n, 0 if kind == "empty" else r, seed=2, col16=kind == "col16",
+                   frac=(0, 1) if kind == "empty" else (2, 100))[0]
+        if kind == "csr":
+            A = H.HSSMatrix("csr", m, n, torch.bfloat16, U=A.U, Vt=A.Vt, row_ptr=A.row_ptr, col_idx=A.col_idx,
+                            values=A.values)
+    At = H.hss_transposed_layer(A)
+    held = [t for t in (At.values, At.U, At.Vt) if t is not None]
+    where = [t.data_ptr() for t in held]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        H.hss_transposed_layer(A, out=At)
+    for rep in range(4):
+        for t in (A.values, A.nm_values, A.U, A.Vt):
+            if t is not None:
+                t.copy_(torch.randn(t.shape, device="cuda"))
+        if rep % 2:
+            graph.replay()
+        else:
+            assert H.hss_transposed_layer(A, out=At) is At
+        new = H.hss_transposed_layer(A)
+        torch.cuda.synchronize()
+        for a, b in ((At.values, new.values), (At.U, new.U), (At.Vt, new.Vt)):
+            assert (a is None and b is None) or torch.equal(a.view(torch.int16), b.view(torch.int16))
+        G = torch.randn(9, m, device="cuda").bfloat16()
+        assert torch.equal(H.hss_apply(At, G), H.hss_apply(new, G))
+    assert where == [t.data_ptr() for t in held]

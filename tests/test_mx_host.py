@@ -423,3 +423,24 @@ def test_a_gradient_workspace_serves_every_smaller_batch(hl, case):
             for b in (1, 33, 600, 2048):
                 assert hl._lib.lib.hss_grad_ckpt_workspace_size(ctypes.byref(s), b, ctypes.byref(out)) == 0
                 assert out.value == sizes[b - 1]
+
+
+def test_transposed_layer_refuses_another_layers(hl):
+    import torch
+    bf = torch.bfloat16
+
+    def layer(m=3, n=33, r=2, nnz=2, mx=None, mx_t=False):
+        rp = torch.zeros(m + 1, dtype=torch.int32)
+        rp[-1:] = nnz
+        return hl.HSSMatrix("csr", m, n, bf, U=torch.zeros(m, r, dtype=bf), Vt=torch.zeros(r, n, dtype=bf), row_ptr=rp,
+                            col_idx=torch.arange(nnz, dtype=torch.int32), values=torch.zeros(nnz, dtype=bf), mx=mx, mx_t=mx_t)
+
+    A = layer()
+    q = hl.MXTensor.empty("fp4", 3, 33, "cpu")
+    for out in (layer(33, 3), layer(33, 4), layer(33, 3, r=3), layer(33, 3, nnz=3), layer(33, 3, mx=q, mx_t=True), A):
+        if out is not A:
+            out.perm_from_s = torch.zeros(2, dtype=torch.int32)
+        if (out.m, out.n, out.r, out.nnz) == (33, 3, 2, 2) and out.mx is None:
+            out.index = 1                                         # on another device
+        with pytest.raises(ValueError):
+            hl.hss_transposed_layer(A, out=out)
