@@ -496,3 +496,23 @@ def test_transposed_layer_written_again(H, kind):
         G = torch.randn(9, m, device="cuda").bfloat16()
         assert torch.equal(H.hss_apply(At, G), H.hss_apply(new, G))
     assert where == [t.data_ptr() for t in held]
+
+
+@pytest.mark.parametrize("route", ["sparse", "dense"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_grad_ckpt_non_finite_gradient(H, hss_opt, route, value):
+    """A non-finite G[c][i] makes row i of dS and of dU, and all of dV^T,
+    non-finite, and nothing else."""
+    import torch
+    hss_opt("grad_ds_route", route)
+    m, n, r, b = 64, 96, 8, 70
+    A, ref, *_ = _layer(H, m, n, r, seed=6, frac=(10, 100))
+    X = torch.randn(b, n, device="cuda").bfloat16() + 3
+    G = torch.randn(b, m, device="cuda").bfloat16()
+    G[17, 40] = value
+    got = H.hss_grad_ckpt(A, H.hss_mx_quantize(X, "int8"), G)
+    hit = torch.arange(m, device="cuda") == 40
+    rows = torch.as_tensor(O.csr_row_of_entry(m, ref["row_ptr"]), device="cuda")
+    for name, at in (("dU", hit), ("dS", hit[rows])):
+        assert not torch.isfinite(got[name][at]).any() and torch.isfinite(got[name][~at]).all()
+    assert not torch.isfinite(got["dVt"]).any()
