@@ -336,10 +336,12 @@ hss_status hss_apply_workspace_size(const hss_matrix* A, int32_t b, size_t* byte
  * HSS_DQ4 matrices always run the fused dense-and-sparse kernel (up to 8
  * columns per pass; no workspace: hss_apply_workspace_size returns 0 and ws
  * may be NULL).
- * HSS_MX4 matrices: X V is kept as two bf16 terms (16 significant bits); D +
- *   S is rounded to bf16 where an entry of S falls on a non-zero of D; all
- *   sums are in fp32.  A NaN or infinity in X reaches every output of its
- *   batch row.  The same call gives the same bits every time.
+ * HSS_MX4 matrices: X V is kept as two bf16 terms (16 significant bits), in
+ *   fp32 for up to four columns of long rows; beyond 256 columns D + S is rounded to bf16
+ *   where an entry of S falls on a non-zero of D; all sums are in fp32.  A NaN
+ *   or infinity in X reaches every output of its batch row; an infinity in U
+ *   or V may give NaN where the formula gives an infinity.  The same call
+ *   gives the same bits every time.
  * Returns HSS_ERR_INVALID_ARG for: A or X or Y null, unknown fmt/dtype,
  *   unknown flags (or HSS_COL16 with a 2:4 matrix or n > 65536; HSS_DQ4 with
  *   a 2:4 matrix, odd n or null dq arrays),
@@ -620,8 +622,10 @@ hss_status hss_mx_dequantize(int32_t fmt, int32_t dt, int32_t rows, int32_t cols
  *   gradients are those of the checkpoint's values X' (dS = G^T X' on S's
  *   support, dU = G^T (X' V), dV^T = (G U)^T X'); layouts, NULL outputs and
  *   the dS route as hss_grad.  X' V and G U are kept as three bf16 terms (24
- *   significant bits), so every output carries fp32 precision.  The same
- *   inputs give the same bits on every call.
+ *   significant bits), so every output carries fp32 precision.  A non-finite
+ *   value of G, U or V makes the outputs that it reaches non-finite, NaN where
+ *   hss_grad may give an infinity, and no others.  The same inputs give the
+ *   same bits on every call.
  *   ws: at least hss_grad_ckpt_workspace_size() bytes (no state kept), which
  *   serve every smaller batch too.
  *   HSS_ERR_UNSUPPORTED: as hss_grad, or max(m, n) round64(b) * 2 or

@@ -17,10 +17,12 @@
 // while those MFMAs run, so the matrix cores cross the barrier with work in
 // hand.
 //
-// Measured: 2048 x 8192, K 8192: 192 us, 1.43 PFLOP/s (k_gemm_h's 128 x 256
-// tiles: 250); matrix cores busy in 68 % of the cycles at the 1.93 GHz the
-// chip holds under this load.  Loads through registers with two stages more in
-// flight waited less (7 against 11 % of the wave cycles) and were 3 % slower.
+// Measured: 2048 x 8192, K 8192, 60 launches back to back: 231 us on average,
+// 1.19 PFLOP/s (202 in the first ones: the clock falls from 1.9 GHz under this
+// load; matrix cores busy in 69 % of the cycles).  The BLAS library's product,
+// counted the same way: 207 (177).  In short runs, where the clock holds: 192,
+// k_gemm_h's 128 x 256 tiles 250.  Loads through registers with two stages more
+// in flight waited less (7 against 11 % of the wave cycles) and were 3 % slower.
 #include <algorithm>
 #include <type_traits>
 
