@@ -32,6 +32,8 @@
  *     bits of binary32).  Matrices are dense row-major unless stated.
  *   - Sizes are int32; every array addressed by the library must have fewer
  *     than 2^31 elements.
+ *   - Workspaces are 16-byte aligned (every device allocation is); a call
+ *     that needs one refuses others with HSS_ERR_WORKSPACE.
  *   - Calls are thread-safe given distinct workspaces; two calls that share a
  *     workspace must be ordered (same stream or explicit events).
  */
@@ -57,7 +59,7 @@ typedef enum {
   HSS_OK = 0,
   HSS_ERR_INVALID_ARG = 1, /* bad size, null pointer, aliasing, unknown enum          */
   HSS_ERR_UNSUPPORTED = 2, /* valid request the library does not implement          */
-  HSS_ERR_WORKSPACE = 3,   /* workspace pointer null or smaller than *_workspace_size */
+  HSS_ERR_WORKSPACE = 3,   /* workspace null, not 16-byte aligned or smaller than *_workspace_size */
   HSS_ERR_NONFINITE = 4,   /* device-side: a NaN/Inf weight was seen by hss_split     */
   HSS_ERR_HIP = 5          /* a HIP runtime call or kernel launch failed              */
 } hss_status;

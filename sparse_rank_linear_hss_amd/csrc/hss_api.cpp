@@ -94,6 +94,10 @@ bool overlap(const void* a, size_t abytes, const void* b, size_t bbytes) {
   return a0 < b0 + bbytes && b0 < a0 + abytes;
 }
 
+// A workspace of `need` bytes: 16-byte aligned, for the vector accesses and the
+// 64-bit words that kernels exchange through it.
+bool ws_ok(const void* ws, size_t ws_bytes, size_t need) { return ws && (uintptr_t)ws % 16 == 0 && ws_bytes >= need; }
+
 }  // namespace
 
 extern "C" {
@@ -124,7 +128,7 @@ const char* hss_status_string(int32_t s) {
     case HSS_OK: return "HSS_OK";
     case HSS_ERR_INVALID_ARG: return "HSS_ERR_INVALID_ARG: invalid argument";
     case HSS_ERR_UNSUPPORTED: return "HSS_ERR_UNSUPPORTED: not implemented for these arguments";
-    case HSS_ERR_WORKSPACE: return "HSS_ERR_WORKSPACE: workspace missing or too small";
+    case HSS_ERR_WORKSPACE: return "HSS_ERR_WORKSPACE: workspace missing, not 16-byte aligned or too small";
     case HSS_ERR_NONFINITE: return "HSS_ERR_NONFINITE: non-finite weight seen by hss_split";
     case HSS_ERR_HIP: return "HSS_ERR_HIP: HIP runtime error";
   }
@@ -168,7 +172,7 @@ hss_status hss_split(int32_t fmt, int32_t dt, int32_t m, int32_t n, const void* 
     if (row_ptr || col_idx || values) return HSS_ERR_INVALID_ARG;
   }
   const size_t need = hss::split_ws_bytes(fmt, m);
-  if (!ws || ws_bytes < need) return HSS_ERR_WORKSPACE;
+  if (!ws_ok(ws, ws_bytes, need)) return HSS_ERR_WORKSPACE;
   if (fmt == HSS_FMT_CSR)
     return hss::launch_split_csr(dt, m, n, W, k, row_ptr, col_idx, values, residual, ws, stream);
   return hss::launch_split_24(dt, m, n, W, nm_values, nm_meta, residual, ws, stream);
@@ -259,7 +263,7 @@ hss_status hss_apply(const hss_matrix* A, int32_t b, const void* X, void* Y, voi
   const hss_status st = hss::check_apply_args(A, b, X, Y);
   if (st != HSS_OK) return st;
   const size_t need = hss::apply_ws_bytes(A, b);
-  if ((need > 0 && !ws) || ws_bytes < need) return HSS_ERR_WORKSPACE;
+  if (need > 0 && !ws_ok(ws, ws_bytes, need)) return HSS_ERR_WORKSPACE;
   return hss::launch_apply(A, b, X, Y, ws, stream);
 }
 
@@ -297,7 +301,7 @@ hss_status hss_apply_group(const hss_matrix* const* A, int32_t G, int32_t b, con
     for (int h = 0; h < g; ++h)
       if (overlap(Y[h], (size_t)b * A[h]->m * es, Y[g], yb)) return HSS_ERR_INVALID_ARG;
   }
-  if (!ws || ws_bytes < hss::apply_group_ws_bytes(A, G, b, false)) return HSS_ERR_WORKSPACE;
+  if (!ws_ok(ws, ws_bytes, hss::apply_group_ws_bytes(A, G, b, false))) return HSS_ERR_WORKSPACE;
   return hss::launch_apply_group(A, G, b, X, Y, ws, stream);
 }
 
@@ -327,7 +331,7 @@ hss_status hss_concentration(int32_t dt, int32_t m, int32_t n, const void* W, co
                              void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!valid_dtype(dt) || m < 1 || n < 1 || (int64_t)m * n >= kLimit || !W || !out) return HSS_ERR_INVALID_ARG;
   if (perm && m != n) return HSS_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < hss::concentration_ws_bytes(n)) return HSS_ERR_WORKSPACE;
+  if (!ws_ok(ws, ws_bytes, hss::concentration_ws_bytes(n))) return HSS_ERR_WORKSPACE;
   return hss::launch_concentration(dt, m, n, W, perm, out, ws, stream);
 }
 
@@ -435,7 +439,7 @@ hss_status hss_grad(const hss_matrix* A, int32_t b, const void* X, const void* G
   const size_t in_bytes[2] = {(size_t)b * A->n * 2, (size_t)b * A->m * 2};
   if (!grad_outputs_ok(A, in, in_bytes, 2, dS, dU, dVt)) return HSS_ERR_INVALID_ARG;
   const size_t need = hss::grad_ws_bytes(A, b);
-  if (!ws || ws_bytes < need) return HSS_ERR_WORKSPACE;
+  if (!ws_ok(ws, ws_bytes, need)) return HSS_ERR_WORKSPACE;
   return hss::launch_grad(A, b, X, G, dS, dU, dVt, ws, stream);
 }
 
@@ -510,7 +514,7 @@ hss_status hss_grad_ckpt(const hss_matrix* A, int32_t b, const int8_t* codes, co
                               (size_t)b * A->m * 2};
   if (!grad_outputs_ok(A, in, in_bytes, 3, dS, dU, dVt)) return HSS_ERR_INVALID_ARG;
   const size_t need = hss::grad_ckpt_ws_bytes(A, b);
-  if (!ws || ws_bytes < need) return HSS_ERR_WORKSPACE;
+  if (!ws_ok(ws, ws_bytes, need)) return HSS_ERR_WORKSPACE;
   return hss::launch_grad_ckpt(A, b, codes, scales, G, dS, dU, dVt, ws, stream);
 }
 

@@ -348,3 +348,24 @@ def test_backward_entry_points_reject_bad_arguments(hl):
     assert lib.hss_nm24_to_csr(4, 6, FAKE, FAKE * 2, FAKE * 3, None) == INV     # n % 4 != 0
     assert lib.hss_nm24_to_csr(4, 8, None, FAKE * 2, FAKE * 3, None) == INV
     assert lib.hss_nm24_to_csr(4, 8, FAKE, FAKE * 2, FAKE * 2 + 8, None) == INV  # overlapping outputs
+
+
+def test_workspaces_off_the_16_byte_grid_are_refused(hl):
+    """Kernels exchange 64-bit words and read 16-byte pieces through a workspace:
+    every call that takes one refuses a base that is not 16-byte aligned, before
+    any device work."""
+    lib, WS = hl._lib.lib, hl._lib.HSS_ERR_WORKSPACE
+    big = 1 << 30
+    s = hl._lib.HssMatrixStruct()
+    s.fmt, s.dtype, s.m, s.n, s.r, s.flags, s.nnz = 0, 1, 16, 32, 4, 0, 10
+    s.row_ptr = s.col_idx = s.values = s.U = s.Vt = FAKE
+    arr = (ctypes.POINTER(hl._lib.HssMatrixStruct) * 1)(ctypes.pointer(s))
+    ys = (ctypes.c_void_p * 1)(FAKE * 3)
+    for off in (1, 4, 8, 12):
+        ws = FAKE * 16 + off
+        assert lib.hss_apply(ctypes.byref(s), 1, FAKE * 2, FAKE * 3, ws, big, None) == WS
+        assert lib.hss_apply_group(arr, 1, 1, FAKE * 2, ys, ws, big, None) == WS
+        assert lib.hss_grad(ctypes.byref(s), 1, FAKE * 2, FAKE * 3, FAKE * 4, FAKE * 5, FAKE * 6, ws, big, None) == WS
+        assert lib.hss_grad_ckpt(ctypes.byref(s), 1, FAKE * 2, FAKE * 7, FAKE * 3, FAKE * 4, FAKE * 5, FAKE * 6, ws, big, None) == WS
+        assert lib.hss_split(0, 1, 16, 32, FAKE * 2, 10, FAKE * 3, FAKE * 4, FAKE * 5, None, None, None, ws, big, None) == WS
+        assert lib.hss_concentration(1, 16, 32, FAKE * 2, None, FAKE * 3, ws, big, None) == WS
