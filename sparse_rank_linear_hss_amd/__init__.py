@@ -359,6 +359,15 @@ class HSSMatrix:
         on = {t.get_device() for t in held if t is not None}
         self.index = on.pop() if len(on) == 1 else None  # the GPU that holds all of it
         self.nnz = int(nnz if nnz is not None else (values.numel() if values is not None else 0))
+        # what the kernels would read out of range, or as other numbers than they are
+        if self.fmt == HSS_FMT_CSR:
+            self._need("row_ptr", row_ptr, (torch.int32,), self.m + 1)
+            if self.nnz > 0:
+                self._need("col_idx", col_idx, (torch.int32, torch.int16), self.nnz)
+                self._need("values", values, (dtype,), self.nnz)
+        else:
+            self._need("nm_values", nm_values, (dtype,), self.m * (self.n // 2))
+            self._need("nm_meta", nm_meta, (torch.int32,), self.m * ((self.n + 31) // 32))
         self._ws, self._ws_sizes = {}, {}
         s = HssMatrixStruct()
         s.fmt, s.dtype = self.fmt, _DT[dtype]
@@ -374,6 +383,11 @@ class HSSMatrix:
             s.dq_codes, s.dq_levels = _ptr(mx.codes), _ptr(mx.scales)
         self.struct = s
         self._ref = ctypes.byref(s)
+
+    @staticmethod
+    def _need(name, t, dtypes, count):
+        if t is None or t.dtype not in dtypes or t.numel() < count or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of {count} {' or '.join(str(d) for d in dtypes)}")
 
     @classmethod
     def from_split(cls, sp: SplitResult, U=None, V=None, Vt=None, dtype=None, mx=None):

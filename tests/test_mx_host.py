@@ -444,3 +444,26 @@ def test_transposed_layer_refuses_another_layers(hl):
             out.index = 1                                         # on another device
         with pytest.raises(ValueError):
             hl.hss_transposed_layer(A, out=out)
+
+
+def test_matrices_refuse_arrays_that_do_not_fit(hl):
+    """Index arrays of 64 bits, short or strided arrays and values of another
+    type would be read out of range or as other numbers."""
+    import torch
+    bf, i32 = torch.bfloat16, torch.int32
+    good = dict(row_ptr=torch.zeros(4, dtype=i32), col_idx=torch.zeros(5, dtype=i32), values=torch.zeros(5, dtype=bf))
+    hl.HSSMatrix("csr", 3, 33, bf, **good)
+    hl.HSSMatrix("csr", 3, 33, bf, row_ptr=good["row_ptr"])
+    hl.HSSMatrix("csr", 3, 33, bf, **{**good, "col_idx": torch.zeros(5, dtype=torch.int16)})
+    for bad in (dict(row_ptr=torch.zeros(4, dtype=torch.int64)), dict(row_ptr=torch.zeros(3, dtype=i32)), dict(row_ptr=None),
+                dict(col_idx=torch.zeros(5, dtype=torch.int64)), dict(col_idx=torch.zeros(4, dtype=i32)), dict(col_idx=None),
+                dict(col_idx=torch.zeros(10, dtype=i32)[::2]), dict(values=torch.zeros(5)), dict(nnz=6),
+                dict(values=torch.zeros(10, dtype=bf)[::2])):
+        with pytest.raises(ValueError):
+            hl.HSSMatrix("csr", 3, 33, bf, **{**good, **bad})
+    nm = dict(nm_values=torch.zeros(3, 18, dtype=bf), nm_meta=torch.zeros(3, 2, dtype=i32))
+    hl.HSSMatrix("2:4", 3, 36, bf, **nm)
+    for bad in (dict(nm_values=None), dict(nm_values=torch.zeros(3, 18)), dict(nm_values=torch.zeros(3, 17, dtype=bf)),
+                dict(nm_meta=torch.zeros(3, 1, dtype=i32)), dict(nm_meta=torch.zeros(3, 2, dtype=torch.int64))):
+        with pytest.raises(ValueError):
+            hl.HSSMatrix("2:4", 3, 36, bf, **{**nm, **bad})
