@@ -739,7 +739,11 @@ def hss_csr_transpose(row_ptr, col_idx, m: int, n: int):
 
 
 def hss_gather_values(values: torch.Tensor, perm: torch.Tensor) -> torch.Tensor:
-    """values[perm] on the device (bits copied)."""
+    """values[perm] on the device (bits copied); perm int32, within values."""
+    if values.dtype not in _DT or not values.is_contiguous():
+        raise ValueError("values must be a contiguous fp32 or bf16 tensor")
+    if perm.dtype != torch.int32 or not perm.is_contiguous() or perm.get_device() != values.get_device():
+        raise ValueError("perm must be a contiguous int32 tensor on the device of values")
     out = torch.empty(perm.numel(), dtype=values.dtype, device=values.device)
     with _on(values):
         check(lib.hss_gather_values(_DT[values.dtype], perm.numel(), _ptr(values), _ptr(perm), _ptr(out),
@@ -749,6 +753,8 @@ def hss_gather_values(values: torch.Tensor, perm: torch.Tensor) -> torch.Tensor:
 
 def hss_transpose(t: torch.Tensor) -> torch.Tensor:
     """A contiguous 2-D fp32 / bf16 device tensor transposed by the library."""
+    if t.dim() != 2 or not t.is_contiguous() or t.dtype not in _DT:
+        raise ValueError("t must be a contiguous 2-D fp32 or bf16 tensor")
     rows, cols = t.shape
     out = torch.empty((cols, rows), dtype=t.dtype, device=t.device)
     with _on(t):

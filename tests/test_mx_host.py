@@ -467,3 +467,19 @@ def test_matrices_refuse_arrays_that_do_not_fit(hl):
                 dict(nm_meta=torch.zeros(3, 1, dtype=i32)), dict(nm_meta=torch.zeros(3, 2, dtype=torch.int64))):
         with pytest.raises(ValueError):
             hl.HSSMatrix("2:4", 3, 36, bf, **{**nm, **bad})
+
+
+def test_transposes_and_gathers_refuse_what_does_not_fit(hl, bound, monkeypatch):
+    import torch
+    calls, elsewhere = bound
+    monkeypatch.setattr(hl, "_stream", lambda device: 0)
+    t, perm = torch.zeros(4, 6), torch.zeros(3, dtype=torch.int32)
+    hl.hss_transpose(t), hl.hss_gather_values(t, perm)
+    assert calls == ["hss_transpose", "hss_gather_values"]
+    for bad in (t.t(), t[:, ::2], t[0], t.half(), torch.zeros(1, 6).expand(4, 6)):
+        with pytest.raises(ValueError):
+            hl.hss_transpose(bad)
+    for v, p in ((t, perm.long()), (t, elsewhere(perm)), (t, perm[:1].expand(3)), (t.t(), perm), (t.int(), perm)):
+        with pytest.raises(ValueError):
+            hl.hss_gather_values(v, p)
+    assert len(calls) == 2
