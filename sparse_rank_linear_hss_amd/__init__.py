@@ -483,8 +483,10 @@ def hss_apply(A: HSSMatrix, X: torch.Tensor, Y: Optional[torch.Tensor] = None,
               ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y (b x m) = X (b x n) (S + U V^T)^T on the current stream."""
     index = X.get_device()
+    if index < 0:
+        _index(X)  # refuses it
     if index != _current_device():
-        with torch.cuda.device(_index(X)):
+        with torch.cuda.device(index):
             return hss_apply(A, X, Y, ws)
     # the checks of _check_x, _check_y and _check_ws, written out: two calls less in a decode step
     shape, dtype = X.shape, A.dtype

@@ -483,3 +483,18 @@ def test_transposes_and_gathers_refuse_what_does_not_fit(hl, bound, monkeypatch)
         with pytest.raises(ValueError):
             hl.hss_gather_values(v, p)
     assert len(calls) == 2
+
+
+def test_calls_refuse_cpu_tensors(hl):
+    """With a ValueError, whether or not the machine has a GPU."""
+    import torch
+    bf = torch.bfloat16
+    A = _cpu_layer(hl, "mx")
+    X, G, Y = torch.zeros(1, 33, dtype=bf), torch.zeros(1, 3, dtype=bf), torch.zeros(1, 3, dtype=bf)
+    ck = hl.MXTensor.empty("int8", 1, 33, "cpu")
+    for call in (lambda: hl.hss_apply(A, X), lambda: hl.hss_apply(A, X, Y), lambda: hl.hss_apply_noalloc(A, X, Y),
+                 lambda: hl.hss_apply_group([A], X), lambda: hl.hss_grad(A, X, G), lambda: hl.hss_grad_ckpt(A, ck, G),
+                 lambda: hl.hss_transpose(X), lambda: hl.hss_gather_values(X, torch.zeros(1, dtype=torch.int32)),
+                 lambda: hl.hss_mx_quantize(X), lambda: hl.hss_mx_dequantize(ck), lambda: hl.hss_split(X)):
+        with pytest.raises(ValueError):
+            call()
