@@ -312,11 +312,11 @@ hss_status hss_apply_workspace_size(const hss_matrix* A, int32_t b, size_t* byte
  *     the current epoch's, so a word left by one of the 4,128,767 calls before
  *     is never taken for this one's; a tag is a signalling NaN, which nothing
  *     that another route computes and leaves there can be).  The caller must
- *     not write to the workspace after the init.  Any number of calls, with any matrices and
- *     batch sizes, may share one workspace if they are ORDERED (one stream,
- *     or events between streams); two calls that overlap in time must use
- *     different workspaces -- overlapping calls on one workspace can make
- *     both return wrong values with no error.
+ *     not write to the workspace after the init.  Any number of calls, with
+ *     any matrices and batch sizes, may share one workspace if they are
+ *     ORDERED (one stream, or events between streams); two calls that overlap
+ *     in time must use different workspaces -- overlapping calls on one
+ *     workspace can make both return wrong values with no error.
  * Execution: bf16 2:4 with 3 <= b <= 64 (n % 128 == 0; nm_values, nm_meta
  * and X 16-byte aligned) runs on the sparse matrix cores: S's stored values
  * and 2-bit indices are the operands of v_smfmac as they are, with fp32
@@ -338,12 +338,12 @@ hss_status hss_apply_workspace_size(const hss_matrix* A, int32_t b, size_t* byte
  * HSS_DQ4 matrices always run the fused dense-and-sparse kernel (up to 8
  * columns per pass; no workspace: hss_apply_workspace_size returns 0 and ws
  * may be NULL).
- * HSS_MX4 matrices: X V is kept as two bf16 terms (16 significant bits), in
- *   fp32 for up to four columns of long rows; beyond 256 columns D + S is rounded to bf16
- *   where an entry of S falls on a non-zero of D; all sums are in fp32.  A NaN
- *   or infinity in X reaches every output of its batch row; an infinity in U
- *   or V may give NaN where the formula gives an infinity.  The same call
- *   gives the same bits every time.
+ * HSS_MX4 matrices: X V is kept as two bf16 terms (16 significant bits), or in
+ *   fp32 for up to four columns of long rows; beyond 256 columns D + S is
+ *   rounded to bf16 where an entry of S falls on a non-zero of D; all sums are
+ *   in fp32.  A NaN or infinity in X reaches every output of its batch row; an
+ *   infinity in U or V may give NaN where the formula gives an infinity.  The
+ *   same call gives the same bits every time.
  * Returns HSS_ERR_INVALID_ARG for: A or X or Y null, unknown fmt/dtype,
  *   unknown flags (or HSS_COL16 with a 2:4 matrix or n > 65536; HSS_DQ4 with
  *   a 2:4 matrix, odd n or null dq arrays),

@@ -15,9 +15,9 @@
 // values and the matrix they were taken from have too; the remainders would
 // take a gather over X^T next to the product (4096^2, 3 % of S, 55 % of it on
 // non-zeros: the relative error of Y is 1.683e-3 with the rounding, 1.659e-3
-// without, as up to 256 columns, nearly all of it Y's own rounding).  Operands whose rows the matrix-core kernels cannot read
-// in 16-byte pieces (n not a multiple of 64, unaligned bases) are copied
-// into padded rows first.
+// without, as up to 256 columns, nearly all of it Y's own rounding).  Operands
+// whose rows the matrix-core kernels cannot read in 16-byte pieces (n not a
+// multiple of 64, unaligned bases) are copied into padded rows first.
 #include <algorithm>
 
 #include "gemm256.h"
