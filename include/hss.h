@@ -309,14 +309,15 @@ hss_status hss_apply_workspace_size(const hss_matrix* A, int32_t b, size_t* byte
  *     kernel keeps state in it from call to call: a call epoch and arrival
  *     counters (in the first 32 KiB) and the tagged words through which its
  *     blocks hand T = V^T x to each other (a word is used only when its tag is
- *     the current epoch's, so a word left by one of the 4,128,767 calls before
- *     is never taken for this one's; a tag is a signalling NaN, which nothing
- *     that another route computes and leaves there can be).  The caller must
- *     not write to the workspace after the init.  Any number of calls, with
- *     any matrices and batch sizes, may share one workspace if they are
- *     ORDERED (one stream, or events between streams); two calls that overlap
- *     in time must use different workspaces -- overlapping calls on one
- *     workspace can make both return wrong values with no error.
+ *     the current epoch + 1, so a word left by an earlier call is never taken
+ *     for this one's; no other route writes where the words are).  The epoch
+ *     wraps after 2^32 - 1 calls and skips the tag that a zero-filled word
+ *     carries.  The caller must not write to the workspace after the init.
+ *     Any number of calls, with any matrices and batch sizes, may share one
+ *     workspace if they are ORDERED (one stream, or events between streams);
+ *     two calls that overlap in time must use different workspaces --
+ *     overlapping calls on one workspace can make both return wrong values
+ *     with no error.
  * Execution: bf16 2:4 with 3 <= b <= 64 (n % 128 == 0; nm_values, nm_meta
  * and X 16-byte aligned) runs on the sparse matrix cores: S's stored values
  * and 2-bit indices are the operands of v_smfmac as they are, with fp32
@@ -360,11 +361,11 @@ hss_status hss_apply(const hss_matrix* A, int32_t b, const void* X, void* Y, voi
  * device memory (code under HIP graph capture, tight serving loops, harnesses
  * that forbid allocation).  Same arguments, arithmetic, routes and errors as
  * hss_apply, with the workspace replaced by a scratch array that the library
- * holds in each GPU's memory: hss_noalloc_scratch_bytes() bytes (16 MiB),
- * kept until the process ends, and cleared by the first call on each device
- * (on that call's stream; one of an HSS_MX4 matrix, which needs no cleared
- * scratch, leaves that to the first other call).  The call allocates and frees
- * nothing.
+ * holds in each GPU's memory: hss_noalloc_scratch_bytes() bytes (16 MiB, next
+ * to 2 MiB for the decode kernel's words), kept until the process ends, and
+ * cleared by the first call on each device (on that call's stream; one of an
+ * HSS_MX4 matrix, which needs no cleared scratch, leaves that to the first
+ * other call).  The call allocates and frees nothing.
  * HSS_ERR_WORKSPACE when the route this call takes needs more workspace
  * than the scratch holds (e.g. a large CSR layer densified for the matrix
  * cores at prefill batches): use hss_apply with a workspace of

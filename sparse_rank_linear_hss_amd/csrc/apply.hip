@@ -26,6 +26,8 @@
 // HSS_OPT_BATCH_ROUTE (hss_set_option; first value from the environment
 // variable HSS_CSR_BATCH_ROUTE) forces the route of a bf16 batch (where that
 // route supports it), for measuring one against another.
+#include <algorithm>
+
 #include "hss_internal.h"
 
 namespace hss {
@@ -33,7 +35,8 @@ namespace hss {
 void launch_decode(const hss_matrix* A, int bc, const void* X, void* Y, void* ws, hipStream_t s);
 void launch_decode_group(const hss_matrix* const* A, int G, int bc, const void* X, void* const* Y, void* ws,
                          hipStream_t s);
-size_t decode_ctl_bytes();
+size_t decode_scratch_off();
+size_t decode_ws_bytes(size_t t);
 size_t decode_t_bytes(const hss_matrix* A);
 int decode_max_cols(const hss_matrix* A);
 int decode_dq_max_cols(const hss_matrix* A);
@@ -118,14 +121,14 @@ static Route batch_route(const hss_matrix* A0, int b, const void* X) {
   return R_DECODE;
 }
 
-// Layout: [decode control region | decode T words or MFMA buffers].  The
-// control region persists between calls; everything after it is per-call
-// scratch, so both paths can share one workspace.
+// Layout: [decode control region | decode T words | the other routes'
+// buffers].  The first two persist between calls, the last is per-call
+// scratch, so every route, with every matrix, can share one workspace.
 size_t apply_ws_bytes(const hss_matrix* A0, int b) {
   if (is_dq(A0)) return 0;
-  if (is_mx(A0)) return decode_ctl_bytes() + mx_apply_ws_bytes(A0, b);
+  if (is_mx(A0)) return decode_scratch_off() + mx_apply_ws_bytes(A0, b);
   // every route the call may take (the route can be forced at call time)
-  const size_t dec = decode_t_bytes(A0);
+  const size_t dec = decode_ws_bytes(decode_t_bytes(A0));
   const hss_matrix F = is_hier(A0) ? flat_view(A0, nullptr, nullptr) : *A0;
   const hss_matrix* A = &F;
   const size_t mf = mfma_supported(A, b) ? mfma_ws_bytes(A, b) : 0;
@@ -134,28 +137,28 @@ size_t apply_ws_bytes(const hss_matrix* A0, int b) {
   size_t mx = mf > sp ? mf : sp;
   mx = mx > nm ? mx : nm;
   if (is_hier(A0) && b >= 2) mx += hier_flat_bytes(A0);
-  return decode_ctl_bytes() + (dec > mx ? dec : mx);
+  return mx > 0 ? std::max(dec, decode_scratch_off() + mx) : dec;
 }
 
 // What hss_apply_workspace_size answers: for HSS_MX4 enough for every smaller
 // batch too.
 size_t apply_ws_query_bytes(const hss_matrix* A, int b) {
-  return is_mx(A) ? decode_ctl_bytes() + mx_apply_ws_bytes_up_to(A, b) : apply_ws_bytes(A, b);
+  return is_mx(A) ? decode_scratch_off() + mx_apply_ws_bytes_up_to(A, b) : apply_ws_bytes(A, b);
 }
 
 // Workspace bytes of the route this call takes (hss_apply_workspace_size
 // covers every route a call could be forced onto).
 size_t apply_route_ws_bytes(const hss_matrix* A0, int b, const void* X) {
   if (is_dq(A0)) return 0;
-  if (is_mx(A0)) return decode_ctl_bytes() + mx_apply_ws_bytes(A0, b);
+  if (is_mx(A0)) return decode_scratch_off() + mx_apply_ws_bytes(A0, b);
   const hss_matrix F = is_hier(A0) ? flat_view(A0, nullptr, nullptr) : *A0;
   const hss_matrix* A = &F;
   const size_t flat = is_hier(A0) ? hier_flat_bytes(A0) : 0;
   switch (batch_route(A0, b, X)) {
-    case R_NM: return decode_ctl_bytes() + flat + nm_mma_ws_bytes(A, b);
-    case R_MFMA: return decode_ctl_bytes() + flat + mfma_ws_bytes(A, b);
-    case R_SPMM: return decode_ctl_bytes() + flat + spmm_ws_bytes(A, b);
-    default: return decode_ctl_bytes() + decode_t_bytes(A0);
+    case R_NM: return decode_scratch_off() + flat + nm_mma_ws_bytes(A, b);
+    case R_MFMA: return decode_scratch_off() + flat + mfma_ws_bytes(A, b);
+    case R_SPMM: return decode_scratch_off() + flat + spmm_ws_bytes(A, b);
+    default: return decode_ws_bytes(decode_t_bytes(A0));
   }
 }
 
@@ -172,9 +175,9 @@ hss_status launch_apply(const hss_matrix* A, int b, const void* X, void* Y, void
     }
     return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
   }
-  if (is_mx(A)) return launch_mx_apply(A, b, X, Y, static_cast<char*>(ws) + decode_ctl_bytes(), stream);
+  if (is_mx(A)) return launch_mx_apply(A, b, X, Y, static_cast<char*>(ws) + decode_scratch_off(), stream);
   const Route route = batch_route(A, b, X);
-  char* scratch = static_cast<char*>(ws) + decode_ctl_bytes();
+  char* scratch = static_cast<char*>(ws) + decode_scratch_off();
   hss_matrix F;
   if (route != R_DECODE && is_hier(A)) {
     const size_t es = A->dtype == HSS_F32 ? 4 : 2;
@@ -228,10 +231,9 @@ size_t apply_group_ws_bytes(const hss_matrix* const* A, int G, int b, bool query
   for (int g = 0; g < G; ++g) {
     if (is_dq(A[g])) continue;  // the dense-and-sparse kernel uses no workspace
     if (!is_mx(A[g])) dec += decode_t_bytes(A[g]);
-    const size_t a = (query ? apply_ws_query_bytes(A[g], b) : apply_ws_bytes(A[g], b)) - decode_ctl_bytes();
-    one = one > a ? one : a;
+    one = std::max(one, query ? apply_ws_query_bytes(A[g], b) : apply_ws_bytes(A[g], b));
   }
-  return decode_ctl_bytes() + (dec > one ? dec : one);
+  return std::max(decode_ws_bytes(dec), one);
 }
 
 hss_status launch_apply_group(const hss_matrix* const* A, int G, int b, const void* X, void* const* Y, void* ws,

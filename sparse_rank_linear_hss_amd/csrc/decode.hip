@@ -32,7 +32,11 @@ static bool col16_of(const hss_matrix* A) { return A->fmt == HSS_FMT_CSR && (A->
 static size_t align16(size_t x) { return (x + 15) / 16 * 16; }
 static constexpr size_t kMaskTabBytes = 256 * 16;  // u_epilogue's mask table (bf16 U pieces)
 
-size_t decode_ctl_bytes() { return kCtlBytes; }
+// Where the scratch of the other routes starts.
+size_t decode_scratch_off() { return kCtlBytes + kTArea; }
+
+// Workspace bytes of a launch with t bytes of T words (launch_decode_group).
+size_t decode_ws_bytes(size_t t) { return kCtlBytes + (t <= kTArea ? t : kTArea + t); }
 
 // Words between T replicas for a matrix of rank r: room for 8 columns, padded
 // to whole 4 KiB pages plus one 128-byte line so copies start on different
@@ -182,12 +186,20 @@ static int merged_plan(const hss_matrix* const* A, int G, int bc, bool fast_bf16
 // One fused decode pass over bc columns (1 <= bc <= decode_max_cols of every
 // matrix) for G matrices sharing X (same n, dtype and format); Y[g] is
 // matrix g's output.  The T words of matrix g follow those of matrix g - 1.
+// Where they need more than kTArea they lie where other routes have their
+// scratch, and are cleared first, by a launch more.
 void launch_decode_group(const hss_matrix* const* A, int G, int bc, const void* X, void* const* Y, void* ws,
                          hipStream_t s) {
   GroupArgs ga = {};
   ga.G = G;
   uint32_t* ctl = static_cast<uint32_t*>(ws);
+  size_t t_bytes = 0;
+  for (int g = 0; g < G; ++g) t_bytes += decode_t_bytes(A[g]);
   char* tw = static_cast<char*>(ws) + kCtlBytes;
+  if (t_bytes > kTArea) {
+    tw += kTArea;
+    launch_zero_fill(tw, t_bytes, s);
+  }
   size_t lds = 0;
   int uq = -1;  // the group's: 0 if any matrix needs element-wise U reads, else the largest
   int cp = 1;

@@ -31,7 +31,7 @@
 //     sparse work, polls a stale word a bounded number of times, then computes
 //     any row still missing itself (same arithmetic, so the same bits).  No
 //     wait can hang and a stale value is never used;
-//   * the call tag is made of the epoch (tag_of), read by every block at its
+//   * the call tag is epoch+1, the epoch being read by every block at its
 //     start.  Each block then bumps one of 64 spread arrival counters of the
 //     set of the epoch's parity; the last block to arrive (two-level count)
 //     stores the next epoch, and block 0 clears the other set for the next
@@ -52,6 +52,7 @@ static constexpr int kCtlLine = 32;                  // words per line
 static constexpr int kNumSub = 64;  // a power of two (arrive_check divides by it with a shift)
 static constexpr int kCtlSetWords = (1 + kNumSub) * kCtlLine;
 static constexpr size_t kCtlBytes = 32768;          // >= (1 + 2 * 65) lines
+// The T words come next (kTArea).
 __device__ __forceinline__ int ctl_top(uint32_t epoch) { return kCtlLine + (int)(epoch & 1u) * kCtlSetWords; }
 __device__ __forceinline__ int ctl_sub(uint32_t epoch, int k) { return ctl_top(epoch) + kCtlLine * (1 + k); }
 // Copies of the tagged T words; block b reads copy b % kTReplicas, so each
@@ -163,20 +164,11 @@ __device__ __forceinline__ float dot16(const u32x4& a, const u32x4& b, float acc
   return acc;
 }
 
-// A call's T words carry a tag made of its epoch: a signalling NaN as fp32,
-// and as bf16 in its upper half.  Other routes leave their buffers where T
-// words go (a dense copy, X^T, partial sums, row tables), and no zero, result
-// of arithmetic or index there can be a tag: arithmetic makes quiet NaNs.
-// (With the call's number as the tag, a pair of bf16 values (x, 0) was one
-// after as many calls as x's bits say: 16256 for x = 1.)  The epoch runs 0 ..
-// kTags - 1 and wraps to 0, keeping the parity alternating, which picks the
-// counter set.
-static constexpr uint32_t kTagFirst = 0xff810000u, kTags = 63u << 16;  // up to 0xffbfffff
-static_assert(kTags % 2 == 0, "the parity of the epoch alternates");
-__device__ __forceinline__ uint32_t tag_of(uint32_t epoch) { return kTagFirst + epoch; }
-__device__ __forceinline__ uint32_t next_epoch(uint32_t tag) {
-  return tag == kTagFirst + kTags - 1u ? 0u : tag - kTagFirst + 1u;
-}
+// A call's T words carry tag epoch + 1.  The epoch runs 0 .. 2^32 - 2 and
+// then wraps to 1 (keeping the parity alternating, which picks the counter
+// set), so no tag is ever 0, the tag of a zero-filled word.
+__device__ __forceinline__ uint32_t tag_of(uint32_t epoch) { return epoch + 1u; }
+__device__ __forceinline__ uint32_t next_epoch(uint32_t tag) { return tag == 0xffffffffu ? 1u : tag; }
 
 // Sum of the NW per-wave partials red[w][c] in a fixed order (NW = 4, 8 or 16).
 template <int BC, int NW>

@@ -10,6 +10,14 @@
 
 namespace hss {
 
+// The part of an apply workspace, behind the decode kernel's control region,
+// that holds its T words and that no other route writes: their tags are call
+// numbers, and dense data left among the words would be taken for one (a pair
+// of bf16 values (x, 0) in the call whose number x's bits say; rows of T^T
+// written in part, with the rest of an old word's tag beside them).  Room for
+// a rank of 4096, in one matrix or in a group.
+static constexpr size_t kTArea = ((size_t)2 << 20) + ((size_t)64 << 10);
+
 // Row length of the compact V^T of an HSS_HIER2 matrix: the wider column half.
 __host__ __device__ inline int hier_vt_ld(int n) { return n - n / 2; }
 

@@ -1,8 +1,9 @@
 // hss_apply_noalloc: hss_apply with the library's own device scratch instead
 // of a caller workspace, for callers that cannot allocate device memory.
 //
-// The scratch is one file-scope device array per GPU (kScratchBytes, held
-// until the process ends).  In host code the array's name is only a host-side
+// The scratch is one file-scope device array per GPU (kScratchBytes, and the
+// part that only the decode kernel's T words use before it; held until the
+// process ends).  In host code the array's name is only a host-side
 // stand-in, so its device address is looked up once per device with
 // hipGetSymbolAddress (with that device current) and only that address is
 // passed on.  The first call on a device that may need it (HSS_MX4 layers keep
@@ -21,7 +22,9 @@ namespace hss {
 static constexpr size_t kScratchBytes = (size_t)16 << 20;  // 16 MiB per GPU
 static constexpr int kMaxDevices = 64;
 
-static __device__ __align__(256) unsigned char scratch[kScratchBytes];
+static constexpr size_t kArrayBytes = kScratchBytes + kTArea;
+
+static __device__ __align__(256) unsigned char scratch[kArrayBytes];
 
 namespace {
 std::mutex g_mu;
@@ -46,7 +49,7 @@ void* device_scratch(bool clear, hipStream_t stream, hss_status* st) {
     g_ptr[dev] = p;
   }
   if (clear && !g_cleared[dev]) {
-    if (launch_zero_fill(g_ptr[dev], kScratchBytes, stream) != HSS_OK) {
+    if (launch_zero_fill(g_ptr[dev], kArrayBytes, stream) != HSS_OK) {
       *st = HSS_ERR_HIP;
       return nullptr;
     }
@@ -65,7 +68,7 @@ extern "C" hss_status hss_apply_noalloc(const hss_matrix* A, int32_t b, const vo
                                         hipStream_t stream) {
   const hss_status st = hss::check_apply_args(A, b, X, Y);
   if (st != HSS_OK) return st;
-  if (hss::apply_route_ws_bytes(A, b, X) > hss::kScratchBytes) return HSS_ERR_WORKSPACE;
+  if (hss::apply_route_ws_bytes(A, b, X) > hss::kArrayBytes) return HSS_ERR_WORKSPACE;
   hss_status sst = HSS_OK;
   void* ws = hss::device_scratch((A->flags & HSS_MX4) == 0, stream, &sst);
   if (!ws) return sst;

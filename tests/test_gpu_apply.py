@@ -458,64 +458,113 @@ def test_apply_group_col16(H):
         assert O.bits_equal(to_host(a), to_host(c))
 
 
-@pytest.mark.parametrize("b", [1, 2])
-def test_apply_tags_are_no_number(H, b):
-    """The tag half of every T word a call leaves is 0 or a signalling NaN (as
-    fp32, and its upper half as bf16), which no result, zero or index of
-    another call's buffers can be."""
-    A, xs, _ = _tagged_layer(H, b, r=24)
-    ws = H.apply_workspace(H.hss_apply_workspace_size(A, b), "cuda")
-    for x in xs:
-        H.hss_apply(A, x, ws=ws)
-    words = to_host(ws)[32768:32768 + (len(to_host(ws)) - 32768) // 8 * 8].view(np.uint32)
-    tags = words[1::2][words[1::2] != 0]
-    assert len(tags) >= 8 * 24 * b
-    for bits, quiet, inf in ((tags, 0x400000, 0x7F800000), (tags >> 16, 0x40, 0x7F80)):
-        assert np.all(bits & inf == inf) and np.all(bits & quiet == 0) and np.all(bits & (quiet - 1) != 0)
+T_WORDS = slice(32768, 32768 + (2 << 20) + (64 << 10))              # of an apply workspace: the decode kernel's words
+
+
+def _tagged_layer(H, b, r, m=1030, n=512, seed=61):
+    W = syn.random_matrix(m, n, O.BF16, seed=seed, kind="t3")
+    ref = O.split_csr(W, O.BF16, O.topk_count(m, n, 5, 100))
+    A = _matrix(H, "csr", O.BF16, m, n, ref, *_factors(m, n, r, O.BF16, seed + 1))
+    xs = [to_dev(syn.random_matrix(b, n, O.BF16, seed=seed + 2 + i, kind="normal", scale=1.0), O.BF16) for i in range(3)]
+    return A, xs, [to_host(H.hss_apply(A, x)) for x in xs]
+
+
+def test_only_decode_calls_write_where_its_words_are(H, hss_opt):
+    """The control region and the T words of a workspace are the same bytes
+    before and after calls on every other route."""
+    import torch
+    n = 512
+    A, xs, _ = _tagged_layer(H, 1, r=40)
+    W = syn.random_matrix(200, n, O.BF16, seed=3, kind="t3")
+    csr, nm = O.split_csr(W, O.BF16, O.topk_count(200, n, 5, 100)), O.split_24(W, O.BF16)
+    U, V = _factors(200, n, 24, O.BF16, 4)
+    mats = {"csr": _matrix(H, "csr", O.BF16, 200, n, csr, U, V), "2:4": _matrix(H, "2:4", O.BF16, 200, n, nm, U, V)}
+    mats["col16"] = mats["csr"].with_col16()
+    q = H.hss_mx_quantize(to_dev(W, O.BF16), "fp4")
+    mats["mx"] = H.HSSMatrix("csr", 200, n, torch.bfloat16, U=mats["csr"].U, Vt=mats["csr"].Vt, mx=q)
+    Uh = [to_dev(syn.random_matrix(100, 6, O.BF16, seed=5 + k, kind="normal", scale=1.0), O.BF16) for k in range(4)]
+    Vh = [to_dev(syn.random_matrix(6, n // 2, O.BF16, seed=9 + k, kind="normal", scale=1.0), O.BF16) for k in range(4)]
+    Uc, Vc = H.hss_hier_pack_compact(Uh, Vh, 200, n)
+    c = mats["csr"]
+    mats["hier"] = H.HSSMatrix("csr", 200, n, torch.bfloat16, U=Uc, Vt=Vc, row_ptr=c.row_ptr, col_idx=c.col_idx,
+                               values=c.values, hier_r=[6] * 4)
+    calls = [(k, M, b, route) for k, M in mats.items() for b in (1, 2, 3, 5, 17, 64, 129, 300)
+             for route in ("auto", "spmm", "densify", "smfmac")]
+    ws = H.apply_workspace(max(H.hss_apply_workspace_size(M, b) for _, M, b, _ in calls), "cuda")
+    H.hss_apply(A, xs[0], ws=ws)
+    kept = ws[:T_WORDS.stop].clone()
+    for kind, M, b, route in calls:
+        if kind != "mx" and (b < 3 or (route == "auto" and kind == "hier")):
+            continue                                               # a decode call
+        hss_opt("batch_route", route)
+        H.hss_apply(M, torch.randn(b, n, device="cuda").bfloat16(), ws=ws)
+        assert torch.equal(ws[:T_WORDS.stop], kept), (kind, b, route)
 
 
 def test_apply_epoch_wraps(H):
-    """Calls around the last epoch, 63 * 2^16 - 1, whose tags are those of the
-    first ones again."""
+    """Calls around the last epoch, 2^32 - 2, after which comes 1."""
     import torch
     A, xs, expect = _tagged_layer(H, 1, r=24)
     ws = H.apply_workspace(H.hss_apply_workspace_size(A, 1), "cuda")
     epoch = ws[:4].view(torch.int32)
-    epoch.fill_((63 << 16) - 3)
+    epoch.fill_(-4)
     for k in range(6):
         assert O.bits_equal(to_host(H.hss_apply(A, xs[k % 3], ws=ws)), expect[k % 3]), k
-        assert int(epoch) == ((63 << 16) - 2 + k) % (63 << 16)
+        assert int(epoch) == (-3, -2, 1, 2, 3, 4)[k]
 
 
-def _tagged_layer(H, b, r, m=1030, n=512):
-    W = syn.random_matrix(m, n, O.BF16, seed=61, kind="t3")
-    ref = O.split_csr(W, O.BF16, O.topk_count(m, n, 5, 100))
-    A = _matrix(H, "csr", O.BF16, m, n, ref, *_factors(m, n, r, O.BF16, 62))
-    xs = [to_dev(syn.random_matrix(b, n, O.BF16, seed=63 + i, kind="normal", scale=1.0), O.BF16) for i in range(3)]
-    return A, xs, [to_host(H.hss_apply(A, x)) for x in xs]
+def test_apply_of_a_rank_past_the_words_room(H):
+    """T words of a rank past 4096 lie where other calls have dense data: each
+    decode call, also in a graph, gives the bits of one with a fresh workspace,
+    whatever was there, in place of words of its own tag too."""
+    import torch
+    m, n, r = 64, 256, 4200
+    A, xs, expect = _tagged_layer(H, 1, r, m, n)
+    size = H.hss_apply_workspace_size(A, 1)
+    assert size > T_WORDS.stop
+    ws = H.apply_workspace(size, "cuda")
+    words = ws[T_WORDS.stop:].view(torch.int32)
+    for k in range(6):
+        words.fill_(k + 1)                                          # every word: the tag of this call
+        assert O.bits_equal(to_host(H.hss_apply(A, xs[k % 3], ws=ws)), expect[k % 3]), k
+    y = torch.empty((1, m), dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        H.hss_apply(A, xs[0], y, ws)
+    for k in range(3):
+        words.fill_(int(ws[:4].view(torch.int32)) + 1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert O.bits_equal(to_host(y), expect[0]), k
 
 
-@pytest.mark.parametrize("kind", ["csr", "mx"])
+@pytest.mark.parametrize("ahead", [0, 1])
+@pytest.mark.parametrize("kind", ["csr", "mx", "spmm"])
 @pytest.mark.parametrize("b", [1, 2])
-def test_apply_after_dense_data_in_its_workspace(H, b, kind):
-    """A batch whose dense weights (a value, then a zero, all along) fill the
-    workspace, then a decode call on it, at the call count whose bits are that
-    value: every result equals the one from a fresh workspace."""
+def test_apply_after_dense_data_in_its_workspace(H, b, kind, ahead):
+    """A batch whose dense data (weights: a value, then a zero, all along; T^T:
+    a value that fills half of a word's tag) fill the workspace, then a decode
+    call on it, at about the call count whose bits are that value: every result
+    equals the one from a fresh workspace."""
     import torch
     A, xs, expect = _tagged_layer(H, b, r=40)
-    dm, dn, db = 64, 1024, 300
+    one = 0x3F80                                                  # bf16's 1
+    dm, dn, db, r = (64, 1024, 300, 0) if kind != "spmm" else (64, 1024, 3, 40)
     row_ptr = torch.arange(0, dm * dn // 2 + 1, dn // 2, dtype=torch.int32, device="cuda")
     cols = torch.arange(0, dn, 2, dtype=torch.int32, device="cuda").repeat(dm)
     values = torch.empty(len(cols), dtype=torch.bfloat16, device="cuda")
     mx = H.hss_mx_quantize(torch.zeros(dm, dn, device="cuda"), "fp4") if kind == "mx" else None
-    D = H.HSSMatrix("csr", dm, dn, torch.bfloat16, row_ptr=row_ptr, col_idx=cols, values=values, mx=mx)
+    U, Vt = torch.ones(dm, r, device="cuda").bfloat16(), torch.zeros(r, dn, device="cuda").bfloat16()
+    Vt[:, 0] = 1.0                                                # T = the first column of X
+    D = H.HSSMatrix("csr", dm, dn, torch.bfloat16, U=U, Vt=Vt, row_ptr=row_ptr, col_idx=cols, values=values, mx=mx)
     dx = torch.ones(db, dn, dtype=torch.bfloat16, device="cuda")
     ws = H.apply_workspace(max(H.hss_apply_workspace_size(A, b), H.hss_apply_workspace_size(D, db)), "cuda")
     y = torch.empty((b, A.m), dtype=torch.bfloat16, device="cuda")
-    one = 0x3F80                                                  # bf16's 1
-    for _ in range(one - 1):
+    for _ in range(one - 1 + ahead):
         H.hss_apply(A, xs[0], y, ws)
     for k in range(12):                                           # 1, and the values after it
         values.view(torch.int16).fill_(one + k)
+        if kind == "spmm":
+            dx[2].view(torch.int16).fill_(one + k)
         H.hss_apply(D, dx, ws=ws)
         assert O.bits_equal(to_host(H.hss_apply(A, xs[k % 3], ws=ws)), expect[k % 3]), k
