@@ -639,6 +639,87 @@ hss_status hss_grad_ckpt_workspace_size(const hss_matrix* A, int32_t b, size_t* 
 hss_status hss_grad_ckpt(const hss_matrix* A, int32_t b, const int8_t* codes, const uint8_t* scales, const void* G,
                          float* dS, float* dU, float* dVt, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * hss_adamw: one AdamW step (decoupled weight decay) over many tensors at
+ * once, e.g. the values of S, U and V^T of every layer, from the gradients of
+ * hss_grad, hss_grad_ckpt or hss_adapters_grad.
+ * ------------------------------------------------------------------------
+ * For every element, in fp32, each operation rounded by itself:
+ *   g = grad * grad_scale
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) (g * g)
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * (m / (sqrt(v) / sqrt(1 - beta2^step) + eps))
+ * (the factors that do not depend on the element are computed in fp64 and
+ * rounded once).  `step` counts from 1.
+ *   config.dtype        of the parameters: HSS_F32, or HSS_BF16 (rounded to
+ *                       nearest even; with `master`, an fp32 copy that the step
+ *                       reads and writes in the parameter's place, so that
+ *                       updates below bf16's step are not lost).
+ *   config.grad_dtype   of the gradients: HSS_F32 or HSS_BF16.
+ *   config.bits = 32    m, v: float[count].
+ *   config.bits = 8     m, v: uint8[count], the e4m3 codes of m and of sqrt(v),
+ *                       each times its block's scale; m_scale, v_scale:
+ *                       float[ceil(count / 256)], one for each 256 elements:
+ *                       the block's largest magnitude / 448 (0 below 2^-100: the
+ *                       block is then kept as zeros).  A value is rounded up or
+ *                       down at random, in proportion: with h the hash below
+ *                       of the element's position i and the step, u = the
+ *                       low (m) or high (sqrt(v)) 16 bits of h, u / 2^16 of a
+ *                       step of the code is added and what is below the step
+ *                       dropped (at most 448; sqrt(v) > 0 takes the smallest
+ *                       code at least).  i counts elements in blocks of 256
+ *                       through the call's tensors in order, each tensor
+ *                       starting a block of its own;
+ *                         h = i * 0x9E3779B1 + step * 0xBB67AE85 (mod 2^32)
+ *                         h = (h ^ h >> 16) * 0x6A09E667
+ *                         h = (h ^ h >> 15) * 0x5BE0CD19
+ *                         h = h ^ h >> 16.
+ *                       All zeros (codes and scales) is the initial state.
+ *   config.lr_dev, step_dev, grad_scale_dev: device scalars that take the
+ *     place of lr, step and grad_scale where not NULL, read when the kernel
+ *     runs (for a captured step: step_dev is not advanced; below 1 it counts
+ *     as 1).
+ * NaN and infinities: reach their element (bits = 32) or their block of 256
+ * elements' m or v (bits = 8: the block reads as NaN from then on).  With eps =
+ * 0 an element whose v is 0 becomes NaN.
+ * The same call gives the same bits every time.  Nothing is copied to the
+ * device but kernel arguments, so the call may be captured into a HIP graph.
+ * `tensors` is a HOST array; arrays are aligned to their element.  The tensors
+ * must be distinct: an array of one must not overlap an array of another (not
+ * checked).
+ * HSS_ERR_INVALID_ARG: null config, tensors (with count > 0) or arrays (of a
+ *   tensor with elements), count < 0, a tensor's count < 0 or >= 2^31, all of
+ *   them 2^39 elements or more, unknown bits or types, master with fp32 parameters,
+ *   misaligned arrays, arrays of one tensor that overlap, beta1 or beta2 outside
+ *   [0, 1), eps < 0, a number that is not finite, step outside [1, 2^31).
+ *   HSS_ERR_HIP.
+ */
+typedef struct hss_adamw_tensor {
+  int64_t count; /* elements; 0 = skipped */
+  void* param;
+  float* master; /* NULL = none */
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale; /* bits = 8 only (else ignored) */
+  float* v_scale;
+} hss_adamw_tensor;
+
+typedef struct hss_adamw_config {
+  int32_t bits;       /* of the moments: 32 or 8 */
+  int32_t dtype;      /* hss_dtype of the parameters */
+  int32_t grad_dtype; /* hss_dtype of the gradients  */
+  int32_t reserved;   /* 0 */
+  double lr, beta1, beta2, eps, weight_decay, grad_scale;
+  int64_t step;
+  const float* lr_dev;
+  const int32_t* step_dev;
+  const float* grad_scale_dev;
+} hss_adamw_config;
+
+hss_status hss_adamw(const hss_adamw_config* config, const hss_adamw_tensor* tensors, int32_t count,
+                     hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -757,3 +757,78 @@ def mx_decode(codes, scales, cols, fmt):
         c = np.stack([c & 15, c >> 4], axis=3).reshape(rows, ng, MX_GROUP)
         v = np.where(c & 8, -1.0, 1.0) * MX_GRID[c & 7] * s
     return v.reshape(rows, -1)[:, :cols]
+
+
+# ---------------------------------------------------------------------------
+# AdamW, with moments in 32 or 8 bits
+# ---------------------------------------------------------------------------
+
+ADAMW_BLOCK = 256  # elements that share one scale of the 8-bit moments
+
+
+def adamw(p, g, m, v, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=1.0, dtype=np.float64):
+    """(p, m, v) after one AdamW step with decoupled weight decay, t = step:
+    m = b1 m + (1 - b1) g, v = b2 v + (1 - b2) g^2,
+    p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps).
+
+    dtype=np.float32: every operation on an element rounded by itself, the
+    constants computed in fp64 and rounded once."""
+    f = dtype
+    p, g, m, v = (np.asarray(a, dtype=f) for a in (p, g, m, v))
+    with np.errstate(all="ignore"):
+        g = g * f(grad_scale)
+        m = f(beta1) * m + f(1.0 - beta1) * g
+        v = f(beta2) * v + f(1.0 - beta2) * (g * g)
+        root = f(1.0 / np.sqrt(1.0 - beta2 ** step))
+        p = p * f(1.0 - lr * weight_decay) - f(lr / (1.0 - beta1 ** step)) * (m / (np.sqrt(v) * root + f(eps)))
+    return p, m, v
+
+
+def adamw_hash(i, step):
+    """32 bits of a position and a step (uint32 array)."""
+    mask = np.uint64(0xFFFFFFFF)
+    h = (np.asarray(i, dtype=np.uint64) * np.uint64(0x9E3779B1) + np.uint64((int(step) * 0xBB67AE85) & 0xFFFFFFFF)) & mask
+    h = ((h ^ (h >> np.uint64(16))) * np.uint64(0x6A09E667)) & mask
+    h = ((h ^ (h >> np.uint64(15))) * np.uint64(0x5BE0CD19)) & mask
+    return (h ^ (h >> np.uint64(16))).astype(np.uint32)
+
+
+def moment8_decode(codes, scales):
+    """The fp64 values of e4m3 codes times their blocks' scales."""
+    c = np.asarray(codes, dtype=np.uint8).astype(np.int64)
+    e, frac = (c >> 3) & 15, c & 7
+    a = np.where(e == 0, frac * 2.0 ** -9, (8 + frac) * 2.0 ** (e - 10.0))
+    s = np.repeat(np.asarray(scales, dtype=np.float64), ADAMW_BLOCK)[:len(c)]
+    with np.errstate(all="ignore"):
+        return np.where(c & 128, -a, a) * s
+
+
+def moment8_scales(x):
+    """The scale of each block of a tensor's values: largest magnitude / 448,
+    0 below 2^-100, not finite where the block holds a NaN or an infinity."""
+    x = np.abs(np.asarray(x))
+    pad = np.zeros(-(-len(x) // ADAMW_BLOCK) * ADAMW_BLOCK, dtype=x.dtype)
+    pad[:len(x)] = x
+    s = pad.reshape(-1, ADAMW_BLOCK).max(axis=1) * x.dtype.type(1.0 / 448)
+    return np.where(s < 2.0 ** -100, x.dtype.type(0), s)
+
+
+def moment8_encode(x, scales, u, least):
+    """Codes of x over its blocks' scales: u / 2^16 of a code's step is added and
+    what is then below the step dropped; `least`: the smallest code of an x
+    that is not 0.  Blocks whose scale is 0 or not finite hold zeros.  fp32 x:
+    1 / scale is rounded, then the product with it."""
+    x = np.asarray(x)
+    f = x.dtype.type
+    codes = np.zeros(len(x), dtype=np.uint8)
+    for b in range(len(scales)):
+        if not (scales[b] > 0 and np.isfinite(scales[b])):
+            continue
+        at = slice(b * ADAMW_BLOCK, min(len(x), (b + 1) * ADAMW_BLOCK))
+        a = np.minimum(np.abs(x[at]) * (f(1) / f(scales[b])), f(448)).astype(np.float64)
+        e = np.where(a > 0, np.maximum(np.frexp(a)[1] - 1, -6), -6)  # 2^e <= a, or the subnormals' exponent
+        k = np.floor(a / 2.0 ** (e - 3.0) + u[at].astype(np.float64) / 65536)  # steps of 2^(e - 3)
+        c = np.minimum(k + 8 * (e + 6), 126)                         # 8 .. 15 of them above a subnormal's 0 .. 7
+        c = np.where(x[at] != 0, np.maximum(c, least), c).astype(np.int64)
+        codes[at] = c | np.where(np.signbit(x[at]), 128, 0)
+    return codes

@@ -22,8 +22,8 @@ import torch
 from ._lib import (HSS_BF16, HSS_COL16, HSS_DQ4, HSS_ERR_NONFINITE, HSS_HIER2, HSS_F32, HSS_FMT_2OF4, HSS_FMT_CSR,
                    HSS_MAX_BATCH, HSS_MX4, HSS_MX4_T, HSS_MX_GROUP, HSS_MXFP4, HSS_MXINT8, HSS_OK, HSS_OPT_BATCH_ROUTE, HSS_OPT_DECODE_FORCE_LOCAL, HSS_OPT_DECODE_MERGED,
                    HSS_OPT_DECODE_RPW, HSS_OPT_DECODE_WAVE_PRODUCERS,
-                   HSS_OPT_DECODE_SPIN, HSS_OPT_GRAD_DS_ROUTE, HSSError, HssMatrixStruct, LIB_PATH, check, lib,
-                   status_string)
+                   HSS_OPT_DECODE_SPIN, HSS_OPT_GRAD_DS_ROUTE, HssAdamwConfigStruct, HssAdamwTensorStruct, HSSError,
+                   HssMatrixStruct, LIB_PATH, check, lib, status_string)
 
 __all__ = [
     "hss_version", "hss_topk_count", "hss_split_workspace_size", "hss_split", "hss_get_error",
@@ -36,6 +36,7 @@ __all__ = [
     "hss_nm24_to_csr",
     "HSS_MX4", "HSS_MX4_T", "HSS_MX_GROUP", "MXTensor", "hss_mx_quantize", "hss_mx_dequantize",
     "hss_grad_ckpt", "hss_grad_ckpt_workspace_size", "grad_ckpt_workspace",
+    "AdamWState", "hss_adamw",
     "HSSMatrix", "SplitResult", "HSSError",
     "LIB_PATH", "status_string",
 ]
@@ -890,3 +891,146 @@ def hss_backward(A: HSSMatrix, X, G: torch.Tensor, At: Optional[HSSMatrix] = Non
     out = hss_grad_ckpt(A, X, G) if isinstance(X, MXTensor) else hss_grad(A, X, G)
     out["dX"] = hss_apply(At, G)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Optimizer
+# ---------------------------------------------------------------------------
+
+_ADAMW_BLOCK = 256  # elements of a tensor that share one scale of the 8-bit moments
+
+
+class AdamWState:
+    """What an AdamW step (hss_adamw) keeps for a list of parameters, e.g.
+    [A.values, A.U, A.Vt] of every layer: contiguous tensors of any shapes, of
+    one dtype (fp32 or bf16) and on one GPU, updated in place.
+
+    bits=32: m and v in fp32.  bits=8: m and v hold the e4m3 codes of the first
+    moment and of the square root of the second, each times m_scale or v_scale,
+    fp32, one for 256 elements: 2.03 bytes a parameter instead of 8.
+    master=True keeps an fp32 copy of bf16 parameters, which the step reads and
+    writes in their place (bf16 alone loses updates below 2^-9 of a value).
+
+    A new state starts from zeros.  To restore one, pass the lists that it held:
+    m, v (float32, or float8_e4m3fn with bits=8), m_scale, v_scale, master."""
+
+    def __init__(self, params, bits=32, master=None, m=None, v=None, m_scale=None, v_scale=None):
+        params = list(params)
+        if bits not in (32, 8):
+            raise ValueError("bits must be 32 or 8")
+        if not params:
+            raise ValueError("no parameters")
+        dtype, index = params[0].dtype, _index(params[0])
+        code = _dt(params[0])
+        dev = params[0].device
+        counts = [p.numel() for p in params]
+        blocks = [-(-k // _ADAMW_BLOCK) for k in counts]
+        moment = torch.float32 if bits == 32 else torch.float8_e4m3fn
+
+        def kept(name, given, dt, sizes, fresh):
+            if given is None:
+                return [fresh(k, dt) for k in sizes]
+            given = list(given)
+            if len(given) != len(sizes):
+                raise ValueError(f"{len(sizes)} parameters, {len(given)} tensors of {name}")
+            for t, k in zip(given, sizes):
+                if t.dtype != dt or t.numel() != k or not t.is_contiguous() or t.get_device() != index:
+                    raise ValueError(f"{name}: contiguous {dt} tensors, {'one value for 256 elements' if sizes is blocks else 'one value an element'}"
+                                     ", on the parameters' device")
+            return given
+
+        def zeros(k, dt):
+            return torch.zeros(k, dtype=torch.uint8, device=dev).view(dt) if dt == torch.float8_e4m3fn else \
+                torch.zeros(k, dtype=dt, device=dev)
+
+        kept("params", params, dtype, counts, None)
+        if master is True:
+            master = [p.detach().float().view(-1) for p in params]
+        elif master is False:
+            master = None
+        if master is not None:
+            if dtype != torch.bfloat16:
+                raise ValueError("a master copy goes with bf16 parameters")
+            master = kept("master", master, torch.float32, counts, None)
+        self.params, self.master, self.bits, self.dtype, self.index = params, master, bits, dtype, index
+        self.m, self.v = kept("m", m, moment, counts, zeros), kept("v", v, moment, counts, zeros)
+        self.m_scale = self.v_scale = None
+        if bits == 8:
+            self.m_scale = kept("m_scale", m_scale, torch.float32, blocks, zeros)
+            self.v_scale = kept("v_scale", v_scale, torch.float32, blocks, zeros)
+        elif m_scale is not None or v_scale is not None:
+            raise ValueError("scales go with bits=8")
+        held = [t for ts in (params, master, self.m, self.v, self.m_scale, self.v_scale) if ts is not None for t in ts]
+        end = 0
+        for a, z in sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in held if t.numel()):
+            if a < end:
+                raise ValueError("the tensors of a state must not share memory")
+            end = z
+        self.counts = counts
+        self._tensors = (HssAdamwTensorStruct * len(params))()
+        for k, t in enumerate(self._tensors):
+            t.param, t.m, t.v = _ptr(params[k]), _ptr(self.m[k]), _ptr(self.v[k])
+            t.master = _ptr(master[k]) if master is not None else None
+            t.m_scale, t.v_scale = (_ptr(self.m_scale[k]), _ptr(self.v_scale[k])) if bits == 8 else (None, None)
+        self._config = HssAdamwConfigStruct(bits=bits, dtype=code)
+
+
+def _device_scalar(name, t, dtype, index):
+    if t.dtype != dtype or t.numel() != 1 or t.get_device() != index:
+        raise ValueError(f"{name}: a number, or one {dtype} value on the parameters' device")
+    return t.data_ptr()
+
+
+def hss_adamw(state: AdamWState, grads, lr, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+              grad_scale=1.0) -> None:
+    """One AdamW step of state's parameters, in one launch for 48 tensors:
+
+        g = grad * grad_scale;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+        p = p (1 - lr weight_decay) - lr / (1 - b1^step) * m / (sqrt(v / (1 - b2^step)) + eps)
+
+    grads: one contiguous fp32 or bf16 tensor of each parameter's element count,
+    all of one dtype (what hss_backward and hss_adapters_grad return fits);
+    None leaves that parameter and its moments as they are.  step counts from 1.
+    lr, step and grad_scale may each be a tensor of one value on the GPU (fp32,
+    int32, fp32), read when the step runs: a captured step then follows them.
+
+    With bits=8 the new moments are rounded up or down at random, in proportion,
+    by a hash of the element's position and the step; the same call gives the
+    same bits."""
+    index = state.index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return hss_adamw(state, grads, lr, step, betas, eps, weight_decay, grad_scale)
+    grads = list(grads)
+    if len(grads) != len(state.counts):
+        raise ValueError(f"{len(state.counts)} parameters, {len(grads)} gradients")
+    dtype = next((g.dtype for g in grads if g is not None), torch.float32)
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}: float32 or bfloat16")
+    for t, g, k in zip(state._tensors, grads, state.counts):
+        if g is None:
+            t.count = 0
+            continue
+        if g.dtype != dtype or g.numel() != k or not g.is_contiguous() or g.get_device() != index:
+            raise ValueError("grads: contiguous tensors of one dtype, of their parameters' element counts and device")
+        t.count, t.grad = k, g.data_ptr()
+    c = state._config
+    c.grad_dtype = _DT[dtype]
+    c.beta1, c.beta2, c.eps, c.weight_decay = betas[0], betas[1], eps, weight_decay
+    c.lr_dev = c.step_dev = c.grad_scale_dev = None
+    c.lr, c.step, c.grad_scale = 0.0, 1, 1.0
+    if isinstance(lr, torch.Tensor):
+        c.lr_dev = _device_scalar("lr", lr, torch.float32, index)
+    else:
+        c.lr = lr
+    if isinstance(step, torch.Tensor):
+        c.step_dev = _device_scalar("step", step, torch.int32, index)
+    else:
+        c.step = step
+    if isinstance(grad_scale, torch.Tensor):
+        c.grad_scale_dev = _device_scalar("grad_scale", grad_scale, torch.float32, index)
+    else:
+        c.grad_scale = grad_scale
+    code = lib.hss_adamw(ctypes.byref(c), state._tensors, len(grads), _raw_stream(index))
+    if code:
+        check(code, "hss_adamw")

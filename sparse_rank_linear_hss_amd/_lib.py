@@ -53,6 +53,20 @@ class HssMatrixStruct(ctypes.Structure):
     ]
 
 
+class HssAdamwTensorStruct(ctypes.Structure):
+    """Mirror of struct hss_adamw_tensor in include/hss.h."""
+    _fields_ = [("count", c_int64), ("param", c_void_p), ("master", c_void_p), ("grad", c_void_p), ("m", c_void_p),
+                ("v", c_void_p), ("m_scale", c_void_p), ("v_scale", c_void_p)]
+
+
+class HssAdamwConfigStruct(ctypes.Structure):
+    """Mirror of struct hss_adamw_config in include/hss.h."""
+    _fields_ = [("bits", c_int32), ("dtype", c_int32), ("grad_dtype", c_int32), ("reserved", c_int32),
+                ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("step", c_int64), ("lr_dev", c_void_p), ("step_dev", c_void_p), ("grad_scale_dev", c_void_p)]
+
+
 class HSSError(RuntimeError):
     def __init__(self, code, where=""):
         self.code = code
@@ -111,6 +125,7 @@ def _load():
         "hss_grad_ckpt_workspace_size": (ctypes.c_int, [P(HssMatrixStruct), c_int32, P(c_size_t)]),
         "hss_grad_ckpt": (ctypes.c_int, [P(HssMatrixStruct), c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                          c_void_p, c_void_p, c_size_t, c_void_p]),
+        "hss_adamw": (ctypes.c_int, [P(HssAdamwConfigStruct), P(HssAdamwTensorStruct), c_int32, c_void_p]),
         "hss_nm24_to_csr": (ctypes.c_int, [c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
     }
     for name, (res, args) in sig.items():

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <vector>
@@ -29,6 +30,8 @@ size_t grad_ckpt_ws_bytes(const hss_matrix* A, int b);
 size_t grad_ckpt_ws_bytes_up_to(const hss_matrix* A, int b);
 hss_status launch_grad_ckpt(const hss_matrix* A, int b, const void* codes, const uint8_t* scales, const void* G,
                             float* dS, float* dU, float* dVt, void* ws, hipStream_t s);
+// adamw.hip
+hss_status launch_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tensors, int count, hipStream_t s);
 }  // namespace hss
 
 // ---------------------------------------------------------------------------
@@ -556,4 +559,46 @@ hss_status hss_nm24_to_csr(int32_t m, int32_t n, const uint32_t* nm_meta, int32_
   const size_t cb = (size_t)m * (n / 2) * 4, rb = (size_t)(m + 1) * 4;
   if (overlap(row_ptr, rb, col_idx, cb)) return HSS_ERR_INVALID_ARG;
   return hss::launch_nm_to_csr(m, n, nm_meta, row_ptr, col_idx, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Optimizer
+// ---------------------------------------------------------------------------
+// The arrays of one tensor: there, aligned to their elements, apart from each other.
+static bool adamw_tensor_ok(const hss_adamw_config* c, const hss_adamw_tensor& t) {
+  const size_t k = (size_t)t.count, state = c->bits == 8 ? 1 : 4, blocks = (k + 255) / 256;
+  struct Range {
+    const void* p;
+    size_t bytes, align;
+  } r[7] = {{t.param, k * dsize(c->dtype), dsize(c->dtype)}, {t.grad, k * dsize(c->grad_dtype), dsize(c->grad_dtype)},
+            {t.m, k * state, state},                         {t.v, k * state, state}};
+  int n = 4;
+  if (t.master) r[n++] = {t.master, k * 4, 4};
+  if (c->bits == 8) r[n++] = {t.m_scale, blocks * 4, 4}, r[n++] = {t.v_scale, blocks * 4, 4};
+  for (int i = 0; i < n; ++i) {
+    if (!r[i].p || (uintptr_t)r[i].p % r[i].align != 0) return false;
+    for (int j = 0; j < i; ++j)
+      if (overlap(r[i].p, r[i].bytes, r[j].p, r[j].bytes)) return false;
+  }
+  return true;
+}
+
+hss_status hss_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tensors, int32_t count, hipStream_t stream) {
+  if (!c || count < 0 || (count > 0 && !tensors)) return HSS_ERR_INVALID_ARG;
+  if ((c->bits != 32 && c->bits != 8) || !valid_dtype(c->dtype) || !valid_dtype(c->grad_dtype) || c->reserved != 0)
+    return HSS_ERR_INVALID_ARG;
+  for (const double x : {c->lr, c->beta1, c->beta2, c->eps, c->weight_decay, c->grad_scale})
+    if (!std::isfinite(x)) return HSS_ERR_INVALID_ARG;
+  if (c->beta1 < 0 || c->beta1 >= 1 || c->beta2 < 0 || c->beta2 >= 1 || c->eps < 0 || c->step < 1 || c->step >= kLimit)
+    return HSS_ERR_INVALID_ARG;
+  int64_t total = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const hss_adamw_tensor& t = tensors[i];
+    if (t.count < 0 || t.count >= kLimit) return HSS_ERR_INVALID_ARG;
+    total += t.count + 256;
+    if (total >= (int64_t)1 << 39) return HSS_ERR_INVALID_ARG;
+    if (t.count == 0) continue;
+    if ((t.master && c->dtype != HSS_BF16) || !adamw_tensor_ok(c, t)) return HSS_ERR_INVALID_ARG;
+  }
+  return hss::launch_adamw(c, tensors, count, stream);
 }
