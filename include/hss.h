@@ -640,6 +640,63 @@ hss_status hss_grad_ckpt(const hss_matrix* A, int32_t b, const int8_t* codes, co
                          float* dS, float* dU, float* dVt, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Adapters: a bank of low-rank updates beside a shared projection, each row of
+ * a batch with its own (many requests served together, or adapters trained
+ * over a frozen compressed layer).  The same factors as the layer's own U V^T,
+ * one pair for each adapter, bf16:
+ *   U      [count][m][r]  row-major      Vt  [count][r][n]  row-major
+ *   scale  float[count], NULL = 1        (device arrays)
+ * An adapter of a smaller rank is padded with zeros; a bank for each rank and
+ * one call for each bank (base = Y, other banks' rows without an adapter)
+ * reads less.
+ * ids    int32[b] (device): row t has the adapter ids[t]; any number outside
+ *        [0, count) means none.  Rows of one adapter may lie anywhere.
+ * ------------------------------------------------------------------------
+ * hss_adapters_apply: Y (b x m, bf16): for each row, l = ids[t],
+ *     Y[t] = base[t] + scale[l] (X[t] Vt_l^T) U_l^T,
+ *   Y[t] = base[t] without an adapter.  base (b x m, bf16): the shared
+ *   projection's output, e.g. hss_apply's; NULL = 0; may be Y itself, else must
+ *   not overlap it.
+ * hss_adapters_grad: for the upstream gradient G (b x m, bf16)
+ *     dX[t]  = base[t] + scale[l] (G[t] U_l) Vt_l             (b x n, bf16)
+ *     dU_l   = scale[l] sum over l's rows of G[t]^T (X[t] Vt_l^T)  (fp32)
+ *     dVt_l  = scale[l] sum over l's rows of (G[t] U_l)^T X[t]     (fp32)
+ *   in U's and Vt's layouts; zeros for an adapter without rows.  base (b x n):
+ *   the shared projection's input gradient, e.g. hss_apply's of the transposed
+ *   layer, as above.  NULL outputs are skipped.
+ * Sums are in fp32.  X Vt^T and G U, times scale in fp32, are kept as two bf16
+ * terms (16 significant bits) for Y and dX, as three (24 bits) for dU and dVt,
+ * so that these carry fp32 precision.  A non-finite value of a row or of an
+ * adapter's factors reaches that row's or that adapter's outputs only, as NaN
+ * where the formula may give an infinity.  The same inputs give the same bits
+ * on every call.
+ * ws: at least hss_adapters_workspace_size() or _grad_workspace_size() bytes
+ *   (no state kept, no initial contents), which serve every smaller batch too.
+ * HSS_ERR_UNSUPPORTED: an fp32 bank.  HSS_ERR_INVALID_ARG: unknown dtype, m, n
+ *   or r < 1, count outside [1, HSS_MAX_ADAPTERS], count r max(m, n) >= 2^31, b
+ *   outside [1, HSS_MAX_BATCH], b max(m, n) >= 2^31, null arrays (base, scale and
+ *   hss_adapters_grad's outputs may be), arrays not aligned to their element,
+ *   an output overlapping an input or another output.  HSS_ERR_WORKSPACE;
+ *   HSS_ERR_HIP. */
+#define HSS_MAX_ADAPTERS 4096
+
+typedef struct hss_adapters {
+  int32_t dtype; /* HSS_BF16 */
+  int32_t m, n, r, count;
+  const void* U;
+  const void* Vt;
+  const float* scale;
+} hss_adapters;
+
+hss_status hss_adapters_workspace_size(const hss_adapters* L, int32_t b, size_t* bytes);
+hss_status hss_adapters_apply(const hss_adapters* L, int32_t b, const void* X, const int32_t* ids, const void* base,
+                              void* Y, void* ws, size_t ws_bytes, hipStream_t stream);
+hss_status hss_adapters_grad_workspace_size(const hss_adapters* L, int32_t b, size_t* bytes);
+hss_status hss_adapters_grad(const hss_adapters* L, int32_t b, const void* X, const void* G, const int32_t* ids,
+                             const void* base, void* dX, float* dU, float* dVt, void* ws, size_t ws_bytes,
+                             hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * hss_adamw: one AdamW step (decoupled weight decay) over many tensors at
  * once, e.g. the values of S, U and V^T of every layer, from the gradients of
  * hss_grad, hss_grad_ckpt or hss_adapters_grad.

@@ -832,3 +832,36 @@ def moment8_encode(x, scales, u, least):
         c = np.where(x[at] != 0, np.maximum(c, least), c).astype(np.int64)
         codes[at] = c | np.where(np.signbit(x[at]), 128, 0)
     return codes
+
+
+# ---------------------------------------------------------------------------
+# Adapters: each row of a batch with its own low-rank update
+# ---------------------------------------------------------------------------
+
+def _adapter_rows(ids, l):
+    return np.flatnonzero(np.asarray(ids) == l)
+
+
+def adapters_apply(U, Vt, scale, X, ids, base=None):
+    """Y (b x m): base plus scale_l (x_t Vt_l^T) U_l^T for each row's adapter l =
+    ids[t]; base alone for a number outside [0, count)."""
+    U, Vt, X = (np.asarray(a, dtype=np.float64) for a in (U, Vt, X))
+    Y = np.zeros((X.shape[0], U.shape[1])) if base is None else np.array(base, dtype=np.float64)
+    for l in range(U.shape[0]):
+        rows = _adapter_rows(ids, l)
+        Y[rows] += scale[l] * (X[rows] @ Vt[l].T) @ U[l].T
+    return Y
+
+
+def adapters_grad(U, Vt, scale, X, G, ids, base=None):
+    """(dX, dU, dVt) of sum(G * adapters_apply(...)): dX has base added."""
+    U, Vt, X, G = (np.asarray(a, dtype=np.float64) for a in (U, Vt, X, G))
+    dX = np.zeros(X.shape) if base is None else np.array(base, dtype=np.float64)
+    dU, dVt = np.zeros(U.shape), np.zeros(Vt.shape)
+    for l in range(U.shape[0]):
+        rows = _adapter_rows(ids, l)
+        T, P = X[rows] @ Vt[l].T, G[rows] @ U[l]
+        dX[rows] += scale[l] * P @ Vt[l]
+        dU[l] = scale[l] * G[rows].T @ T
+        dVt[l] = scale[l] * P.T @ X[rows]
+    return dX, dU, dVt

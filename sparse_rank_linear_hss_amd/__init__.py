@@ -22,8 +22,8 @@ import torch
 from ._lib import (HSS_BF16, HSS_COL16, HSS_DQ4, HSS_ERR_NONFINITE, HSS_HIER2, HSS_F32, HSS_FMT_2OF4, HSS_FMT_CSR,
                    HSS_MAX_BATCH, HSS_MX4, HSS_MX4_T, HSS_MX_GROUP, HSS_MXFP4, HSS_MXINT8, HSS_OK, HSS_OPT_BATCH_ROUTE, HSS_OPT_DECODE_FORCE_LOCAL, HSS_OPT_DECODE_MERGED,
                    HSS_OPT_DECODE_RPW, HSS_OPT_DECODE_WAVE_PRODUCERS,
-                   HSS_OPT_DECODE_SPIN, HSS_OPT_GRAD_DS_ROUTE, HssAdamwConfigStruct, HssAdamwTensorStruct, HSSError,
-                   HssMatrixStruct, LIB_PATH, check, lib, status_string)
+                   HSS_OPT_DECODE_SPIN, HSS_OPT_GRAD_DS_ROUTE, HssAdamwConfigStruct, HssAdamwTensorStruct,
+                   HssAdaptersStruct, HSSError, HssMatrixStruct, LIB_PATH, check, lib, status_string)
 
 __all__ = [
     "hss_version", "hss_topk_count", "hss_split_workspace_size", "hss_split", "hss_get_error",
@@ -36,6 +36,8 @@ __all__ = [
     "hss_nm24_to_csr",
     "HSS_MX4", "HSS_MX4_T", "HSS_MX_GROUP", "MXTensor", "hss_mx_quantize", "hss_mx_dequantize",
     "hss_grad_ckpt", "hss_grad_ckpt_workspace_size", "grad_ckpt_workspace",
+    "HSSAdapters", "hss_adapters_apply", "hss_adapters_workspace_size", "adapters_workspace",
+    "hss_adapters_grad", "hss_adapters_grad_workspace_size", "adapters_grad_workspace",
     "AdamWState", "hss_adamw",
     "HSSMatrix", "SplitResult", "HSSError",
     "LIB_PATH", "status_string",
@@ -890,6 +892,151 @@ def hss_backward(A: HSSMatrix, X, G: torch.Tensor, At: Optional[HSSMatrix] = Non
         At = hss_transposed_layer(A)
     out = hss_grad_ckpt(A, X, G) if isinstance(X, MXTensor) else hss_grad(A, X, G)
     out["dX"] = hss_apply(At, G)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Adapters
+# ---------------------------------------------------------------------------
+
+class HSSAdapters:
+    """A bank of low-rank adapters beside a shared m x n projection, in device
+    memory; keeps its tensors alive.
+
+    U: [count, m, r], Vt: [count, r, n], contiguous bf16, the layouts of an
+    HSSMatrix's own factors; scale: float32 [count], None = 1.  An adapter of a
+    smaller rank is padded with zeros."""
+
+    __slots__ = ("U", "Vt", "scale", "count", "m", "n", "r", "dtype", "index", "struct", "_ref", "_sizes")
+
+    def __init__(self, U, Vt, scale=None):
+        if U.dim() != 3 or Vt.dim() != 3 or Vt.shape[:2] != (U.shape[0], U.shape[2]) or U.dtype != Vt.dtype or \
+                not U.is_contiguous() or not Vt.is_contiguous():
+            raise ValueError("U [count, m, r] and Vt [count, r, n] must be contiguous tensors of one dtype")
+        index = U.get_device()
+        if Vt.get_device() != index or (scale is not None and scale.get_device() != index):
+            raise ValueError("U, Vt and scale must be on one device")
+        self.count, self.m, self.r = U.shape
+        self.n = Vt.shape[2]
+        if scale is not None and (scale.dtype != torch.float32 or scale.shape != (self.count,) or not scale.is_contiguous()):
+            raise ValueError("scale must be a contiguous float32 tensor, one value an adapter")
+        self.U, self.Vt, self.scale, self.dtype, self.index = U, Vt, scale, U.dtype, index
+        self.struct = HssAdaptersStruct(dtype=_dt(U), m=self.m, n=self.n, r=self.r, count=self.count, U=_ptr(U), Vt=_ptr(Vt),
+                                        scale=_ptr(scale))
+        self._ref = ctypes.byref(self.struct)
+        self._sizes = {}
+
+
+def _adapters_size(L: HSSAdapters, b: int, call: str) -> int:
+    size = L._sizes.get((b, call))
+    if size is None:
+        out = ctypes.c_size_t(0)
+        check(getattr(lib, call)(L._ref, int(b), ctypes.byref(out)), call)
+        size = L._sizes[b, call] = int(out.value)
+    return size
+
+
+def hss_adapters_workspace_size(L: HSSAdapters, b: int) -> int:
+    return _adapters_size(L, b, "hss_adapters_workspace_size")
+
+
+def hss_adapters_grad_workspace_size(L: HSSAdapters, b: int) -> int:
+    return _adapters_size(L, b, "hss_adapters_grad_workspace_size")
+
+
+def adapters_workspace(L: HSSAdapters, b: int, device) -> torch.Tensor:
+    """A workspace of hss_adapters_apply for up to b rows.  It keeps no state
+    between calls; calls that share it must be ordered (one stream, or events)."""
+    return torch.empty(hss_adapters_workspace_size(L, b), dtype=torch.uint8, device=device)
+
+
+def adapters_grad_workspace(L: HSSAdapters, b: int, device) -> torch.Tensor:
+    """The same of hss_adapters_grad."""
+    return torch.empty(hss_adapters_grad_workspace_size(L, b), dtype=torch.uint8, device=device)
+
+
+def _check_adapter_rows(L: HSSAdapters, X: torch.Tensor, ids: torch.Tensor, index: int) -> int:
+    if X.dim() != 2 or X.shape[1] != L.n or X.dtype != L.dtype or not X.is_contiguous():
+        raise ValueError("X must be a contiguous b x n tensor of the adapters' dtype")
+    if L.index != index:
+        raise ValueError(f"the adapters must be on X's device, {X.device}")
+    if ids.dtype != torch.int32 or ids.shape != (X.shape[0],) or not ids.is_contiguous() or ids.get_device() != index:
+        raise ValueError("ids must be a contiguous int32 tensor, one for each row, on X's device")
+    return X.shape[0]
+
+
+def _check_like(name, t, shape, dtype, index):
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {tuple(shape)}, on X's device")
+
+
+def hss_adapters_apply(L: HSSAdapters, X: torch.Tensor, ids: torch.Tensor, base: Optional[torch.Tensor] = None,
+                       Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y (b x m) = base + each row's own adapter of X (b x n), l = ids[t]:
+
+        Y[t] = base[t] + scale[l] (X[t] Vt_l^T) U_l^T
+
+    ids: int32, one for each row; a number outside [0, count) means no adapter.
+    base: the shared projection's output (None = 0), e.g. of hss_apply with the
+    same X; Y may be base itself, to add in place."""
+    index = _index(X)
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return hss_adapters_apply(L, X, ids, base, Y, ws)
+    b = _check_adapter_rows(L, X, ids, index)
+    shape = (b, L.m)
+    if base is not None:
+        _check_like("base", base, shape, L.dtype, index)
+    if Y is None:
+        Y = torch.empty(shape, dtype=L.dtype, device=X.device)
+    elif Y is not base:
+        _check_like("Y", Y, shape, L.dtype, index)
+    if ws is None:
+        ws = adapters_workspace(L, b, X.device)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        _check_ws(ws, index)
+    code = lib.hss_adapters_apply(L._ref, b, X.data_ptr(), ids.data_ptr(), None if base is None else base.data_ptr(),
+                                  Y.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(index))
+    if code:
+        check(code, "hss_adapters_apply")
+    return Y
+
+
+def hss_adapters_grad(L: HSSAdapters, X: torch.Tensor, G: torch.Tensor, ids: torch.Tensor,
+                      base: Optional[torch.Tensor] = None, dX=True, dU=True, dVt=True, out: Optional[dict] = None,
+                      ws: Optional[torch.Tensor] = None) -> dict:
+    """The backward pass of hss_adapters_apply for the upstream gradient G
+    (b x m): dX (b x n, bf16) = base + scale[l] (G[t] U_l) Vt_l for each row,
+    and dU, dVt in fp32, in the layouts of U and Vt, zeros for an adapter without rows.
+
+    base: the shared projection's input gradient (None = 0), e.g. the dX of
+    hss_backward; dX may be base itself.  Pass False to skip an output.  out:
+    tensors to write (a dict with the keys wanted); then dX, dU and dVt are ignored."""
+    index = _index(X)
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return hss_adapters_grad(L, X, G, ids, base, dX, dU, dVt, out, ws)
+    b = _check_adapter_rows(L, X, ids, index)
+    _check_like("G", G, (b, L.m), L.dtype, index)
+    if base is not None:
+        _check_like("base", base, (b, L.n), L.dtype, index)
+    specs = {"dX": ((b, L.n), L.dtype), "dU": (L.U.shape, torch.float32), "dVt": (L.Vt.shape, torch.float32)}
+    if out is None:
+        out = {k: torch.empty(specs[k][0], dtype=specs[k][1], device=X.device)
+               for k, wanted in (("dX", dX), ("dU", dU), ("dVt", dVt)) if wanted}
+    else:
+        for k, t in out.items():
+            if k not in specs:
+                raise ValueError("out must hold 'dX', 'dU' or 'dVt'")
+            _check_like(k, t, *specs[k], index)
+    if ws is None:
+        ws = adapters_grad_workspace(L, b, X.device)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        _check_ws(ws, index)
+    code = lib.hss_adapters_grad(L._ref, b, X.data_ptr(), G.data_ptr(), ids.data_ptr(), _ptr(base), _ptr(out.get("dX")),
+                                 _ptr(out.get("dU")), _ptr(out.get("dVt")), ws.data_ptr(), ws.nbytes, _raw_stream(index))
+    if code:
+        check(code, "hss_adapters_grad")
     return out
 
 

@@ -53,6 +53,12 @@ class HssMatrixStruct(ctypes.Structure):
     ]
 
 
+class HssAdaptersStruct(ctypes.Structure):
+    """Mirror of struct hss_adapters in include/hss.h."""
+    _fields_ = [("dtype", c_int32), ("m", c_int32), ("n", c_int32), ("r", c_int32), ("count", c_int32),
+                ("U", c_void_p), ("Vt", c_void_p), ("scale", c_void_p)]
+
+
 class HssAdamwTensorStruct(ctypes.Structure):
     """Mirror of struct hss_adamw_tensor in include/hss.h."""
     _fields_ = [("count", c_int64), ("param", c_void_p), ("master", c_void_p), ("grad", c_void_p), ("m", c_void_p),
@@ -125,6 +131,12 @@ def _load():
         "hss_grad_ckpt_workspace_size": (ctypes.c_int, [P(HssMatrixStruct), c_int32, P(c_size_t)]),
         "hss_grad_ckpt": (ctypes.c_int, [P(HssMatrixStruct), c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                          c_void_p, c_void_p, c_size_t, c_void_p]),
+        "hss_adapters_workspace_size": (ctypes.c_int, [P(HssAdaptersStruct), c_int32, P(c_size_t)]),
+        "hss_adapters_apply": (ctypes.c_int, [P(HssAdaptersStruct), c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                              c_void_p, c_size_t, c_void_p]),
+        "hss_adapters_grad_workspace_size": (ctypes.c_int, [P(HssAdaptersStruct), c_int32, P(c_size_t)]),
+        "hss_adapters_grad": (ctypes.c_int, [P(HssAdaptersStruct), c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                             c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
         "hss_adamw": (ctypes.c_int, [P(HssAdamwConfigStruct), P(HssAdamwTensorStruct), c_int32, c_void_p]),
         "hss_nm24_to_csr": (ctypes.c_int, [c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
     }

@@ -27,8 +27,8 @@ ARCH = os.environ.get("HSS_OFFLOAD_ARCH", "gfx950")
 SOURCES = ["decode_inst_bf16_csr_b1.hip", "decode_inst_bf16_csr_bn.hip", "decode_inst_bf16_csr16_b1.hip",
            "decode_inst_bf16_csr16_bn.hip", "decode_inst_bf16_nm.hip", "decode_inst_f32.hip", "decode.hip",
            "mfma.hip", "spmm.hip", "nm_mma.hip", "grad.hip", "split.hip", "apply.hip", "hier.hip", "noalloc.hip",
-           "mx.hip", "mx_apply.hip", "mx_skinny.hip", "mx_gemm.hip", "mm_group.hip", "gemm256.hip", "grad_ckpt.hip", "adamw.hip",
-           "hss_api.cpp"]
+           "mx.hip", "mx_apply.hip", "mx_skinny.hip", "mx_gemm.hip", "mm_group.hip", "gemm256.hip", "grad_ckpt.hip", "adapters.hip",
+           "adamw.hip", "hss_api.cpp"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

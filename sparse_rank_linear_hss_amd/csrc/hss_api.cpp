@@ -30,6 +30,13 @@ size_t grad_ckpt_ws_bytes(const hss_matrix* A, int b);
 size_t grad_ckpt_ws_bytes_up_to(const hss_matrix* A, int b);
 hss_status launch_grad_ckpt(const hss_matrix* A, int b, const void* codes, const uint8_t* scales, const void* G,
                             float* dS, float* dU, float* dVt, void* ws, hipStream_t s);
+// adapters.hip
+size_t adapters_ws_bytes(const hss_adapters* L, int b, bool grad);
+size_t adapters_ws_bytes_up_to(const hss_adapters* L, int b, bool grad);
+hss_status launch_adapters_apply(const hss_adapters* L, int b, const void* X, const int32_t* ids, const void* base,
+                                 void* Y, void* ws, hipStream_t s);
+hss_status launch_adapters_grad(const hss_adapters* L, int b, const void* X, const void* G, const int32_t* ids,
+                                const void* base, void* dX, float* dU, float* dVt, void* ws, hipStream_t s);
 // adamw.hip
 hss_status launch_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tensors, int count, hipStream_t s);
 }  // namespace hss
@@ -559,6 +566,92 @@ hss_status hss_nm24_to_csr(int32_t m, int32_t n, const uint32_t* nm_meta, int32_
   const size_t cb = (size_t)m * (n / 2) * 4, rb = (size_t)(m + 1) * 4;
   if (overlap(row_ptr, rb, col_idx, cb)) return HSS_ERR_INVALID_ARG;
   return hss::launch_nm_to_csr(m, n, nm_meta, row_ptr, col_idx, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Adapters
+// ---------------------------------------------------------------------------
+static hss_status check_adapters(const hss_adapters* L, int32_t b) {
+  if (!L || !valid_dtype(L->dtype) || L->m < 1 || L->n < 1 || L->r < 1 || L->count < 1 || L->count > HSS_MAX_ADAPTERS ||
+      b < 1 || b > HSS_MAX_BATCH)
+    return HSS_ERR_INVALID_ARG;
+  const int64_t wide = std::max(L->m, L->n);
+  // count r < 2^31 comes first: the product of all three could overflow
+  if ((int64_t)L->count * L->r >= kLimit || (int64_t)L->count * L->r * wide >= kLimit || b * wide >= kLimit)
+    return HSS_ERR_INVALID_ARG;
+  if (!L->U || !L->Vt || (uintptr_t)L->U % 2 != 0 || (uintptr_t)L->Vt % 2 != 0 || (uintptr_t)L->scale % 4 != 0)
+    return HSS_ERR_INVALID_ARG;
+  return L->dtype == HSS_BF16 ? HSS_OK : HSS_ERR_UNSUPPORTED;
+}
+
+namespace {
+struct AdRange {
+  const void* p;
+  size_t bytes;
+};
+}  // namespace
+
+// Outputs (null ones are skipped) against the inputs and each other; `base` may
+// be outs[0] itself.
+static bool adapters_ranges_ok(const AdRange* outs, int nout, const AdRange* in, int nin, const void* base) {
+  for (int i = 0; i < nout; ++i) {
+    if (!outs[i].p) continue;
+    for (int k = 0; k < nin; ++k)
+      if (in[k].p && overlap(outs[i].p, outs[i].bytes, in[k].p, in[k].bytes)) return false;
+    for (int k = 0; k < i; ++k)
+      if (outs[k].p && overlap(outs[i].p, outs[i].bytes, outs[k].p, outs[k].bytes)) return false;
+    if (base && !(i == 0 && base == outs[0].p) && overlap(outs[i].p, outs[i].bytes, base, outs[0].bytes)) return false;
+  }
+  return true;
+}
+
+hss_status hss_adapters_workspace_size(const hss_adapters* L, int32_t b, size_t* bytes) {
+  if (!bytes) return HSS_ERR_INVALID_ARG;
+  const hss_status st = check_adapters(L, b);
+  if (st != HSS_OK) return st;
+  *bytes = hss::adapters_ws_bytes_up_to(L, b, false);
+  return HSS_OK;
+}
+
+hss_status hss_adapters_grad_workspace_size(const hss_adapters* L, int32_t b, size_t* bytes) {
+  if (!bytes) return HSS_ERR_INVALID_ARG;
+  const hss_status st = check_adapters(L, b);
+  if (st != HSS_OK) return st;
+  *bytes = hss::adapters_ws_bytes_up_to(L, b, true);
+  return HSS_OK;
+}
+
+hss_status hss_adapters_apply(const hss_adapters* L, int32_t b, const void* X, const int32_t* ids, const void* base,
+                              void* Y, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const hss_status st = check_adapters(L, b);
+  if (st != HSS_OK) return st;
+  if (!X || !ids || !Y || (uintptr_t)X % 2 != 0 || (uintptr_t)Y % 2 != 0 || (uintptr_t)base % 2 != 0 ||
+      (uintptr_t)ids % 4 != 0)
+    return HSS_ERR_INVALID_ARG;
+  const size_t factor = (size_t)L->count * L->r * 2;
+  const AdRange out = {Y, (size_t)b * L->m * 2};
+  const AdRange in[5] = {{X, (size_t)b * L->n * 2}, {ids, (size_t)b * 4}, {L->U, factor * L->m}, {L->Vt, factor * L->n},
+                         {L->scale, (size_t)L->count * 4}};
+  if (!adapters_ranges_ok(&out, 1, in, 5, base)) return HSS_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, hss::adapters_ws_bytes(L, b, false))) return HSS_ERR_WORKSPACE;
+  return hss::launch_adapters_apply(L, b, X, ids, base, Y, ws, stream);
+}
+
+hss_status hss_adapters_grad(const hss_adapters* L, int32_t b, const void* X, const void* G, const int32_t* ids,
+                             const void* base, void* dX, float* dU, float* dVt, void* ws, size_t ws_bytes,
+                             hipStream_t stream) {
+  const hss_status st = check_adapters(L, b);
+  if (st != HSS_OK) return st;
+  if (!X || !G || !ids || (uintptr_t)X % 2 != 0 || (uintptr_t)G % 2 != 0 || (uintptr_t)dX % 2 != 0 ||
+      (uintptr_t)base % 2 != 0 || (uintptr_t)ids % 4 != 0 || (uintptr_t)dU % 4 != 0 || (uintptr_t)dVt % 4 != 0)
+    return HSS_ERR_INVALID_ARG;
+  const size_t factor = (size_t)L->count * L->r;
+  const AdRange out[3] = {{dX, (size_t)b * L->n * 2}, {dU, factor * L->m * 4}, {dVt, factor * L->n * 4}};
+  const AdRange in[6] = {{X, (size_t)b * L->n * 2},  {G, (size_t)b * L->m * 2},  {ids, (size_t)b * 4},
+                         {L->U, factor * L->m * 2},  {L->Vt, factor * L->n * 2}, {L->scale, (size_t)L->count * 4}};
+  if (!adapters_ranges_ok(out, 3, in, 6, dX ? base : nullptr)) return HSS_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, hss::adapters_ws_bytes(L, b, true))) return HSS_ERR_WORKSPACE;
+  return hss::launch_adapters_grad(L, b, X, G, ids, base, dX, dU, dVt, ws, stream);
 }
 
 // ---------------------------------------------------------------------------
