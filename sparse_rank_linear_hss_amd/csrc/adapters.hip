@@ -46,8 +46,9 @@ struct AdArgs {
   float* dVt;
   // Workspace.  A tile's rows have the slots TM tile .. TM tile + rows - 1.
   float* part[2];   // partial sums of T and P: [split][slots][rg]
-  uint16_t* t2;     // two terms of P: [slots][2][rp], zeros past r; null = none
-  uint16_t* t3[2];  // three terms of T and P: [3][rg][slots]; null = none
+  // Terms as the matrix cores' operands, 64 lanes of 8 values (null = none):
+  uint16_t* t2;     // two of P: [tile][rp / 32][term][half of the rows], lane: row % 16 + 16 (rank / 8 % 4)
+  uint16_t* t3[2];  // three of T and P: [tile][rg / 16][term], lane: rank % 16 + 16 (slot / 8 % 4)
   int2* info;       // [tiles]: adapter (-1: none) and rows (0: no such tile)
   uint16_t* rows;   // [slots]
   int2* first;      // [count]: an adapter's first tile and its rows (more than kAdSmall rows)
@@ -188,20 +189,21 @@ __device__ __forceinline__ u32x4 ad_column(const AdPiece<CW> (&v)[8], int f) {
   return o;
 }
 
-// CW bf16 at any 2-byte aligned address.
+// CW bf16 at a byte offset (a multiple of 2) from a base that the wave shares.
 template <int CW>
-__device__ __forceinline__ AdPiece<CW> ad_piece(const uint16_t* at) {
+__device__ __forceinline__ AdPiece<CW> ad_piece_at(const void* base, uint32_t at) {
   struct __attribute__((packed, aligned(2))) Raw {
     uint32_t w[CW / 2];
   };
-  const Raw raw = *reinterpret_cast<const Raw*>(at);
+  const Raw raw = *reinterpret_cast<const Raw*>(static_cast<const char*>(base) + at);
   AdPiece<CW> p;
 #pragma unroll
   for (int d = 0; d < CW / 2; ++d) p.w[d] = raw.w[d];
   return p;
 }
 
-// The first `left` of them, zeros behind: the slow way, for ends.
+// The first `left` of them, zeros behind: element by element, for the ends of rows
+// shorter than a piece.
 template <int CW>
 __device__ __forceinline__ AdPiece<CW> ad_piece_end(const uint16_t* at, int left) {
   AdPiece<CW> p;
@@ -213,6 +215,39 @@ __device__ __forceinline__ AdPiece<CW> ad_piece_end(const uint16_t* at, int left
   return p;
 }
 
+template <int CW>
+__device__ __forceinline__ AdPiece<CW> ad_nothing() {
+  AdPiece<CW> p;
+#pragma unroll
+  for (int d = 0; d < CW / 2; ++d) p.w[d] = 0u;
+  return p;
+}
+
+// Eight bf16 without the first s, zeros behind (s >= 8: zeros).  A row's last
+// columns are loaded as the eight that end with the row, and shifted.
+__device__ __forceinline__ u32x4 ad_drop(u32x4 v, int s) {
+  uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+  if (s >= 4) lo = hi, hi = 0, s -= 4;
+  const int bits = 16 * min(s, 3);
+  lo = lo >> bits | (hi << 1) << (63 - bits);
+  hi >>= bits;
+  if (s >= 4) lo = 0, hi = 0;
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// Eight bf16 of a row of n at column k, zeros past the end, in one load (n >= 8).
+__device__ __forceinline__ u32x4 ad_tail8(const uint16_t* row, int k, int n) {
+  const int from = min(k, n - 8);
+  return ad_drop(load8(row + from), k - from);
+}
+
+// 16 bytes at a byte offset from a base that the whole wave shares (arrays have
+// fewer than 2^31 elements of two bytes: one register an address).
+__device__ __forceinline__ u32x4 ad_load(const void* base, uint32_t at) {
+  const Bytes16 v = *reinterpret_cast<const Bytes16*>(static_cast<const char*>(base) + at);
+  return u32x4{v.w[0], v.w[1], v.w[2], v.w[3]};
+}
+
 // What this wave wrote to its part of LDS before is read after (LDS takes a
 // wave's accesses in order; this keeps the compiler to it).
 __device__ __forceinline__ void ad_wave_sync() {
@@ -220,28 +255,42 @@ __device__ __forceinline__ void ad_wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// The next bf16 term of x, which loses it (an infinity leaves 0, not the NaN of
-// inf - inf).
-__device__ __forceinline__ uint32_t ad_term(float& x) {
-  const uint32_t t = f32_to_bf16(x);
-  x = (t & 0x7fffu) == 0x7f80u ? 0.f : x - __uint_as_float(t << 16);
+// Two fp32 values as bf16 (to nearest even), in a dword.
+__device__ __forceinline__ uint32_t ad_pack(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, mx_bf16x2));
+}
+
+// The next bf16 terms of two values, which lose them (an infinity leaves 0, not the
+// NaN of inf - inf).
+__device__ __forceinline__ uint32_t ad_term2(float& x, float& y) {
+  const uint32_t t = ad_pack(x, y);
+  x = (t & 0x7fffu) == 0x7f80u ? 0.f : x - bf16lo(t);
+  y = (t & 0x7fff0000u) == 0x7f800000u ? 0.f : y - bf16hi(t);
   return t;
 }
 
 // ---------------------------------------------------------------------------
 // T = X Vt^T and P = G U, partial sums over a block's part of K; the blocks of split
 // 0 also write the table of tiles.
-//   D[rank][row] += A[rank][k] B[row][k]: A = Vt_l as stored, or U_l transposed
-//   through the wave's part of LDS.  Wave w takes units w, w + 4, .. of the block's;
-//   the next one's loads are in flight while one is multiplied.  The four waves'
-//   sums meet in LDS.
+//   D[rank][row] += A[rank][k] B[row][k]: A = Vt_l as stored, or U_l transposed.
+//   Wave w takes units w, w + 4, .. of the block's, each through the wave's own part
+//   of LDS, with no barrier: eight lanes load 128 adjacent bytes of a row (loaded as
+//   the matrix cores take it, neighbouring lanes would have different rows, and each
+//   lane's 16 bytes be an access of its own to the cache: 4 times as many; prefill
+//   of 2048 rows 4096 x 11008 r 64: 37 us).  The next unit's loads are in flight
+//   while one is multiplied.  The four waves' sums meet in LDS.
 // grid: (splits of T and of P, tiles, groups of 16 NR ranks)
 // ---------------------------------------------------------------------------
 static constexpr int kAdPitch = kAdUnit + 8;  // of U^T in LDS
 
+// Slot of 16-byte chunk c of a 128-byte row in LDS: eight rows' reads of one chunk
+// fall on different banks.
+__device__ __forceinline__ int ad_slot(int row, int c) { return row * kAdUnit + 8 * (c ^ (row & 7)); }
+
 template <int TM, int NR>
 __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
-  constexpr int MF = TM / 16;
+  constexpr int MF = TM / 16, XL = TM / 8, VL = 2 * NR;
   extern __shared__ __align__(16) char smem[];
   __shared__ uint16_t rows[TM];
   __shared__ int part[6];
@@ -249,149 +298,169 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
   const int side = (int)blockIdx.x >= a.splits[0];
   const int z = (int)blockIdx.x - (side ? a.splits[0] : 0);
   const bool lead = blockIdx.x == 0 && blockIdx.z == 0;
-  const AdTile at = ad_tile<TM>(a, tile, rows, part, reinterpret_cast<int*>(smem), lead && tile == 0 ? a.first : nullptr);
-  if (lead) {
+  AdTile at = ad_tile<TM>(a, tile, rows, part, reinterpret_cast<int*>(smem), lead && tile == 0 ? a.first : nullptr);
+  at = {uniform(at.adapter), uniform(at.rows)};
+  if (lead) {  // (a tile's free slots repeat its last row, so that all of them may be read)
     if (threadIdx.x == 0) a.info[tile] = make_int2(at.adapter, at.rows);
-    if ((int)threadIdx.x < at.rows) a.rows[TM * tile + threadIdx.x] = rows[threadIdx.x];
+    if (threadIdx.x < TM && at.rows) a.rows[TM * tile + threadIdx.x] = rows[min((int)threadIdx.x, at.rows - 1)];
   }
   if (at.rows == 0 || at.adapter < 0) return;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int K = side ? a.m : a.n;
   const int u0 = z * a.units[side], u1 = min(u0 + a.units[side], (K + kAdUnit - 1) / kAdUnit);
-  const uint16_t* xrow[MF];
+  const int whole = min(u1, K / kAdUnit);  // units before here end inside the row
+  const int c8 = lane & 7, r8 = lane >> 3;
+  uint16_t* xs = reinterpret_cast<uint16_t*>(smem) + w * (TM * kAdUnit + 16 * NR * kAdPitch);  // the wave's: [TM][64]
+  uint16_t* vs = xs + TM * kAdUnit;  // [16 NR][64], or of U^T [16 NR][kAdPitch]
+  const uint16_t* X = side ? a.G : a.X;
+  int xrow[XL];
 #pragma unroll
-  for (int f = 0; f < MF; ++f)
-    xrow[f] = (side ? a.G : a.X) + (int64_t)rows[min(16 * f + i, at.rows - 1)] * K;
+  for (int j = 0; j < XL; ++j) xrow[j] = rows[min(8 * j + r8, at.rows - 1)] * K;
 
   f32x4 acc[MF][NR];
 #pragma unroll
   for (int f = 0; f < MF; ++f)
 #pragma unroll
     for (int g = 0; g < NR; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 x[XL];
+  auto put_x = [&]() {
+#pragma unroll
+    for (int j = 0; j < XL; ++j) *reinterpret_cast<u32x4*>(xs + ad_slot(8 * j + r8, c8)) = x[j];
+  };
 
-  const int whole = min(u1, K / kAdUnit);  // units before here end inside the row
   if (!side) {
-    const uint16_t* vrow[NR];
+    const uint16_t* V = a.Vt + (int64_t)at.adapter * a.r * K;
+    int vrow[VL];
 #pragma unroll
-    for (int g = 0; g < NR; ++g)
-      vrow[g] = a.Vt + ((int64_t)at.adapter * a.r + min(rank0 + 16 * g + i, a.r - 1)) * K;
-    struct Regs {
-      u32x4 x[2][MF], v[2][NR];
-    };
-    auto load = [&](int u, Regs& r) {
+    for (int j = 0; j < VL; ++j) vrow[j] = min(rank0 + 8 * j + r8, a.r - 1) * K;
+    u32x4 v[VL];
+    auto load = [&](int u) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = u * kAdUnit + 32 * h + 8 * q;
+      for (int j = 0; j < XL; ++j) x[j] = ad_load(X, 2u * (xrow[j] + u * kAdUnit + 8 * c8));
 #pragma unroll
-        for (int f = 0; f < MF; ++f) r.x[h][f] = load8(xrow[f] + k);
-#pragma unroll
-        for (int g = 0; g < NR; ++g) r.v[h][g] = load8(vrow[g] + k);
-      }
-    };
-    auto multiply = [&](const Regs& r) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int f = 0; f < MF; ++f)
-#pragma unroll
-          for (int g = 0; g < NR; ++g)
-            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(r.v[h][g]), as_bf16(r.x[h][f]), acc[f][g], 0, 0, 0);
-    };
-    int u = u0 + w;
-    if (u < whole) {
-      Regs ra, rb;
-      load(u, ra);
-      for (; u + 4 < whole; u += 8) {
-        load(u + 4, rb);
-        __builtin_amdgcn_sched_barrier(0);  // the loads first: the compiler would sink them
-        multiply(ra);
-        load(min(u + 8, whole - 1), ra);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(rb);
-      }
-      if (u < whole) multiply(ra), u += 4;
-    }
-    if (u < u1) {  // the unit in which the rows end
-      Regs re;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = u * kAdUnit + 32 * h + 8 * q;
-#pragma unroll
-        for (int f = 0; f < MF; ++f) re.x[h][f] = load_row8(xrow[f], k, K);
-#pragma unroll
-        for (int g = 0; g < NR; ++g) re.v[h][g] = load_row8(vrow[g], k, K);
-      }
-      multiply(re);
-    }
-  } else {
-    uint16_t* ut = reinterpret_cast<uint16_t*>(smem) + w * 16 * NR * kAdPitch;  // the wave's: [16 NR][kAdPitch]
-    // 8 x 8 pieces, one a lane: 8 of the unit's j times 2 NR of the ranks.  A piece
-    // in which the ranks end holds the next row's first values (its ranks are not
-    // stored), so the factors' last rows are read the slow way.
-    const int kb = lane % (2 * NR), jb = lane / (2 * NR), rank = min(rank0 + 8 * kb, (a.r - 1) & ~7);
-    const uint16_t* U = a.U + (int64_t)at.adapter * a.m * a.r + rank;
-    const bool over = (a.r & 7) != 0 && at.adapter == a.count - 1;
-    const int safe = over ? min(whole, (K - 8) / kAdUnit) : whole;
-    AdPiece<8> v[8];
-    auto load_x = [&](int u, u32x4 (&x)[2][MF]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int f = 0; f < MF; ++f) x[h][f] = load8(xrow[f] + u * kAdUnit + 32 * h + 8 * q);
-    };
-    auto load_v = [&](int u) {
-      if (jb < 8) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = ad_piece<8>(U + (int64_t)(u * kAdUnit + 8 * jb + e) * a.r);
-      }
+      for (int j = 0; j < VL; ++j) v[j] = ad_load(V, 2u * (vrow[j] + u * kAdUnit + 8 * c8));
     };
     auto put = [&]() {
-      if (jb < 8) {
+      put_x();
 #pragma unroll
-        for (int f = 0; f < 8; ++f) *reinterpret_cast<u32x4*>(ut + (8 * kb + f) * kAdPitch + 8 * jb) = ad_column<8>(v, f);
+      for (int j = 0; j < VL; ++j) *reinterpret_cast<u32x4*>(vs + ad_slot(8 * j + r8, c8)) = v[j];
+      ad_wave_sync();
+    };
+    auto multiply = [&]() {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        u32x4 xf[MF];
+#pragma unroll
+        for (int f = 0; f < MF; ++f) xf[f] = *reinterpret_cast<const u32x4*>(xs + ad_slot(16 * f + i, 4 * h + q));
+#pragma unroll
+        for (int g = 0; g < NR; ++g) {
+          const u32x4 vf = *reinterpret_cast<const u32x4*>(vs + ad_slot(16 * g + i, 4 * h + q));
+#pragma unroll
+          for (int f = 0; f < MF; ++f)
+            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf), as_bf16(xf[f]), acc[f][g], 0, 0, 0);
+        }
       }
       ad_wave_sync();
     };
-    auto multiply = [&](const u32x4 (&x)[2][MF]) {
+    int u = u0 + w;
+    if (u < whole) {
+      load(u);
+      for (; u + 4 < whole; u += 4) {
+        put();
+        load(u + 4);
+        multiply();
+      }
+      put(), multiply();
+      u += 4;
+    }
+    if (u < u1) {  // the unit in which the rows end
+      const int k = u * kAdUnit + 8 * c8;
+      if (K >= 8) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < XL; ++j) x[j] = ad_tail8(X + xrow[j], k, K);
+#pragma unroll
+        for (int j = 0; j < VL; ++j) v[j] = ad_tail8(V + vrow[j], k, K);
+      } else {
+#pragma unroll
+        for (int j = 0; j < XL; ++j) x[j] = __builtin_bit_cast(u32x4, ad_piece_end<8>(X + xrow[j], k < K ? K - k : 0));
+#pragma unroll
+        for (int j = 0; j < VL; ++j) v[j] = __builtin_bit_cast(u32x4, ad_piece_end<8>(V + vrow[j], k < K ? K - k : 0));
+      }
+      put(), multiply();
+    }
+  } else {
+    // 8 x 8 pieces, one a lane: 8 of the unit's j times 2 NR of the ranks.  The piece
+    // in which the ranks end is loaded as the row's last eight, and stored behind the
+    // one before it.
+    const int kb = lane % (2 * NR), jb = lane / (2 * NR), want = rank0 + 8 * kb, rank = max(0, min(want, a.r - 8));
+    const uint16_t* U = a.U + (int64_t)at.adapter * a.m * a.r;
+    const int off = 8 * kb - (want - rank);  // its row in LDS; below 0 or past the ranks: none
+    const bool mine = jb < 8 && want < a.r;
+    const int safe = a.r >= 8 ? whole : u0;  // rows shorter than a piece: the slow way
+    AdPiece<8> v[8];
+    auto load = [&](int u) {
+#pragma unroll
+      for (int j = 0; j < XL; ++j) x[j] = ad_load(X, 2u * (xrow[j] + u * kAdUnit + 8 * c8));
+      if (mine) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __builtin_bit_cast(AdPiece<8>, ad_load(U, 2u * ((u * kAdUnit + 8 * jb + e) * a.r + rank)));
+      }
+    };
+    auto put = [&]() {
+      put_x();
+      if (mine) {
+#pragma unroll
+        for (int f = 0; f < 8; ++f)
+          if (off + f >= 0) *reinterpret_cast<u32x4*>(vs + (off + f) * kAdPitch + 8 * jb) = ad_column<8>(v, f);
+      }
+      ad_wave_sync();
+    };
+    auto multiply = [&]() {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        u32x4 xf[MF];
+#pragma unroll
+        for (int f = 0; f < MF; ++f) xf[f] = *reinterpret_cast<const u32x4*>(xs + ad_slot(16 * f + i, 4 * h + q));
 #pragma unroll
         for (int g = 0; g < NR; ++g) {
-          const u32x4 t = *reinterpret_cast<const u32x4*>(ut + (16 * g + i) * kAdPitch + 32 * h + 8 * q);
+          const u32x4 vf = *reinterpret_cast<const u32x4*>(vs + (16 * g + i) * kAdPitch + 32 * h + 8 * q);
 #pragma unroll
           for (int f = 0; f < MF; ++f)
-            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t), as_bf16(x[h][f]), acc[f][g], 0, 0, 0);
+            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf), as_bf16(xf[f]), acc[f][g], 0, 0, 0);
         }
+      }
       ad_wave_sync();
     };
     int u = u0 + w;
     if (u < safe) {
-      u32x4 xa[2][MF], xb[2][MF];
-      load_v(u), load_x(u, xa);
-      for (; u + 4 < safe; u += 8) {
+      load(u);
+      for (; u + 4 < safe; u += 4) {
         put();
-        load_v(u + 4), load_x(u + 4, xb);
-        multiply(xa);
-        put();
-        const int next = min(u + 8, safe - 1);
-        load_v(next), load_x(next, xa);
-        multiply(xb);
+        load(u + 4);
+        multiply();
       }
-      if (u < safe) put(), multiply(xa), u += 4;
+      put(), multiply();
+      u += 4;
     }
     for (; u < u1; u += 4) {
-      u32x4 x[2][MF];
+      const int k = u * kAdUnit + 8 * c8;
+      if (K >= 8) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < XL; ++j) x[j] = ad_tail8(X + xrow[j], k, K);
+      } else {
 #pragma unroll
-        for (int f = 0; f < MF; ++f) x[h][f] = load_row8(xrow[f], u * kAdUnit + 32 * h + 8 * q, K);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int j = u * kAdUnit + 8 * jb + e;
-        v[e] = ad_piece_end<8>(U + (int64_t)min(j, K - 1) * a.r, jb < 8 && j < K ? a.r - rank : 0);
+        for (int j = 0; j < XL; ++j) x[j] = __builtin_bit_cast(u32x4, ad_piece_end<8>(X + xrow[j], k < K ? K - k : 0));
       }
-      put();
-      multiply(x);
+      if (mine) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = u * kAdUnit + 8 * jb + e;
+          const uint16_t* from = U + min(j, K - 1) * a.r + rank;
+          v[e] = a.r >= 8 ? ad_piece_at<8>(from, 0) : ad_piece_end<8>(from, a.r);
+          if (j >= K) v[e] = ad_nothing<8>();
+        }
+      }
+      put(), multiply();
     }
   }
 
@@ -414,24 +483,15 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
   }
 }
 
-// The splits' sum of N values at p, added in order; 8 loads in flight.
-template <typename V>
-__device__ __forceinline__ V ad_sum(const float* p, int splits, int64_t stride) {
-  V s = *reinterpret_cast<const V*>(p);
-  int z = 1;
-  for (; z + 8 <= splits; z += 8) {
-    V v[8];
+// The splits' sum of four values at p, added in order; four loads in flight.
+__device__ __forceinline__ f32x4 ad_sum(const float* p, int splits, int64_t stride) {
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  for (int z = 0; z < splits; z += 4) {
+    f32x4 v[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = *reinterpret_cast<const V*>(p + (z + k) * stride);
+    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const f32x4*>(p + min(z + k, splits - 1) * stride);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += v[k];
-  }
-  if (z < splits) {
-    V v[7];
-#pragma unroll
-    for (int k = 0; k < 7; ++k) v[k] = *reinterpret_cast<const V*>(p + min(z + k, splits - 1) * stride);
-#pragma unroll
-    for (int k = 0; k < 7; ++k)
+    for (int k = 0; k < 4; ++k)
       if (z + k < splits) s += v[k];
   }
   return s;
@@ -443,7 +503,8 @@ __device__ __forceinline__ V ad_sum(const float* p, int splits, int64_t stride) 
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void k_ad_terms(AdArgs a) {
   const int tile = blockIdx.x, side = a.splits[0] == 0 ? 1 : (int)blockIdx.z;
-  const int2 at = a.info[tile];
+  int2 at = a.info[tile];
+  at = make_int2(uniform(at.x), uniform(at.y));
   if (at.x < 0 || at.y == 0) return;
   const int rank = (int)blockIdx.y * 64 + (threadIdx.x & 63), i0 = 8 * (threadIdx.x >> 6);
   if (rank >= a.rp) return;
@@ -458,18 +519,23 @@ __global__ __launch_bounds__(256) void k_ad_terms(AdArgs a) {
     for (int e = 0; e < 8; ++e) v[e] += p[z * stride + e * a.rg];
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = rank < a.r && i0 + e < at.y ? v[e] * scale : 0.f;  // a slot without a row holds anything
+  // the lane of an operand that holds these eight slots of this rank (dU, dVt), or
+  // slot i0 + e of this rank's eight (dX)
   uint16_t* three = a.t3[side];
+  const int g = rank >> 4, step = rank >> 5;
 #pragma unroll
   for (int h = 0; h < 3; ++h) {
-    uint32_t t[8];
+    uint32_t t[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = ad_term(v[e]);
+    for (int e = 0; e < 4; ++e) t[e] = ad_term2(v[2 * e], v[2 * e + 1]);
     if (three && rank < a.rg)
-      *reinterpret_cast<u32x4*>(three + ((int64_t)h * a.rg + rank) * a.slots + 32 * tile + i0) =
-          u32x4{t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16};
+      *reinterpret_cast<u32x4*>(three + ((((int64_t)tile * (a.rg >> 4) + g) * 3 + h) * 64 + 2 * i0 + (rank & 15)) * 8) =
+          u32x4{t[0], t[1], t[2], t[3]};
     if (a.t2 && side && h < 2) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a.t2[((int64_t)(32 * tile + i0 + e) * 2 + h) * a.rp + rank] = (uint16_t)t[e];
+      for (int e = 0; e < 8; ++e)
+        a.t2[((((int64_t)tile * (a.rp >> 5) + step) * 4 + 2 * h + ((i0 + e) >> 4)) * 64 + 16 * ((rank >> 3) & 3) +
+              ((i0 + e) & 15)) * 8 + (rank & 7)] = (uint16_t)(t[e >> 1] >> (16 * (e & 1)));
     }
   }
 }
@@ -477,29 +543,37 @@ __global__ __launch_bounds__(256) void k_ad_terms(AdArgs a) {
 // ---------------------------------------------------------------------------
 // Outputs in bf16
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t ad_pack(float lo, float hi) { return f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16; }
-
-// Eight values in bf16: old + v.
-__device__ __forceinline__ void ad_store8_on(uint16_t* out, const Bytes16& old, const float* v) {
+// Eight values in bf16: old + v, at a byte offset.
+__device__ __forceinline__ void ad_store8(void* base, uint32_t at, const u32x4& old, const float* v) {
   Bytes16 o;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) o.w[k] = ad_pack(v[2 * k] + bf16lo(old.w[k]), v[2 * k + 1] + bf16hi(old.w[k]));
-  *reinterpret_cast<Bytes16*>(out) = o;
+  for (int k = 0; k < 4; ++k) o.w[k] = ad_pack(v[2 * k] + bf16lo(old[k]), v[2 * k + 1] + bf16hi(old[k]));
+  *reinterpret_cast<Bytes16*>(static_cast<char*>(base) + at) = o;
 }
 
-// Eight columns of a row of the output: base + v, in bf16.
-__device__ __forceinline__ void ad_store8(const AdArgs& a, int64_t row, int col, int cols, const float* v) {
-  const uint16_t* in = a.base ? a.base + row * cols : nullptr;
-  uint16_t* out = a.Y + row * cols;
-  if (col + 8 <= cols) {
-    Bytes16 old = {{0u, 0u, 0u, 0u}};
-    if (in) old = *reinterpret_cast<const Bytes16*>(in + col);
-    ad_store8_on(out + col, old, v);
-  } else {
+// 16 rows of a wave's 128 columns at the end of the rows: through the wave's 8 KB of
+// LDS, element by element.  D: rows 4 q + e, columns 8 i + f.
+__device__ __forceinline__ void ad_store_end(const AdArgs& a, const uint16_t* rows, int live, int c0, int cols,
+                                             const f32x4 (&acc)[8], float* stage) {
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  ad_wave_sync();
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (col + k < cols) out[col + k] = f32_to_bf16((in ? __uint_as_float((uint32_t)in[col + k] << 16) : 0.f) + v[k]);
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int f = 0; f < 8; ++f) stage[(4 * q + e) * 128 + 8 * i + f] = acc[f][e];
+  ad_wave_sync();
+  const int width = min(128, cols - c0);
+#pragma unroll 1
+  for (int row = 0; row < live; ++row) {
+    const int64_t at = (int64_t)rows[row] * cols + c0;
+#pragma unroll
+    for (int c = 0; c < 128; c += 64)
+      if (c + lane < width) {
+        const float old = a.base ? __uint_as_float((uint32_t)a.base[at + c + lane] << 16) : 0.f;
+        a.Y[at + c + lane] = f32_to_bf16(old + stage[row * 128 + c + lane]);
+      }
   }
+  ad_wave_sync();
 }
 
 // Rows without an adapter: the output is base (nothing to do in place).
@@ -514,135 +588,164 @@ __device__ __forceinline__ void ad_copy(const AdArgs& a, const AdTile& at, const
 }
 
 // ---------------------------------------------------------------------------
-// Y = base + scale T U^T.  D[column][row], A = U_l as stored: row i of piece f is
-// column 32 (f / 2) + 8 (i / 4) + 4 (f % 2) + i % 4 of the wave's 64, so that a
-// lane ends up with two runs of eight columns of one row, and four lanes with 64
-// adjacent bytes.
-// The block's terms of T are made first, in LDS, for all its columns.
-// grid: (tiles, column blocks of 256 NC)
+// Y = base + scale T U^T.  D[row][column], B = U_l as stored, 128 columns a wave:
+// piece f of the operand holds columns 8 i + f, so that a lane ends up with eight
+// adjacent columns of four rows, and 16 lanes read and write 256 bytes of a row.  U
+// comes through the wave's own part of LDS, 32 ranks at a time (four lanes a row),
+// the next ones in flight.  The block's terms of T are made first, in LDS, for all
+// its columns.
+// grid: (tiles, column blocks of 512 NC)
 // ---------------------------------------------------------------------------
-// Eight ranks from k on of a row of r, zeros past r (what lies there is the next
-// row's).  `inside`: the 16 bytes are inside the factors.
-__device__ __forceinline__ u32x4 ad_ranks(const uint16_t* row, int k, int r, bool inside) {
-  if (inside) {
-    u32x4 v = load8(row + min(k, (r - 1) & ~7));
-    const int keep = r - k;
-    if (__builtin_amdgcn_ballot_w64(keep < 8)) {
-#pragma unroll
-      for (int d = 0; d < 4; ++d) v[d] &= (keep > 2 * d ? 0xffffu : 0u) | (keep > 2 * d + 1 ? 0xffff0000u : 0u);
-    }
-    return v;
-  }
-  return __builtin_bit_cast(u32x4, ad_piece_end<8>(row + min(k, r - 1), r - k));
-}
+// Where U's row 8 i + f goes in LDS: rows of 32 ranks, those of one piece side by
+// side, 16-byte chunks spread over the banks.
+__device__ __forceinline__ int ad_place(int i, int f, int q) { return (16 * f + i) * 32 + 8 * (q ^ ((i >> 1) & 3)); }
 
 template <int TM>
-__global__ __launch_bounds__(256) void k_ad_expand(AdArgs a, int nc) {
+__global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, int nc) {
   constexpr int MF = TM / 16;
-  extern __shared__ __align__(16) uint16_t terms[];  // [TM][2][ranks of a chunk, + 4]
-  const int tile = blockIdx.x, cb = (int)blockIdx.y * 256 * nc;
+  extern __shared__ __align__(16) uint16_t lds[];
+  const int tile = blockIdx.x, cb = (int)blockIdx.y * 512 * nc;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int2 info = a.info[tile];
   const uint16_t* rows = a.rows + TM * tile;
-  int64_t out[MF];  // (of a tile that is not there: any number, not used)
+  uint32_t out[MF][4];  // byte offsets (of a tile that is not there: any number, not used)
 #pragma unroll
-  for (int g = 0; g < MF; ++g) out[g] = rows[16 * g + i];
-  const AdTile at = {info.x, info.y};
+  for (int g = 0; g < MF; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[g][e] = 2u * (rows[16 * g + 4 * q + e] * a.m + 8 * i);
+  const AdTile at = {uniform(info.x), uniform(info.y)};
   if (at.rows == 0) return;
   if (at.adapter < 0) {
-    ad_copy(a, at, rows, cb, 256 * nc, a.m);
+    ad_copy(a, at, rows, cb, 512 * nc, a.m);
     return;
   }
+  uint16_t* us = lds + w * 128 * 32;
+  uint16_t* terms = lds + 4 * 128 * 32;  // [TM][2][ranks of a chunk, + 4]
   const int wide = min(a.rp, kAdChunk), pitch = 2 * wide + 8;
   const float scale = a.scale ? a.scale[at.adapter] : 1.f;
   auto fill = [&](int rank0) {  // two terms of a chunk's ranks, zeros past r
-    const int quads = min(wide, a.rp - rank0) / 4;
+    const uint32_t quads = (uint32_t)min(wide, a.rp - rank0) / 4;
     const float* p = a.part[0] + (int64_t)TM * tile * a.rg + rank0;
-    for (int e = threadIdx.x; e < at.rows * quads; e += 256) {
+    for (uint32_t e = threadIdx.x; e < at.rows * quads; e += 256) {
       const int row = e / quads, k = e % quads * 4;
       f32x4 v = {0.f, 0.f, 0.f, 0.f};
-      if (rank0 + k < a.rg) v = ad_sum<f32x4>(p + row * a.rg + k, a.splits[0], (int64_t)a.slots * a.rg);
+      if (rank0 + k < a.rg) v = ad_sum(p + row * a.rg + k, a.splits[0], (int64_t)a.slots * a.rg);
       float x[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[c] = rank0 + k + c < a.r ? v[c] * scale : 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t t[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) t[c] = ad_term(x[c]);
-        *reinterpret_cast<mx_u32x2*>(terms + row * pitch + h * wide + k) = mx_u32x2{t[0] | t[1] << 16, t[2] | t[3] << 16};
+        const uint32_t lo = ad_term2(x[0], x[1]), hi = ad_term2(x[2], x[3]);
+        *reinterpret_cast<mx_u32x2*>(terms + row * pitch + h * wide + k) = mx_u32x2{lo, hi};
       }
     }
   };
   const uint16_t* trow[MF];
 #pragma unroll
   for (int g = 0; g < MF; ++g) trow[g] = terms + min(16 * g + i, at.rows - 1) * pitch + 8 * q;
-  const int64_t end = (int64_t)a.count * a.m * a.r;
+  const uint16_t* U = a.U + (int64_t)at.adapter * a.m * a.r;
   const bool one = a.rp <= kAdChunk;
+  const int col = lane >> 2, c4 = lane & 3;  // of 16 columns' loads, four lanes a row of 32 ranks
   bool filled = false;
-  for (int c0 = cb + 64 * w; c0 < cb + 256 * nc; c0 += 256) {
-    const uint16_t* urow[4];
+  for (int c0 = cb + 128 * w; c0 < cb + 512 * nc; c0 += 512) {
+    const bool full = c0 + 128 <= a.m;
+    u32x4 u[8];
+    uint32_t from[8];  // byte offsets of the rows
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
-      urow[f] = a.U + ((int64_t)at.adapter * a.m + min(c0 + 32 * (f >> 1) + 8 * (i >> 2) + 4 * (f & 1) + (i & 3), a.m - 1)) * a.r;
-    const bool inside = ((int64_t)at.adapter * a.m + min(c0 + 64, a.m)) * a.r + 8 <= end;
-    const bool full = c0 + 64 <= a.m && a.base;
+    for (int j = 0; j < 8; ++j) from[j] = 2u * (min(c0 + 16 * j + col, a.m - 1) * a.r);
+    auto load = [&](int k) {  // ranks k .. k + 31; at the end of the ranks the row's last eight, shifted in place()
+      if (a.r >= 8) {
+        const int at8 = min(k + 8 * c4, a.r - 8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = ad_load(U, from[j] + 2u * at8);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = u32x4{0u, 0u, 0u, 0u};
+        if (c4 == 0)
+#pragma unroll 1
+          for (int e = 0; e < a.r; ++e) {
+            const int d = e >> 1, sh = 16 * (e & 1);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t x = (uint32_t)U[from[j] / 2 + e] << sh;
+              u[j].x |= d == 0 ? x : 0u, u[j].y |= d == 1 ? x : 0u, u[j].z |= d == 2 ? x : 0u, u[j].w |= d == 3 ? x : 0u;
+            }
+          }
+      }
+    };
+    auto place = [&](int k) {  // column 16 j + col = 8 (2 j + col / 8) + col % 8
+      if (k + 32 > a.r && a.r >= 8) {
+        const int s = k + 8 * c4 - min(k + 8 * c4, a.r - 8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = ad_drop(u[j], s);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4*>(us + ad_place(2 * j + (col >> 3), col & 7, c4)) = u[j];
+      ad_wave_sync();
+    };
     // the first ranks of U and the rows' base are on their way while the terms are made
-    u32x4 u[4];
-    Bytes16 old[MF][2];
+    load(0);
+    u32x4 old[MF][4];
 #pragma unroll
-    for (int f = 0; f < 4; ++f) u[f] = ad_ranks(urow[f], 8 * q, a.r, inside);
-    if (full) {
+    for (int g = 0; g < MF; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) old[g][e] = u32x4{0u, 0u, 0u, 0u};
+    if (full && a.base) {
 #pragma unroll
       for (int g = 0; g < MF; ++g)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (16 * g + i < at.rows)
-            old[g][h] = *reinterpret_cast<const Bytes16*>(a.base + out[g] * a.m + c0 + 32 * h + 8 * q);
+        for (int e = 0; e < 4; ++e) old[g][e] = ad_load(a.base, out[g][e] + 2u * c0);
     }
-    f32x4 acc[4][MF];
+    if (one && !filled) {
+      fill(0);
+      __syncthreads();
+      filled = true;
+    }
+    f32x4 acc[MF][8];
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
+    for (int g = 0; g < MF; ++g)
 #pragma unroll
-      for (int g = 0; g < MF; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int f = 0; f < 8; ++f) acc[g][f] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int rank0 = 0; rank0 < a.rp; rank0 += kAdChunk) {
-      if (!one || !filled) {  // every wave comes here as often
+      if (!one) {  // every wave comes here as often
         __syncthreads();
         fill(rank0);
         __syncthreads();
-        filled = true;
       }
       for (int s = 0; s < min(wide, a.rp - rank0); s += 32) {
+        place(rank0 + s);
+        if (rank0 + s + 32 < a.rp) load(rank0 + s + 32);
         u32x4 t[2][MF];
 #pragma unroll
         for (int g = 0; g < MF; ++g)
 #pragma unroll
           for (int h = 0; h < 2; ++h) t[h][g] = *reinterpret_cast<const u32x4*>(trow[g] + h * wide + s);
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
+        for (int f = 0; f < 8; ++f) {
+          const u32x4 uf = *reinterpret_cast<const u32x4*>(us + ad_place(i, f, q));
 #pragma unroll
           for (int g = 0; g < MF; ++g)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(u[f]), as_bf16(t[h][g]), acc[f][g], 0, 0, 0);
-        if (rank0 + s + 32 < a.rp) {
-#pragma unroll
-          for (int f = 0; f < 4; ++f) u[f] = ad_ranks(urow[f], rank0 + s + 32 + 8 * q, a.r, inside);
+              acc[g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t[h][g]), as_bf16(uf), acc[g][f], 0, 0, 0);
         }
+        ad_wave_sync();
       }
     }
+    if (full) {
 #pragma unroll
-    for (int g = 0; g < MF; ++g) {
-      if (16 * g + i >= at.rows) continue;
+      for (int g = 0; g < MF; ++g)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float v[8];
+        for (int e = 0; e < 4; ++e) {
+          float v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = acc[2 * h + (k >> 2)][g][k & 3];
-        const int col = c0 + 32 * h + 8 * q;
-        if (full) ad_store8_on(a.Y + out[g] * a.m + col, old[g][h], v);
-        else ad_store8(a, out[g], col, a.m, v);
-      }
+          for (int f = 0; f < 8; ++f) v[f] = acc[g][f][e];
+          if (16 * g + 4 * q + e < at.rows) ad_store8(a.Y, out[g][e] + 2u * c0, old[g][e], v);
+        }
+    } else if (c0 < a.m) {
+#pragma unroll
+      for (int g = 0; g < MF; ++g)
+        ad_store_end(a, rows + 16 * g, at.rows - 16 * g < 16 ? at.rows - 16 * g : 16, c0, a.m, acc[g], reinterpret_cast<float*>(us));
     }
   }
 }
@@ -651,61 +754,67 @@ __global__ __launch_bounds__(256) void k_ad_expand(AdArgs a, int nc) {
 // The backward's last launch: blocks of dU, then of dVt, then of dX.
 // ---------------------------------------------------------------------------
 // dX = base + scale P Vt: as k_ad_expand, with Vt's 8 x 8 pieces transposed in
-// registers: a lane's eight ranks and eight columns are eight operands.  128
-// columns a wave; row i of each operand is the run of eight columns i / 4 + 4 (i %
-// 4), so that four lanes store 64 adjacent bytes.
-__device__ __forceinline__ void ad_dx(const AdArgs& a, int block) {
+// registers: a lane's eight ranks and eight columns are eight operands.
+__device__ __forceinline__ void ad_dx(const AdArgs& a, int block, char* smem) {
   constexpr int MF = 2;
   const int tile = block / a.cols_y, cb = block % a.cols_y * 512;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int2 info = a.info[tile];
   const uint16_t* rows = a.rows + 32 * tile;
-  const uint16_t* trow[MF];
-  int64_t out[MF];  // (of a tile that is not there: any number, not used)
+  const uint16_t* t2 = a.t2 + ((int64_t)tile * (a.rp >> 5) * 4 * 64 + lane) * 8;
+  uint32_t out[MF][4];  // byte offsets (of a tile that is not there: any number, not used)
 #pragma unroll
-  for (int g = 0; g < MF; ++g) {
-    out[g] = rows[16 * g + i];
-    trow[g] = a.t2 + (int64_t)(32 * tile + 16 * g + i) * 2 * a.rp + 8 * q;
-  }
-  const AdTile at = {info.x, info.y};
+  for (int g = 0; g < MF; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[g][e] = 2u * (rows[16 * g + 4 * q + e] * a.n + 8 * i);
+  const AdTile at = {uniform(info.x), uniform(info.y)};
   if (at.rows == 0) return;
   if (at.adapter < 0) {
     ad_copy(a, at, rows, cb, 512, a.n);
     return;
   }
-  const int c0 = cb + 128 * w, col = c0 + 8 * ((i >> 2) + 4 * (i & 3));
+  const int c0 = cb + 128 * w, col = c0 + 8 * i;
   if (c0 >= a.n) return;
-  const uint16_t* V = a.Vt + (int64_t)at.adapter * a.r * a.n + col;
-  const bool inside = c0 + 128 <= a.n, full = inside && a.base;
-  Bytes16 old[MF][4];
-  if (full) {
+  const uint16_t* V = a.Vt + (int64_t)at.adapter * a.r * a.n;
+  const bool full = c0 + 128 <= a.n;
+  u32x4 old[MF][4];
+#pragma unroll
+  for (int g = 0; g < MF; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) old[g][e] = u32x4{0u, 0u, 0u, 0u};
+  if (full && a.base) {
 #pragma unroll
     for (int g = 0; g < MF; ++g)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (16 * g + i < at.rows) old[g][e] = *reinterpret_cast<const Bytes16*>(a.base + out[g] * a.n + c0 + 8 * (q + 4 * e));
+      for (int e = 0; e < 4; ++e) old[g][e] = ad_load(a.base, out[g][e] + 2u * c0);
   }
-  f32x4 acc[8][MF];
+  f32x4 acc[MF][8];
 #pragma unroll
-  for (int f = 0; f < 8; ++f)
+  for (int g = 0; g < MF; ++g)
 #pragma unroll
-    for (int g = 0; g < MF; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int f = 0; f < 8; ++f) acc[g][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int from = min(col, a.n - 8);  // (columns past the end: not stored)
   for (int s = 0; s < a.rp; s += 32) {
     // past the ranks: the last one again, times the zeros that the terms hold there
     AdPiece<8> v[8];
-    if (inside) {
+    if (a.n >= 8) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = ad_piece<8>(V + (int64_t)min(s + 8 * q + e, a.r - 1) * a.n);
+      for (int e = 0; e < 8; ++e) v[e] = __builtin_bit_cast(AdPiece<8>, ad_load(V, 2u * (min(s + 8 * q + e, a.r - 1) * a.n + from)));
+      if (!full) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          v[e] = __builtin_bit_cast(AdPiece<8>, ad_drop(__builtin_bit_cast(u32x4, v[e]), col - from));
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        v[e] = ad_piece_end<8>(V + (int64_t)min(s + 8 * q + e, a.r - 1) * a.n, a.n - col);
+        v[e] = ad_piece_end<8>(V + min(s + 8 * q + e, a.r - 1) * a.n, i == 0 ? a.n : 0);
     }
     u32x4 t[2][MF];
 #pragma unroll
-    for (int g = 0; g < MF; ++g)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) t[h][g] = *reinterpret_cast<const u32x4*>(trow[g] + h * a.rp + s);
+      for (int g = 0; g < MF; ++g) t[h][g] = *reinterpret_cast<const u32x4*>(t2 + (4 * (s >> 5) + 2 * h + g) * 64 * 8);
 #pragma unroll
     for (int f = 0; f < 8; ++f) {
       const bf16x8 u = as_bf16(ad_column<8>(v, f));
@@ -713,20 +822,24 @@ __device__ __forceinline__ void ad_dx(const AdArgs& a, int block) {
       for (int g = 0; g < MF; ++g)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, as_bf16(t[h][g]), acc[f][g], 0, 0, 0);
+          acc[g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t[h][g]), u, acc[g][f], 0, 0, 0);
     }
   }
+  if (full) {
 #pragma unroll
-  for (int g = 0; g < MF; ++g) {
-    if (16 * g + i >= at.rows) continue;
+    for (int g = 0; g < MF; ++g)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float v[8];
+      for (int e = 0; e < 4; ++e) {
+        float v[8];
 #pragma unroll
-      for (int f = 0; f < 8; ++f) v[f] = acc[f][g][e];
-      if (full) ad_store8_on(a.Y + out[g] * a.n + c0 + 8 * (q + 4 * e), old[g][e], v);
-      else ad_store8(a, out[g], c0 + 8 * (q + 4 * e), a.n, v);
-    }
+        for (int f = 0; f < 8; ++f) v[f] = acc[g][f][e];
+        if (16 * g + 4 * q + e < at.rows) ad_store8(a.Y, out[g][e] + 2u * c0, old[g][e], v);
+      }
+  } else {
+#pragma unroll
+    for (int g = 0; g < MF; ++g)
+      ad_store_end(a, rows + 16 * g, at.rows - 16 * g < 16 ? at.rows - 16 * g : 16, c0, a.n, acc[g],
+                   reinterpret_cast<float*>(smem) + w * 16 * 128);
   }
 }
 
@@ -746,17 +859,14 @@ __device__ __forceinline__ void ad_dfactor(const AdArgs& a, int block, char* sme
   uint64_t same = 0;
   if (a.b > kAdSmall) {
     const int2 first = a.first[l];
-    tile0 = first.x, total = first.y;
+    tile0 = uniform(first.x), total = uniform(first.y);
   } else {  // a tile starts at each 32nd of its rows
     same = __ballot(lane < a.b && a.ids[min(lane, a.b - 1)] == l);
     total = __popcll(same);
   }
   const uint16_t* src = DV ? a.X : a.G;
-  const uint16_t* terms[NR];
-#pragma unroll
-  for (int g = 0; g < NR; ++g)
-    terms[g] = a.t3[DV] + (int64_t)min(rank0 + 16 * g + i, a.rg - 1) * a.slots + 8 * q;
-  const int64_t term = (int64_t)a.rg * a.slots;
+  const uint16_t* terms = a.t3[DV] + lane * 8;
+  const int groups = a.rg >> 4;
   f32x4 acc[CW][NR];
 #pragma unroll
   for (int f = 0; f < CW; ++f)
@@ -765,7 +875,6 @@ __device__ __forceinline__ void ad_dfactor(const AdArgs& a, int block, char* sme
   // Rows past the end: a row of the tile again, times the zeros that the terms
   // hold there.
   const bool inside = c0 + 16 * CW <= cols;
-  const uint16_t* at = src + c0 + CW * i;
   auto tile_of = [&](int s) {
     if (a.b > kAdSmall) return tile0 + s;
     uint64_t rest = same;
@@ -776,29 +885,30 @@ __device__ __forceinline__ void ad_dfactor(const AdArgs& a, int block, char* sme
     AdPiece<CW> v[8];
     u32x4 t[NR <= 2 ? NR : 1][3];
   };
-  auto load_terms = [&](int pos, int g, u32x4 (&t)[3]) {
+  auto load_terms = [&](int tile, int g, u32x4 (&t)[3]) {  // (past the ranks: the last ones, not stored)
+    const int64_t from = ((int64_t)tile * groups + min(rank0 / 16 + g, groups - 1)) * 3 * 64 * 8;
 #pragma unroll
-    for (int h = 0; h < 3; ++h) t[h] = *reinterpret_cast<const u32x4*>(terms[g] + h * term + pos);
+    for (int h = 0; h < 3; ++h) t[h] = *reinterpret_cast<const u32x4*>(terms + from + h * 64 * 8);
   };
   auto load = [&](int s, Regs& r) {
-    const int pos = 32 * tile_of(s), left = total - 32 * s;
+    const int tile = tile_of(s), pos = 32 * tile, left = total - 32 * s;
     if (NR <= 2) {
 #pragma unroll
-      for (int g = 0; g < NR; ++g) load_terms(pos, g, r.t[g]);
+      for (int g = 0; g < NR; ++g) load_terms(tile, g, r.t[g]);
     }
-    int64_t row[8];
+    int row[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) row[e] = (int64_t)list[pos + min(8 * q + e, left - 1)] * cols;
+    for (int e = 0; e < 8; ++e) row[e] = list[pos + min(8 * q + e, left - 1)] * cols;
     if (inside) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r.v[e] = ad_piece<CW>(at + row[e]);
+      for (int e = 0; e < 8; ++e) r.v[e] = ad_piece_at<CW>(src, 2u * (row[e] + c0 + CW * i));
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r.v[e] = ad_piece_end<CW>(at + row[e], cols - (c0 + CW * i));
+      for (int e = 0; e < 8; ++e) r.v[e] = ad_piece_end<CW>(src + row[e] + min(c0 + CW * i, cols - 1), cols - (c0 + CW * i));
     }
   };
   auto multiply = [&](int s, const Regs& r) {
-    const int pos = 32 * tile_of(s);
+    const int tile = tile_of(s);
 #pragma unroll
     for (int g = 0; g < NR; ++g) {
       u32x4 t[3];
@@ -806,7 +916,7 @@ __device__ __forceinline__ void ad_dfactor(const AdArgs& a, int block, char* sme
 #pragma unroll
         for (int h = 0; h < 3; ++h) t[h] = r.t[g][h];
       } else {
-        load_terms(pos, g, t);
+        load_terms(tile, g, t);
       }
 #pragma unroll
       for (int f = 0; f < CW; ++f) {
@@ -881,7 +991,7 @@ __global__ __launch_bounds__(256, 2) void k_ad_back(AdArgs a) {
     ad_dfactor<NR, CW, true>(a, block, smem);
     return;
   }
-  ad_dx(a, block - a.blocks_v);
+  ad_dx(a, block - a.blocks_v, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -961,8 +1071,8 @@ static AdArgs ad_args(const hss_adapters* A, int b, const AdPlan& p, const void*
 
 template <int TM, int NR>
 static void launch_rank_nr(const AdArgs& a, hipStream_t s) {
-  size_t lds = std::max<size_t>((size_t)4 * (TM / 16) * NR * 64 * 16, (size_t)(a.count + 1) * 4);
-  if (a.splits[1]) lds = std::max<size_t>(lds, (size_t)4 * 16 * NR * kAdPitch * 2);
+  const size_t lds = std::max<size_t>((size_t)4 * (TM * kAdUnit + 16 * NR * kAdPitch) * 2, (size_t)(a.count + 1) * 4);
+  static_assert(4 * (TM * kAdUnit + 16 * NR * kAdPitch) * 2 >= 4 * (TM / 16) * NR * 64 * 16, "the waves' sums fit");
   const dim3 grid(a.splits[0] + a.splits[1], a.tiles, (a.rg + 16 * NR - 1) / (16 * NR));
   hipLaunchKernelGGL((k_ad_rank<TM, NR>), grid, dim3(256), lds, s, a);
 }
@@ -977,10 +1087,10 @@ static void launch_rank(const AdArgs& a, int nr, hipStream_t s) {
 template <int TM>
 static void launch_expand(const AdArgs& a, hipStream_t s) {
   const int busy = std::max((a.b + TM - 1) / TM, std::min(a.b, a.count));
-  const int cols = (a.m + 255) / 256;
+  const int cols = (a.m + 511) / 512;
   const int nc = std::max(1, std::min(cols, cols * busy / 512));
   const dim3 grid(a.tiles, (cols + nc - 1) / nc);
-  const size_t lds = (size_t)TM * (2 * std::min(a.rp, kAdChunk) + 8) * 2;
+  const size_t lds = (size_t)(4 * 128 * 32 + TM * (2 * std::min(a.rp, kAdChunk) + 8)) * 2;
   hipLaunchKernelGGL(k_ad_expand<TM>, grid, dim3(256), lds, s, a, nc);
 }
 
@@ -996,7 +1106,7 @@ hss_status launch_adapters_apply(const hss_adapters* A, int b, const void* X, co
 
 template <int NR, int CW>
 static void launch_back(AdArgs a, hipStream_t s) {
-  const size_t lds = (size_t)CW * NR * 64 * 16;
+  const size_t lds = std::max<size_t>((size_t)CW * NR * 64 * 16, a.Y && a.n % 128 ? 4 * 16 * 128 * 4 : 0);
   a.chunks = (a.rg + 16 * NR - 1) / (16 * NR);
   a.cols_u = (a.m + 16 * CW - 1) / (16 * CW), a.cols_v = (a.n + 16 * CW - 1) / (16 * CW);
   a.cols_y = (a.n + 511) / 512;
