@@ -30,7 +30,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 static constexpr int kAdSmall = 64;     // batches up to here: tiles found by one ballot
 static constexpr int kAdUnit = 64;      // columns of K that a wave takes at a time: a cache line of each row
-static constexpr int kAdBlocks = 768;   // blocks of k_ad_rank that K is split for
+static constexpr int kAdBlocks = 704;   // blocks of k_ad_rank that K is split for
 static constexpr int kAdChunk = 256;    // ranks of T that k_ad_expand keeps in LDS
 
 struct AdArgs {
@@ -71,10 +71,23 @@ struct AdTile {
   int rows;     // 0: no such tile
 };
 
-// Exclusive prefix sum over the block's 256 threads, and the total.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int ad_dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+
+// Exclusive prefix sum over the block's 256 threads, and the total.  (In a wave by
+// DPP shifts within rows of 16 lanes, then each row's last lane to the rows behind:
+// the permutes through LDS of wave_excl_scan_u32 take 1 us of a tile's search.)
 __device__ __forceinline__ int ad_scan(int v, int* part, int* total) {
   const int w = threadIdx.x >> 6;
-  const int before = (int)wave_excl_scan_u32((uint32_t)v);
+  int incl = ad_dpp_add<0x111, 0xF>(v);   // row_shr 1, 2, 4, 8
+  incl = ad_dpp_add<0x112, 0xF>(incl);
+  incl = ad_dpp_add<0x114, 0xF>(incl);
+  incl = ad_dpp_add<0x118, 0xF>(incl);
+  incl = ad_dpp_add<0x142, 0xA>(incl);    // row_bcast 15 into rows 1 and 3
+  incl = ad_dpp_add<0x143, 0xC>(incl);    // row_bcast 31 into rows 2 and 3
+  const int before = incl - v;
   if ((threadIdx.x & 63) == 63) part[w] = before + v;
   __syncthreads();
   int base = 0, all = 0;
@@ -119,9 +132,11 @@ __device__ __forceinline__ AdTile ad_tile(const AdArgs& a, int tile, uint16_t* r
   constexpr int per = HSS_MAX_BATCH / 256;
   int id[per];
 #pragma unroll
+  for (int k = 0; k < per; ++k) id[k] = a.ids[min(per * t + k, b - 1)];  // all in flight
+#pragma unroll
   for (int k = 0; k < per; ++k) {
-    id[k] = per * t + k < b ? ad_id(a.ids, per * t + k, count) : -2;
-    if (id[k] == -1) id[k] = count;
+    if (id[k] < 0 || id[k] >= count) id[k] = count;
+    if (per * t + k >= b) id[k] = -2;
   }
   for (int k = t; k <= count; k += 256) bins[k] = 0;
   __syncthreads();
@@ -235,6 +250,18 @@ __device__ __forceinline__ u32x4 ad_drop(u32x4 v, int s) {
   return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
+template <int CW>
+__device__ __forceinline__ AdPiece<CW> ad_drop(const AdPiece<CW>& p, int s) {
+  u32x4 v = {p.w[0], 0u, 0u, 0u};
+#pragma unroll
+  for (int d = 1; d < CW / 2; ++d) v[d] = p.w[d];
+  v = ad_drop(v, s);
+  AdPiece<CW> o;
+#pragma unroll
+  for (int d = 0; d < CW / 2; ++d) o.w[d] = v[d];
+  return o;
+}
+
 // Eight bf16 of a row of n at column k, zeros past the end, in one load (n >= 8).
 __device__ __forceinline__ u32x4 ad_tail8(const uint16_t* row, int k, int n) {
   const int from = min(k, n - 8);
@@ -282,11 +309,11 @@ __device__ __forceinline__ uint32_t ad_term2(float& x, float& y) {
 //   while one is multiplied.  The four waves' sums meet in LDS.
 // grid: (splits of T and of P, tiles, groups of 16 NR ranks)
 // ---------------------------------------------------------------------------
-static constexpr int kAdPitch = kAdUnit + 8;  // of U^T in LDS
-
-// Slot of 16-byte chunk c of a 128-byte row in LDS: eight rows' reads of one chunk
-// fall on different banks.
-__device__ __forceinline__ int ad_slot(int row, int c) { return row * kAdUnit + 8 * (c ^ (row & 7)); }
+// Where 16-byte chunk c of a 128-byte row lies in LDS.  A read takes one chunk of 16
+// rows, half of them in each half of the 256 bytes of banks: (row / 2) % 8 tells
+// each half's eight apart.  A transposed piece's write takes one chunk of eight rows
+// that are 8 apart: (row / 8) % 8 tells those apart.
+__device__ __forceinline__ int ad_slot(int row, int c) { return row * kAdUnit + 8 * (c ^ ((row >> 1) & 7) ^ ((row >> 3) & 7)); }
 
 template <int TM, int NR>
 __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
@@ -310,8 +337,8 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
   const int u0 = z * a.units[side], u1 = min(u0 + a.units[side], (K + kAdUnit - 1) / kAdUnit);
   const int whole = min(u1, K / kAdUnit);  // units before here end inside the row
   const int c8 = lane & 7, r8 = lane >> 3;
-  uint16_t* xs = reinterpret_cast<uint16_t*>(smem) + w * (TM * kAdUnit + 16 * NR * kAdPitch);  // the wave's: [TM][64]
-  uint16_t* vs = xs + TM * kAdUnit;  // [16 NR][64], or of U^T [16 NR][kAdPitch]
+  uint16_t* xs = reinterpret_cast<uint16_t*>(smem) + w * (TM + 16 * NR) * kAdUnit;  // the wave's: [TM][64]
+  uint16_t* vs = xs + TM * kAdUnit;  // [16 NR][64], of Vt or U^T
   const uint16_t* X = side ? a.G : a.X;
   int xrow[XL];
 #pragma unroll
@@ -411,7 +438,7 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
       if (mine) {
 #pragma unroll
         for (int f = 0; f < 8; ++f)
-          if (off + f >= 0) *reinterpret_cast<u32x4*>(vs + (off + f) * kAdPitch + 8 * jb) = ad_column<8>(v, f);
+          if (off + f >= 0) *reinterpret_cast<u32x4*>(vs + ad_slot(off + f, jb)) = ad_column<8>(v, f);
       }
       ad_wave_sync();
     };
@@ -423,7 +450,7 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
         for (int f = 0; f < MF; ++f) xf[f] = *reinterpret_cast<const u32x4*>(xs + ad_slot(16 * f + i, 4 * h + q));
 #pragma unroll
         for (int g = 0; g < NR; ++g) {
-          const u32x4 vf = *reinterpret_cast<const u32x4*>(vs + (16 * g + i) * kAdPitch + 32 * h + 8 * q);
+          const u32x4 vf = *reinterpret_cast<const u32x4*>(vs + ad_slot(16 * g + i, 4 * h + q));
 #pragma unroll
           for (int f = 0; f < MF; ++f)
             acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf), as_bf16(xf[f]), acc[f][g], 0, 0, 0);
@@ -483,20 +510,6 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
   }
 }
 
-// The splits' sum of four values at p, added in order; four loads in flight.
-__device__ __forceinline__ f32x4 ad_sum(const float* p, int splits, int64_t stride) {
-  f32x4 s = {0.f, 0.f, 0.f, 0.f};
-  for (int z = 0; z < splits; z += 4) {
-    f32x4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const f32x4*>(p + min(z + k, splits - 1) * stride);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (z + k < splits) s += v[k];
-  }
-  return s;
-}
-
 // ---------------------------------------------------------------------------
 // Backward: the terms of T and P.  A lane has one rank of eight slots.
 // grid: (tiles, ranks / 64, sides)
@@ -551,39 +564,70 @@ __device__ __forceinline__ void ad_store8(void* base, uint32_t at, const u32x4& 
   *reinterpret_cast<Bytes16*>(static_cast<char*>(base) + at) = o;
 }
 
-// 16 rows of a wave's 128 columns at the end of the rows: through the wave's 8 KB of
-// LDS, element by element.  D: rows 4 q + e, columns 8 i + f.
-__device__ __forceinline__ void ad_store_end(const AdArgs& a, const uint16_t* rows, int live, int c0, int cols,
-                                             const f32x4 (&acc)[8], float* stage) {
-  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+// 16 rows of a wave's 128 columns where the rows of the output end: through the wave's
+// 8 KB of LDS, a lane every 64th element, all rows' base in flight.  D: rows 4 q + e,
+// columns 8 i + f; row: this lane % 16's row of the output.
+__device__ __forceinline__ void ad_store_end(const AdArgs& a, int row, int live, int c0, int cols, const f32x4 (&acc)[8],
+                                             float* stage) {
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4, width = min(128, cols - c0);
+  if (live <= 0) return;
+  uint32_t old[16][2];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const uint16_t* in = a.base + (int64_t)__builtin_amdgcn_readlane(row, k) * cols + c0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) old[k][c] = a.base ? in[min(64 * c + lane, width - 1)] : 0u;
+  }
   ad_wave_sync();
 #pragma unroll
   for (int e = 0; e < 4; ++e)
 #pragma unroll
     for (int f = 0; f < 8; ++f) stage[(4 * q + e) * 128 + 8 * i + f] = acc[f][e];
   ad_wave_sync();
-  const int width = min(128, cols - c0);
-#pragma unroll 1
-  for (int row = 0; row < live; ++row) {
-    const int64_t at = (int64_t)rows[row] * cols + c0;
 #pragma unroll
-    for (int c = 0; c < 128; c += 64)
-      if (c + lane < width) {
-        const float old = a.base ? __uint_as_float((uint32_t)a.base[at + c + lane] << 16) : 0.f;
-        a.Y[at + c + lane] = f32_to_bf16(old + stage[row * 128 + c + lane]);
-      }
+  for (int k = 0; k < 16; ++k) {
+    if (k >= live) break;
+    uint16_t* out = a.Y + (int64_t)__builtin_amdgcn_readlane(row, k) * cols + c0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (64 * c + lane < width)
+        out[64 * c + lane] = f32_to_bf16(__uint_as_float(old[k][c] << 16) + stage[k * 128 + 64 * c + lane]);
   }
   ad_wave_sync();
 }
 
-// Rows without an adapter: the output is base (nothing to do in place).
+// Rows without an adapter: the output is base (nothing to do in place).  Eight
+// columns a lane, four of them in flight.
 __device__ __forceinline__ void ad_copy(const AdArgs& a, const AdTile& at, const uint16_t* rows, int col, int width,
                                         int cols) {
   if (a.base == a.Y) return;
-  for (int e = threadIdx.x; e < at.rows * width; e += 256) {
-    const int c = col + e % width;
-    const int64_t row = rows[e / width];
-    if (c < cols) a.Y[row * cols + c] = a.base ? a.base[row * cols + c] : (uint16_t)0;
+  const int pieces = (min(width, cols - col) + 7) / 8, total = at.rows * pieces;
+  for (int e0 = threadIdx.x; e0 < total; e0 += 1024) {
+    uint32_t to[4];
+    int left[4];
+    u32x4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = min(e0 + 256 * j, total - 1), c = col + e % pieces * 8;
+      to[j] = rows[e / pieces] * cols + c;
+      left[j] = cols - c;
+      v[j] = u32x4{0u, 0u, 0u, 0u};
+    }
+    if (a.base) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (left[j] >= 8) v[j] = ad_load(a.base, 2u * to[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (e0 + 256 * j >= total) continue;
+      if (left[j] >= 8) {
+        *reinterpret_cast<Bytes16*>(a.Y + to[j]) = Bytes16{{v[j].x, v[j].y, v[j].z, v[j].w}};
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < left[j]; ++k) a.Y[to[j] + k] = a.base ? a.base[to[j] + k] : (uint16_t)0;
+      }
+    }
   }
 }
 
@@ -596,11 +640,13 @@ __device__ __forceinline__ void ad_copy(const AdArgs& a, const AdTile& at, const
 // its columns.
 // grid: (tiles, column blocks of 512 NC)
 // ---------------------------------------------------------------------------
-// Where U's row 8 i + f goes in LDS: rows of 32 ranks, those of one piece side by
-// side, 16-byte chunks spread over the banks.
-__device__ __forceinline__ int ad_place(int i, int f, int q) { return (16 * f + i) * 32 + 8 * (q ^ ((i >> 1) & 3)); }
+// Where 16-byte chunk q of U's row 8 i + f (32 ranks, 64 bytes) lies in LDS: the 16
+// rows of a piece side by side, so that a read's 16 fall on different banks (chunks
+// spread by i / 4), and the four rows of a write too (rows spread by f).
+__device__ __forceinline__ int ad_place(int i, int f, int q) { return (16 * f + (i ^ (f & 3))) * 32 + 8 * (q ^ ((i >> 2) & 3)); }
 
-template <int TM>
+// SHORT: rows of U with fewer than eight ranks, loaded one by one.
+template <int TM, bool SHORT>
 __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, int nc) {
   constexpr int MF = TM / 16;
   extern __shared__ __align__(16) uint16_t lds[];
@@ -623,20 +669,46 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
   uint16_t* terms = lds + 4 * 128 * 32;  // [TM][2][ranks of a chunk, + 4]
   const int wide = min(a.rp, kAdChunk), pitch = 2 * wide + 8;
   const float scale = a.scale ? a.scale[at.adapter] : 1.f;
-  auto fill = [&](int rank0) {  // two terms of a chunk's ranks, zeros past r
-    const uint32_t quads = (uint32_t)min(wide, a.rp - rank0) / 4;
+  auto fill = [&](int rank0) {  // two terms of a chunk's ranks, zeros past r; 4 J loads in flight
+    const uint32_t quads = (uint32_t)min(wide, a.rp - rank0) / 4, items = at.rows * quads;
     const float* p = a.part[0] + (int64_t)TM * tile * a.rg + rank0;
-    for (uint32_t e = threadIdx.x; e < at.rows * quads; e += 256) {
-      const int row = e / quads, k = e % quads * 4;
-      f32x4 v = {0.f, 0.f, 0.f, 0.f};
-      if (rank0 + k < a.rg) v = ad_sum(p + row * a.rg + k, a.splits[0], (int64_t)a.slots * a.rg);
-      float x[4];
+    const int64_t stride = (int64_t)a.slots * a.rg;
+    const int splits = a.splits[0];
+    constexpr int J = MF;
+    for (uint32_t e0 = threadIdx.x; e0 < items; e0 += 256 * J) {
+      int row[J], k[J];
+      const float* from[J];
+      f32x4 sum[J];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = rank0 + k + c < a.r ? v[c] * scale : 0.f;
+      for (int j = 0; j < J; ++j) {
+        const uint32_t e = min(e0 + 256 * j, items - 1);
+        row[j] = e / quads, k[j] = e % quads * 4;
+        from[j] = p + row[j] * a.rg + min(k[j], a.rg - 4 - rank0);
+        sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      for (int z = 0; z < splits; z += 4) {
+        f32x4 v[J][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t lo = ad_term2(x[0], x[1]), hi = ad_term2(x[2], x[3]);
-        *reinterpret_cast<mx_u32x2*>(terms + row * pitch + h * wide + k) = mx_u32x2{lo, hi};
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[j][c] = *reinterpret_cast<const f32x4*>(from[j] + min(z + c, splits - 1) * stride);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (z + c < splits) sum[j] += v[j][c];
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (e0 + 256 * j >= items) continue;
+        float x[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = rank0 + k[j] + c < a.r ? sum[j][c] * scale : 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t lo = ad_term2(x[0], x[1]), hi = ad_term2(x[2], x[3]);
+          *reinterpret_cast<mx_u32x2*>(terms + row[j] * pitch + h * wide + k[j]) = mx_u32x2{lo, hi};
+        }
       }
     }
   };
@@ -646,61 +718,65 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
   const uint16_t* U = a.U + (int64_t)at.adapter * a.m * a.r;
   const bool one = a.rp <= kAdChunk;
   const int col = lane >> 2, c4 = lane & 3;  // of 16 columns' loads, four lanes a row of 32 ranks
-  bool filled = false;
-  for (int c0 = cb + 128 * w; c0 < cb + 512 * nc; c0 += 512) {
-    const bool full = c0 + 128 <= a.m;
-    u32x4 u[8];
+  u32x4 u[8];
+  // ranks k .. k + 31 of the 128 columns from c0 on; at the end of the ranks the row's
+  // last eight, shifted in place()
+  auto load = [&](int c0, int k) {
     uint32_t from[8];  // byte offsets of the rows
 #pragma unroll
     for (int j = 0; j < 8; ++j) from[j] = 2u * (min(c0 + 16 * j + col, a.m - 1) * a.r);
-    auto load = [&](int k) {  // ranks k .. k + 31; at the end of the ranks the row's last eight, shifted in place()
-      if (a.r >= 8) {
-        const int at8 = min(k + 8 * c4, a.r - 8);
+    if constexpr (!SHORT) {
+      const int at8 = min(k + 8 * c4, a.r - 8);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = ad_load(U, from[j] + 2u * at8);
-      } else {
+      for (int j = 0; j < 8; ++j) u[j] = ad_load(U, from[j] + 2u * at8);
+    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = u32x4{0u, 0u, 0u, 0u};
-        if (c4 == 0)
+      for (int j = 0; j < 8; ++j) u[j] = u32x4{0u, 0u, 0u, 0u};
+      if (c4 != 0) return;
 #pragma unroll 1
-          for (int e = 0; e < a.r; ++e) {
-            const int d = e >> 1, sh = 16 * (e & 1);
+      for (int e = 0; e < a.r; ++e) {
+        const int d = e >> 1, sh = 16 * (e & 1);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t x = (uint32_t)U[from[j] / 2 + e] << sh;
-              u[j].x |= d == 0 ? x : 0u, u[j].y |= d == 1 ? x : 0u, u[j].z |= d == 2 ? x : 0u, u[j].w |= d == 3 ? x : 0u;
-            }
-          }
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t x = (uint32_t)U[from[j] / 2 + e] << sh;
+          u[j].x |= d == 0 ? x : 0u, u[j].y |= d == 1 ? x : 0u, u[j].z |= d == 2 ? x : 0u, u[j].w |= d == 3 ? x : 0u;
+        }
       }
-    };
-    auto place = [&](int k) {  // column 16 j + col = 8 (2 j + col / 8) + col % 8
-      if (k + 32 > a.r && a.r >= 8) {
-        const int s = k + 8 * c4 - min(k + 8 * c4, a.r - 8);
+    }
+  };
+  auto place = [&](int k) {  // column 16 j + col = 8 (2 j + col / 8) + col % 8
+    if (!SHORT && k + 32 > a.r) {
+      const int s = k + 8 * c4 - min(k + 8 * c4, a.r - 8);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = ad_drop(u[j], s);
-      }
+      for (int j = 0; j < 8; ++j) u[j] = ad_drop(u[j], s);
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4*>(us + ad_place(2 * j + (col >> 3), col & 7, c4)) = u[j];
-      ad_wave_sync();
-    };
-    // the first ranks of U and the rows' base are on their way while the terms are made
-    load(0);
-    u32x4 old[MF][4];
-#pragma unroll
-    for (int g = 0; g < MF; ++g)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) old[g][e] = u32x4{0u, 0u, 0u, 0u};
-    if (full && a.base) {
+    for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4*>(us + ad_place(2 * j + (col >> 3), col & 7, c4)) = u[j];
+    ad_wave_sync();
+  };
+  u32x4 old[MF][4];
+  auto load_base = [&](int c0) {
+    if (c0 + 128 <= a.m && a.base) {
 #pragma unroll
       for (int g = 0; g < MF; ++g)
 #pragma unroll
         for (int e = 0; e < 4; ++e) old[g][e] = ad_load(a.base, out[g][e] + 2u * c0);
     }
-    if (one && !filled) {
-      fill(0);
-      __syncthreads();
-      filled = true;
-    }
+  };
+#pragma unroll
+  for (int g = 0; g < MF; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) old[g][e] = u32x4{0u, 0u, 0u, 0u};
+  // the first columns' U and base are on their way while the terms are made, the
+  // next ones' while a column block is multiplied
+  load(cb + 128 * w, 0);
+  load_base(cb + 128 * w);
+  if (one) {
+    fill(0);
+    __syncthreads();
+  }
+  const int stop = cb + 512 * nc;
+  for (int c0 = cb + 128 * w; c0 < stop; c0 += 512) {
     f32x4 acc[MF][8];
 #pragma unroll
     for (int g = 0; g < MF; ++g)
@@ -714,7 +790,8 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
       }
       for (int s = 0; s < min(wide, a.rp - rank0); s += 32) {
         place(rank0 + s);
-        if (rank0 + s + 32 < a.rp) load(rank0 + s + 32);
+        if (rank0 + s + 32 < a.rp) load(c0, rank0 + s + 32);
+        else if (c0 + 512 < stop) load(c0 + 512, 0);
         u32x4 t[2][MF];
 #pragma unroll
         for (int g = 0; g < MF; ++g)
@@ -732,7 +809,7 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
         ad_wave_sync();
       }
     }
-    if (full) {
+    if (c0 + 128 <= a.m) {
 #pragma unroll
       for (int g = 0; g < MF; ++g)
 #pragma unroll
@@ -742,10 +819,11 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
           for (int f = 0; f < 8; ++f) v[f] = acc[g][f][e];
           if (16 * g + 4 * q + e < at.rows) ad_store8(a.Y, out[g][e] + 2u * c0, old[g][e], v);
         }
+      if (c0 + 512 < stop) load_base(c0 + 512);
     } else if (c0 < a.m) {
 #pragma unroll
       for (int g = 0; g < MF; ++g)
-        ad_store_end(a, rows + 16 * g, at.rows - 16 * g < 16 ? at.rows - 16 * g : 16, c0, a.m, acc[g], reinterpret_cast<float*>(us));
+        ad_store_end(a, rows[16 * g + i], min(16, at.rows - 16 * g), c0, a.m, acc[g], reinterpret_cast<float*>(us));
     }
   }
 }
@@ -803,7 +881,7 @@ __device__ __forceinline__ void ad_dx(const AdArgs& a, int block, char* smem) {
       if (!full) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          v[e] = __builtin_bit_cast(AdPiece<8>, ad_drop(__builtin_bit_cast(u32x4, v[e]), col - from));
+          v[e] = ad_drop<8>(v[e], col - from);
       }
     } else {
 #pragma unroll
@@ -838,7 +916,7 @@ __device__ __forceinline__ void ad_dx(const AdArgs& a, int block, char* smem) {
   } else {
 #pragma unroll
     for (int g = 0; g < MF; ++g)
-      ad_store_end(a, rows + 16 * g, at.rows - 16 * g < 16 ? at.rows - 16 * g : 16, c0, a.n, acc[g],
+      ad_store_end(a, rows[16 * g + i], min(16, at.rows - 16 * g), c0, a.n, acc[g],
                    reinterpret_cast<float*>(smem) + w * 16 * 128);
   }
 }
@@ -902,9 +980,13 @@ __device__ __forceinline__ void ad_dfactor(const AdArgs& a, int block, char* sme
     if (inside) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) r.v[e] = ad_piece_at<CW>(src, 2u * (row[e] + c0 + CW * i));
+    } else if (cols >= CW) {
+      const int from = min(c0 + CW * i, cols - CW);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.v[e] = ad_drop<CW>(ad_piece_at<CW>(src, 2u * (row[e] + from)), c0 + CW * i - from);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r.v[e] = ad_piece_end<CW>(src + row[e] + min(c0 + CW * i, cols - 1), cols - (c0 + CW * i));
+      for (int e = 0; e < 8; ++e) r.v[e] = ad_piece_end<CW>(src + row[e], i == 0 ? cols : 0);
     }
   };
   auto multiply = [&](int s, const Regs& r) {
@@ -978,6 +1060,120 @@ __device__ __forceinline__ void ad_dfactor(const AdArgs& a, int block, char* sme
       }
 }
 
+// The same where there are many columns in all: the block's waves take 64 columns
+// each and all of the adapter's rows, and share a tile's terms through LDS (12 KB of
+// 64 ranks, one contiguous piece in memory; the next tile's are on their way).
+template <bool DV>
+__device__ __forceinline__ void ad_dfactor_wide(const AdArgs& a, int block, char* smem) {
+  constexpr int NR = 4, CW = 4, kTerms = NR * 3 * 64;  // 16-byte pieces of a tile's terms
+  const int cols = DV ? a.n : a.m, blocks = DV ? a.cols_v : a.cols_u;
+  const int rest = block / blocks, rank0 = rest % a.chunks * 16 * NR, l = rest / a.chunks;
+  const int t = threadIdx.x, w = t >> 6, lane = t & 63, i = lane & 15, q = lane >> 4;
+  const int c0 = block % blocks * 64 * CW + w * 16 * CW;
+  const int2 first = a.first[l];
+  const int tile0 = uniform(first.x), total = uniform(first.y), steps = (total + 31) / 32;
+  const int groups = a.rg >> 4, pieces = min(NR, groups - rank0 / 16) * 3 * 64;
+  const uint16_t* src = DV ? a.X : a.G;
+  const u32x4* terms = reinterpret_cast<const u32x4*>(a.t3[DV]) + rank0 / 16 * 3 * 64;
+  u32x4* buf = reinterpret_cast<u32x4*>(smem);  // [2][kTerms]
+  f32x4 acc[CW][NR];
+#pragma unroll
+  for (int f = 0; f < CW; ++f)
+#pragma unroll
+    for (int g = 0; g < NR; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const bool inside = c0 + 16 * CW <= cols;
+  const int from = cols >= CW ? min(c0 + CW * i, cols - CW) : 0, drop = c0 + CW * i - from;
+  struct Regs {
+    AdPiece<CW> v[8];
+  };
+  auto load = [&](int s, Regs& r) {
+    const int pos = 32 * (tile0 + s);
+    int row[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) row[e] = a.rows[pos + 8 * q + e] * cols;
+    if (cols >= CW) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.v[e] = ad_piece_at<CW>(src, 2u * (row[e] + from));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.v[e] = ad_piece_end<CW>(src + row[e], c0 + i == 0 ? cols : 0);
+    }
+  };
+  u32x4 next[3];
+  auto load_terms = [&](int s) {  // (past the ranks: the last piece again, not stored)
+    const u32x4* p = terms + (int64_t)(tile0 + s) * groups * 3 * 64;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) next[k] = p[min(256 * k + t, pieces - 1)];
+  };
+  auto put_terms = [&](int s) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) buf[(s & 1) * kTerms + 256 * k + t] = next[k];
+  };
+  auto multiply = [&](int s, Regs& r) {
+    if (!inside && cols >= CW) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.v[e] = ad_drop<CW>(r.v[e], drop);
+    }
+    u32x4 x[CW];
+#pragma unroll
+    for (int f = 0; f < CW; ++f) x[f] = ad_column<CW>(r.v, f);
+#pragma unroll
+    for (int g = 0; g < NR; ++g)
+#pragma unroll
+      for (int h = 0; h < 3; ++h) {
+        const u32x4 y = buf[(s & 1) * kTerms + (3 * g + h) * 64 + lane];
+#pragma unroll
+        for (int f = 0; f < CW; ++f)
+          acc[f][g] = DV ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(y), as_bf16(x[f]), acc[f][g], 0, 0, 0)
+                         : __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(x[f]), as_bf16(y), acc[f][g], 0, 0, 0);
+      }
+  };
+  if (steps > 0) {
+    Regs ra, rb;
+    load_terms(0), load(0, ra);
+    put_terms(0);
+    __syncthreads();
+    for (int s = 0; s < steps; s += 2) {  // the block's waves go through it together
+      load_terms(min(s + 1, steps - 1)), load(min(s + 1, steps - 1), rb);
+      multiply(s, ra);
+      put_terms(s + 1);
+      __syncthreads();
+      if (s + 1 >= steps) break;
+      load_terms(min(s + 2, steps - 1)), load(min(s + 2, steps - 1), ra);
+      multiply(s + 1, rb);
+      put_terms(s + 2);
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < NR; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int f = 0; f < CW; ++f) {
+        const int rank = rank0 + 16 * g + (DV ? 4 * q + e : i), col = c0 + CW * (DV ? i : 4 * q + e) + f;
+        if (rank < a.r && col < cols) {
+          if (DV) a.dVt[((int64_t)l * a.r + rank) * a.n + col] = acc[f][g][e];
+          else a.dU[((int64_t)l * a.m + col) * a.r + rank] = acc[f][g][e];
+        }
+      }
+}
+
+__global__ __launch_bounds__(256, 2) void k_ad_back_wide(AdArgs a) {
+  extern __shared__ __align__(16) char smem[];
+  int block = blockIdx.x;
+  if (block < a.blocks_u) {
+    ad_dfactor_wide<false>(a, block, smem);
+    return;
+  }
+  block -= a.blocks_u;
+  if (block < a.blocks_v) {
+    ad_dfactor_wide<true>(a, block, smem);
+    return;
+  }
+  ad_dx(a, block - a.blocks_v, smem);
+}
+
 template <int NR, int CW>
 __global__ __launch_bounds__(256, 2) void k_ad_back(AdArgs a) {
   extern __shared__ __align__(16) char smem[];
@@ -1002,13 +1198,12 @@ struct AdPlan {
   size_t part[2], t2, t3[2], info, rows, first, total;  // offsets in the workspace
 };
 
-// K splits that give about kAdBlocks blocks in all, of whole units for the four
-// waves.
-static void ad_split(int K, int blocks, int* splits, int* per) {
-  const int units = (K + kAdUnit - 1) / kAdUnit;
-  const int want = std::max(1, std::min((units + 3) / 4, kAdBlocks / std::max(1, blocks)));
-  *per = (units + want - 1) / want;
-  *splits = (units + *per - 1) / *per;
+// K splits of `units` a block takes `per` of (whole ones for the four waves).
+static void ad_split(int K, int per, int* splits, int* units) {
+  const int all = (K + kAdUnit - 1) / kAdUnit;
+  *splits = (all + per - 1) / per;
+  *units = (all + *splits - 1) / *splits;
+  *splits = (all + *units - 1) / *units;
 }
 
 static AdPlan ad_plan(const hss_adapters* A, int b, bool grad) {
@@ -1021,9 +1216,12 @@ static AdPlan ad_plan(const hss_adapters* A, int b, bool grad) {
   p.rg = (A->r + 15) / 16 * 16;
   // tiles with rows: at least those of one adapter, as if all had some
   const int groups = (p.rg + 16 * p.nr - 1) / (16 * p.nr);
-  const int busy = std::max((b + p.tm - 1) / p.tm, std::min(b, A->count)) * groups * (grad ? 2 : 1);
-  ad_split(A->n, busy, &p.splits[0], &p.units[0]);
-  ad_split(A->m, busy, &p.splits[1], &p.units[1]);
+  const int busy = std::max((b + p.tm - 1) / p.tm, std::min(b, A->count)) * groups;
+  // the same share of K for each block, whatever side it is on
+  const int64_t all = (int64_t)busy * ((A->n + kAdUnit - 1) / kAdUnit + (grad ? (A->m + kAdUnit - 1) / kAdUnit : 0));
+  const int per = (int)std::max<int64_t>(4, (all + kAdBlocks - 1) / kAdBlocks);
+  ad_split(A->n, per, &p.splits[0], &p.units[0]);
+  ad_split(A->m, per, &p.splits[1], &p.units[1]);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -1071,8 +1269,8 @@ static AdArgs ad_args(const hss_adapters* A, int b, const AdPlan& p, const void*
 
 template <int TM, int NR>
 static void launch_rank_nr(const AdArgs& a, hipStream_t s) {
-  const size_t lds = std::max<size_t>((size_t)4 * (TM * kAdUnit + 16 * NR * kAdPitch) * 2, (size_t)(a.count + 1) * 4);
-  static_assert(4 * (TM * kAdUnit + 16 * NR * kAdPitch) * 2 >= 4 * (TM / 16) * NR * 64 * 16, "the waves' sums fit");
+  const size_t lds = std::max<size_t>((size_t)4 * (TM + 16 * NR) * kAdUnit * 2, (size_t)(a.count + 1) * 4);
+  static_assert(4 * (TM + 16 * NR) * kAdUnit * 2 >= 4 * (TM / 16) * NR * 64 * 16, "the waves' sums fit");
   const dim3 grid(a.splits[0] + a.splits[1], a.tiles, (a.rg + 16 * NR - 1) / (16 * NR));
   hipLaunchKernelGGL((k_ad_rank<TM, NR>), grid, dim3(256), lds, s, a);
 }
@@ -1091,7 +1289,8 @@ static void launch_expand(const AdArgs& a, hipStream_t s) {
   const int nc = std::max(1, std::min(cols, cols * busy / 512));
   const dim3 grid(a.tiles, (cols + nc - 1) / nc);
   const size_t lds = (size_t)(4 * 128 * 32 + TM * (2 * std::min(a.rp, kAdChunk) + 8)) * 2;
-  hipLaunchKernelGGL(k_ad_expand<TM>, grid, dim3(256), lds, s, a, nc);
+  if (a.r >= 8) hipLaunchKernelGGL((k_ad_expand<TM, false>), grid, dim3(256), lds, s, a, nc);
+  else hipLaunchKernelGGL((k_ad_expand<TM, true>), grid, dim3(256), lds, s, a, nc);
 }
 
 hss_status launch_adapters_apply(const hss_adapters* A, int b, const void* X, const int32_t* ids, const void* base,
@@ -1131,11 +1330,24 @@ hss_status launch_adapters_grad(const hss_adapters* A, int b, const void* X, con
   launch_rank<32>(a, p.nr, s);
   const dim3 grid(a.tiles, (a.rp + 63) / 64, a.splits[0] && a.splits[1] ? 2 : 1);
   hipLaunchKernelGGL(k_ad_terms, grid, dim3(256), 0, s, a);
-  // few blocks of dU and dVt: narrower ones
+  // Blocks of 256 columns that share the terms, where they fill the chip; else
+  // waves share the rows of fewer columns.
+  const int64_t wide = (int64_t)A->count * ((A->r + 63) / 64) * (((int64_t)A->m + 255) / 256 + (A->n + 255) / 256);
   const bool narrow = (int64_t)A->count * ((A->r + 63) / 64) * ((int64_t)A->m + A->n) / 128 < 256;
-  if (p.nr == 1) narrow ? launch_back<1, 2>(a, s) : launch_back<1, 8>(a, s);
-  else if (p.nr == 2) narrow ? launch_back<2, 2>(a, s) : launch_back<2, 4>(a, s);
-  else narrow ? launch_back<4, 2>(a, s) : launch_back<4, 4>(a, s);
+  if (b > kAdSmall && p.nr == 4 && wide >= 192) {
+    a.chunks = (a.rg + 63) / 64;
+    a.cols_u = (a.m + 255) / 256, a.cols_v = (a.n + 255) / 256, a.cols_y = (a.n + 511) / 512;
+    a.blocks_u = dU ? a.cols_u * a.chunks * a.count : 0;
+    a.blocks_v = dVt ? a.cols_v * a.chunks * a.count : 0;
+    const dim3 blocks(a.blocks_u + a.blocks_v + (dX ? a.cols_y * a.tiles : 0));
+    hipLaunchKernelGGL(k_ad_back_wide, blocks, dim3(256), 32768, s, a);
+  } else if (p.nr == 1) {
+    narrow ? launch_back<1, 2>(a, s) : launch_back<1, 8>(a, s);
+  } else if (p.nr == 2) {
+    narrow ? launch_back<2, 2>(a, s) : launch_back<2, 4>(a, s);
+  } else {
+    narrow ? launch_back<4, 2>(a, s) : launch_back<4, 4>(a, s);
+  }
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 
