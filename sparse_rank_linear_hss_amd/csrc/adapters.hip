@@ -30,7 +30,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 static constexpr int kAdSmall = 64;     // batches up to here: tiles found by one ballot
 static constexpr int kAdUnit = 64;      // columns of K that a wave takes at a time: a cache line of each row
-static constexpr int kAdBlocks = 704;   // blocks of k_ad_rank that K is split for
+static constexpr int kAdBlocks = 512;   // blocks of k_ad_rank that K is split for
 static constexpr int kAdChunk = 256;    // ranks of T that k_ad_expand keeps in LDS
 
 struct AdArgs {
@@ -602,13 +602,14 @@ __device__ __forceinline__ void ad_copy(const AdArgs& a, const AdTile& at, const
                                         int cols) {
   if (a.base == a.Y) return;
   const int pieces = (min(width, cols - col) + 7) / 8, total = at.rows * pieces;
-  for (int e0 = threadIdx.x; e0 < total; e0 += 1024) {
+  const int threads = blockDim.x;
+  for (int e0 = threadIdx.x; e0 < total; e0 += 4 * threads) {
     uint32_t to[4];
     int left[4];
     u32x4 v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int e = min(e0 + 256 * j, total - 1), c = col + e % pieces * 8;
+      const int e = min(e0 + threads * j, total - 1), c = col + e % pieces * 8;
       to[j] = rows[e / pieces] * cols + c;
       left[j] = cols - c;
       v[j] = u32x4{0u, 0u, 0u, 0u};
@@ -620,7 +621,7 @@ __device__ __forceinline__ void ad_copy(const AdArgs& a, const AdTile& at, const
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (e0 + 256 * j >= total) continue;
+      if (e0 + threads * j >= total) continue;
       if (left[j] >= 8) {
         *reinterpret_cast<Bytes16*>(a.Y + to[j]) = Bytes16{{v[j].x, v[j].y, v[j].z, v[j].w}};
       } else {
@@ -644,6 +645,27 @@ __device__ __forceinline__ void ad_copy(const AdArgs& a, const AdTile& at, const
 // rows of a piece side by side, so that a read's 16 fall on different banks (chunks
 // spread by i / 4), and the four rows of a write too (rows spread by f).
 __device__ __forceinline__ int ad_place(int i, int f, int q) { return (16 * f + (i ^ (f & 3))) * 32 + 8 * (q ^ ((i >> 2) & 3)); }
+
+// Ranks k .. k + 31 of U's rows c0 .. c0 + 127, four lanes a row; at the end of the
+// ranks the row's last eight, which ad_put_u shifts.
+__device__ __forceinline__ void ad_load_u(u32x4 (&u)[8], const uint16_t* U, int m, int r, int c0, int k) {
+  const int lane = threadIdx.x & 63, col = lane >> 2, from = min(k + 8 * (lane & 3), r - 8);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) u[j] = ad_load(U, 2u * (min(c0 + 16 * j + col, m - 1) * r + from));
+}
+
+// The same to the wave's part of LDS: column 16 j + col = 8 (2 j + col / 8) + col % 8.
+__device__ __forceinline__ void ad_put_u(u32x4 (&u)[8], uint16_t* us, int r, int k) {
+  const int lane = threadIdx.x & 63, col = lane >> 2, c4 = lane & 3;
+  if (k + 32 > r && r >= 8) {
+    const int drop = k + 8 * c4 - min(k + 8 * c4, r - 8);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = ad_drop(u[j], drop);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4*>(us + ad_place(2 * j + (col >> 3), col & 7, c4)) = u[j];
+  ad_wave_sync();
+}
 
 // SHORT: rows of U with fewer than eight ranks, loaded one by one.
 template <int TM, bool SHORT>
@@ -717,42 +739,24 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
   for (int g = 0; g < MF; ++g) trow[g] = terms + min(16 * g + i, at.rows - 1) * pitch + 8 * q;
   const uint16_t* U = a.U + (int64_t)at.adapter * a.m * a.r;
   const bool one = a.rp <= kAdChunk;
-  const int col = lane >> 2, c4 = lane & 3;  // of 16 columns' loads, four lanes a row of 32 ranks
   u32x4 u[8];
-  // ranks k .. k + 31 of the 128 columns from c0 on; at the end of the ranks the row's
-  // last eight, shifted in place()
   auto load = [&](int c0, int k) {
-    uint32_t from[8];  // byte offsets of the rows
-#pragma unroll
-    for (int j = 0; j < 8; ++j) from[j] = 2u * (min(c0 + 16 * j + col, a.m - 1) * a.r);
     if constexpr (!SHORT) {
-      const int at8 = min(k + 8 * c4, a.r - 8);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = ad_load(U, from[j] + 2u * at8);
+      ad_load_u(u, U, a.m, a.r, c0, k);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) u[j] = u32x4{0u, 0u, 0u, 0u};
-      if (c4 != 0) return;
+      if ((lane & 3) != 0) return;
 #pragma unroll 1
       for (int e = 0; e < a.r; ++e) {
         const int d = e >> 1, sh = 16 * (e & 1);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint32_t x = (uint32_t)U[from[j] / 2 + e] << sh;
+          const uint32_t x = (uint32_t)U[min(c0 + 16 * j + (lane >> 2), a.m - 1) * a.r + e] << sh;
           u[j].x |= d == 0 ? x : 0u, u[j].y |= d == 1 ? x : 0u, u[j].z |= d == 2 ? x : 0u, u[j].w |= d == 3 ? x : 0u;
         }
       }
     }
-  };
-  auto place = [&](int k) {  // column 16 j + col = 8 (2 j + col / 8) + col % 8
-    if (!SHORT && k + 32 > a.r) {
-      const int s = k + 8 * c4 - min(k + 8 * c4, a.r - 8);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = ad_drop(u[j], s);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4*>(us + ad_place(2 * j + (col >> 3), col & 7, c4)) = u[j];
-    ad_wave_sync();
   };
   u32x4 old[MF][4];
   auto load_base = [&](int c0) {
@@ -789,7 +793,7 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
         __syncthreads();
       }
       for (int s = 0; s < min(wide, a.rp - rank0); s += 32) {
-        place(rank0 + s);
+        ad_put_u(u, us, a.r, rank0 + s);
         if (rank0 + s + 32 < a.rp) load(c0, rank0 + s + 32);
         else if (c0 + 512 < stop) load(c0 + 512, 0);
         u32x4 t[2][MF];
@@ -825,6 +829,159 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
       for (int g = 0; g < MF; ++g)
         ad_store_end(a, rows[16 * g + i], min(16, at.rows - 16 * g), c0, a.m, acc[g], reinterpret_cast<float*>(us));
     }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Both in one launch, for a few rows and small factors: each block makes all of its
+// tile's T for itself (16 waves share K), then its columns of Y.  Vt_l comes from L2
+// for all blocks but the first; a launch, a round trip of T through memory and a
+// workspace are saved.
+// grid: (tiles, column blocks of 512 NC)
+// ---------------------------------------------------------------------------
+static constexpr int kAdFusedWaves = 16, kAdFusedColumns = 8;
+
+template <int NR>
+__global__ __launch_bounds__(64 * kAdFusedWaves) void k_ad_fused(AdArgs a, int nc) {
+  constexpr int TM = 16, XL = TM / 8, VL = 2 * NR, UN = NR == 1 ? 4 : 2;  // units in flight
+  constexpr int kStage = (TM + 16 * NR) * kAdUnit, kPitch = 2 * 32 + 8;
+  __shared__ __align__(16) uint16_t lds[kAdFusedWaves * kStage];  // a wave's unit; the waves' sums; U of the columns
+  __shared__ __align__(16) uint16_t terms[TM * kPitch];           // [row][term][32]
+  __shared__ uint16_t rows[TM];
+  static_assert(kAdFusedWaves * kStage >= kAdFusedWaves * NR * 64 * 8 &&
+                    kAdFusedWaves * kStage >= kAdFusedColumns * 128 * 32, "what shares LDS fits");
+  const AdTile at = ad_tile<TM>(a, blockIdx.x, rows, nullptr, nullptr, nullptr);
+  if (at.rows == 0) return;
+  const int cb = (int)blockIdx.y * 512 * nc;
+  if (at.adapter < 0) {
+    ad_copy(a, at, rows, cb, 512 * nc, a.m);
+    return;
+  }
+  const int adapter = uniform(at.adapter), live = uniform(at.rows);
+  const int w = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int c8 = lane & 7, r8 = lane >> 3, K = a.n, units = (K + kAdUnit - 1) / kAdUnit, whole = K / kAdUnit;
+  uint16_t* xs = lds + w * kStage;
+  uint16_t* vs = xs + TM * kAdUnit;
+  const uint16_t* V = a.Vt + (int64_t)adapter * a.r * K;
+  const float scale = a.scale ? a.scale[adapter] : 1.f;
+  int xrow[XL], vrow[VL];
+#pragma unroll
+  for (int j = 0; j < XL; ++j) xrow[j] = rows[min(8 * j + r8, live - 1)] * K;
+#pragma unroll
+  for (int j = 0; j < VL; ++j) vrow[j] = min(8 * j + r8, a.r - 1) * K;
+  f32x4 acc[NR];
+#pragma unroll
+  for (int g = 0; g < NR; ++g) acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const u32x4 (&x)[XL], const u32x4 (&v)[VL]) {
+#pragma unroll
+    for (int j = 0; j < XL; ++j) *reinterpret_cast<u32x4*>(xs + ad_slot(8 * j + r8, c8)) = x[j];
+#pragma unroll
+    for (int j = 0; j < VL; ++j) *reinterpret_cast<u32x4*>(vs + ad_slot(8 * j + r8, c8)) = v[j];
+    ad_wave_sync();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 xf = *reinterpret_cast<const u32x4*>(xs + ad_slot(i, 4 * h + q));
+#pragma unroll
+      for (int g = 0; g < NR; ++g) {
+        const u32x4 vf = *reinterpret_cast<const u32x4*>(vs + ad_slot(16 * g + i, 4 * h + q));
+        acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf), as_bf16(xf), acc[g], 0, 0, 0);
+      }
+    }
+    ad_wave_sync();
+  };
+  for (int u0 = w; u0 < units; u0 += UN * kAdFusedWaves) {
+    u32x4 x[UN][XL], v[UN][VL];
+#pragma unroll
+    for (int p = 0; p < UN; ++p) {
+      const int u = u0 + p * kAdFusedWaves;
+      if (u < whole) {
+#pragma unroll
+        for (int j = 0; j < XL; ++j) x[p][j] = ad_load(a.X, 2u * (xrow[j] + u * kAdUnit + 8 * c8));
+#pragma unroll
+        for (int j = 0; j < VL; ++j) v[p][j] = ad_load(V, 2u * (vrow[j] + u * kAdUnit + 8 * c8));
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < UN; ++p) {
+      const int u = u0 + p * kAdFusedWaves;
+      if (u >= units) break;
+      if (u >= whole) {  // the unit in which the rows end
+#pragma unroll
+        for (int j = 0; j < XL; ++j) x[p][j] = ad_tail8(a.X + xrow[j], u * kAdUnit + 8 * c8, K);
+#pragma unroll
+        for (int j = 0; j < VL; ++j) v[p][j] = ad_tail8(V + vrow[j], u * kAdUnit + 8 * c8, K);
+      }
+      multiply(x[p], v[p]);
+    }
+  }
+  // the columns' U and base are on their way while the waves' sums meet
+  const uint16_t* U = a.U + (int64_t)adapter * a.m * a.r;
+  const int stop = min(cb + 512 * nc, a.m);
+  uint32_t out[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[e] = 2u * (rows[min(4 * q + e, live - 1)] * a.m + 8 * i);
+  u32x4 u[8], old[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) old[e] = u32x4{0u, 0u, 0u, 0u};
+  auto load = [&](int c0) {
+    ad_load_u(u, U, a.m, a.r, c0, 0);
+    if (c0 + 128 <= a.m && a.base) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) old[e] = ad_load(a.base, out[e] + 2u * c0);
+    }
+  };
+  const int first = cb + 128 * w;
+  if (first < stop && w < kAdFusedColumns) load(first);
+  f32x4* sum = reinterpret_cast<f32x4*>(lds);  // [waves][NR][64]
+  __syncthreads();
+#pragma unroll
+  for (int g = 0; g < NR; ++g) sum[(w * NR + g) * 64 + lane] = acc[g];
+  __syncthreads();
+  if (w < 2) {  // wave g: ranks 16 g + 4 q .. + 3 of row i, as terms; zeros past r
+    f32x4 t = {0.f, 0.f, 0.f, 0.f};
+    if (w < NR) {
+#pragma unroll
+      for (int k = 0; k < kAdFusedWaves; ++k) t += sum[(k * NR + w) * 64 + lane];
+    }
+    const int rank = 16 * w + 4 * q;
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = rank + e < a.r ? t[e] * scale : 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t lo = ad_term2(x[0], x[1]), hi = ad_term2(x[2], x[3]);
+      *reinterpret_cast<mx_u32x2*>(terms + i * kPitch + 32 * h + rank) = mx_u32x2{lo, hi};
+    }
+  }
+  __syncthreads();
+  u32x4 t[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) t[h] = *reinterpret_cast<const u32x4*>(terms + i * kPitch + 32 * h + 8 * q);
+  // 8 KB of LDS a wave: the first half of the waves take columns at a time
+  uint16_t* us = lds + w * 128 * 32;
+  for (int c0 = first; c0 < stop && w < kAdFusedColumns; c0 += 128 * kAdFusedColumns) {
+    ad_put_u(u, us, a.r, 0);
+    f32x4 y[8];
+#pragma unroll
+    for (int f = 0; f < 8; ++f) {
+      const u32x4 uf = *reinterpret_cast<const u32x4*>(us + ad_place(i, f, q));
+      y[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) y[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t[h]), as_bf16(uf), y[f], 0, 0, 0);
+    }
+    ad_wave_sync();
+    if (c0 + 128 <= a.m) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v[8];
+#pragma unroll
+        for (int f = 0; f < 8; ++f) v[f] = y[f][e];
+        if (4 * q + e < live) ad_store8(a.Y, out[e] + 2u * c0, old[e], v);
+      }
+    } else {
+      ad_store_end(a, rows[min(i, live - 1)], live, c0, a.m, y, reinterpret_cast<float*>(us));
+    }
+    if (c0 + 128 * kAdFusedColumns < stop) load(c0 + 128 * kAdFusedColumns);
   }
 }
 
@@ -1286,11 +1443,18 @@ template <int TM>
 static void launch_expand(const AdArgs& a, hipStream_t s) {
   const int busy = std::max((a.b + TM - 1) / TM, std::min(a.b, a.count));
   const int cols = (a.m + 511) / 512;
-  const int nc = std::max(1, std::min(cols, cols * busy / 512));
+  const int nc = std::max(1, std::min(cols, cols * busy / 256));
   const dim3 grid(a.tiles, (cols + nc - 1) / nc);
   const size_t lds = (size_t)(4 * 128 * 32 + TM * (2 * std::min(a.rp, kAdChunk) + 8)) * 2;
   if (a.r >= 8) hipLaunchKernelGGL((k_ad_expand<TM, false>), grid, dim3(256), lds, s, a, nc);
   else hipLaunchKernelGGL((k_ad_expand<TM, true>), grid, dim3(256), lds, s, a, nc);
+}
+
+// One launch: up to 64 rows, and a Vt_l that a block reads in the time a launch
+// takes (at most 256 KB with its ranks rounded up to 16).
+static bool ad_fused(const hss_adapters* A, int b) {
+  const int nr = (A->r + 15) / 16;
+  return b <= kAdSmall && A->r >= 8 && nr <= 2 && A->n >= 8 && nr * (int64_t)A->n <= 8192;
 }
 
 hss_status launch_adapters_apply(const hss_adapters* A, int b, const void* X, const int32_t* ids, const void* base,
@@ -1298,7 +1462,12 @@ hss_status launch_adapters_apply(const hss_adapters* A, int b, const void* X, co
   const AdPlan p = ad_plan(A, b, false);
   AdArgs a = ad_args(A, b, p, X, ids, base, Y, ws);
   a.first = nullptr;
-  if (p.tm == 16) launch_rank<16>(a, p.nr, s), launch_expand<16>(a, s);
+  if (ad_fused(A, b)) {
+    const int cols = (a.m + 511) / 512, nc = std::max(1, std::min(cols, cols * a.tiles / 256));
+    const dim3 grid(a.tiles, (cols + nc - 1) / nc), block(64 * kAdFusedWaves);
+    if (a.r <= 16) hipLaunchKernelGGL(k_ad_fused<1>, grid, block, 0, s, a, nc);
+    else hipLaunchKernelGGL(k_ad_fused<2>, grid, block, 0, s, a, nc);
+  } else if (p.tm == 16) launch_rank<16>(a, p.nr, s), launch_expand<16>(a, s);
   else launch_rank<32>(a, p.nr, s), launch_expand<32>(a, s);
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
