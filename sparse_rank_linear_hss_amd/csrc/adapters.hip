@@ -32,6 +32,7 @@ static constexpr int kAdSmall = 64;     // batches up to here: tiles found by on
 static constexpr int kAdUnit = 64;      // columns of K that a wave takes at a time: a cache line of each row
 static constexpr int kAdBlocks = 512;   // blocks of k_ad_rank that K is split for
 static constexpr int kAdChunk = 256;    // ranks of T that k_ad_expand keeps in LDS
+static constexpr int kAdWhole = 16;     // units of K that the backward pass does not split
 
 struct AdArgs {
   const uint16_t* U;
@@ -59,6 +60,7 @@ struct AdArgs {
   int blocks_u, blocks_v;            // of k_ad_back
   int cols_y, cols_u, cols_v;        // column blocks of dX, dU, dVt
   int chunks;                        // passes of dU and dVt over the ranks
+  int direct;                        // K is not split: k_ad_rank makes the terms (backward)
 };
 
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
@@ -505,8 +507,30 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
     f32x4 v = sum[c * 64 + lane];
 #pragma unroll
     for (int k = 1; k < 4; ++k) v += sum[(k * MF * NR + c) * 64 + lane];
-    const int rank = rank0 + 16 * g + 4 * q;  // .. rank + 3 of row 16 f + i
-    if (16 * f + i < at.rows && rank < a.rg) *reinterpret_cast<f32x4*>(out + (16 * f + i) * a.rg + rank) = v;
+    const int rank = rank0 + 16 * g + 4 * q, slot = 16 * f + i;  // ranks .. rank + 3 of a slot
+    if (rank >= a.rg) continue;
+    if (!a.direct) {
+      if (slot < at.rows) *reinterpret_cast<f32x4*>(out + slot * a.rg + rank) = v;
+      continue;
+    }
+    // K was not split: the terms at once, as k_ad_terms writes them
+    const float scale = a.scale ? a.scale[at.adapter] : 1.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = slot < at.rows && rank + e < a.r ? v[e] * scale : 0.f;
+    float x[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int h = 0; h < 3; ++h) {
+      const uint32_t lo = ad_term2(x[0], x[1]), hi = ad_term2(x[2], x[3]);
+      if (a.t3[side]) {
+        uint16_t* to = a.t3[side] + ((((int64_t)tile * (a.rg >> 4) + (rank >> 4)) * 3 + h) * 64 + 2 * (slot & ~7) + 4 * q) * 8 + (slot & 7);
+        to[0] = (uint16_t)lo, to[8] = (uint16_t)(lo >> 16), to[16] = (uint16_t)hi, to[24] = (uint16_t)(hi >> 16);
+      }
+      if (a.t2 && side && h < 2) {
+        uint16_t* to = a.t2 + ((((int64_t)tile * (a.rp >> 5) + (rank >> 5)) * 4 + 2 * h + f) * 64 + 16 * ((rank >> 3) & 3) + i) * 8 + (rank & 7);
+        *reinterpret_cast<mx_u32x2*>(to) = mx_u32x2{lo, hi};
+        if (rank + 16 >= a.rg && a.rg < a.rp) *reinterpret_cast<mx_u32x2*>(to + 2 * 16 * 8) = mx_u32x2{0u, 0u};  // ranks + 16
+      }
+    }
   }
 }
 
@@ -556,44 +580,59 @@ __global__ __launch_bounds__(256) void k_ad_terms(AdArgs a) {
 // ---------------------------------------------------------------------------
 // Outputs in bf16
 // ---------------------------------------------------------------------------
-// Eight values in bf16: old + v, at a byte offset.
-__device__ __forceinline__ void ad_store8(void* base, uint32_t at, const u32x4& old, const float* v) {
-  Bytes16 o;
+// Eight columns of 4 MF rows of base, from byte offsets `at` + 2 c0 on.  Where a row
+// ends before them (`back` columns too many), its last eight, which ad_store8_end
+// shifts; rows of fewer than eight one by one.
+template <int MF>
+__device__ __forceinline__ void ad_load_base(u32x4 (&old)[MF][4], const void* base, const uint32_t (&at)[MF][4], int c0,
+                                             int back, int cols) {
+  if (!base) return;
+  if (cols >= 8) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) o.w[k] = ad_pack(v[2 * k] + bf16lo(old[k]), v[2 * k + 1] + bf16hi(old[k]));
-  *reinterpret_cast<Bytes16*>(static_cast<char*>(base) + at) = o;
+    for (int g = 0; g < MF; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) old[g][e] = ad_load(base, at[g][e] + 2u * (c0 - back));
+    return;
+  }
+#pragma unroll 1
+  for (int k = 0; k < 8 - back; ++k)
+#pragma unroll
+    for (int g = 0; g < MF; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint16_t raw = *reinterpret_cast<const uint16_t*>(static_cast<const char*>(base) + at[g][e] + 2 * (c0 + k));
+        const uint32_t x = (uint32_t)raw << 16 * (k & 1);
+        u32x4& v = old[g][e];
+        v.x |= k >> 1 == 0 ? x : 0u, v.y |= k >> 1 == 1 ? x : 0u, v.z |= k >> 1 == 2 ? x : 0u, v.w |= k >> 1 == 3 ? x : 0u;
+      }
 }
 
-// 16 rows of a wave's 128 columns where the rows of the output end: through the wave's
-// 8 KB of LDS, a lane every 64th element, all rows' base in flight.  D: rows 4 q + e,
-// columns 8 i + f; row: this lane % 16's row of the output.
-__device__ __forceinline__ void ad_store_end(const AdArgs& a, int row, int live, int c0, int cols, const f32x4 (&acc)[8],
-                                             float* stage) {
-  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4, width = min(128, cols - c0);
-  if (live <= 0) return;
-  uint32_t old[16][2];
+__device__ __forceinline__ u32x4 ad_sum8(const u32x4& old, const float* v) {
+  u32x4 o;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const uint16_t* in = a.base + (int64_t)__builtin_amdgcn_readlane(row, k) * cols + c0;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) old[k][c] = a.base ? in[min(64 * c + lane, width - 1)] : 0u;
-  }
-  ad_wave_sync();
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-#pragma unroll
-    for (int f = 0; f < 8; ++f) stage[(4 * q + e) * 128 + 8 * i + f] = acc[f][e];
-  ad_wave_sync();
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    if (k >= live) break;
-    uint16_t* out = a.Y + (int64_t)__builtin_amdgcn_readlane(row, k) * cols + c0;
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-      if (64 * c + lane < width)
-        out[64 * c + lane] = f32_to_bf16(__uint_as_float(old[k][c] << 16) + stage[k * 128 + 64 * c + lane]);
-  }
-  ad_wave_sync();
+  for (int k = 0; k < 4; ++k) o[k] = ad_pack(v[2 * k] + bf16lo(old[k]), v[2 * k + 1] + bf16hi(old[k]));
+  return o;
+}
+
+// Eight values in bf16, old + v, at a byte offset of the output.
+__device__ __forceinline__ void ad_store8(void* base, uint32_t at, const u32x4& old, const float* v) {
+  const u32x4 o = ad_sum8(old, v);
+  *reinterpret_cast<Bytes16*>(static_cast<char*>(base) + at) = Bytes16{{o.x, o.y, o.z, o.w}};
+}
+
+// The same where the row ends after 8 - back of them: by fours, twos and ones.
+__device__ __forceinline__ void ad_store8_end(void* base, uint32_t at, u32x4 old, const float* v, int back, int cols) {
+  struct __attribute__((packed, aligned(2))) Two { uint32_t w[1]; };
+  struct __attribute__((packed, aligned(2))) Four { uint32_t w[2]; };
+  if (cols >= 8) old = ad_drop(old, back);
+  u32x4 o = ad_sum8(old, v);
+  char* to = static_cast<char*>(base) + at;
+  const int left = 8 - back;
+  if (left >= 8) *reinterpret_cast<Bytes16*>(to) = Bytes16{{o.x, o.y, o.z, o.w}};
+  if (left <= 0 || left >= 8) return;
+  if (left & 4) *reinterpret_cast<Four*>(to) = Four{{o.x, o.y}}, to += 8, o = u32x4{o.z, o.w, 0u, 0u};
+  if (left & 2) *reinterpret_cast<Two*>(to) = Two{{o.x}}, to += 4, o.x = o.y;
+  if (left & 1) *reinterpret_cast<uint16_t*>(to) = (uint16_t)o.x;
 }
 
 // Rows without an adapter: the output is base (nothing to do in place).  Eight
@@ -759,14 +798,6 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
     }
   };
   u32x4 old[MF][4];
-  auto load_base = [&](int c0) {
-    if (c0 + 128 <= a.m && a.base) {
-#pragma unroll
-      for (int g = 0; g < MF; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) old[g][e] = ad_load(a.base, out[g][e] + 2u * c0);
-    }
-  };
 #pragma unroll
   for (int g = 0; g < MF; ++g)
 #pragma unroll
@@ -774,7 +805,8 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
   // the first columns' U and base are on their way while the terms are made, the
   // next ones' while a column block is multiplied
   load(cb + 128 * w, 0);
-  load_base(cb + 128 * w);
+  auto back = [&](int c0) { return max(0, c0 + 8 * i + 8 - a.m); };  // columns past the end of a row
+  if (cb + 128 * w < a.m) ad_load_base<MF>(old, a.base, out, cb + 128 * w, back(cb + 128 * w), a.m);
   if (one) {
     fill(0);
     __syncthreads();
@@ -813,22 +845,20 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
         ad_wave_sync();
       }
     }
-    if (c0 + 128 <= a.m) {
+    if (c0 >= a.m) continue;
+    const bool full = c0 + 128 <= a.m;
 #pragma unroll
-      for (int g = 0; g < MF; ++g)
+    for (int g = 0; g < MF; ++g)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v[8];
+      for (int e = 0; e < 4; ++e) {
+        float v[8];
 #pragma unroll
-          for (int f = 0; f < 8; ++f) v[f] = acc[g][f][e];
-          if (16 * g + 4 * q + e < at.rows) ad_store8(a.Y, out[g][e] + 2u * c0, old[g][e], v);
-        }
-      if (c0 + 512 < stop) load_base(c0 + 512);
-    } else if (c0 < a.m) {
-#pragma unroll
-      for (int g = 0; g < MF; ++g)
-        ad_store_end(a, rows[16 * g + i], min(16, at.rows - 16 * g), c0, a.m, acc[g], reinterpret_cast<float*>(us));
-    }
+        for (int f = 0; f < 8; ++f) v[f] = acc[g][f][e];
+        if (16 * g + 4 * q + e >= at.rows) continue;
+        if (full) ad_store8(a.Y, out[g][e] + 2u * c0, old[g][e], v);
+        else ad_store8_end(a.Y, out[g][e] + 2u * c0, old[g][e], v, back(c0), a.m);
+      }
+    if (c0 + 512 < min(stop, a.m)) ad_load_base<MF>(old, a.base, out, c0 + 512, back(c0 + 512), a.m);
   }
 }
 
@@ -917,18 +947,16 @@ __global__ __launch_bounds__(64 * kAdFusedWaves) void k_ad_fused(AdArgs a, int n
   // the columns' U and base are on their way while the waves' sums meet
   const uint16_t* U = a.U + (int64_t)adapter * a.m * a.r;
   const int stop = min(cb + 512 * nc, a.m);
-  uint32_t out[4];
+  uint32_t out[1][4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) out[e] = 2u * (rows[min(4 * q + e, live - 1)] * a.m + 8 * i);
-  u32x4 u[8], old[4];
+  for (int e = 0; e < 4; ++e) out[0][e] = 2u * (rows[min(4 * q + e, live - 1)] * a.m + 8 * i);
+  u32x4 u[8], old[1][4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) old[e] = u32x4{0u, 0u, 0u, 0u};
+  for (int e = 0; e < 4; ++e) old[0][e] = u32x4{0u, 0u, 0u, 0u};
+  auto back = [&](int c0) { return max(0, c0 + 8 * i + 8 - a.m); };  // columns past the end of a row
   auto load = [&](int c0) {
     ad_load_u(u, U, a.m, a.r, c0, 0);
-    if (c0 + 128 <= a.m && a.base) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) old[e] = ad_load(a.base, out[e] + 2u * c0);
-    }
+    ad_load_base<1>(old, a.base, out, c0, back(c0), a.m);
   };
   const int first = cb + 128 * w;
   if (first < stop && w < kAdFusedColumns) load(first);
@@ -970,16 +998,15 @@ __global__ __launch_bounds__(64 * kAdFusedWaves) void k_ad_fused(AdArgs a, int n
       for (int h = 0; h < 2; ++h) y[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t[h]), as_bf16(uf), y[f], 0, 0, 0);
     }
     ad_wave_sync();
-    if (c0 + 128 <= a.m) {
+    const bool full = c0 + 128 <= a.m;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float v[8];
+    for (int e = 0; e < 4; ++e) {
+      float v[8];
 #pragma unroll
-        for (int f = 0; f < 8; ++f) v[f] = y[f][e];
-        if (4 * q + e < live) ad_store8(a.Y, out[e] + 2u * c0, old[e], v);
-      }
-    } else {
-      ad_store_end(a, rows[min(i, live - 1)], live, c0, a.m, y, reinterpret_cast<float*>(us));
+      for (int f = 0; f < 8; ++f) v[f] = y[f][e];
+      if (4 * q + e >= live) continue;
+      if (full) ad_store8(a.Y, out[0][e] + 2u * c0, old[0][e], v);
+      else ad_store8_end(a.Y, out[0][e] + 2u * c0, old[0][e], v, back(c0), a.m);
     }
     if (c0 + 128 * kAdFusedColumns < stop) load(c0 + 128 * kAdFusedColumns);
   }
@@ -990,7 +1017,7 @@ __global__ __launch_bounds__(64 * kAdFusedWaves) void k_ad_fused(AdArgs a, int n
 // ---------------------------------------------------------------------------
 // dX = base + scale P Vt: as k_ad_expand, with Vt's 8 x 8 pieces transposed in
 // registers: a lane's eight ranks and eight columns are eight operands.
-__device__ __forceinline__ void ad_dx(const AdArgs& a, int block, char* smem) {
+__device__ __forceinline__ void ad_dx(const AdArgs& a, int block) {
   constexpr int MF = 2;
   const int tile = block / a.cols_y, cb = block % a.cols_y * 512;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
@@ -1017,18 +1044,14 @@ __device__ __forceinline__ void ad_dx(const AdArgs& a, int block, char* smem) {
   for (int g = 0; g < MF; ++g)
 #pragma unroll
     for (int e = 0; e < 4; ++e) old[g][e] = u32x4{0u, 0u, 0u, 0u};
-  if (full && a.base) {
-#pragma unroll
-    for (int g = 0; g < MF; ++g)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) old[g][e] = ad_load(a.base, out[g][e] + 2u * c0);
-  }
+  const int back = max(0, col + 8 - a.n);  // columns past the end of a row
+  ad_load_base<MF>(old, a.base, out, c0, back, a.n);
   f32x4 acc[MF][8];
 #pragma unroll
   for (int g = 0; g < MF; ++g)
 #pragma unroll
     for (int f = 0; f < 8; ++f) acc[g][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int from = min(col, a.n - 8);  // (columns past the end: not stored)
+  const int from = col - back;
   for (int s = 0; s < a.rp; s += 32) {
     // past the ranks: the last one again, times the zeros that the terms hold there
     AdPiece<8> v[8];
@@ -1060,21 +1083,60 @@ __device__ __forceinline__ void ad_dx(const AdArgs& a, int block, char* smem) {
           acc[g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t[h][g]), u, acc[g][f], 0, 0, 0);
     }
   }
-  if (full) {
 #pragma unroll
-    for (int g = 0; g < MF; ++g)
+  for (int g = 0; g < MF; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float v[8];
+#pragma unroll
+      for (int f = 0; f < 8; ++f) v[f] = acc[g][f][e];
+      if (16 * g + 4 * q + e >= at.rows) continue;
+      if (full) ad_store8(a.Y, out[g][e] + 2u * c0, old[g][e], v);
+      else ad_store8_end(a.Y, out[g][e] + 2u * c0, old[g][e], v, back, a.n);
+    }
+}
+
+// A wave's part of dU_l (m x r) or dVt_l (r x n): D[rank][column], a lane has ranks
+// 4 q .. 4 q + 3 of columns CW i + f.  Four ranks of a row of dU, or CW columns of
+// a row of dVt, are one store.
+template <int NR, int CW, bool DV>
+__device__ __forceinline__ void ad_store_factor(const AdArgs& a, int l, int rank0, int c0, const f32x4 (&acc)[CW][NR]) {
+  typedef float Packed __attribute__((ext_vector_type(DV ? CW : 4), aligned(4)));
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4, cols = DV ? a.n : a.m, col0 = c0 + CW * i;
+  float* out = (DV ? a.dVt : a.dU) + (int64_t)l * a.r * cols;
+#pragma unroll
+  for (int g = 0; g < NR; ++g) {
+    const int rank = rank0 + 16 * g + 4 * q;
+    if constexpr (DV) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float v[8];
+        if (rank + e >= a.r) break;
+        float* at = out + (int64_t)(rank + e) * cols + col0;
+        if (col0 + CW <= cols) {
+          Packed v;
 #pragma unroll
-        for (int f = 0; f < 8; ++f) v[f] = acc[g][f][e];
-        if (16 * g + 4 * q + e < at.rows) ad_store8(a.Y, out[g][e] + 2u * c0, old[g][e], v);
+          for (int f = 0; f < CW; ++f) v[f] = acc[f][g][e];
+          *reinterpret_cast<Packed*>(at) = v;
+        } else {
+#pragma unroll
+          for (int f = 0; f < CW; ++f)
+            if (col0 + f < cols) at[f] = acc[f][g][e];
+        }
       }
-  } else {
+    } else {
 #pragma unroll
-    for (int g = 0; g < MF; ++g)
-      ad_store_end(a, rows[16 * g + i], min(16, at.rows - 16 * g), c0, a.n, acc[g],
-                   reinterpret_cast<float*>(smem) + w * 16 * 128);
+      for (int f = 0; f < CW; ++f) {
+        if (col0 + f >= cols) break;
+        float* at = out + (int64_t)(col0 + f) * a.r + rank;
+        if (rank + 4 <= a.r) {
+          *reinterpret_cast<Packed*>(at) = acc[f][g];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (rank + e < a.r) at[e] = acc[f][g][e];
+        }
+      }
+    }
   }
 }
 
@@ -1162,8 +1224,7 @@ __device__ __forceinline__ void ad_dfactor(const AdArgs& a, int block, char* sme
         const bf16x8 x = as_bf16(ad_column<CW>(r.v, f));
 #pragma unroll
         for (int h = 0; h < 3; ++h)
-          acc[f][g] = DV ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t[h]), x, acc[f][g], 0, 0, 0)
-                         : __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, as_bf16(t[h]), acc[f][g], 0, 0, 0);
+          acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t[h]), x, acc[f][g], 0, 0, 0);
       }
     }
   };
@@ -1202,19 +1263,7 @@ __device__ __forceinline__ void ad_dfactor(const AdArgs& a, int block, char* sme
     }
   }
   if (w != 0) return;
-#pragma unroll
-  for (int g = 0; g < NR; ++g)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int f = 0; f < CW; ++f) {
-        // a lane holds rows 4 q + e, column i of D: columns of G (X) are CW apart
-        const int rank = rank0 + 16 * g + (DV ? 4 * q + e : i), col = c0 + CW * (DV ? i : 4 * q + e) + f;
-        if (rank < a.r && col < cols) {
-          if (DV) a.dVt[((int64_t)l * a.r + rank) * a.n + col] = acc[f][g][e];
-          else a.dU[((int64_t)l * a.m + col) * a.r + rank] = acc[f][g][e];
-        }
-      }
+  ad_store_factor<NR, CW, DV>(a, l, rank0, c0, acc);
 }
 
 // The same where there are many columns in all: the block's waves take 64 columns
@@ -1281,8 +1330,7 @@ __device__ __forceinline__ void ad_dfactor_wide(const AdArgs& a, int block, char
         const u32x4 y = buf[(s & 1) * kTerms + (3 * g + h) * 64 + lane];
 #pragma unroll
         for (int f = 0; f < CW; ++f)
-          acc[f][g] = DV ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(y), as_bf16(x[f]), acc[f][g], 0, 0, 0)
-                         : __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(x[f]), as_bf16(y), acc[f][g], 0, 0, 0);
+          acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(y), as_bf16(x[f]), acc[f][g], 0, 0, 0);
       }
   };
   if (steps > 0) {
@@ -1302,18 +1350,7 @@ __device__ __forceinline__ void ad_dfactor_wide(const AdArgs& a, int block, char
       __syncthreads();
     }
   }
-#pragma unroll
-  for (int g = 0; g < NR; ++g)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int f = 0; f < CW; ++f) {
-        const int rank = rank0 + 16 * g + (DV ? 4 * q + e : i), col = c0 + CW * (DV ? i : 4 * q + e) + f;
-        if (rank < a.r && col < cols) {
-          if (DV) a.dVt[((int64_t)l * a.r + rank) * a.n + col] = acc[f][g][e];
-          else a.dU[((int64_t)l * a.m + col) * a.r + rank] = acc[f][g][e];
-        }
-      }
+  ad_store_factor<NR, CW, DV>(a, l, rank0, c0, acc);
 }
 
 __global__ __launch_bounds__(256, 2) void k_ad_back_wide(AdArgs a) {
@@ -1328,7 +1365,7 @@ __global__ __launch_bounds__(256, 2) void k_ad_back_wide(AdArgs a) {
     ad_dfactor_wide<true>(a, block, smem);
     return;
   }
-  ad_dx(a, block - a.blocks_v, smem);
+  ad_dx(a, block - a.blocks_v);
 }
 
 template <int NR, int CW>
@@ -1344,14 +1381,14 @@ __global__ __launch_bounds__(256, 2) void k_ad_back(AdArgs a) {
     ad_dfactor<NR, CW, true>(a, block, smem);
     return;
   }
-  ad_dx(a, block - a.blocks_v, smem);
+  ad_dx(a, block - a.blocks_v);
 }
 
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
 struct AdPlan {
-  int tm, nr, tiles, slots, rp, rg, splits[2], units[2];
+  int tm, nr, tiles, slots, rp, rg, splits[2], units[2], direct;
   size_t part[2], t2, t3[2], info, rows, first, total;  // offsets in the workspace
 };
 
@@ -1376,7 +1413,11 @@ static AdPlan ad_plan(const hss_adapters* A, int b, bool grad) {
   const int busy = std::max((b + p.tm - 1) / p.tm, std::min(b, A->count)) * groups;
   // the same share of K for each block, whatever side it is on
   const int64_t all = (int64_t)busy * ((A->n + kAdUnit - 1) / kAdUnit + (grad ? (A->m + kAdUnit - 1) / kAdUnit : 0));
-  const int per = (int)std::max<int64_t>(4, (all + kAdBlocks - 1) / kAdBlocks);
+  int per = (int)std::max<int64_t>(4, (all + kAdBlocks - 1) / kAdBlocks);
+  // Short rows of a few tiles are not split: a launch (k_ad_terms) less.
+  const int longest = (std::max(A->m, A->n) + kAdUnit - 1) / kAdUnit;
+  if (grad && longest <= kAdWhole) per = std::max(per, longest);
+  p.direct = grad && per >= longest;
   ad_split(A->n, per, &p.splits[0], &p.units[0]);
   ad_split(A->m, per, &p.splits[1], &p.units[1]);
   size_t off = 0;
@@ -1474,7 +1515,7 @@ hss_status launch_adapters_apply(const hss_adapters* A, int b, const void* X, co
 
 template <int NR, int CW>
 static void launch_back(AdArgs a, hipStream_t s) {
-  const size_t lds = std::max<size_t>((size_t)CW * NR * 64 * 16, a.Y && a.n % 128 ? 4 * 16 * 128 * 4 : 0);
+  const size_t lds = (size_t)CW * NR * 64 * 16;
   a.chunks = (a.rg + 16 * NR - 1) / (16 * NR);
   a.cols_u = (a.m + 16 * CW - 1) / (16 * CW), a.cols_v = (a.n + 16 * CW - 1) / (16 * CW);
   a.cols_y = (a.n + 511) / 512;
@@ -1496,9 +1537,12 @@ hss_status launch_adapters_grad(const hss_adapters* A, int b, const void* X, con
   a.t3[1] = dVt ? reinterpret_cast<uint16_t*>(at + p.t3[1]) : nullptr;
   if (!dU) a.splits[0] = 0;
   if (dX || dVt) a.splits[1] = p.splits[1], a.units[1] = p.units[1];
+  a.direct = p.direct;
   launch_rank<32>(a, p.nr, s);
-  const dim3 grid(a.tiles, (a.rp + 63) / 64, a.splits[0] && a.splits[1] ? 2 : 1);
-  hipLaunchKernelGGL(k_ad_terms, grid, dim3(256), 0, s, a);
+  if (!a.direct) {
+    const dim3 grid(a.tiles, (a.rp + 63) / 64, a.splits[0] && a.splits[1] ? 2 : 1);
+    hipLaunchKernelGGL(k_ad_terms, grid, dim3(256), 0, s, a);
+  }
   // Blocks of 256 columns that share the terms, where they fill the chip; else
   // waves share the rows of fewer columns.
   const int64_t wide = (int64_t)A->count * ((A->r + 63) / 64) * (((int64_t)A->m + 255) / 256 + (A->n + 255) / 256);
@@ -1509,7 +1553,7 @@ hss_status launch_adapters_grad(const hss_adapters* A, int b, const void* X, con
     a.blocks_u = dU ? a.cols_u * a.chunks * a.count : 0;
     a.blocks_v = dVt ? a.cols_v * a.chunks * a.count : 0;
     const dim3 blocks(a.blocks_u + a.blocks_v + (dX ? a.cols_y * a.tiles : 0));
-    hipLaunchKernelGGL(k_ad_back_wide, blocks, dim3(256), 32768, s, a);
+    hipLaunchKernelGGL(k_ad_back_wide, blocks, dim3(256), 2 * 4 * 3 * 64 * 16, s, a);
   } else if (p.nr == 1) {
     narrow ? launch_back<1, 2>(a, s) : launch_back<1, 8>(a, s);
   } else if (p.nr == 2) {
