@@ -378,16 +378,17 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
     auto multiply = [&]() {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        u32x4 xf[MF];
+        u32x4 xf[MF], vf[NR];
 #pragma unroll
         for (int f = 0; f < MF; ++f) xf[f] = *reinterpret_cast<const u32x4*>(xs + ad_slot(16 * f + i, 4 * h + q));
 #pragma unroll
-        for (int g = 0; g < NR; ++g) {
-          const u32x4 vf = *reinterpret_cast<const u32x4*>(vs + ad_slot(16 * g + i, 4 * h + q));
+        for (int g = 0; g < NR; ++g) vf[g] = *reinterpret_cast<const u32x4*>(vs + ad_slot(16 * g + i, 4 * h + q));
+        __builtin_amdgcn_sched_barrier(0);  // the reads first: one wait instead of one for each product
+#pragma unroll
+        for (int g = 0; g < NR; ++g)
 #pragma unroll
           for (int f = 0; f < MF; ++f)
-            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf), as_bf16(xf[f]), acc[f][g], 0, 0, 0);
-        }
+            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf[g]), as_bf16(xf[f]), acc[f][g], 0, 0, 0);
       }
       ad_wave_sync();
     };
@@ -447,16 +448,17 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
     auto multiply = [&]() {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        u32x4 xf[MF];
+        u32x4 xf[MF], vf[NR];
 #pragma unroll
         for (int f = 0; f < MF; ++f) xf[f] = *reinterpret_cast<const u32x4*>(xs + ad_slot(16 * f + i, 4 * h + q));
 #pragma unroll
-        for (int g = 0; g < NR; ++g) {
-          const u32x4 vf = *reinterpret_cast<const u32x4*>(vs + ad_slot(16 * g + i, 4 * h + q));
+        for (int g = 0; g < NR; ++g) vf[g] = *reinterpret_cast<const u32x4*>(vs + ad_slot(16 * g + i, 4 * h + q));
+        __builtin_amdgcn_sched_barrier(0);  // the reads first: one wait instead of one for each product
+#pragma unroll
+        for (int g = 0; g < NR; ++g)
 #pragma unroll
           for (int f = 0; f < MF; ++f)
-            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf), as_bf16(xf[f]), acc[f][g], 0, 0, 0);
-        }
+            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf[g]), as_bf16(xf[f]), acc[f][g], 0, 0, 0);
       }
       ad_wave_sync();
     };
@@ -834,13 +836,18 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
 #pragma unroll
           for (int h = 0; h < 2; ++h) t[h][g] = *reinterpret_cast<const u32x4*>(trow[g] + h * wide + s);
 #pragma unroll
-        for (int f = 0; f < 8; ++f) {
-          const u32x4 uf = *reinterpret_cast<const u32x4*>(us + ad_place(i, f, q));
+        for (int f0 = 0; f0 < 8; f0 += 4) {
+          u32x4 uf[4];
 #pragma unroll
-          for (int g = 0; g < MF; ++g)
+          for (int f = 0; f < 4; ++f) uf[f] = *reinterpret_cast<const u32x4*>(us + ad_place(i, f0 + f, q));
+          __builtin_amdgcn_sched_barrier(0);  // four reads, then their products
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              acc[g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t[h][g]), as_bf16(uf), acc[g][f], 0, 0, 0);
+          for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int g = 0; g < MF; ++g)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                acc[g][f0 + f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t[h][g]), as_bf16(uf[f]), acc[g][f0 + f], 0, 0, 0);
         }
         ad_wave_sync();
       }
@@ -920,13 +927,14 @@ __global__ __launch_bounds__(64 * kAdFusedWaves) void k_ad_fused(AdArgs a, int n
     ad_wave_sync();
   };
   for (int u0 = w; u0 < units; u0 += UN * kAdFusedWaves) {
-    u32x4 x[UN][XL], v[UN][VL];
+    u32x4 x[UN][XL] = {}, v[UN][VL];  // (rows that the tile lacks: zeros)
 #pragma unroll
     for (int p = 0; p < UN; ++p) {
       const int u = u0 + p * kAdFusedWaves;
       if (u < whole) {
 #pragma unroll
-        for (int j = 0; j < XL; ++j) x[p][j] = ad_load(a.X, 2u * (xrow[j] + u * kAdUnit + 8 * c8));
+        for (int j = 0; j < XL; ++j)
+          if (8 * j + r8 < live) x[p][j] = ad_load(a.X, 2u * (xrow[j] + u * kAdUnit + 8 * c8));
 #pragma unroll
         for (int j = 0; j < VL; ++j) v[p][j] = ad_load(V, 2u * (vrow[j] + u * kAdUnit + 8 * c8));
       }
@@ -968,8 +976,12 @@ __global__ __launch_bounds__(64 * kAdFusedWaves) void k_ad_fused(AdArgs a, int n
   if (w < 2) {  // wave g: ranks 16 g + 4 q .. + 3 of row i, as terms; zeros past r
     f32x4 t = {0.f, 0.f, 0.f, 0.f};
     if (w < NR) {
+      f32x4 part[kAdFusedWaves];
 #pragma unroll
-      for (int k = 0; k < kAdFusedWaves; ++k) t += sum[(k * NR + w) * 64 + lane];
+      for (int k = 0; k < kAdFusedWaves; ++k) part[k] = sum[(k * NR + w) * 64 + lane];
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < kAdFusedWaves; ++k) t += part[k];
     }
     const int rank = 16 * w + 4 * q;
     float x[4];
@@ -990,12 +1002,15 @@ __global__ __launch_bounds__(64 * kAdFusedWaves) void k_ad_fused(AdArgs a, int n
   for (int c0 = first; c0 < stop && w < kAdFusedColumns; c0 += 128 * kAdFusedColumns) {
     ad_put_u(u, us, a.r, 0);
     f32x4 y[8];
+    u32x4 uf[8];
+#pragma unroll
+    for (int f = 0; f < 8; ++f) uf[f] = *reinterpret_cast<const u32x4*>(us + ad_place(i, f, q));
+    __builtin_amdgcn_sched_barrier(0);  // all reads, then the products: one wait instead of eight
 #pragma unroll
     for (int f = 0; f < 8; ++f) {
-      const u32x4 uf = *reinterpret_cast<const u32x4*>(us + ad_place(i, f, q));
       y[f] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) y[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t[h]), as_bf16(uf), y[f], 0, 0, 0);
+      for (int h = 0; h < 2; ++h) y[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(t[h]), as_bf16(uf[f]), y[f], 0, 0, 0);
     }
     ad_wave_sync();
     const bool full = c0 + 128 <= a.m;
