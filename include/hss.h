@@ -741,11 +741,13 @@ hss_status hss_adapters_grad(const hss_adapters* L, int32_t b, const void* X, co
  * 0 an element whose v is 0 becomes NaN.
  * The same call gives the same bits every time.  Nothing is copied to the
  * device but kernel arguments, so the call may be captured into a HIP graph.
- * `tensors` is a HOST array; arrays are aligned to their element.  The tensors
- * must be distinct: an array of one must not overlap an array of another (not
- * checked).
- * HSS_ERR_INVALID_ARG: null config, tensors (with count > 0) or arrays (of a
- *   tensor with elements), count < 0, a tensor's count < 0 or >= 2^31, all of
+ * `tensors` and `grads` are HOST arrays of `count` entries: what stays from step
+ * to step, and each tensor's gradient (grad_dtype[tensor's count], device; NULL =
+ * the tensor is left as it is, and its elements are not counted by i).  Arrays
+ * are aligned to their element.  The tensors must be distinct: an array of one
+ * must not overlap an array of another (not checked).
+ * HSS_ERR_INVALID_ARG: null config, tensors or grads (with count > 0) or arrays
+ *   (of a tensor with elements and a gradient), count < 0, a tensor's count < 0 or >= 2^31, all of
  *   them 2^39 elements or more, unknown bits or types, master with fp32 parameters,
  *   misaligned arrays, arrays of one tensor that overlap, beta1 or beta2 outside
  *   [0, 1), eps < 0, a number that is not finite, step outside [1, 2^31).
@@ -755,7 +757,6 @@ typedef struct hss_adamw_tensor {
   int64_t count; /* elements; 0 = skipped */
   void* param;
   float* master; /* NULL = none */
-  const void* grad;
   void* m;
   void* v;
   float* m_scale; /* bits = 8 only (else ignored) */
@@ -774,8 +775,8 @@ typedef struct hss_adamw_config {
   const float* grad_scale_dev;
 } hss_adamw_config;
 
-hss_status hss_adamw(const hss_adamw_config* config, const hss_adamw_tensor* tensors, int32_t count,
-                     hipStream_t stream);
+hss_status hss_adamw(const hss_adamw_config* config, const hss_adamw_tensor* tensors, const void* const* grads,
+                     int32_t count, hipStream_t stream);
 
 #ifdef __cplusplus
 }

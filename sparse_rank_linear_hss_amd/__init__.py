@@ -1116,10 +1116,12 @@ class AdamWState:
         self.counts = counts
         self._tensors = (HssAdamwTensorStruct * len(params))()
         for k, t in enumerate(self._tensors):
-            t.param, t.m, t.v = _ptr(params[k]), _ptr(self.m[k]), _ptr(self.v[k])
+            t.count, t.param, t.m, t.v = counts[k], _ptr(params[k]), _ptr(self.m[k]), _ptr(self.v[k])
             t.master = _ptr(master[k]) if master is not None else None
             t.m_scale, t.v_scale = (_ptr(self.m_scale[k]), _ptr(self.v_scale[k])) if bits == 8 else (None, None)
         self._config = HssAdamwConfigStruct(bits=bits, dtype=code)
+        self._ref = ctypes.byref(self._config)
+        self._grads = ctypes.c_void_p * len(params)
 
 
 def _device_scalar(name, t, dtype, index):
@@ -1148,19 +1150,15 @@ def hss_adamw(state: AdamWState, grads, lr, step, betas=(0.9, 0.999), eps=1e-8, 
     if index != _current_device():
         with torch.cuda.device(index):
             return hss_adamw(state, grads, lr, step, betas, eps, weight_decay, grad_scale)
-    grads = list(grads)
-    if len(grads) != len(state.counts):
-        raise ValueError(f"{len(state.counts)} parameters, {len(grads)} gradients")
+    grads, counts = list(grads), state.counts
+    if len(grads) != len(counts):
+        raise ValueError(f"{len(counts)} parameters, {len(grads)} gradients")
     dtype = next((g.dtype for g in grads if g is not None), torch.float32)
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype}: float32 or bfloat16")
-    for t, g, k in zip(state._tensors, grads, state.counts):
-        if g is None:
-            t.count = 0
-            continue
-        if g.dtype != dtype or g.numel() != k or not g.is_contiguous() or g.get_device() != index:
+    for g, k in zip(grads, counts):
+        if g is not None and (g.numel() != k or g.dtype is not dtype or g.get_device() != index or not g.is_contiguous()):
             raise ValueError("grads: contiguous tensors of one dtype, of their parameters' element counts and device")
-        t.count, t.grad = k, g.data_ptr()
     c = state._config
     c.grad_dtype = _DT[dtype]
     c.beta1, c.beta2, c.eps, c.weight_decay = betas[0], betas[1], eps, weight_decay
@@ -1178,6 +1176,7 @@ def hss_adamw(state: AdamWState, grads, lr, step, betas=(0.9, 0.999), eps=1e-8, 
         c.grad_scale_dev = _device_scalar("grad_scale", grad_scale, torch.float32, index)
     else:
         c.grad_scale = grad_scale
-    code = lib.hss_adamw(ctypes.byref(c), state._tensors, len(grads), _raw_stream(index))
+    pointers = state._grads(*[None if g is None else g.data_ptr() for g in grads])
+    code = lib.hss_adamw(state._ref, state._tensors, pointers, len(grads), _raw_stream(index))
     if code:
         check(code, "hss_adamw")

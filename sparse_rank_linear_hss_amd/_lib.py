@@ -61,8 +61,8 @@ class HssAdaptersStruct(ctypes.Structure):
 
 class HssAdamwTensorStruct(ctypes.Structure):
     """Mirror of struct hss_adamw_tensor in include/hss.h."""
-    _fields_ = [("count", c_int64), ("param", c_void_p), ("master", c_void_p), ("grad", c_void_p), ("m", c_void_p),
-                ("v", c_void_p), ("m_scale", c_void_p), ("v_scale", c_void_p)]
+    _fields_ = [("count", c_int64), ("param", c_void_p), ("master", c_void_p), ("m", c_void_p), ("v", c_void_p),
+                ("m_scale", c_void_p), ("v_scale", c_void_p)]
 
 
 class HssAdamwConfigStruct(ctypes.Structure):
@@ -137,7 +137,7 @@ def _load():
         "hss_adapters_grad_workspace_size": (ctypes.c_int, [P(HssAdaptersStruct), c_int32, P(c_size_t)]),
         "hss_adapters_grad": (ctypes.c_int, [P(HssAdaptersStruct), c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
                                              c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
-        "hss_adamw": (ctypes.c_int, [P(HssAdamwConfigStruct), P(HssAdamwTensorStruct), c_int32, c_void_p]),
+        "hss_adamw": (ctypes.c_int, [P(HssAdamwConfigStruct), P(HssAdamwTensorStruct), c_void_p, c_int32, c_void_p]),
         "hss_nm24_to_csr": (ctypes.c_int, [c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
     }
     for name, (res, args) in sig.items():

@@ -31,7 +31,7 @@ namespace hss {
 
 static constexpr int kAwBlock = 256;    // elements that share a scale
 static constexpr int kAwChunk = 8;      // blocks of one tensor that a workgroup takes at a time
-static constexpr int kAwTensors = 48;   // tensors of one launch: 3.5 KB of the 4 KB of kernel arguments
+static constexpr int kAwTensors = 48;   // tensors of one launch: 3.8 KB of the 4 KB of kernel arguments
 
 struct AwTensor {
   void* p;
@@ -57,6 +57,7 @@ struct AwHyper {
 struct AwArgs {
   AwHyper h;
   AwTensor t[kAwTensors];
+  uint32_t first[64];  // the tensors' first chunks, then the largest number: a lane each
   int tensors;
   uint32_t chunks;
 };
@@ -206,10 +207,10 @@ __global__ __launch_bounds__(256) void k_adamw(AwArgs a) {
     h.decay = s[0], h.size = s[1], h.root = s[2], h.gscale = s[3], h.key = __float_as_uint(s[4]);
   }
   const int lane = threadIdx.x & 31;
-  int which = 0;
+  // (walking the table takes a round trip to memory for each tensor)
+  const uint32_t first = a.first[threadIdx.x & 63];
   for (uint32_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
-    while (which + 1 < a.tensors && chunk >= a.t[which + 1].first) ++which;
-    const AwTensor& t = a.t[which];
+    const AwTensor& t = a.t[__popcll(__ballot(first <= chunk)) - 1];
     const uint32_t own = (chunk - t.first) * kAwChunk + (threadIdx.x >> 5);
     const int64_t i = (int64_t)own * kAwBlock + 8 * lane, rest = t.count - i;
     const int left = rest >= 8 ? 8 : rest > 0 ? (int)rest : 0;
@@ -272,7 +273,8 @@ static void launch_aw(int bits, unsigned grid, const AwArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((k_adamw<PT, GT, 8>), dim3(grid), dim3(256), 0, s, a);
 }
 
-hss_status launch_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tensors, int count, hipStream_t s) {
+hss_status launch_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tensors, const void* const* grads, int count,
+                        hipStream_t s) {
   AwArgs a;
   AwHyper& h = a.h;
   h.b1 = (float)c->beta1, h.c1 = (float)(1.0 - c->beta1);
@@ -293,16 +295,17 @@ hss_status launch_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tenso
     bool master = false;
     for (; at < count && a.tensors < kAwTensors; ++at) {
       const hss_adamw_tensor& q = tensors[at];
-      if (q.count == 0) continue;
+      if (q.count == 0 || !grads[at]) continue;
       const bool own = q.master != nullptr;
       if (a.tensors && own != master) break;  // one kernel variant a launch
       const uint32_t blocks = (uint32_t)((q.count + kAwBlock - 1) / kAwBlock);
       master = own;
-      a.t[a.tensors++] = AwTensor{q.param, q.master, q.grad, q.m, q.v, q.m_scale, q.v_scale, q.count, a.chunks, pos};
+      a.t[a.tensors++] = AwTensor{q.param, q.master, grads[at], q.m, q.v, q.m_scale, q.v_scale, q.count, a.chunks, pos};
       a.chunks += (blocks + kAwChunk - 1) / kAwChunk;
       pos += blocks;
     }
-    if (!a.tensors) return HSS_OK;  // only tensors without elements were left
+    for (int k = 0; k < 64; ++k) a.first[k] = k < a.tensors ? a.t[k].first : 0xffffffffu;
+    if (!a.tensors) return HSS_OK;  // only tensors without elements or gradients were left
     const unsigned grid = std::min<uint32_t>(a.chunks, 2048);
     const int pt = c->dtype == HSS_F32 ? 0 : master ? 2 : 1;
     if (c->grad_dtype == HSS_F32) {

@@ -38,7 +38,8 @@ hss_status launch_adapters_apply(const hss_adapters* L, int b, const void* X, co
 hss_status launch_adapters_grad(const hss_adapters* L, int b, const void* X, const void* G, const int32_t* ids,
                                 const void* base, void* dX, float* dU, float* dVt, void* ws, hipStream_t s);
 // adamw.hip
-hss_status launch_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tensors, int count, hipStream_t s);
+hss_status launch_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tensors, const void* const* grads, int count,
+                        hipStream_t s);
 }  // namespace hss
 
 // ---------------------------------------------------------------------------
@@ -658,12 +659,12 @@ hss_status hss_adapters_grad(const hss_adapters* L, int32_t b, const void* X, co
 // Optimizer
 // ---------------------------------------------------------------------------
 // The arrays of one tensor: there, aligned to their elements, apart from each other.
-static bool adamw_tensor_ok(const hss_adamw_config* c, const hss_adamw_tensor& t) {
+static bool adamw_tensor_ok(const hss_adamw_config* c, const hss_adamw_tensor& t, const void* grad) {
   const size_t k = (size_t)t.count, state = c->bits == 8 ? 1 : 4, blocks = (k + 255) / 256;
   struct Range {
     const void* p;
     size_t bytes, align;
-  } r[7] = {{t.param, k * dsize(c->dtype), dsize(c->dtype)}, {t.grad, k * dsize(c->grad_dtype), dsize(c->grad_dtype)},
+  } r[7] = {{t.param, k * dsize(c->dtype), dsize(c->dtype)}, {grad, k * dsize(c->grad_dtype), dsize(c->grad_dtype)},
             {t.m, k * state, state},                         {t.v, k * state, state}};
   int n = 4;
   if (t.master) r[n++] = {t.master, k * 4, 4};
@@ -676,8 +677,9 @@ static bool adamw_tensor_ok(const hss_adamw_config* c, const hss_adamw_tensor& t
   return true;
 }
 
-hss_status hss_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tensors, int32_t count, hipStream_t stream) {
-  if (!c || count < 0 || (count > 0 && !tensors)) return HSS_ERR_INVALID_ARG;
+hss_status hss_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tensors, const void* const* grads, int32_t count,
+                     hipStream_t stream) {
+  if (!c || count < 0 || (count > 0 && (!tensors || !grads))) return HSS_ERR_INVALID_ARG;
   if ((c->bits != 32 && c->bits != 8) || !valid_dtype(c->dtype) || !valid_dtype(c->grad_dtype) || c->reserved != 0)
     return HSS_ERR_INVALID_ARG;
   for (const double x : {c->lr, c->beta1, c->beta2, c->eps, c->weight_decay, c->grad_scale})
@@ -690,8 +692,8 @@ hss_status hss_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tensors,
     if (t.count < 0 || t.count >= kLimit) return HSS_ERR_INVALID_ARG;
     total += t.count + 256;
     if (total >= (int64_t)1 << 39) return HSS_ERR_INVALID_ARG;
-    if (t.count == 0) continue;
-    if ((t.master && c->dtype != HSS_BF16) || !adamw_tensor_ok(c, t)) return HSS_ERR_INVALID_ARG;
+    if (t.count == 0 || !grads[i]) continue;
+    if ((t.master && c->dtype != HSS_BF16) || !adamw_tensor_ok(c, t, grads[i])) return HSS_ERR_INVALID_ARG;
   }
-  return hss::launch_adamw(c, tensors, count, stream);
+  return hss::launch_adamw(c, tensors, grads, count, stream);
 }

@@ -102,14 +102,19 @@ def test_hash_bits_are_even_and_apart():
 def _call(hl, n=1, tensors=None, config=None, **kw):
     c = hl._lib.HssAdamwConfigStruct(bits=32, dtype=1, grad_dtype=0, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
                                      weight_decay=0.01, grad_scale=1.0, step=1)
-    t = (hl._lib.HssAdamwTensorStruct * max(n, 1))()
+    t, g = (hl._lib.HssAdamwTensorStruct * max(n, 1))(), (ctypes.c_void_p * max(n, 1))()
     for k in range(n):
         at = FAKE * (1 + 8 * (n - 1 - k))   # the last one, which kw changes, from FAKE on
-        t[k].count, t[k].param, t[k].grad, t[k].m, t[k].v = 1000, at, at + FAKE, at + 2 * FAKE, at + 3 * FAKE
+        t[k].count, t[k].param, t[k].m, t[k].v = 1000, at, at + 2 * FAKE, at + 3 * FAKE
+        g[k] = at + FAKE
         t[k].m_scale, t[k].v_scale = at + 5 * FAKE, at + 6 * FAKE
     for k, x in kw.items():
-        setattr(c if hasattr(c, k) else t[n - 1], k, x)
-    return hl._lib.lib.hss_adamw(ctypes.byref(c) if config is None else config, t if tensors is None else tensors, n, None)
+        if k == "grad":
+            g[n - 1] = x
+        elif k != "grads":
+            setattr(c if hasattr(c, k) else t[n - 1], k, x)
+    return hl._lib.lib.hss_adamw(ctypes.byref(c) if config is None else config, t if tensors is None else tensors,
+                                 kw.get("grads", g), n, None)
 
 
 def test_library_refuses(hl):
@@ -122,7 +127,7 @@ def test_library_refuses(hl):
     for bad in (dict(bits=16), dict(bits=0), dict(dtype=2), dict(grad_dtype=-1), dict(reserved=1), dict(lr=nan), dict(lr=inf),
                 dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(beta2=nan), dict(eps=-1e-9), dict(eps=inf),
                 dict(weight_decay=nan), dict(grad_scale=inf), dict(step=0), dict(step=-3), dict(step=2 ** 31),
-                dict(count=-1), dict(count=2 ** 31), dict(param=None), dict(grad=None), dict(m=None), dict(v=None),
+                dict(count=-1), dict(count=2 ** 31), dict(param=None), dict(grads=None), dict(m=None), dict(v=None),
                 dict(param=FAKE + 1), dict(grad=2 * FAKE + 2), dict(m=3 * FAKE + 1), dict(v=4 * FAKE + 2),
                 dict(dtype=0, master=5 * FAKE), dict(master=5 * FAKE + 2), dict(master=2 * FAKE),
                 dict(grad=FAKE), dict(m=FAKE + 1996), dict(v=3 * FAKE + 3996),
@@ -132,7 +137,8 @@ def test_library_refuses(hl):
         if not any(hasattr(hl._lib.HssAdamwConfigStruct, k) for k in bad):
             assert _call(hl, n=3, **bad) == INV, bad                    # in a later tensor
     assert _call(hl, n=0) == hl._lib.HSS_OK
-    assert _call(hl, count=0, param=None, grad=None) == hl._lib.HSS_OK  # no element: nothing to do
+    assert _call(hl, count=0, param=None) == hl._lib.HSS_OK             # no element: nothing to do
+    assert _call(hl, param=None, grad=None) == hl._lib.HSS_OK           # no gradient
 
 
 @pytest.fixture
@@ -191,7 +197,7 @@ def test_steps_refuse_what_does_not_fit(hl, bound):
     hl.hss_adamw(s, [z(300), z(20)], 1e-3, 1)
     hl.hss_adamw(s, [None, z((4, 5), torch.bfloat16)], z(1), z(1, torch.int32), grad_scale=z(()))
     hl.hss_adamw(s, [None, None], 1e-3, 1)
-    assert len(calls) == 3 and [t.count for t in s._tensors] == [0, 0]
+    assert len(calls) == 3 and [list(c[2]) for c in calls][2] == [None, None] and calls[1][2][0] is None and calls[1][2][1]
     for grads, lr, step, kw in (([z(300)], 1e-3, 1, {}), ([z(300), z(21)], 1e-3, 1, {}), ([z(600)[::2], z(20)], 1e-3, 1, {}),
                                 ([z(300), z(20, torch.bfloat16)], 1e-3, 1, {}), ([z(300), elsewhere(z(20))], 1e-3, 1, {}),
                                 ([z(300), z(20)], z(2), 1, {}), ([z(300), z(20)], z(1, torch.float64), 1, {}),
