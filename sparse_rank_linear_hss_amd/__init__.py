@@ -956,17 +956,19 @@ def adapters_grad_workspace(L: HSSAdapters, b: int, device) -> torch.Tensor:
 
 
 def _check_adapter_rows(L: HSSAdapters, X: torch.Tensor, ids: torch.Tensor, index: int) -> int:
-    if X.dim() != 2 or X.shape[1] != L.n or X.dtype != L.dtype or not X.is_contiguous():
+    shape = X.shape
+    if len(shape) != 2 or shape[1] != L.n or X.dtype is not L.dtype or not X.is_contiguous():
         raise ValueError("X must be a contiguous b x n tensor of the adapters' dtype")
     if L.index != index:
         raise ValueError(f"the adapters must be on X's device, {X.device}")
-    if ids.dtype != torch.int32 or ids.shape != (X.shape[0],) or not ids.is_contiguous() or ids.get_device() != index:
+    b = shape[0]
+    if ids.dtype is not torch.int32 or ids.shape != (b,) or ids.get_device() != index or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 tensor, one for each row, on X's device")
-    return X.shape[0]
+    return b
 
 
 def _check_like(name, t, shape, dtype, index):
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != index:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {tuple(shape)}, on X's device")
 
 
@@ -1020,21 +1022,31 @@ def hss_adapters_grad(L: HSSAdapters, X: torch.Tensor, G: torch.Tensor, ids: tor
     _check_like("G", G, (b, L.m), L.dtype, index)
     if base is not None:
         _check_like("base", base, (b, L.n), L.dtype, index)
-    specs = {"dX": ((b, L.n), L.dtype), "dU": (L.U.shape, torch.float32), "dVt": (L.Vt.shape, torch.float32)}
     if out is None:
-        out = {k: torch.empty(specs[k][0], dtype=specs[k][1], device=X.device)
-               for k, wanted in (("dX", dX), ("dU", dU), ("dVt", dVt)) if wanted}
+        out = {}
+        if dX:
+            out["dX"] = torch.empty((b, L.n), dtype=L.dtype, device=X.device)
+        if dU:
+            out["dU"] = torch.empty(L.U.shape, dtype=torch.float32, device=X.device)
+        if dVt:
+            out["dVt"] = torch.empty(L.Vt.shape, dtype=torch.float32, device=X.device)
+        dX, dU, dVt = out.get("dX"), out.get("dU"), out.get("dVt")
     else:
-        for k, t in out.items():
-            if k not in specs:
-                raise ValueError("out must hold 'dX', 'dU' or 'dVt'")
-            _check_like(k, t, *specs[k], index)
+        dX, dU, dVt = out.get("dX"), out.get("dU"), out.get("dVt")
+        if (dX is not None) + (dU is not None) + (dVt is not None) != len(out):
+            raise ValueError("out must hold 'dX', 'dU' or 'dVt'")
+        if dX is not None:
+            _check_like("dX", dX, (b, L.n), L.dtype, index)
+        if dU is not None:
+            _check_like("dU", dU, L.U.shape, torch.float32, index)
+        if dVt is not None:
+            _check_like("dVt", dVt, L.Vt.shape, torch.float32, index)
     if ws is None:
         ws = adapters_grad_workspace(L, b, X.device)
     elif ws.get_device() != index or not ws.is_contiguous():
         _check_ws(ws, index)
-    code = lib.hss_adapters_grad(L._ref, b, X.data_ptr(), G.data_ptr(), ids.data_ptr(), _ptr(base), _ptr(out.get("dX")),
-                                 _ptr(out.get("dU")), _ptr(out.get("dVt")), ws.data_ptr(), ws.nbytes, _raw_stream(index))
+    code = lib.hss_adapters_grad(L._ref, b, X.data_ptr(), G.data_ptr(), ids.data_ptr(), _ptr(base), _ptr(dX), _ptr(dU),
+                                 _ptr(dVt), ws.data_ptr(), ws.nbytes, _raw_stream(index))
     if code:
         check(code, "hss_adapters_grad")
     return out
