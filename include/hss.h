@@ -672,13 +672,16 @@ hss_status hss_grad_ckpt(const hss_matrix* A, int32_t b, const int8_t* codes, co
  * on every call.
  * ws: at least hss_adapters_workspace_size() or _grad_workspace_size() bytes
  *   (no state kept, no initial contents), which serve every smaller batch too.
- * HSS_ERR_UNSUPPORTED: an fp32 bank.  HSS_ERR_INVALID_ARG: unknown dtype, m, n
- *   or r < 1, count outside [1, HSS_MAX_ADAPTERS], count r max(m, n) >= 2^31, b
- *   outside [1, HSS_MAX_BATCH], b max(m, n) >= 2^31, null arrays (base, scale and
+ * HSS_ERR_UNSUPPORTED: an fp32 bank.  HSS_ERR_INVALID_ARG: unknown dtype, m or
+ *   n outside [1, HSS_MAX_ADAPTER_COLS], r outside [1, HSS_MAX_ADAPTER_RANK],
+ *   count outside [1, HSS_MAX_ADAPTERS], count r max(m, n) >= 2^31, b outside
+ *   [1, HSS_MAX_BATCH], b max(m, n) >= 2^31, null arrays (base, scale and
  *   hss_adapters_grad's outputs may be), arrays not aligned to their element,
  *   an output overlapping an input or another output.  HSS_ERR_WORKSPACE;
  *   HSS_ERR_HIP. */
 #define HSS_MAX_ADAPTERS 4096
+#define HSS_MAX_ADAPTER_RANK 65536
+#define HSS_MAX_ADAPTER_COLS (1 << 28)
 
 typedef struct hss_adapters {
   int32_t dtype; /* HSS_BF16 */

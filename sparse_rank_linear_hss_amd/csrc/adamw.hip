@@ -308,9 +308,9 @@ hss_status launch_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tenso
     if (!a.tensors) return HSS_OK;  // only tensors without elements or gradients were left
     // A workgroup for each chunk (38 M elements, fp32 and 8-bit moments: 210 and 130
     // us; 2048 workgroups that go round 237 and 150), but for device scalars, whose
-    // powers each workgroup computes.
+    // powers each workgroup computes.  (A launch takes fewer than 2^32 threads.)
     const bool scalars = c->lr_dev || c->step_dev || c->grad_scale_dev;
-    const unsigned grid = scalars ? std::min<uint32_t>(a.chunks, 2048) : a.chunks;
+    const unsigned grid = std::min<uint32_t>(a.chunks, scalars ? 2048 : 1u << 23);
     const int pt = c->dtype == HSS_F32 ? 0 : master ? 2 : 1;
     if (c->grad_dtype == HSS_F32) {
       if (pt == 0) launch_aw<0, 0>(c->bits, grid, a, s);

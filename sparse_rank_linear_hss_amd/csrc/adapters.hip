@@ -57,7 +57,7 @@ struct AdArgs {
   int rp, rg;       // r rounded up to 32 and to 16
   int slots, tiles;
   int splits[2], units[2];           // K splits of T and P (0: not wanted), units of each
-  int blocks_u, blocks_v;            // of k_ad_back
+  int blocks_u, blocks_v, blocks_y;  // of k_ad_back
   int cols_y, cols_u, cols_v;        // column blocks of dX, dU, dVt
   int chunks;                        // passes of dU and dVt over the ranks
   int direct;                        // K is not split: k_ad_rank makes the terms (backward)
@@ -1370,7 +1370,8 @@ __device__ __forceinline__ void ad_dfactor_wide(const AdArgs& a, int block, char
 
 __global__ __launch_bounds__(256, 2) void k_ad_back_wide(AdArgs a) {
   extern __shared__ __align__(16) char smem[];
-  int block = blockIdx.x;
+  int block = (int)(blockIdx.y * gridDim.x + blockIdx.x);
+  if (block >= a.blocks_u + a.blocks_v + a.blocks_y) return;
   if (block < a.blocks_u) {
     ad_dfactor_wide<false>(a, block, smem);
     return;
@@ -1386,7 +1387,8 @@ __global__ __launch_bounds__(256, 2) void k_ad_back_wide(AdArgs a) {
 template <int NR, int CW>
 __global__ __launch_bounds__(256, 2) void k_ad_back(AdArgs a) {
   extern __shared__ __align__(16) char smem[];
-  int block = blockIdx.x;
+  int block = (int)(blockIdx.y * gridDim.x + blockIdx.x);
+  if (block >= a.blocks_u + a.blocks_v + a.blocks_y) return;
   if (block < a.blocks_u) {
     ad_dfactor<NR, CW, false>(a, block, smem);
     return;
@@ -1528,16 +1530,22 @@ hss_status launch_adapters_apply(const hss_adapters* A, int b, const void* X, co
   return hipGetLastError() == hipSuccess ? HSS_OK : HSS_ERR_HIP;
 }
 
-template <int NR, int CW>
-static void launch_back(AdArgs a, hipStream_t s) {
-  const size_t lds = (size_t)CW * NR * 64 * 16;
-  a.chunks = (a.rg + 16 * NR - 1) / (16 * NR);
-  a.cols_u = (a.m + 16 * CW - 1) / (16 * CW), a.cols_v = (a.n + 16 * CW - 1) / (16 * CW);
-  a.cols_y = (a.n + 511) / 512;
+// k_ad_back's blocks for dU and dVt of `width` columns by `ranks` ranks.
+static dim3 ad_back_grid(AdArgs& a, int width, int ranks) {
+  a.chunks = (a.rg + ranks - 1) / ranks;
+  a.cols_u = (a.m + width - 1) / width, a.cols_v = (a.n + width - 1) / width, a.cols_y = (a.n + 511) / 512;
   a.blocks_u = a.dU ? a.cols_u * a.chunks * a.count : 0;
   a.blocks_v = a.dVt ? a.cols_v * a.chunks * a.count : 0;
-  const dim3 grid(a.blocks_u + a.blocks_v + (a.Y ? a.cols_y * a.tiles : 0));
-  hipLaunchKernelGGL((k_ad_back<NR, CW>), grid, dim3(256), lds, s, a);
+  a.blocks_y = a.Y ? a.cols_y * a.tiles : 0;
+  // (a launch takes fewer than 2^32 threads along x)
+  const unsigned all = (unsigned)a.blocks_u + a.blocks_v + a.blocks_y, x = std::min(all, 1u << 22);
+  return dim3(x, (all + x - 1) / x);
+}
+
+template <int NR, int CW>
+static void launch_back(AdArgs a, hipStream_t s) {
+  const dim3 grid = ad_back_grid(a, 16 * CW, 16 * NR);
+  hipLaunchKernelGGL((k_ad_back<NR, CW>), grid, dim3(256), (size_t)CW * NR * 64 * 16, s, a);
 }
 
 hss_status launch_adapters_grad(const hss_adapters* A, int b, const void* X, const void* G, const int32_t* ids,
@@ -1563,12 +1571,8 @@ hss_status launch_adapters_grad(const hss_adapters* A, int b, const void* X, con
   const int64_t wide = (int64_t)A->count * ((A->r + 63) / 64) * (((int64_t)A->m + 255) / 256 + (A->n + 255) / 256);
   const bool narrow = (int64_t)A->count * ((A->r + 63) / 64) * ((int64_t)A->m + A->n) / 128 < 256;
   if (b > kAdSmall && p.nr == 4 && wide >= 192) {
-    a.chunks = (a.rg + 63) / 64;
-    a.cols_u = (a.m + 255) / 256, a.cols_v = (a.n + 255) / 256, a.cols_y = (a.n + 511) / 512;
-    a.blocks_u = dU ? a.cols_u * a.chunks * a.count : 0;
-    a.blocks_v = dVt ? a.cols_v * a.chunks * a.count : 0;
-    const dim3 blocks(a.blocks_u + a.blocks_v + (dX ? a.cols_y * a.tiles : 0));
-    hipLaunchKernelGGL(k_ad_back_wide, blocks, dim3(256), 2 * 4 * 3 * 64 * 16, s, a);
+    const dim3 grid = ad_back_grid(a, 256, 64);
+    hipLaunchKernelGGL(k_ad_back_wide, grid, dim3(256), 2 * 4 * 3 * 64 * 16, s, a);
   } else if (p.nr == 1) {
     narrow ? launch_back<1, 2>(a, s) : launch_back<1, 8>(a, s);
   } else if (p.nr == 2) {

@@ -577,6 +577,7 @@ static hss_status check_adapters(const hss_adapters* L, int32_t b) {
       b < 1 || b > HSS_MAX_BATCH)
     return HSS_ERR_INVALID_ARG;
   const int64_t wide = std::max(L->m, L->n);
+  if (wide > HSS_MAX_ADAPTER_COLS || L->r > HSS_MAX_ADAPTER_RANK) return HSS_ERR_INVALID_ARG;
   // count r < 2^31 comes first: the product of all three could overflow
   if ((int64_t)L->count * L->r >= kLimit || (int64_t)L->count * L->r * wide >= kLimit || b * wide >= kLimit)
     return HSS_ERR_INVALID_ARG;

@@ -122,6 +122,20 @@ def test_library_refuses(hl):
     assert _grad(hl, dX=None, dU=None, dVt=None) == hl._lib.HSS_OK              # nothing asked for
 
 
+def test_ranks_and_columns_have_limits(hl):
+    INV = hl._lib.HSS_ERR_INVALID_ARG
+    size = ctypes.c_size_t(0)
+    for kw, b in ((dict(m=(1 << 28) + 1, n=1, r=1, count=1), 1), (dict(m=1, n=(1 << 28) + 1, r=1, count=1), 1),
+                  (dict(m=1, n=1, r=65537, count=1), 1)):
+        assert _apply(hl, _bank(hl, **kw), b=b) == INV and _grad(hl, _bank(hl, **kw), b=b) == INV
+        for call in ("hss_adapters_workspace_size", "hss_adapters_grad_workspace_size"):
+            query = getattr(hl._lib.lib, call)
+            assert query(ctypes.byref(_bank(hl, **kw)), b, ctypes.byref(size)) == INV
+            kw = {k: x - (x in (65537, (1 << 28) + 1)) for k, x in kw.items()}
+            assert query(ctypes.byref(_bank(hl, **kw)), b, ctypes.byref(size)) == 0 and size.value > 0
+            kw = {k: x + (x in (65536, 1 << 28)) for k, x in kw.items()}
+
+
 def test_workspaces_grow_with_the_batch(hl):
     size = ctypes.c_size_t(0)
     for call in ("hss_adapters_workspace_size", "hss_adapters_grad_workspace_size"):

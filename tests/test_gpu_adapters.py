@@ -158,6 +158,70 @@ def test_large_banks(H, count, b):
     c.check_grad(c.grad())
 
 
+@pytest.mark.parametrize("m,n,r", [(90, 70, 257), (40, 600, 300), (530, 100, 513)])
+@pytest.mark.parametrize("b,count,kind", [(1, 1, "one"), (30, 4, "mixed"), (100, 3, "mixed")])
+def test_large_ranks(H, m, n, r, b, count, kind):
+    """More of them than the forward keeps of T at a time."""
+    c = Case(H, m, n, r, b, count, kind, seed=r + b)
+    c.check_apply(c.apply(ws=_nan_ws(H.hss_adapters_workspace_size(c.L, b))))
+    c.check_grad(c.grad(ws=_nan_ws(H.hss_adapters_grad_workspace_size(c.L, b))))
+
+
+@pytest.mark.parametrize("m,n,r,count", [(300, 520, 41, 40), (300, 520, 100, 20), (255, 1025, 64, 40), (3, 257, 33, 64),
+                                         (258, 2, 200, 20), (1000, 511, 48, 33)])
+@pytest.mark.parametrize("b,kind", [(65, "mixed"), (300, "runs"), (515, "one")])
+def test_gradients_of_many_columns_in_all(H, m, n, r, count, b, kind):
+    """Blocks of 256 columns that share the terms (count ceil(r / 64) (ceil(m / 256) +
+    ceil(n / 256)) >= 192), at ends of rows and ranks, with outputs left out."""
+    import torch
+    c = Case(H, m, n, r, b, count, kind, seed=r + b, shift=b % 2)
+    full = c.grad(ws=_nan_ws(H.hss_adapters_grad_workspace_size(c.L, b)))
+    c.check_grad(full)
+    for keys in (("dU",), ("dVt",), ("dX", "dVt")):
+        got = c.grad(**{k: k in keys for k in ("dX", "dU", "dVt")})
+        assert all(torch.equal(got[k], full[k]) for k in keys)
+
+
+def test_the_largest_bank(H):
+    """4096 adapters of 524287 x 64, r = 1: 2^31 - 4096 values of U, 4 rows, more
+    gradient blocks than one row of a grid takes.  The rows' adapters against the
+    formula, all others' gradients zeros."""
+    import torch
+    count, m, n = 4096, 524287, 64
+    ids = np.array([4095, 0, 4095, 2048])
+    rng = np.random.default_rng(0)
+    used = sorted(set(ids.tolist()))
+    U = torch.zeros(count, m, 1, dtype=torch.bfloat16, device="cuda")
+    Vt = torch.zeros(count, 1, n, dtype=torch.bfloat16, device="cuda")
+    f = {}
+    for l in used:
+        u, v = _rand((m, 1), l + 1, 0.1), _rand((1, n), l + 2, 0.1)
+        U[l], Vt[l] = to_dev(u, BF), to_dev(v, BF)
+        f[l] = (O.widen(u, BF), O.widen(v, BF))
+    X, G = _rand((4, n), 5, 1.0), _rand((4, m), 6, 0.1)
+    L = H.HSSAdapters(U, Vt)
+    Xd, Gd = to_dev(X, BF), to_dev(G, BF)
+    ids_d = torch.from_numpy(ids.astype(np.int32)).cuda()
+    X, G = O.widen(X, BF), O.widen(G, BF)
+    at = {l: k for k, l in enumerate(used)}
+    args = [np.stack([f[l][k] for l in used]) for k in (0, 1)] + [np.ones(len(used))]
+    small = np.array([at[l] for l in ids])
+    absolute = [np.abs(a) for a in args]
+    got = H.hss_adapters_apply(L, Xd, ids_d).double().cpu().numpy()
+    want, N = O.adapters_apply(*args, X, small), O.adapters_apply(*absolute, np.abs(X), small)
+    assert np.all(np.abs(got - want) <= 1.01 * (2.0 ** -8 * np.abs(want) + ((n + 5) * U24 + 2.0 ** -16) * N))
+    out = {"dU": torch.full((count, m, 1), float("nan"), device="cuda"), "dVt": torch.full((count, 1, n), float("nan"), device="cuda"),
+           "dX": torch.empty_like(Xd)}
+    H.hss_adapters_grad(L, Xd, Gd, ids_d, out=out)
+    want, N = O.adapters_grad(*args, X, G, small), O.adapters_grad(*absolute, np.abs(X), np.abs(G), small)
+    tol = [2.0 ** -8 * np.abs(want[0]) + ((m + 5) * U24 + 2.0 ** -16) * N[0], (n + 15) * U24 * N[1], (m + 15) * U24 * N[2]]
+    for k, got in enumerate((out["dX"], out["dU"][used], out["dVt"][used])):
+        assert np.all(np.abs(got.double().cpu().numpy() - want[k]) <= 1.01 * tol[k])
+    out["dU"][used], out["dVt"][used] = 0, 0
+    for k in ("dU", "dVt"):
+        assert all(not part.any() for part in out[k].split(256))     # (a NaN counts)
+
+
 @pytest.mark.parametrize("m,n,r,b,count", [(96, 64, 8, 5, 2), (130, 514, 33, 70, 3), (1000, 1000, 64, 100, 2)])
 def test_arrays_off_the_16_byte_grid(H, m, n, r, b, count):
     for shift in (1, 3, 4):
