@@ -65,9 +65,32 @@ struct AdArgs {
 
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
+// 16 bytes at a byte offset from a base that the whole wave shares (arrays have
+// fewer than 2^31 elements of two bytes: one register an address).
+__device__ __forceinline__ u32x4 ad_load(const void* base, uint32_t at) {
+  const Bytes16 v = *reinterpret_cast<const Bytes16*>(static_cast<const char*>(base) + at);
+  return u32x4{v.w[0], v.w[1], v.w[2], v.w[3]};
+}
+
 // ---------------------------------------------------------------------------
 // Tiles
 // ---------------------------------------------------------------------------
+// Blocks go to the chip's eight dies in turn, each with a cache of its own.  Work is
+// (tile, part), and adjacent tiles mostly share an adapter: eight of them with the
+// same part of its factors go to one die.  (Gradients of 2048 rows 11008 x 4096 of 8,
+// r 64, whose 64 tiles read 124 MB of U and Vt: k_ad_rank 34 -> 25 us, with a quicker
+// search for the tiles, which alone took 1.5 us off a forward pass of 2048 rows.)
+struct AdWork {
+  int tile, part;  // tile: may lie past the last one
+};
+
+__device__ __forceinline__ AdWork ad_work(uint32_t block, uint32_t parts) {
+  const uint32_t group = (block & 7) + 8 * (block >> 6);
+  return {(int)(8 * (group / parts) + ((block >> 3) & 7)), (int)(group % parts)};
+}
+
+static inline int ad_work_blocks(int tiles, int parts) { return ((tiles + 7) / 8 * parts + 7) / 8 * 64; }
+
 struct AdTile {
   int adapter;  // -1: rows without one
   int rows;     // 0: no such tile
@@ -103,6 +126,10 @@ __device__ __forceinline__ int ad_scan(int v, int* part, int* total) {
   return base + before;
 }
 
+// Copies of the bins, and the bins in all.
+__host__ __device__ __forceinline__ int ad_copies(int count) { return count < 512 ? 8 : 1; }
+__host__ __device__ __forceinline__ int ad_bins(int count) { return (count + 1) * (ad_copies(count) == 1 ? 1 : 9); }
+
 __device__ __forceinline__ int ad_id(const int32_t* ids, int t, int count) {
   const int id = ids[t];
   return id >= 0 && id < count ? id : -1;
@@ -111,7 +138,7 @@ __device__ __forceinline__ int ad_id(const int32_t* ids, int t, int count) {
 // Tile `tile` of the batch: its adapter and its rows (in LDS).  Up to 64 rows
 // tile t starts at row t, if that is the first, or TM rows after the last start,
 // of its adapter; beyond, tiles are counted through the adapters, rows without one
-// last.  bins: count + 1 ints; part: 6.  table: null, or where each adapter's
+// last.  bins: ad_bins ints; part: 6.  table: null, or where each adapter's
 // first tile and rows go.
 template <int TM>
 __device__ __forceinline__ AdTile ad_tile(const AdArgs& a, int tile, uint16_t* rows, int* part, int* bins, int2* table) {
@@ -132,30 +159,42 @@ __device__ __forceinline__ AdTile ad_tile(const AdArgs& a, int tile, uint16_t* r
     return r;
   }
   constexpr int per = HSS_MAX_BATCH / 256;
+  static_assert(per == 8, "two loads of 16 bytes a thread");
   int id[per];
+  if (per * t + per <= b) {
+    const u32x4 lo = ad_load(a.ids, 4 * per * t), hi = ad_load(a.ids, 4 * per * t + 16);
 #pragma unroll
-  for (int k = 0; k < per; ++k) id[k] = a.ids[min(per * t + k, b - 1)];  // all in flight
+    for (int k = 0; k < 4; ++k) id[k] = (int)lo[k], id[4 + k] = (int)hi[k];
+  } else {
+#pragma unroll
+    for (int k = 0; k < per; ++k) id[k] = a.ids[min(per * t + k, b - 1)];  // all in flight
+  }
+  // A batch of few adapters would have lanes add to the same places: eight copies of
+  // the bins, summed below.
+  const int copies = ad_copies(count);
+  int* bin8 = copies == 1 ? bins : bins + count + 1;
+  for (int k = t; k < (count + 1) * copies; k += 256) bin8[k] = 0;
 #pragma unroll
   for (int k = 0; k < per; ++k) {
     if (id[k] < 0 || id[k] >= count) id[k] = count;
     if (per * t + k >= b) id[k] = -2;
   }
-  for (int k = t; k <= count; k += 256) bins[k] = 0;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < per; ++k) {  // lanes of one adapter's rows add once
-    const int head = __builtin_amdgcn_readfirstlane(id[k]);
-    const uint64_t same = __ballot(id[k] == head);
-    if (id[k] == head) {
-      if (head >= 0 && __popcll(same & lanemask_lt()) == 0) atomicAdd(&bins[head], __popcll(same));
-    } else if (id[k] >= 0) {
-      atomicAdd(&bins[id[k]], 1);
-    }
-  }
+  for (int k = 0; k < per; ++k)
+    if (id[k] >= 0) atomicAdd(&bin8[id[k] * copies + (t & (copies - 1))], 1);
   __syncthreads();
   const int many = (count + 256) / 256, k0 = t * many;
   int own = 0, total;
-  for (int k = k0; k < min(k0 + many, count + 1); ++k) own += (bins[k] + TM - 1) / TM;
+  for (int k = k0; k < min(k0 + many, count + 1); ++k) {
+    if (copies == 8) {
+      int sum = 0;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum += bin8[8 * k + c];
+      bins[k] = sum;
+    }
+    own += (bins[k] + TM - 1) / TM;
+  }
   int at = ad_scan(own, part, &total);
   if (table) {
     int next = at;
@@ -270,13 +309,6 @@ __device__ __forceinline__ u32x4 ad_tail8(const uint16_t* row, int k, int n) {
   return ad_drop(load8(row + from), k - from);
 }
 
-// 16 bytes at a byte offset from a base that the whole wave shares (arrays have
-// fewer than 2^31 elements of two bytes: one register an address).
-__device__ __forceinline__ u32x4 ad_load(const void* base, uint32_t at) {
-  const Bytes16 v = *reinterpret_cast<const Bytes16*>(static_cast<const char*>(base) + at);
-  return u32x4{v.w[0], v.w[1], v.w[2], v.w[3]};
-}
-
 // What this wave wrote to its part of LDS before is read after (LDS takes a
 // wave's accesses in order; this keeps the compiler to it).
 __device__ __forceinline__ void ad_wave_sync() {
@@ -309,7 +341,7 @@ __device__ __forceinline__ uint32_t ad_term2(float& x, float& y) {
 //   lane's 16 bytes be an access of its own to the cache: 4 times as many; prefill
 //   of 2048 rows 4096 x 11008 r 64: 37 us).  The next unit's loads are in flight
 //   while one is multiplied.  The four waves' sums meet in LDS.
-// grid: (splits of T and of P, tiles, groups of 16 NR ranks)
+// grid: (tiles by splits of T and of P, groups of 16 NR ranks)
 // ---------------------------------------------------------------------------
 // Where 16-byte chunk c of a 128-byte row lies in LDS.  A read takes one chunk of 16
 // rows, half of them in each half of the 256 bytes of banks: (row / 2) % 8 tells
@@ -323,10 +355,11 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
   extern __shared__ __align__(16) char smem[];
   __shared__ uint16_t rows[TM];
   __shared__ int part[6];
-  const int tile = blockIdx.y, rank0 = (int)blockIdx.z * 16 * NR;
-  const int side = (int)blockIdx.x >= a.splits[0];
-  const int z = (int)blockIdx.x - (side ? a.splits[0] : 0);
-  const bool lead = blockIdx.x == 0 && blockIdx.z == 0;
+  const AdWork work = ad_work(blockIdx.x, a.splits[0] + a.splits[1]);
+  const int tile = work.tile, rank0 = (int)blockIdx.y * 16 * NR;
+  if (tile >= a.tiles) return;
+  const int side = work.part >= a.splits[0], z = work.part - (side ? a.splits[0] : 0);
+  const bool lead = work.part == 0 && blockIdx.y == 0;
   AdTile at = ad_tile<TM>(a, tile, rows, part, reinterpret_cast<int*>(smem), lead && tile == 0 ? a.first : nullptr);
   at = {uniform(at.adapter), uniform(at.rows)};
   if (lead) {  // (a tile's free slots repeat its last row, so that all of them may be read)
@@ -1484,9 +1517,9 @@ static AdArgs ad_args(const hss_adapters* A, int b, const AdPlan& p, const void*
 
 template <int TM, int NR>
 static void launch_rank_nr(const AdArgs& a, hipStream_t s) {
-  const size_t lds = std::max<size_t>((size_t)4 * (TM + 16 * NR) * kAdUnit * 2, (size_t)(a.count + 1) * 4);
+  const size_t lds = std::max<size_t>((size_t)4 * (TM + 16 * NR) * kAdUnit * 2, (size_t)ad_bins(a.count) * 4);
   static_assert(4 * (TM + 16 * NR) * kAdUnit * 2 >= 4 * (TM / 16) * NR * 64 * 16, "the waves' sums fit");
-  const dim3 grid(a.splits[0] + a.splits[1], a.tiles, (a.rg + 16 * NR - 1) / (16 * NR));
+  const dim3 grid(ad_work_blocks(a.tiles, a.splits[0] + a.splits[1]), (a.rg + 16 * NR - 1) / (16 * NR));
   hipLaunchKernelGGL((k_ad_rank<TM, NR>), grid, dim3(256), lds, s, a);
 }
 
