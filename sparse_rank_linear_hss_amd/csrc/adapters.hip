@@ -12,13 +12,21 @@
 // them: a tile is an adapter and up to 16 or 32 of its rows, found by each block
 // from ids (no launch for a plan, nothing on the host).
 //
-// Forward: two launches.  k_ad_rank makes T, K split over blocks into partial sums in
-// fp32, for a few tiles would not fill the chip, and k_ad_expand adds the splits in
-// order on its way to the matrix cores.  Backward: k_ad_rank makes T and P,
-// k_ad_terms adds the splits once for all that read them, k_ad_back makes dU, dVt and
-// dX.  T and P, times scale in fp32, go to the matrix cores as bf16 terms: two (16
+// Forward: k_ad_rank makes T, K split over blocks into partial sums in fp32, for a few
+// tiles would not fill the chip, and k_ad_expand adds the splits in order on its way to
+// the matrix cores.  A few rows and small factors take one launch, k_ad_fused.
+// Backward: k_ad_rank makes T and P, k_ad_terms adds the splits once for all that read
+// them (short K is not split, and k_ad_rank makes the terms), k_ad_back makes dU, dVt
+// and dX.  T and P, times scale in fp32, go to the matrix cores as bf16 terms: two (16
 // significant bits) where the result is rounded to bf16 anyway, three (24 bits)
 // for the fp32 gradients.
+//
+// Measured (a whole call in a graph, bytes moved at least / time): 64 requests of
+// their own 11008 x 4096 r 64 127 MB in 32 us, 3.9 TB/s; 2048 rows of 4 4096 x 11008 r 64
+// 86 MB in 36 us, 2.4 TB/s, of which 5 us are launches, 5 the search for tiles and 5
+// the way from the partial sums to the first product; gradients of 2048 rows of 8
+// 11008 x 4096 r 64 142 MB in 70 us (X and G are read twice: 204 MB, 2.9 TB/s).  One
+// row 4096 x 4096 r 16: 6.6 us, of which a launch takes 2.
 #include <algorithm>
 
 #include "mx_common.h"
@@ -28,11 +36,21 @@ namespace hss {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-static constexpr int kAdSmall = 64;     // batches up to here: tiles found by one ballot
+// Batches up to here (a lane for each row): tiles found by one ballot, of 16 rows in
+// the forward pass; beyond, by a histogram, of 32.  4096 x 4096 r 64, the last batch
+// of the one and the first of the other: of 4 adapters 10.8 and 13.0 us, an adapter a
+// row 18.7 and 23.9.
+static constexpr int kAdSmall = 64;
 static constexpr int kAdUnit = 64;      // columns of K that a wave takes at a time: a cache line of each row
-static constexpr int kAdBlocks = 512;   // blocks of k_ad_rank that K is split for
-static constexpr int kAdChunk = 256;    // ranks of T that k_ad_expand keeps in LDS
-static constexpr int kAdWhole = 16;     // units of K that the backward pass does not split
+// Blocks of k_ad_rank that K is split for, of at least four units, one a wave.  128,
+// 256, 512, 1024: 2048 rows 4096 x 11008 43.1, 41.0, 40.1, 43.7 us.  At least 4, 8, 16
+// units: 77 rows 2731 x 5003 14.7, 15.3, 16.6.
+static constexpr int kAdBlocks = 512;
+static constexpr int kAdChunk = 256;    // ranks of T that k_ad_expand keeps in LDS: 2 KB a row
+// Units of K that the backward pass does not split, so that k_ad_rank makes the terms
+// and a launch is saved: not split and split, 64 rows of 4 512 x 512 9.2 and 11.0 us,
+// 16 rows 1024 x 1024 10.1 and 10.6, past the limit 2048 x 2048 12.8 and 10.9.
+static constexpr int kAdWhole = 16;
 
 struct AdArgs {
   const uint16_t* U;
@@ -102,8 +120,7 @@ __device__ __forceinline__ int ad_dpp_add(int v) {
 }
 
 // Exclusive prefix sum over the block's 256 threads, and the total.  (In a wave by
-// DPP shifts within rows of 16 lanes, then each row's last lane to the rows behind:
-// the permutes through LDS of wave_excl_scan_u32 take 1 us of a tile's search.)
+// DPP shifts within rows of 16 lanes, then each row's last lane to the rows behind.)
 __device__ __forceinline__ int ad_scan(int v, int* part, int* total) {
   const int w = threadIdx.x >> 6;
   int incl = ad_dpp_add<0x111, 0xF>(v);   // row_shr 1, 2, 4, 8
@@ -1541,8 +1558,11 @@ static void launch_expand(const AdArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((k_ad_expand<TM, true>), grid, dim3(256), lds, s, a, nc);
 }
 
-// One launch: up to 64 rows, and a Vt_l that a block reads in the time a launch
-// takes (at most 256 KB with its ranks rounded up to 16).
+// One launch: up to 64 rows, and a Vt_l that a block reads in the time that a launch
+// takes (at most 256 KB with its ranks rounded up to 16).  In one / in two, 4096
+// columns of Y and an adapter a row: n 4096 r 16, 1 row 6.9 / 8.4 us, 64 rows 8.6 /
+// 11.6; n 4096 r 32, 64 rows 11.8 / 13.2; n 8192 r 16, 1 row 9.0 / 9.8, 64 rows
+// 11.8 / 12.6; past the limit n 16384 r 16, 1 row 13.7 / 12.9, 64 rows 16.9 / 14.7.
 static bool ad_fused(const hss_adapters* A, int b) {
   const int nr = (A->r + 15) / 16;
   return b <= kAdSmall && A->r >= 8 && nr <= 2 && A->n >= 8 && nr * (int64_t)A->n <= 8192;
@@ -1554,7 +1574,9 @@ hss_status launch_adapters_apply(const hss_adapters* A, int b, const void* X, co
   AdArgs a = ad_args(A, b, p, X, ids, base, Y, ws);
   a.first = nullptr;
   if (ad_fused(A, b)) {
-    const int cols = (a.m + 511) / 512, nc = std::max(1, std::min(cols, cols * a.tiles / 256));
+    // at most a block for each compute unit: each makes its tile's T again (64 rows
+    // 11008 x 4096 r 16: 11.7 us, 16.5 with 320 blocks)
+    const int cols = (a.m + 511) / 512, nc = std::max(1, (int)std::min<int64_t>(cols, ((int64_t)cols * a.tiles + 255) / 256));
     const dim3 grid(a.tiles, (cols + nc - 1) / nc), block(64 * kAdFusedWaves);
     if (a.r <= 16) hipLaunchKernelGGL(k_ad_fused<1>, grid, block, 0, s, a, nc);
     else hipLaunchKernelGGL(k_ad_fused<2>, grid, block, 0, s, a, nc);
@@ -1599,11 +1621,17 @@ hss_status launch_adapters_grad(const hss_adapters* A, int b, const void* X, con
     const dim3 grid(a.tiles, (a.rp + 63) / 64, a.splits[0] && a.splits[1] ? 2 : 1);
     hipLaunchKernelGGL(k_ad_terms, grid, dim3(256), 0, s, a);
   }
-  // Blocks of 256 columns that share the terms, where they fill the chip; else
-  // waves share the rows of fewer columns.
-  const int64_t wide = (int64_t)A->count * ((A->r + 63) / 64) * (((int64_t)A->m + 255) / 256 + (A->n + 255) / 256);
-  const bool narrow = (int64_t)A->count * ((A->r + 63) / 64) * ((int64_t)A->m + A->n) / 128 < 256;
-  if (b > kAdSmall && p.nr == 4 && wide >= 192) {
+  // dU and dVt by blocks of 256 columns that share the terms, where there are 96 of
+  // them; else by blocks of 64 whose waves share the rows (2048 rows r 64: 4096 x
+  // 4096 of 2, 64 blocks, 54.2 and 47.7 us; of 3, 96 blocks, 46.6 and 52.8; of 8 11008
+  // x 4096, 472 blocks, 60.6 and 76.3).  With up to 32 ranks there are few terms to share.
+  // Very few columns in all are split further, 32 a block (r 16, 512 rows 1024 x 1024
+  // of 1 13.8 and 15.1 us, of 4, where the rule ends, 13.9 and 12.8; r 64, 201 rows
+  // 1501 x 2777 of 1 18.8 and 21.0, of 2 20.1 and 19.6).
+  const int64_t passes = (int64_t)A->count * ((A->r + 63) / 64);
+  const int64_t wide = passes * (((int64_t)A->m + 255) / 256 + (A->n + 255) / 256);
+  const bool narrow = passes * ((int64_t)A->m + A->n) < 64 * 128;
+  if (b > kAdSmall && p.nr == 4 && wide >= 96) {
     const dim3 grid = ad_back_grid(a, 256, 64);
     hipLaunchKernelGGL(k_ad_back_wide, grid, dim3(256), 2 * 4 * 3 * 64 * 16, s, a);
   } else if (p.nr == 1) {

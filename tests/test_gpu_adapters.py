@@ -172,7 +172,7 @@ def test_large_ranks(H, m, n, r, b, count, kind):
 @pytest.mark.parametrize("b,kind", [(65, "mixed"), (300, "runs"), (515, "one")])
 def test_gradients_of_many_columns_in_all(H, m, n, r, count, b, kind):
     """Blocks of 256 columns that share the terms (count ceil(r / 64) (ceil(m / 256) +
-    ceil(n / 256)) >= 192), at ends of rows and ranks, with outputs left out."""
+    ceil(n / 256)) >= 96), at ends of rows and ranks, with outputs left out."""
     import torch
     c = Case(H, m, n, r, b, count, kind, seed=r + b, shift=b % 2)
     full = c.grad(ws=_nan_ws(H.hss_adapters_grad_workspace_size(c.L, b)))
