@@ -21,7 +21,7 @@
 // significant bits) where the result is rounded to bf16 anyway, three (24 bits)
 // for the fp32 gradients.
 //
-// Measured (a whole call in a graph, bytes moved at least / time): 64 requests of
+// Measured (calls back to back over three sets of arrays, bytes moved at least / time): 64 requests of
 // their own 11008 x 4096 r 64 127 MB in 32 us, 3.9 TB/s; 2048 rows of 4 4096 x 11008 r 64
 // 86 MB in 36 us, 2.4 TB/s, of which 5 us are launches, 5 the search for tiles and 5
 // the way from the partial sums to the first product; gradients of 2048 rows of 8
@@ -358,6 +358,8 @@ __device__ __forceinline__ uint32_t ad_term2(float& x, float& y) {
 //   lane's 16 bytes be an access of its own to the cache: 4 times as many; prefill
 //   of 2048 rows 4096 x 11008 r 64: 37 us).  The next unit's loads are in flight
 //   while one is multiplied.  The four waves' sums meet in LDS.
+//   2048 rows 4096 x 11008 of 4, r 64: 17 us for 51 MB, 3 of them the search for the
+//   tile, 1 the sums; gradients of 2048 rows 11008 x 4096 of 8: 25 us for 77 MB.
 // grid: (tiles by splits of T and of P, groups of 16 NR ranks)
 // ---------------------------------------------------------------------------
 // Where 16-byte chunk c of a 128-byte row lies in LDS.  A read takes one chunk of 16
@@ -587,7 +589,9 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Backward: the terms of T and P.  A lane has one rank of eight slots.
+// Backward: the terms of T and P.  A lane has one rank of eight slots.  4 to 6 us, most
+// of it a launch and one chain of loads, instead of the sums in each block of dU, dVt and
+// dX (2048 rows 11008 x 4096 of 8, r 64: 552 of them).
 // grid: (tiles, ranks / 64, sides)
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void k_ad_terms(AdArgs a) {
@@ -729,7 +733,11 @@ __device__ __forceinline__ void ad_copy(const AdArgs& a, const AdTile& at, const
 // adjacent columns of four rows, and 16 lanes read and write 256 bytes of a row.  U
 // comes through the wave's own part of LDS, 32 ranks at a time (four lanes a row),
 // the next ones in flight.  The block's terms of T are made first, in LDS, for all
-// its columns.
+// its columns, of which it takes about as many as give each compute unit a block (64
+// requests 11008 x 4096 r 64, NC 1, 2, 4, 6, 8: 37.0, 35.0, 34.1, 33.2, 36.3 us a call;
+// 2048 rows 4096 x 11008: 43.8, 39.7, 39.9, 45.3, 50.0).  Bound by memory where U is
+// read once (64 requests: 20 us, 4.6 TB/s), by the way to the first product where
+// blocks are short (2048 rows: 17 us for 36 MB, 5 until the terms are made).
 // grid: (tiles, column blocks of 512 NC)
 // ---------------------------------------------------------------------------
 // Where 16-byte chunk q of U's row 8 i + f (32 ranks, 64 bytes) lies in LDS: the 16
@@ -923,7 +931,7 @@ __global__ __launch_bounds__(256, TM == 16 ? 3 : 2) void k_ad_expand(AdArgs a, i
 // Both in one launch, for a few rows and small factors: each block makes all of its
 // tile's T for itself (16 waves share K), then its columns of Y.  Vt_l comes from L2
 // for all blocks but the first; a launch, a round trip of T through memory and a
-// workspace are saved.
+// workspace are saved.  One row 4096 x 4096 r 16: 7.0 us, a launch and a chain of loads.
 // grid: (tiles, column blocks of 512 NC)
 // ---------------------------------------------------------------------------
 static constexpr int kAdFusedWaves = 16, kAdFusedColumns = 8;
@@ -1078,7 +1086,10 @@ __global__ __launch_bounds__(64 * kAdFusedWaves) void k_ad_fused(AdArgs a, int n
 }
 
 // ---------------------------------------------------------------------------
-// The backward's last launch: blocks of dU, then of dVt, then of dX.
+// The backward's last launch: blocks of dU, then of dVt (the long ones first), then of
+// dX.  Bound by memory (2048 rows 4096 x 4096 r 16: 19 us for 68 MB, 3.6 TB/s) unless one
+// adapter has most of the rows, whose blocks are a chain of 32 at a time, 1 us each (2048
+// rows 11008 x 4096 of 8, r 64: 31 us for 126 MB with the rows about even, 43 else).
 // ---------------------------------------------------------------------------
 // dX = base + scale P Vt: as k_ad_expand, with Vt's 8 x 8 pieces transposed in
 // registers: a lane's eight ranks and eight columns are eight operands.
