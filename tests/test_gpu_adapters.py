@@ -182,6 +182,42 @@ def test_gradients_of_many_columns_in_all(H, m, n, r, count, b, kind):
         assert all(torch.equal(got[k], full[k]) for k in keys)
 
 
+@pytest.mark.parametrize("m,n,r,b,count,kind", [
+    (1501, 2777, 41, 201, 5, "mixed"), (1300, 1100, 64, 2000, 4, "one"), (1300, 1101, 20, 1000, 5, "mixed"),
+    (2049, 2100, 9, 2048, 2, "runs"), (4100, 4099, 30, 300, 1, "one"), (4099, 4100, 1, 64, 1, "mixed")])
+def test_gradients_of_blocks_whose_waves_share_the_rows(H, m, n, r, b, count, kind):
+    """Fewer columns in all than above, more than are split 32 a block ((m + n) count ceil(r / 64) >= 8192)."""
+    c = Case(H, m, n, r, b, count, kind, seed=r + b)
+    c.check_apply(c.apply(ws=_nan_ws(H.hss_adapters_workspace_size(c.L, b))))
+    c.check_grad(c.grad(ws=_nan_ws(H.hss_adapters_grad_workspace_size(c.L, b))))
+
+
+@pytest.mark.parametrize("b,r", [(30, 16), (30, 70), (300, 40)])
+def test_two_streams_at_once(H, b, r):
+    """One bank from two streams, each with outputs and a workspace of its own, one call after another."""
+    import torch
+    cases = [Case(H, 500, 700, r, b, 5, "mixed", seed=1)]
+    cases.append(Case(H, 500, 700, r, b, 5, "each", seed=2))
+    cases[1].L, cases[1].scale = cases[0].L, cases[0].scale
+    want = [[c.apply(), *c.grad().values()] for c in cases]
+    got = [[torch.empty_like(t) for t in w] for w in want]
+    ws = [(H.adapters_workspace(c.L, b, "cuda"), H.adapters_grad_workspace(c.L, b, "cuda")) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for rep in range(10):
+        for g in got:
+            for t in g:
+                t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for c, g, w, s in zip(cases, got, ws, streams):
+                with torch.cuda.stream(s):
+                    c.apply(Y=g[0], ws=w[0])
+                    c.grad(out=dict(zip(("dX", "dU", "dVt"), g[1:])), ws=w[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, e) for g, w in zip(got, want) for a, e in zip(g, w))
+
+
 def test_the_largest_bank(H):
     """4096 adapters of 524287 x 64, r = 1: 2^31 - 4096 values of U, 4 rows, more
     gradient blocks than one row of a grid takes.  The rows' adapters against the
