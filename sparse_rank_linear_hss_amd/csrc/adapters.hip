@@ -591,25 +591,39 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
 // ---------------------------------------------------------------------------
 // Backward: the terms of T and P.  A lane has one rank of eight slots.  4 to 6 us, most
 // of it a launch and one chain of loads, instead of the sums in each block of dU, dVt and
-// dX (2048 rows 11008 x 4096 of 8, r 64: 552 of them).
+// dX (2048 rows 11008 x 4096 of 8, r 64: 1056 of them).
 // grid: (tiles, ranks / 64, sides)
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void k_ad_terms(AdArgs a) {
   const int tile = blockIdx.x, side = a.splits[0] == 0 ? 1 : (int)blockIdx.z;
-  int2 at = a.info[tile];
-  at = make_int2(uniform(at.x), uniform(at.y));
-  if (at.x < 0 || at.y == 0) return;
   const int rank = (int)blockIdx.y * 64 + (threadIdx.x & 63), i0 = 8 * (threadIdx.x >> 6);
   if (rank >= a.rp) return;
-  const float scale = a.scale ? a.scale[at.x] : 1.f;
+  const int2 info = a.info[tile];
   const int splits = a.splits[side];
   const int64_t stride = (int64_t)a.slots * a.rg;
   const float* p = a.part[side] + (int64_t)(32 * tile + i0) * a.rg + min(rank, a.rg - 1);
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int z = 0; z < splits; ++z)
+  for (int z = 0; z < splits; z += 8) {  // (the tile's adapter and rows are on their way with the first ones)
+    float x[8][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += p[z * stride + e * a.rg];
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[c][e] = p[min(z + c, splits - 1) * stride + e * a.rg];
+    if (z + 4 < splits) {
+#pragma unroll
+      for (int c = 4; c < 8; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[c][e] = p[min(z + c, splits - 1) * stride + e * a.rg];
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (z + c < splits) v[e] += x[c][e];
+  }
+  const int2 at = make_int2(uniform(info.x), uniform(info.y));
+  if (at.x < 0 || at.y == 0) return;
+  const float scale = a.scale ? a.scale[at.x] : 1.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = rank < a.r && i0 + e < at.y ? v[e] * scale : 0.f;  // a slot without a row holds anything
   // the lane of an operand that holds these eight slots of this rank (dU, dVt), or
