@@ -1103,7 +1103,7 @@ __global__ __launch_bounds__(64 * kAdFusedWaves) void k_ad_fused(AdArgs a, int n
 // The backward's last launch: blocks of dU, then of dVt (the long ones first), then of
 // dX.  Bound by memory (2048 rows 4096 x 4096 r 16: 19 us for 68 MB, 3.6 TB/s) unless one
 // adapter has most of the rows, whose blocks are a chain of 32 at a time, 1 us each (2048
-// rows 11008 x 4096 of 8, r 64: 31 us for 126 MB with the rows about even, 43 else).
+// rows 11008 x 4096 of 8, r 64: 31 us for 126 MB with the rows about even, 42 else).
 // ---------------------------------------------------------------------------
 // dX = base + scale P Vt: as k_ad_expand, with Vt's 8 x 8 pieces transposed in
 // registers: a lane's eight ranks and eight columns are eight operands.
@@ -1378,7 +1378,7 @@ __device__ __forceinline__ void ad_dfactor_wide(const AdArgs& a, int block, char
 #pragma unroll
     for (int g = 0; g < NR; ++g) acc[f][g] = f32x4{0.f, 0.f, 0.f, 0.f};
   const bool inside = c0 + 16 * CW <= cols;
-  const int from = cols >= CW ? min(c0 + CW * i, cols - CW) : 0, drop = c0 + CW * i - from;
+  const int from = min(c0 + CW * i, cols - CW), drop = c0 + CW * i - from;
   struct Regs {
     AdPiece<CW> v[8];
   };
@@ -1387,13 +1387,8 @@ __device__ __forceinline__ void ad_dfactor_wide(const AdArgs& a, int block, char
     int row[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) row[e] = a.rows[pos + 8 * q + e] * cols;
-    if (cols >= CW) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r.v[e] = ad_piece_at<CW>(src, 2u * (row[e] + from));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) r.v[e] = ad_piece_end<CW>(src + row[e], c0 + i == 0 ? cols : 0);
-    }
+    for (int e = 0; e < 8; ++e) r.v[e] = ad_piece_at<CW>(src, 2u * (row[e] + from));
   };
   u32x4 next[3];
   auto load_terms = [&](int s) {  // (past the ranks: the last piece again, not stored)
@@ -1406,7 +1401,7 @@ __device__ __forceinline__ void ad_dfactor_wide(const AdArgs& a, int block, char
     for (int k = 0; k < 3; ++k) buf[(s & 1) * kTerms + 256 * k + t] = next[k];
   };
   auto multiply = [&](int s, Regs& r) {
-    if (!inside && cols >= CW) {
+    if (!inside) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) r.v[e] = ad_drop<CW>(r.v[e], drop);
     }
@@ -1656,7 +1651,7 @@ hss_status launch_adapters_grad(const hss_adapters* A, int b, const void* X, con
   const int64_t passes = (int64_t)A->count * ((A->r + 63) / 64);
   const int64_t wide = passes * (((int64_t)A->m + 255) / 256 + (A->n + 255) / 256);
   const bool narrow = passes * ((int64_t)A->m + A->n) < 64 * 128;
-  if (b > kAdSmall && p.nr == 4 && wide >= 96) {
+  if (b > kAdSmall && p.nr == 4 && wide >= 96 && std::min(A->m, A->n) >= 4) {  // (rows of a piece at least)
     const dim3 grid = ad_back_grid(a, 256, 64);
     hipLaunchKernelGGL(k_ad_back_wide, grid, dim3(256), 2 * 4 * 3 * 64 * 16, s, a);
   } else if (p.nr == 1) {
