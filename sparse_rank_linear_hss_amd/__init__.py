@@ -1062,7 +1062,8 @@ _ADAMW_BLOCK = 256  # elements of a tensor that share one scale of the 8-bit mom
 class AdamWState:
     """What an AdamW step (hss_adamw) keeps for a list of parameters, e.g.
     [A.values, A.U, A.Vt] of every layer: contiguous tensors of any shapes, of
-    one dtype (fp32 or bf16) and on one GPU, updated in place.
+    one dtype (fp32 or bf16) and on one GPU, updated in place, in the memory that
+    they have now (a parameter that is given other memory needs a new state).
 
     bits=32: m and v in fp32.  bits=8: m and v hold the e4m3 codes of the first
     moment and of the square root of the second, each times m_scale or v_scale,
@@ -1183,7 +1184,7 @@ def hss_adamw(state: AdamWState, grads, lr, step, betas=(0.9, 0.999), eps=1e-8, 
     if isinstance(step, torch.Tensor):
         c.step_dev = _device_scalar("step", step, torch.int32, index)
     else:
-        c.step = step
+        c.step = min(max(step, 0), 1 << 31)  # (ctypes would take any number modulo 2^64; the library refuses both ends)
     if isinstance(grad_scale, torch.Tensor):
         c.grad_scale_dev = _device_scalar("grad_scale", grad_scale, torch.float32, index)
     else:

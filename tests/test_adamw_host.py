@@ -210,6 +210,16 @@ def test_steps_refuse_what_does_not_fit(hl, bound):
     assert len(calls) == 3
 
 
+@pytest.mark.parametrize("step,seen", [(2 ** 64 + 1, 1 << 31), (2 ** 31, 1 << 31), (-2 ** 64 + 1, 0), (0, 0), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_a_step_out_of_range_does_not_wrap(hl, bound, step, seen):
+    """The library refuses 0 and 2^31 (test_library_refuses)."""
+    import torch
+    calls, _ = bound
+    s = hl.AdamWState([torch.zeros(3)])
+    hl.hss_adamw(s, [torch.zeros(3)], 1e-3, step)
+    assert len(calls) == 1 and s._config.step == seen
+
+
 def test_cpu_tensors_are_refused(hl):
     import torch
     with pytest.raises(ValueError):
