@@ -49,7 +49,7 @@ struct AwTensor {
 
 struct AwHyper {
   float b1, c1, b2, c2, eps, decay, size, root, gscale;
-  double beta1, beta2, lr, wd;
+  double beta1, beta2, lr, wd, bias1;  // bias1 = 1 - beta1^step
   const float* lr_dev;
   const int32_t* step_dev;
   const float* gscale_dev;
@@ -63,6 +63,7 @@ struct AwArgs {
   int tensors;
   uint32_t chunks;
 };
+static_assert(sizeof(AwArgs) <= 4096, "kernel arguments");
 
 struct __attribute__((packed, aligned(1))) AwF8 { float f[8]; };
 struct __attribute__((packed, aligned(1))) AwU4 { uint32_t w[4]; };
@@ -192,17 +193,17 @@ __global__ __launch_bounds__(256) void k_adamw(AwArgs a) {
     __shared__ float s[6];
     if (threadIdx.x == 0) {
       const double lr = h.lr_dev ? (double)*h.lr_dev : h.lr;
-      s[0] = h.decay, s[1] = h.size, s[2] = h.root;
+      double bias1 = h.bias1;
+      s[2] = h.root;
       s[3] = h.gscale_dev ? *h.gscale_dev : h.gscale;
       s[4] = __uint_as_float(h.key);
       if (h.step_dev) {
         const int t = max(*h.step_dev, 1);
         s[4] = __uint_as_float((uint32_t)t * 0xBB67AE85u);
         s[2] = (float)(1.0 / sqrt(1.0 - pow(h.beta2, (double)t)));
-        s[1] = (float)(lr / (1.0 - pow(h.beta1, (double)t)));
-      } else if (h.lr_dev) {
-        s[1] = (float)(lr / (double)h.size);  // size holds 1 - b1^t then
+        bias1 = 1.0 - pow(h.beta1, (double)t);
       }
+      s[1] = (float)(lr / bias1);
       s[0] = (float)(1.0 - lr * h.wd);
     }
     __syncthreads();
@@ -286,8 +287,8 @@ hss_status launch_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tenso
   h.decay = (float)(1.0 - c->lr * c->weight_decay);
   h.gscale = (float)c->grad_scale;
   h.lr_dev = c->lr_dev, h.step_dev = c->step_dev, h.gscale_dev = c->grad_scale_dev;
-  const double bias1 = 1.0 - std::pow(c->beta1, (double)c->step);
-  h.size = (float)(c->lr_dev ? bias1 : c->lr / bias1);
+  h.bias1 = 1.0 - std::pow(c->beta1, (double)c->step);
+  h.size = (float)(c->lr / h.bias1);
   h.root = (float)(1.0 / std::sqrt(1.0 - std::pow(c->beta2, (double)c->step)));
   h.key = (uint32_t)c->step * 0xBB67AE85u;
   if (count == 0) return HSS_OK;

@@ -344,3 +344,28 @@ def test_a_million_elements_a_tensor(H):
     c = Case(H, [4_500_001, 5], "bf16+f32", "f32", 8, seed=12)
     H.hss_adamw(c.state, c.dev["grad"], lr=1e-3, step=100)
     c.check(100)
+
+
+@pytest.mark.parametrize("on", ["lr", "lr and grad_scale", "lr and step"])
+def test_a_rate_on_the_device_rounds_as_the_number(H, on):
+    """The step's size lr / (1 - b1^t), in fp64 and rounded once, wherever lr is: the bits of the number
+    at 1000 steps of several rates, from p = 0, where p = -size * quotient shows the size's last bit."""
+    import torch
+    rates = [float(np.float32(x)) for x in (1e-3, 3e-4, 1e-4, 0.7, 6.1e-6)]
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    g = torch.randn(64, device="cuda", generator=gen)
+    states = [H.AdamWState([torch.zeros(64, device="cuda")]) for _ in range(2)]
+    lr = torch.zeros(1, device="cuda")
+    scale = torch.full((1,), 0.5, device="cuda")
+    steps = torch.arange(1, 1001, dtype=torch.int32, device="cuda")
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    assert any(np.float32(x / np.float32(1 - 0.9 ** t)) != np.float32(x / (1 - 0.9 ** t)) for x in rates for t in range(1, 9))
+    for x in rates:
+        lr.fill_(x)
+        for t in range(1, 1001):
+            for s in states:
+                s.params[0].zero_()
+            H.hss_adamw(states[0], [g], lr=x, step=t, grad_scale=0.5)
+            H.hss_adamw(states[1], [g], lr=lr, step=steps[t - 1] if "step" in on else t, grad_scale=scale if "grad" in on else 0.5)
+            wrong += (states[0].params[0] != states[1].params[0]).sum()
+    assert wrong.item() == 0
