@@ -144,11 +144,12 @@ __device__ __forceinline__ float aw_decode(uint32_t code) {
 }
 
 // x / scale (inv = 1 / scale) as a code: u / 2^16 of a step is added, and what is
-// then below the step dropped.  `least`: the smallest code of an x that is not 0.
+// then below the step dropped, in integers: a sum in fp32 would round up to the next
+// code where little is missing.  `least`: the smallest code of an x that is not 0.
 __device__ __forceinline__ uint32_t aw_encode(float x, float inv, uint32_t u, uint32_t least) {
   const float a = fminf(fabsf(x) * inv, 448.f);
   const uint32_t normal = ((__float_as_uint(a) + (u << 4)) >> 20) - 960u;
-  const uint32_t small = (uint32_t)(a * 512.f + (float)u * 0x1p-16f);
+  const uint32_t small = ((uint32_t)fminf(a * 0x1p25f, 0x1p20f) + u) >> 16;  // steps of 2^-9 (below 2^-6: less than 2^19)
   uint32_t k = min(a < 0x1p-6f ? small : normal, 126u);
   if (x != 0.f) k = max(k, least);
   return k | (__float_as_uint(x) >> 31) << 7;

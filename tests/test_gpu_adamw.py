@@ -369,3 +369,28 @@ def test_a_rate_on_the_device_rounds_as_the_number(H, on):
             H.hss_adamw(states[1], [g], lr=lr, step=steps[t - 1] if "step" in on else t, grad_scale=scale if "grad" in on else 0.5)
             wrong += (states[0].params[0] != states[1].params[0]).sum()
     assert wrong.item() == 0
+
+
+def test_small_codes_round_as_they_are_defined(H):
+    """Values below the codes' smallest step, 2^-9 of a scale: the upper code only where share + u / 2^16 >=
+    1, exactly.  At the elements whose random numbers are the largest, shares just below 1 - u / 2^16, by
+    less than fp32 tells from 1 once the two are added."""
+    import torch
+    n, step = 1 << 18, 1
+    h = O.adamw_hash(np.arange(n), step)
+    g = np.full(n, 1e-6, np.float32)
+    g[::256] = 1.0                                                       # the blocks' largest
+    m1 = np.float32(1.0 - 0.9) * np.float32(1.0)
+    scale = m1 * np.float32(1.0 / 448)
+    u = (h & 0xffff).astype(np.int64)
+    at = np.flatnonzero((u >= 65536 - 64) & (np.arange(n) % 256 != 0))
+    share = (65536 - u[at]) / 65536.0 * (1 - 2.0 ** -16)
+    g[at] = (share / 512 * float(scale) / float(np.float32(1.0 - 0.9))).astype(np.float32)
+    m = np.float32(1.0 - 0.9) * g
+    want = O.moment8_encode(m, O.moment8_scales(m), h & 0xffff, 0)
+    a = np.abs(m) * (np.float32(1) / scale)
+    summed = (a[at] * np.float32(512) + u[at].astype(np.float32) * np.float32(2.0 ** -16)).astype(np.int64)
+    assert len(at) > 50 and not want[at].any() and np.count_nonzero(summed) > 50      # what a sum in fp32 would give
+    s = H.AdamWState([torch.zeros(n, device="cuda")], bits=8)
+    H.hss_adamw(s, [torch.from_numpy(g).cuda()], lr=1e-3, step=step)
+    assert np.array_equal(s.m[0].view(torch.uint8).cpu().numpy(), want)
