@@ -309,7 +309,10 @@ hss_status launch_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tenso
       pos += blocks;
     }
     for (int k = 0; k < 64; ++k) a.first[k] = k < a.tensors ? a.t[k].first : 0xffffffffu;
-    if (!a.tensors) return HSS_OK;  // only tensors without elements or gradients were left
+    if (!a.tensors) {  // only tensors without elements or gradients were left
+      if (!pos) return HSS_OK;  // nothing was launched
+      break;
+    }
     // A workgroup for each chunk (38 M elements, fp32 and 8-bit moments: 210 and 130
     // us; 2048 workgroups that go round 237 and 150), but for device scalars, whose
     // powers each workgroup computes.  (A launch takes fewer than 2^32 threads.)

@@ -224,3 +224,35 @@ def test_cpu_tensors_are_refused(hl):
     import torch
     with pytest.raises(ValueError):
         hl.AdamWState([torch.zeros(3)])
+
+
+_NO_DEVICE = """
+import ctypes, sys
+import torch
+assert torch.cuda.device_count() == 0
+import sparse_rank_linear_hss_amd as hl
+live, left_out = int(sys.argv[1]), int(sys.argv[2])
+n = live + left_out
+c = hl._lib.HssAdamwConfigStruct(bits=32, dtype=0, grad_dtype=0, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
+                                 weight_decay=0.01, grad_scale=1.0, step=1)
+t, g = (hl._lib.HssAdamwTensorStruct * n)(), (ctypes.c_void_p * n)()
+for k in range(n):
+    at = (k + 1) << 24
+    t[k].count, t[k].param, t[k].m, t[k].v = 8, at, at + 4096, at + 8192
+    g[k] = at + 12288 if k < live else None
+print("status", hl._lib.lib.hss_adamw(ctypes.byref(c), t, g, n, None))
+"""
+
+
+@pytest.mark.parametrize("live,left_out", [(1, 0), (48, 0), (48, 1), (96, 7), (50, 3), (0, 5)])
+def test_a_launch_that_fails_is_reported(hl, live, left_out):
+    """On no device every launch fails, and the call says so, also where nothing but tensors without
+    gradients comes after the last full launch (of 48 tensors)."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _NO_DEVICE, str(live), str(left_out)], cwd=root, capture_output=True, text=True,
+                       timeout=300, env=dict(os.environ, HIP_VISIBLE_DEVICES="-1"))
+    want = hl._lib.HSS_ERR_HIP if live else hl._lib.HSS_OK
+    assert r.stdout.split()[-2:] == ["status", str(want)], r.stdout + r.stderr
