@@ -752,7 +752,7 @@ hss_status hss_adapters_grad(const hss_adapters* L, int32_t b, const void* X, co
  * HSS_ERR_INVALID_ARG: null config, tensors or grads (with count > 0) or arrays
  *   (of a tensor with elements and a gradient), count < 0, a tensor's count < 0 or >= 2^31, all of
  *   them 2^39 elements or more, unknown bits or types, master with fp32 parameters,
- *   misaligned arrays, arrays of one tensor that overlap, beta1 or beta2 outside
+ *   misaligned arrays or device scalars, arrays of one tensor that overlap, beta1 or beta2 outside
  *   [0, 1), eps < 0, a number that is not finite, step outside [1, 2^31).
  *   HSS_ERR_HIP.
  */

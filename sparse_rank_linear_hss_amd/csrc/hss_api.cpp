@@ -687,6 +687,8 @@ hss_status hss_adamw(const hss_adamw_config* c, const hss_adamw_tensor* tensors,
     if (!std::isfinite(x)) return HSS_ERR_INVALID_ARG;
   if (c->beta1 < 0 || c->beta1 >= 1 || c->beta2 < 0 || c->beta2 >= 1 || c->eps < 0 || c->step < 1 || c->step >= kLimit)
     return HSS_ERR_INVALID_ARG;
+  if ((uintptr_t)c->lr_dev % 4 != 0 || (uintptr_t)c->step_dev % 4 != 0 || (uintptr_t)c->grad_scale_dev % 4 != 0)
+    return HSS_ERR_INVALID_ARG;
   int64_t total = 0;
   for (int32_t i = 0; i < count; ++i) {
     const hss_adamw_tensor& t = tensors[i];

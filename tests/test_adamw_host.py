@@ -256,3 +256,13 @@ def test_a_launch_that_fails_is_reported(hl, live, left_out):
                        timeout=300, env=dict(os.environ, HIP_VISIBLE_DEVICES="-1"))
     want = hl._lib.HSS_ERR_HIP if live else hl._lib.HSS_OK
     assert r.stdout.split()[-2:] == ["status", str(want)], r.stdout + r.stderr
+
+
+def test_scalars_off_their_grid_are_refused(hl):
+    """The kernel reads a device scalar by its aligned word."""
+    INV = hl._lib.HSS_ERR_INVALID_ARG
+    for name in ("lr_dev", "step_dev", "grad_scale_dev"):
+        for off in (1, 2, 3):
+            assert _call(hl, **{name: 40 * FAKE + off}) == INV, (name, off)
+            assert _call(hl, n=0, **{name: 40 * FAKE + off}) == INV, (name, off)
+        assert _call(hl, n=0, **{name: 40 * FAKE + 4}) == hl._lib.HSS_OK
