@@ -1057,13 +1057,16 @@ def hss_adapters_grad(L: HSSAdapters, X: torch.Tensor, G: torch.Tensor, ids: tor
 # ---------------------------------------------------------------------------
 
 _ADAMW_BLOCK = 256  # elements of a tensor that share one scale of the 8-bit moments
+_data_ptr = torch.Tensor.data_ptr
 
 
 class AdamWState:
     """What an AdamW step (hss_adamw) keeps for a list of parameters, e.g.
     [A.values, A.U, A.Vt] of every layer: contiguous tensors of any shapes, of
     one dtype (fp32 or bf16) and on one GPU, updated in place, in the memory that
-    they have now (a parameter that is given other memory needs a new state).
+    they have now: a step refuses a parameter that was given other memory since
+    (by `p.data = ..`, a module's .to()), which needs a new state, made with the
+    moments of this one.  The state's own tensors are changed in place, if at all.
 
     bits=32: m and v in fp32.  bits=8: m and v hold the e4m3 codes of the first
     moment and of the square root of the second, each times m_scale or v_scale,
@@ -1071,8 +1074,8 @@ class AdamWState:
     master=True keeps an fp32 copy of bf16 parameters, which the step reads and
     writes in their place (bf16 alone loses updates below 2^-9 of a value).
 
-    A new state starts from zeros.  To restore one, pass the lists that it held:
-    m, v (float32, or float8_e4m3fn with bits=8), m_scale, v_scale, master."""
+    A new state starts from zeros.  To restore one, pass what it held: m, v
+    (float32, or float8_e4m3fn with bits=8), m_scale, v_scale, master."""
 
     def __init__(self, params, bits=32, master=None, m=None, v=None, m_scale=None, v_scale=None):
         params = list(params)
@@ -1112,21 +1115,25 @@ class AdamWState:
             if dtype != torch.bfloat16:
                 raise ValueError("a master copy goes with bf16 parameters")
             master = kept("master", master, torch.float32, counts, None)
-        self.params, self.master, self.bits, self.dtype, self.index = params, master, bits, dtype, index
-        self.m, self.v = kept("m", m, moment, counts, zeros), kept("v", v, moment, counts, zeros)
+        self.bits, self.dtype, self.index = bits, dtype, index
+        self.params, self.master = tuple(params), None if master is None else tuple(master)
+        self.m, self.v = tuple(kept("m", m, moment, counts, zeros)), tuple(kept("v", v, moment, counts, zeros))
         self.m_scale = self.v_scale = None
         if bits == 8:
-            self.m_scale = kept("m_scale", m_scale, torch.float32, blocks, zeros)
-            self.v_scale = kept("v_scale", v_scale, torch.float32, blocks, zeros)
+            self.m_scale = tuple(kept("m_scale", m_scale, torch.float32, blocks, zeros))
+            self.v_scale = tuple(kept("v_scale", v_scale, torch.float32, blocks, zeros))
         elif m_scale is not None or v_scale is not None:
             raise ValueError("scales go with bits=8")
-        held = [t for ts in (params, master, self.m, self.v, self.m_scale, self.v_scale) if ts is not None for t in ts]
+        own = [t for ts in (self.master, self.m, self.v, self.m_scale, self.v_scale) if ts is not None for t in ts]
         end = 0
-        for a, z in sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in held if t.numel()):
+        for a, z in sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in params + own if t.numel()):
             if a < end:
                 raise ValueError("the tensors of a state must not share memory")
             end = z
         self.counts = counts
+        # steps write to the addresses below: the parameters' are compared first, the rest is kept
+        self._addresses = [*map(_data_ptr, params)]
+        self._memory = [t.untyped_storage() for t in own]
         self._tensors = (HssAdamwTensorStruct * len(params))()
         for k, t in enumerate(self._tensors):
             t.count, t.param, t.m, t.v = counts[k], _ptr(params[k]), _ptr(self.m[k]), _ptr(self.v[k])
@@ -1166,12 +1173,19 @@ def hss_adamw(state: AdamWState, grads, lr, step, betas=(0.9, 0.999), eps=1e-8, 
     grads, counts = list(grads), state.counts
     if len(grads) != len(counts):
         raise ValueError(f"{len(counts)} parameters, {len(grads)} gradients")
+    if [*map(_data_ptr, state.params)] != state._addresses:
+        raise ValueError("a parameter has other memory than when the state was made: make a new one with this one's moments")
     dtype = next((g.dtype for g in grads if g is not None), torch.float32)
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype}: float32 or bfloat16")
+    pointers = []
     for g, k in zip(grads, counts):
-        if g is not None and (g.numel() != k or g.dtype is not dtype or g.get_device() != index or not g.is_contiguous()):
+        if g is None:
+            pointers.append(None)
+            continue
+        if g.numel() != k or g.dtype is not dtype or g.get_device() != index or not g.is_contiguous():
             raise ValueError("grads: contiguous tensors of one dtype, of their parameters' element counts and device")
+        pointers.append(g.data_ptr())
     c = state._config
     c.grad_dtype = _DT[dtype]
     c.beta1, c.beta2, c.eps, c.weight_decay = betas[0], betas[1], eps, weight_decay
@@ -1189,7 +1203,6 @@ def hss_adamw(state: AdamWState, grads, lr, step, betas=(0.9, 0.999), eps=1e-8, 
         c.grad_scale_dev = _device_scalar("grad_scale", grad_scale, torch.float32, index)
     else:
         c.grad_scale = grad_scale
-    pointers = state._grads(*[None if g is None else g.data_ptr() for g in grads])
-    code = lib.hss_adamw(state._ref, state._tensors, pointers, len(grads), _raw_stream(index))
+    code = lib.hss_adamw(state._ref, state._tensors, state._grads(*pointers), len(pointers), _raw_stream(index))
     if code:
         check(code, "hss_adamw")

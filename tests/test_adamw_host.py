@@ -266,3 +266,37 @@ def test_scalars_off_their_grid_are_refused(hl):
             assert _call(hl, **{name: 40 * FAKE + off}) == INV, (name, off)
             assert _call(hl, n=0, **{name: 40 * FAKE + off}) == INV, (name, off)
         assert _call(hl, n=0, **{name: 40 * FAKE + 4}) == hl._lib.HSS_OK
+
+
+def test_a_step_refuses_parameters_with_other_memory(hl, bound):
+    """The state holds the addresses that the step writes to: a parameter's memory may be someone else's
+    by now.  Moments whose tensor was given other memory keep what the step writes to."""
+    import gc
+    import weakref
+
+    import torch
+    calls, _ = bound
+    p, q = torch.nn.Parameter(torch.zeros(300)), torch.zeros(20)
+    s = hl.AdamWState([p, q])
+    hl.hss_adamw(s, [None, torch.zeros(20)], 1e-3, 1)
+    held = p.data
+    p.data = torch.ones(300)
+    for grads in ([torch.zeros(300), None], [None, torch.zeros(20)], [None, None]):
+        with pytest.raises(ValueError, match="memory"):
+            hl.hss_adamw(s, grads, 1e-3, 1)
+    p.data = held                                                       # the old memory again
+    hl.hss_adamw(s, [torch.zeros(300), None], 1e-3, 1)
+    q.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="memory"):
+        hl.hss_adamw(s, [torch.zeros(300), None], 1e-3, 1)
+    assert len(calls) == 2
+    with pytest.raises(TypeError):
+        s.m[0] = torch.zeros(300)
+    own = np.ones(64, np.float32)
+    alive = weakref.ref(own)
+    m = torch.from_numpy(own)
+    s = hl.AdamWState([torch.zeros(64)], m=[m])
+    m.data = torch.zeros(64)
+    del own
+    gc.collect()
+    assert alive() is not None
