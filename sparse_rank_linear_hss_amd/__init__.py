@@ -1058,6 +1058,7 @@ def hss_adapters_grad(L: HSSAdapters, X: torch.Tensor, G: torch.Tensor, ids: tor
 
 _ADAMW_BLOCK = 256  # elements of a tensor that share one scale of the 8-bit moments
 _data_ptr = torch.Tensor.data_ptr
+_increment_version = torch.autograd.graph.increment_version
 
 
 class AdamWState:
@@ -1165,7 +1166,11 @@ def hss_adamw(state: AdamWState, grads, lr, step, betas=(0.9, 0.999), eps=1e-8, 
 
     With bits=8 the new moments are rounded up or down at random, in proportion,
     by a hash of the element's position and the step; the same call gives the
-    same bits."""
+    same bits.
+
+    To autograd the parameters with a gradient are changed in place: a backward
+    pass that has saved their old values raises an error.  (The replay of a
+    captured step cannot tell it so.)"""
     index = state.index
     if index != _current_device():
         with torch.cuda.device(index):
@@ -1206,3 +1211,4 @@ def hss_adamw(state: AdamWState, grads, lr, step, betas=(0.9, 0.999), eps=1e-8, 
     code = lib.hss_adamw(state._ref, state._tensors, state._grads(*pointers), len(pointers), _raw_stream(index))
     if code:
         check(code, "hss_adamw")
+    _increment_version(state.params if None not in pointers else [p for p, g in zip(state.params, pointers) if g is not None])

@@ -300,3 +300,23 @@ def test_a_step_refuses_parameters_with_other_memory(hl, bound):
     del own
     gc.collect()
     assert alive() is not None
+
+
+def test_a_step_is_a_change_in_place_for_autograd(hl, bound):
+    """A backward pass that has saved a parameter's old values is refused after the step, as after any
+    change in place; a parameter that the step leaves alone stays usable."""
+    import torch
+    w, o = torch.nn.Parameter(torch.ones(8)), torch.nn.Parameter(torch.ones(8))
+    x = torch.ones(8, requires_grad=True)
+    s = hl.AdamWState([w, o])
+    y, z = (x * w).sum(), (x * o).sum()
+    hl.hss_adamw(s, [torch.zeros(8), None], 1e-3, 1)
+    z.backward()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        s = hl.AdamWState([torch.zeros(8)])
+        hl.hss_adamw(s, [torch.zeros(8)], 1e-3, 1)
+    with pytest.raises(ValueError):                                     # a refused step changes nothing
+        hl.hss_adamw(hl.AdamWState([w]), [torch.zeros(9)], 1e-3, 1)
+    (x * w).sum().backward()
