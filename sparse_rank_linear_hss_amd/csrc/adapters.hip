@@ -339,10 +339,16 @@ __device__ __forceinline__ uint32_t ad_pack(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, mx_bf16x2));
 }
 
+// A finite value past bf16's largest, which would round to an infinity, cut to the
+// largest; any other as it is.
+__device__ __forceinline__ float ad_cut(float x) {
+  return fabsf(x) > 0x1.fep127f ? __uint_as_float(__float_as_uint(x) & 0xffff0000u) : x;
+}
+
 // The next bf16 terms of two values, which lose them (an infinity leaves 0, not the
 // NaN of inf - inf).
 __device__ __forceinline__ uint32_t ad_term2(float& x, float& y) {
-  const uint32_t t = ad_pack(x, y);
+  const uint32_t t = ad_pack(ad_cut(x), ad_cut(y));
   x = (t & 0x7fffu) == 0x7f80u ? 0.f : x - bf16lo(t);
   y = (t & 0x7fff0000u) == 0x7f800000u ? 0.f : y - bf16hi(t);
   return t;

@@ -467,3 +467,37 @@ def test_a_decode_batch_and_a_prefill_at_full_size(H):
         for got, want, N, K in ((g["dU"][l, js], s * c.f["G"][mine][:, js].T @ T, abs(s) * np.abs(c.f["G"][mine][:, js]).T @ aT, 11008),
                                 (g["dVt"][l][:, js], s * P.T @ c.f["X"][mine][:, js], abs(s) * aP.T @ np.abs(c.f["X"][mine][:, js]), 4096)):
             assert np.all(np.abs(got.double().cpu().numpy() - want) <= 1.01 * (K + 3 * len(mine) + 3) * U24 * N)
+
+
+@pytest.mark.parametrize("b,m,n,r", [(1, 600, 600, 8), (64, 600, 600, 40), (5, 1100, 1100, 3), (70, 600, 600, 20), (70, 1100, 1300, 65)])
+def test_finite_products_past_the_largest_bf16(H, b, m, n, r):
+    """T and P of 2^128 - 2^118, a finite fp32 that bf16 rounds to infinity, times 2^-100 of the next
+    factor: outputs of 2^28 (1 - 2^-10), not infinities."""
+    import torch
+    top = [2.0 ** 128 - 2.0 ** 120, 2.0 ** 119, 2.0 ** 118]
+    scale = np.array([1.0, -1.0], np.float32)
+    ids = np.arange(b) % 2
+    tall = lambda shape: np.broadcast_to(np.array(top + [0.0] * (shape[1] - 3)), shape)   # noqa: E731
+    first = np.zeros(r)
+    first[r - 1] = 1.0
+    for grad in (False, True):
+        # forward: X tall, Vt ones, U 2^-100; dU of it with G 2^-100.  Backward: G tall, U ones, Vt and X 2^-100
+        X = np.full((b, n), 2.0 ** -100) if grad else tall((b, n))
+        G = tall((b, m)) if grad else np.full((b, m), 2.0 ** -100)
+        U = np.broadcast_to(first * (1.0 if grad else 2.0 ** -100), (2, m, r))
+        Vt = np.broadcast_to((first * (2.0 ** -100 if grad else 1.0))[:, None], (2, r, n))
+        dev = [torch.from_numpy(np.array(a)).to("cuda", torch.bfloat16) for a in (U, Vt, X, G)]
+        assert all(np.array_equal(t.double().cpu().numpy(), a) for t, a in zip(dev, (U, Vt, X, G)))
+        L = H.HSSAdapters(dev[0], dev[1], torch.from_numpy(scale).cuda())
+        ids_d = torch.from_numpy(ids.astype(np.int32)).cuda()
+        want = O.adapters_grad(U, Vt, scale.astype(np.float64), X, G, ids)
+        got = H.hss_adapters_grad(L, dev[2], dev[3], ids_d, dX=grad, dU=not grad, dVt=grad)
+        # every sum has terms of one sign: as at the top, with |value| for N
+        for key, w, bound in (("dX", want[0], 2.0 ** -8 + (m + 2 * r + 3) * U24 + 2.0 ** -16), ("dU", want[1], (n + 3 * b + 3) * U24),
+                              ("dVt", want[2], (m + 3 * b + 3) * U24)):
+            if key in got:
+                assert np.all(np.abs(got[key].double().cpu().numpy() - w) <= 1.01 * bound * np.abs(w)), key
+        if not grad:
+            Y = H.hss_adapters_apply(L, dev[2], ids_d).double().cpu().numpy()
+            want = O.adapters_apply(U, Vt, scale.astype(np.float64), X, ids)
+            assert np.all(np.abs(Y - want) <= 1.01 * (2.0 ** -8 + (n + 2 * r + 3) * U24 + 2.0 ** -16) * np.abs(want))
