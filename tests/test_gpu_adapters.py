@@ -501,3 +501,65 @@ def test_finite_products_past_the_largest_bf16(H, b, m, n, r):
             Y = H.hss_adapters_apply(L, dev[2], ids_d).double().cpu().numpy()
             want = O.adapters_apply(U, Vt, scale.astype(np.float64), X, ids)
             assert np.all(np.abs(Y - want) <= 1.01 * (2.0 ** -8 + (n + 2 * r + 3) * U24 + 2.0 ** -16) * np.abs(want))
+
+
+@pytest.mark.parametrize("m,n,r,b,count,kind", [
+    (11003, 520, 9, 64, 64, "each"), (5003, 520, 16, 64, 9, "mixed"), (11003, 517, 32, 64, 12, "mixed"),
+    (5003, 520, 32, 64, 64, "each"), (11003, 520, 16, 40, 7, "one"), (16384, 64, 8, 64, 5, "mixed")])
+@pytest.mark.parametrize("based", [True, False])
+def test_one_launch_of_many_column_blocks(H, m, n, r, b, count, kind, based):
+    """Few rows and small factors, more column blocks than compute units (ceil(m / 512) b > 256): a
+    block goes through 2 to 8 times 512 columns, with and without base, and in place."""
+    import torch
+    c = Case(H, m, n, r, b, count, kind, seed=m + r, based=based)
+    Y = c.apply()
+    c.check_apply(Y)
+    if based:
+        again = c.d["base"].clone()
+        H.hss_adapters_apply(c.L, c.d["X"], c.ids_d, base=again, Y=again)
+        assert torch.equal(again, Y)
+
+
+@pytest.mark.parametrize("m,n,r,b,count,kind", [
+    (4099, 200, 40, 64, 64, "each"), (4099, 200, 40, 2048, 3, "mixed"), (11003, 96, 33, 2048, 5, "runs"),
+    (4099, 130, 300, 2048, 3, "mixed"), (4610, 130, 5, 2048, 2, "mixed"), (65539, 72, 257, 64, 2, "mixed")])
+@pytest.mark.parametrize("based", [True, False])
+def test_many_column_blocks_a_tile(H, m, n, r, b, count, kind, based):
+    """ceil(m / 512) times the busy tiles >= 512: a block goes through several times 512 columns, the
+    last of them ragged, with ranks that are kept in LDS at once and ranks (past 256) that are not."""
+    import torch
+    c = Case(H, m, n, r, b, count, kind, seed=m + r, based=based)
+    Y = c.apply(ws=_nan_ws(H.hss_adapters_workspace_size(c.L, b)))
+    c.check_apply(Y)
+    if based:
+        again = c.d["base"].clone()
+        H.hss_adapters_apply(c.L, c.d["X"], c.ids_d, base=again, Y=again)
+        assert torch.equal(again, Y)
+
+
+@pytest.mark.parametrize("m,n,r,count", [(4, 257, 33, 64), (5, 300, 64, 40), (258, 4, 200, 20), (700, 5, 49, 33), (4, 4, 64, 60)])
+@pytest.mark.parametrize("b,kind", [(65, "mixed"), (300, "runs"), (515, "one")])
+def test_shared_terms_with_rows_of_four_columns(H, m, n, r, count, b, kind):
+    """The shortest rows that the blocks of 256 columns take, of which most lanes have none."""
+    import torch
+    c = Case(H, m, n, r, b, count, kind, seed=r + b, shift=b % 2)
+    full = c.grad(ws=_nan_ws(H.hss_adapters_grad_workspace_size(c.L, b)))
+    c.check_grad(full)
+    for keys in (("dU",), ("dVt",)):
+        got = c.grad(**{k: k in keys for k in ("dX", "dU", "dVt")})
+        assert all(torch.equal(got[k], full[k]) for k in keys)
+
+
+@pytest.mark.parametrize("m,n,r,b,count,kind", [(11008, 4096, 64, 2048, 8, "runs"), (11008, 4096, 64, 2048, 8, "one"),
+                                                (4096, 4096, 16, 2048, 1, "one")])
+def test_same_bits_again_at_full_size(H, m, n, r, b, count, kind):
+    """One call after another without a wait, another input's between them, one workspace for all."""
+    import torch
+    a, o = (Case(H, m, n, r, b, count, kind, seed=s) for s in (1, 20))
+    ws, gws = H.adapters_workspace(a.L, b, "cuda"), H.adapters_grad_workspace(a.L, b, "cuda")
+    want = [a.apply(), *a.grad().values()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [a.apply(ws=ws), *a.grad(ws=gws).values()]
+        o.apply(ws=ws), o.grad(ws=gws)
+        assert all(torch.equal(x, w) for x, w in zip(got, want))
