@@ -486,7 +486,7 @@ def test_finite_products_past_the_largest_bf16(H, b, m, n, r):
         G = tall((b, m)) if grad else np.full((b, m), 2.0 ** -100)
         U = np.broadcast_to(first * (1.0 if grad else 2.0 ** -100), (2, m, r))
         Vt = np.broadcast_to((first * (2.0 ** -100 if grad else 1.0))[:, None], (2, r, n))
-        dev = [torch.from_numpy(np.array(a)).to("cuda", torch.bfloat16) for a in (U, Vt, X, G)]
+        dev = [torch.from_numpy(np.array(a, order="C")).to("cuda", torch.bfloat16) for a in (U, Vt, X, G)]
         assert all(np.array_equal(t.double().cpu().numpy(), a) for t, a in zip(dev, (U, Vt, X, G)))
         L = H.HSSAdapters(dev[0], dev[1], torch.from_numpy(scale).cuda())
         ids_d = torch.from_numpy(ids.astype(np.int32)).cuda()
