@@ -1647,17 +1647,28 @@ hss_status launch_adapters_grad(const hss_adapters* A, int b, const void* X, con
     const dim3 grid(a.tiles, (a.rp + 63) / 64, a.splits[0] && a.splits[1] ? 2 : 1);
     hipLaunchKernelGGL(k_ad_terms, grid, dim3(256), 0, s, a);
   }
-  // dU and dVt by blocks of 256 columns that share the terms, where there are 96 of
-  // them; else by blocks of 64 whose waves share the rows (2048 rows r 64: 4096 x
-  // 4096 of 2, 64 blocks, 54.2 and 47.7 us; of 3, 96 blocks, 46.6 and 52.8; of 8 11008
-  // x 4096, 472 blocks, 60.6 and 76.3).  With up to 32 ranks there are few terms to share.
+  // dU and dVt by blocks of 256 columns that share the terms, where there are enough of
+  // them; else by blocks of 64 whose waves share the rows.  The first walk all of an
+  // adapter's rows one tile after another, so that many rows an adapter ask for more of
+  // them (us with 256 and with 64, rows even):
+  //   2048 rows an adapter: 118 blocks (11008 x 4096 r 128 of 1) 103 and 90, 128 (8192 x
+  //     8192 r 128) 103 and 93, 144 (8192 x 4096 r 192) 104 and 111, 236 (11008 x 4096 r 256) 123 and 143
+  //   1024: 118 (11008 x 4096 r 64 of 2) 64.9 and 60.6, 128 (4096 x 4096 r 256 of 1) 54.8
+  //     and 51.9, (8192 x 8192 r 64 of 2) 65.7 and 68.0, 150 (11008 x 8192 of 2) 75.6 and 83.9
+  //   682: 96 (4096 x 4096 r 64 of 3) 45.4 and 42.2, 177 (11008 x 4096 of 3) 57.8 and 68.6
+  //   512: 118 (11008 x 4096 r 128 of 1) 38.4 and 38.9, 128 (4096 x 4096 r 64 of 4) 39.1 and 41.2
+  //   256: 64 (4096 x 4096 r 64 of 2) 27.0 and 26.9, 118 (11008 x 4096 of 2) 29.0 and 31.0, 472
+  //     (of 8) 61.6 and 76.7; with half of the 2048 rows on one adapter of the 8 76.7 and 75.7,
+  //     all of them 110.6 and 75.5, which the host does not see.
+  // With up to 32 ranks there are few terms to share.
   // Very few columns in all are split further, 32 a block (r 16, 512 rows 1024 x 1024
   // of 1 13.8 and 15.1 us, of 4, where the rule ends, 13.9 and 12.8; r 64, 201 rows
   // 1501 x 2777 of 1 18.8 and 21.0, of 2 20.1 and 19.6).
   const int64_t passes = (int64_t)A->count * ((A->r + 63) / 64);
   const int64_t wide = passes * (((int64_t)A->m + 255) / 256 + (A->n + 255) / 256);
+  const int64_t enough = b / std::min(b, A->count) >= 640 ? 136 : 96;
   const bool narrow = passes * ((int64_t)A->m + A->n) < 64 * 128;
-  if (b > kAdSmall && p.nr == 4 && wide >= 96 && std::min(A->m, A->n) >= 4) {  // (rows of a piece at least)
+  if (b > kAdSmall && p.nr == 4 && wide >= enough && std::min(A->m, A->n) >= 4) {  // (rows of a piece at least)
     const dim3 grid = ad_back_grid(a, 256, 64);
     hipLaunchKernelGGL(k_ad_back_wide, grid, dim3(256), 2 * 4 * 3 * 64 * 16, s, a);
   } else if (p.nr == 1) {

@@ -563,3 +563,13 @@ def test_same_bits_again_at_full_size(H, m, n, r, b, count, kind):
         got = [a.apply(ws=ws), *a.grad(ws=gws).values()]
         o.apply(ws=ws), o.grad(ws=gws)
         assert all(torch.equal(x, w) for x, w in zip(got, want))
+
+
+@pytest.mark.parametrize("m,n,r,b,count,kind", [
+    (4100, 3001, 200, 700, 1, "one"), (4100, 3001, 300, 700, 1, "one"), (4100, 3001, 200, 600, 1, "one"),
+    (5003, 4099, 65, 1300, 2, "runs"), (5003, 4099, 130, 1300, 2, "mixed")])
+def test_gradients_of_many_rows_an_adapter(H, m, n, r, b, count, kind):
+    """On both sides of where their blocks share the terms: 96 blocks of 256 columns up to 640 rows an adapter,
+    136 beyond (here 116, 145, 116, 148 and 222)."""
+    c = Case(H, m, n, r, b, count, kind, seed=r + b)
+    c.check_grad(c.grad(ws=_nan_ws(H.hss_adapters_grad_workspace_size(c.L, b))))
