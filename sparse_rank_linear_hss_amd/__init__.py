@@ -1057,7 +1057,7 @@ def hss_adapters_grad(L: HSSAdapters, X: torch.Tensor, G: torch.Tensor, ids: tor
 # ---------------------------------------------------------------------------
 
 _ADAMW_BLOCK = 256  # elements of a tensor that share one scale of the 8-bit moments
-_data_ptr = torch.Tensor.data_ptr
+_data_ptr, _numel, _is_contiguous = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
 _increment_version = torch.autograd.graph.increment_version
 
 
@@ -1180,17 +1180,23 @@ def hss_adamw(state: AdamWState, grads, lr, step, betas=(0.9, 0.999), eps=1e-8, 
         raise ValueError(f"{len(counts)} parameters, {len(grads)} gradients")
     if [*map(_data_ptr, state.params)] != state._addresses:
         raise ValueError("a parameter has other memory than when the state was made: make a new one with this one's moments")
-    dtype = next((g.dtype for g in grads if g is not None), torch.float32)
+    # (a step of a few thousand elements is bound by its host side: one pass for each question)
+    try:
+        pointers = [*map(_data_ptr, grads)]
+        live, sizes, params = grads, counts, state.params
+    except TypeError:  # some have no gradient
+        there = [k for k, g in enumerate(grads) if g is not None]
+        pointers = [None if g is None else g.data_ptr() for g in grads]
+        live, sizes, params = [grads[k] for k in there], [counts[k] for k in there], [state.params[k] for k in there]
+    dtype = live[0].dtype if live else torch.float32
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype}: float32 or bfloat16")
-    pointers = []
-    for g, k in zip(grads, counts):
-        if g is None:
-            pointers.append(None)
-            continue
-        if g.numel() != k or g.dtype is not dtype or g.get_device() != index or not g.is_contiguous():
-            raise ValueError("grads: contiguous tensors of one dtype, of their parameters' element counts and device")
-        pointers.append(g.data_ptr())
+    fits = [*map(_numel, live)] == sizes and all(map(_is_contiguous, live))
+    for g in live:
+        if g.dtype is not dtype or g.get_device() != index:
+            fits = False
+    if not fits:
+        raise ValueError("grads: contiguous tensors of one dtype, of their parameters' element counts and device")
     c = state._config
     c.grad_dtype = _DT[dtype]
     c.beta1, c.beta2, c.eps, c.weight_decay = betas[0], betas[1], eps, weight_decay
@@ -1211,4 +1217,4 @@ def hss_adamw(state: AdamWState, grads, lr, step, betas=(0.9, 0.999), eps=1e-8, 
     code = lib.hss_adamw(state._ref, state._tensors, state._grads(*pointers), len(pointers), _raw_stream(index))
     if code:
         check(code, "hss_adamw")
-    _increment_version(state.params if None not in pointers else [p for p, g in zip(state.params, pointers) if g is not None])
+    _increment_version(params)
