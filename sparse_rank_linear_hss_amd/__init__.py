@@ -905,7 +905,9 @@ class HSSAdapters:
 
     U: [count, m, r], Vt: [count, r, n], contiguous bf16, the layouts of an
     HSSMatrix's own factors; scale: float32 [count], None = 1.  An adapter of a
-    smaller rank is padded with zeros."""
+    smaller rank is padded with zeros.  Calls read them where they are now, with
+    the values of the moment (hss_adamw changes them in place); tensors that are
+    given other memory need a new bank."""
 
     __slots__ = ("U", "Vt", "scale", "count", "m", "n", "r", "dtype", "index", "struct", "_ref", "_sizes")
 
@@ -1010,6 +1012,8 @@ def hss_adapters_grad(L: HSSAdapters, X: torch.Tensor, G: torch.Tensor, ids: tor
     """The backward pass of hss_adapters_apply for the upstream gradient G
     (b x m): dX (b x n, bf16) = base + scale[l] (G[t] U_l) Vt_l for each row,
     and dU, dVt in fp32, in the layouts of U and Vt, zeros for an adapter without rows.
+    They are written, not added to: a batch of more than 2048 rows takes several
+    calls, whose dU and dVt are to be summed.
 
     base: the shared projection's input gradient (None = 0), e.g. the dX of
     hss_backward; dX may be base itself.  Pass False to skip an output.  out:
@@ -1166,7 +1170,8 @@ def hss_adamw(state: AdamWState, grads, lr, step, betas=(0.9, 0.999), eps=1e-8, 
 
     With bits=8 the new moments are rounded up or down at random, in proportion,
     by a hash of the element's position and the step; the same call gives the
-    same bits.
+    same bits.  sqrt(v) settles 1 to 2 % above its fp32 value for elements down to
+    10^-4 of their block's largest, and further above for smaller ones.
 
     To autograd the parameters with a gradient are changed in place: a backward
     pass that has saved their old values raises an error.  (The replay of a

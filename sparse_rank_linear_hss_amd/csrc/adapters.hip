@@ -46,7 +46,10 @@ static constexpr int kAdUnit = 64;      // columns of K that a wave takes at a t
 // 256, 512, 1024: 2048 rows 4096 x 11008 43.1, 41.0, 40.1, 43.7 us.  At least 4, 8, 16
 // units: 77 rows 2731 x 5003 14.7, 15.3, 16.6.
 static constexpr int kAdBlocks = 512;
-static constexpr int kAdChunk = 256;    // ranks of T that k_ad_expand keeps in LDS: 2 KB a row
+// Ranks of T that k_ad_expand keeps in LDS, 1 KB a row (two terms of two bytes): with
+// U's 32 KB two blocks of 32 rows (65 KB) or three of 16 (49 KB) share a compute unit's
+// 160 KB, as many as their registers allow.
+static constexpr int kAdChunk = 256;
 // Units of K that the backward pass does not split, so that k_ad_rank makes the terms
 // and a launch is saved: not split and split, 64 rows of 4 512 x 512 9.2 and 11.0 us,
 // 16 rows 1024 x 1024 10.1 and 10.6, past the limit 2048 x 2048 12.8 and 10.9.
