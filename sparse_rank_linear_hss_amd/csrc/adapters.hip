@@ -417,6 +417,23 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
 #pragma unroll
     for (int j = 0; j < XL; ++j) *reinterpret_cast<u32x4*>(xs + ad_slot(8 * j + r8, c8)) = x[j];
   };
+  auto multiply = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4 xf[MF], vf[NR];
+#pragma unroll
+      for (int f = 0; f < MF; ++f) xf[f] = *reinterpret_cast<const u32x4*>(xs + ad_slot(16 * f + i, 4 * h + q));
+#pragma unroll
+      for (int g = 0; g < NR; ++g) vf[g] = *reinterpret_cast<const u32x4*>(vs + ad_slot(16 * g + i, 4 * h + q));
+      __builtin_amdgcn_sched_barrier(0);  // the reads first: one wait instead of one for each product
+#pragma unroll
+      for (int g = 0; g < NR; ++g)
+#pragma unroll
+        for (int f = 0; f < MF; ++f)
+          acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf[g]), as_bf16(xf[f]), acc[f][g], 0, 0, 0);
+    }
+    ad_wave_sync();
+  };
 
   if (!side) {
     const uint16_t* V = a.Vt + (int64_t)at.adapter * a.r * K;
@@ -434,23 +451,6 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
       put_x();
 #pragma unroll
       for (int j = 0; j < VL; ++j) *reinterpret_cast<u32x4*>(vs + ad_slot(8 * j + r8, c8)) = v[j];
-      ad_wave_sync();
-    };
-    auto multiply = [&]() {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 xf[MF], vf[NR];
-#pragma unroll
-        for (int f = 0; f < MF; ++f) xf[f] = *reinterpret_cast<const u32x4*>(xs + ad_slot(16 * f + i, 4 * h + q));
-#pragma unroll
-        for (int g = 0; g < NR; ++g) vf[g] = *reinterpret_cast<const u32x4*>(vs + ad_slot(16 * g + i, 4 * h + q));
-        __builtin_amdgcn_sched_barrier(0);  // the reads first: one wait instead of one for each product
-#pragma unroll
-        for (int g = 0; g < NR; ++g)
-#pragma unroll
-          for (int f = 0; f < MF; ++f)
-            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf[g]), as_bf16(xf[f]), acc[f][g], 0, 0, 0);
-      }
       ad_wave_sync();
     };
     int u = u0 + w;
@@ -503,23 +503,6 @@ __global__ __launch_bounds__(256, NR == 4 ? 3 : 4) void k_ad_rank(AdArgs a) {
 #pragma unroll
         for (int f = 0; f < 8; ++f)
           if (off + f >= 0) *reinterpret_cast<u32x4*>(vs + ad_slot(off + f, jb)) = ad_column<8>(v, f);
-      }
-      ad_wave_sync();
-    };
-    auto multiply = [&]() {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 xf[MF], vf[NR];
-#pragma unroll
-        for (int f = 0; f < MF; ++f) xf[f] = *reinterpret_cast<const u32x4*>(xs + ad_slot(16 * f + i, 4 * h + q));
-#pragma unroll
-        for (int g = 0; g < NR; ++g) vf[g] = *reinterpret_cast<const u32x4*>(vs + ad_slot(16 * g + i, 4 * h + q));
-        __builtin_amdgcn_sched_barrier(0);  // the reads first: one wait instead of one for each product
-#pragma unroll
-        for (int g = 0; g < NR; ++g)
-#pragma unroll
-          for (int f = 0; f < MF; ++f)
-            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf[g]), as_bf16(xf[f]), acc[f][g], 0, 0, 0);
       }
       ad_wave_sync();
     };
